@@ -513,6 +513,159 @@ int fastar_annca_quant_attention(fastar_dtype dt, const void* q, const void* k_p
                                  uint32_t* sel_mask, void* ws, size_t ws_bytes,
                                  int32_t* dev_status, cudaStream_t stream);
 
+/*
+ * Branched rollouts: B rollouts ("branches") that continue one history.
+ *
+ * Passage: FAST-AR summary (paperlayer.ai) section 3 (attention over the
+ * cache of past frames together with the current frame's keys) and appendix
+ * A, Lemma A.1 (+ log m_t bias of merged groups).  The branches share the
+ * history as a prefix (the merged cache of one layer, or plain key and value
+ * rows), and each keeps its own keys and values in pages.  One layer's step
+ * is fastar_page_append (rotate the new queries and keys by their positions,
+ * put keys and values into the pages) and fastar_branch_attention.
+ *
+ * Tokens of all branches lie one after the other: branch b owns the tokens
+ * cu[b] .. cu[b+1] - 1 of N; cu [B + 1] int32 on the device, ascending from
+ * cu[0] = 0 (FASTAR_ERR_DEVICE_ARG otherwise).  Tokens from cu[B] on are
+ * padding: they are neither read into a result nor written.
+ */
+
+/*
+ * Rotary positions with several axes, e.g. time, height and width.  The
+ * first 2 * pairs channels of a row turn, the rest is copied; pair p takes
+ * its position from axis[p] and turns by turn[p] / 2^64 of a full turn per
+ * position.  FASTAR_PAIRS_ADJACENT: pair p is channels (2 p, 2 p + 1);
+ * FASTAR_PAIRS_HALVES: channels (p, p + pairs).  Fill it with
+ * fastar_rope_plan_init and keep it: it is read during a call only.
+ */
+#define FASTAR_ROPE_MAX_AXES 4
+#define FASTAR_ROPE_MAX_PAIRS 64
+#define FASTAR_PAIRS_ADJACENT 0
+#define FASTAR_PAIRS_HALVES 1
+typedef struct {
+  int D, axes, pairs, pairing;
+  uint64_t turn[FASTAR_ROPE_MAX_PAIRS];
+  uint8_t axis[FASTAR_ROPE_MAX_PAIRS];
+} fastar_rope_plan;
+
+/*
+ * fastar_rope_plan_init -- fill a plan (host memory only, no device needed).
+ * dims[a] channels (even, >= 0) turn by axis a, axis after axis from pair 0;
+ * their sum is at most D, positive, and with FASTAR_PAIRS_HALVES a multiple
+ * of 16.  freq [sum / 2]: radians per position of each pair, finite; NULL:
+ * pair i of axis a has 10000^(-2 i / dims[a]).  1 <= axes <=
+ * FASTAR_ROPE_MAX_AXES.  FASTAR_ERR_UNSUPPORTED for D not in {64, 128},
+ * FASTAR_ERR_ARG for anything else that does not hold.
+ */
+int fastar_rope_plan_init(fastar_rope_plan* plan, int D, int axes,
+                          const int* dims, int pairing, const double* freq);
+
+/*
+ * fastar_rope -- rotate rows by their positions.
+ *
+ *   (y0, y1) = (x0 cos - x1 sin, x0 sin + x1 cos), angle pos[n][axis(p)] freq(p)
+ *
+ * with -sin when inverse is not 0 (the transposed rotation: it undoes the
+ * forward one, and is its gradient).  x, out: row n of head h at element
+ * h * x_head + n * x_token, D contiguous elements (so the token-major output
+ * of a projection goes straight to head-major rows); every row starts on a
+ * 16-byte boundary.  out may be x itself with the same strides; it must not
+ * overlap x otherwise, nor itself.  pos [N][axes] int32, any value: angles
+ * are taken modulo one turn in 64-bit integers, so far positions lose
+ * nothing.  Products and sums in fp32, rounded once.
+ */
+int fastar_rope(fastar_dtype dt, const void* x, int64_t x_head, int64_t x_token,
+                int H, int N, int D, const int32_t* pos,
+                const fastar_rope_plan* plan, int inverse, void* out,
+                int64_t out_head, int64_t out_token, int32_t* dev_status,
+                cudaStream_t stream);
+
+/*
+ * The pages of one layer's branches, all buffers caller-owned device memory.
+ * Position p of branch b is row p % page of page table[b][p / page].
+ *   K, V    [n_pages][H][page][D] dt
+ *   table   [B][max_pages] int32  page ids; read only where a position needs it
+ *   len     [B] int32             positions of each branch, the new tokens included
+ * page is a power of two, 16..256; n_pages * H * page < 2^31; max_pages *
+ * page < 2^31.  Pages may be shared by branches that only read them.
+ */
+typedef struct {
+  int H, D, page, n_pages, B, max_pages;
+  fastar_dtype dt;
+  void* K;
+  void* V;
+  const int32_t* table;
+  const int32_t* len;
+} fastar_pages;
+
+/*
+ * fastar_page_append -- rotate new keys and put them and their values into
+ * the pages (and rotate the queries in the same pass).
+ *
+ * Token cu[b] + i of branch b (n_b tokens) becomes position len[b] - n_b + i.
+ * k, v: rows as in fastar_rope, H = pages->H heads; k is rotated by plan and
+ * pos [N][axes] (both NULL: stored as it is), v is copied.  Optional q (Hq
+ * heads; NULL and 0: none): rotated into q_out [Hq][N][D].  Rows of the pages
+ * and of q_out that no token owns stay as they were.  A position outside the
+ * table, or a page id outside 0..n_pages-1, sets FASTAR_ERR_DEVICE_ARG and
+ * that token is skipped.  Two tokens of one call must not share a row.
+ */
+int fastar_page_append(const fastar_pages* pages, const void* k, int64_t k_head,
+                       int64_t k_token, const void* v, int64_t v_head,
+                       int64_t v_token, int N, const int32_t* cu,
+                       const int32_t* pos, const fastar_rope_plan* plan,
+                       const void* q, int64_t q_head, int64_t q_token, int Hq,
+                       void* q_out, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * The rows that every branch attends: K, V [H][C][D] dt; size [H] int32 live
+ * rows of each head (NULL: C); m [H][C] int32 counts, added as + ln m (NULL:
+ * 1 everywhere; m <= 0 hides the row).  A fastar_cache is one: its K, V, m
+ * and size.  H * C < 2^31.
+ */
+typedef struct {
+  int H, C, D;
+  fastar_dtype dt;
+  const void* K;
+  const void* V;
+  const int32_t* m;
+  const int32_t* size;
+} fastar_prefix;
+
+/*
+ * fastar_branch_attention -- attention of every branch's new tokens over the
+ * shared prefix and the branch's own pages.
+ *
+ *   x(j) = scale q . K[j] + ln m[j]          prefix rows j < size[h]
+ *   x(p) = scale q . K_b[p]                  positions p < seen of branch b
+ *   out = sum softmax(x) v,  lse = ln sum exp(x)    (0 and -inf over nothing)
+ *
+ * Query head h' attends key/value head h' / (Hq / H).  Token i of branch b's
+ * n_b new tokens stands at position t = len[b] - n_b + i; block = 0: it sees
+ * all len[b] positions; block = n > 0: positions p with p / n <= t / n (1:
+ * causal by token; the tokens of a frame: causal by frame, tokens of one
+ * frame see each other; a t < 0 sees the prefix only).  The prefix is read
+ * once for the tokens of all branches.
+ *
+ * q [Hq][N][D] dt, out [Hq][N][D] dt, optional lse [Hq][N] float; rows of
+ * padding tokens are not written.  prefix NULL: none.  What lies behind
+ * size[h] and behind the positions that a branch sees may hold anything.
+ * Values that some token sees must be finite (a hidden value times 0 is
+ * added where another token of the call sees it).
+ * ws: fastar_workspace_size(FASTAR_OP_BRANCH, Hq, N, D, H, 0, 0) bytes; two
+ * calls that may overlap need one each.  bf16: probabilities are rounded to
+ * bf16 for the product with the values; scores, statistics and sums are fp32.
+ * D in {64, 128}; Hq a multiple of H; N * (Hq / H) < 2^31 - 256.
+ * FASTAR_ERR_DEVICE_ARG: cu not ascending within 0..N, a length outside
+ * 0..max_pages * page, a size outside 0..C, a page id outside the pool.
+ */
+#define FASTAR_OP_BRANCH 7
+int fastar_branch_attention(fastar_dtype dt, const void* q, int Hq, int N,
+                            const int32_t* cu, const fastar_prefix* prefix,
+                            const fastar_pages* pages, float scale, int block,
+                            void* out, float* lse, void* ws, size_t ws_bytes,
+                            int32_t* dev_status, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

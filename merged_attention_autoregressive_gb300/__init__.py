@@ -23,6 +23,9 @@ REP_LAST, REP_MEAN = 0, 1
 REPS = {"last": REP_LAST, "mean": REP_MEAN}
 SEARCH_PREV, SEARCH_LSH, SEARCH_QUANT = 0, 1, 2
 OP_QUANT = 6
+OP_BRANCH = 7
+ROPE_MAX_AXES, ROPE_MAX_PAIRS = 4, 64
+PAIRINGS = {"adjacent": 0, "halves": 1}
 
 
 def search_code(search: str) -> int:
@@ -44,7 +47,8 @@ EXPORTS = ["fastar_status_string", "fastar_version", "fastar_launch_count",
            "fastar_tempcache_merge", "fastar_tempcache_merge_ev", "fastar_annca_prune", "fastar_annca_attention",
            "fastar_annsa_attention", "fastar_check_bounded_wait", "fastar_tempcache_merge_rep",
            "fastar_annsa_attention_part", "fastar_annsa_combine", "fastar_tempcache_merge_search",
-           "fastar_annsa_quant_attention", "fastar_annca_quant_attention"]
+           "fastar_annsa_quant_attention", "fastar_annca_quant_attention",
+           "fastar_rope_plan_init", "fastar_rope", "fastar_page_append", "fastar_branch_attention"]
 
 
 class FastarError(RuntimeError):
@@ -63,8 +67,28 @@ class CacheStruct(ctypes.Structure):
                 ("offsets", ctypes.c_void_p)]
 
 
+class RopePlanStruct(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int), ("axes", ctypes.c_int), ("pairs", ctypes.c_int),
+                ("pairing", ctypes.c_int), ("turn", ctypes.c_uint64 * ROPE_MAX_PAIRS),
+                ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS)]
+
+
+class PagesStruct(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("D", ctypes.c_int), ("page", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("B", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("dt", ctypes.c_int), ("K", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("len", ctypes.c_void_p)]
+
+
+class PrefixStruct(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("C", ctypes.c_int), ("D", ctypes.c_int), ("dt", ctypes.c_int),
+                ("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("size", ctypes.c_void_p)]
+
+
 _lib = None
 _VP, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_I64 = ctypes.c_int64
 MAX_HASH_JOBS = 4
 
 
@@ -117,6 +141,11 @@ def lib() -> ctypes.CDLL:
                                                    _VP, _VP, _SZ, _VP, _VP]
         L.fastar_annca_quant_attention.argtypes = [_I, _VP, _VP, _VP, _I, _I, _I, _I, _F, _I, _I, _VP, _VP, _VP,
                                                    _SZ, _VP, _VP]
+        L.fastar_rope_plan_init.argtypes = [_VP, _I, _I, ctypes.POINTER(_I), _I, ctypes.POINTER(ctypes.c_double)]
+        L.fastar_rope.argtypes = [_I, _VP, _I64, _I64, _I, _I, _I, _VP, _VP, _I, _VP, _I64, _I64, _VP, _VP]
+        L.fastar_page_append.argtypes = [_VP, _VP, _I64, _I64, _VP, _I64, _I64, _I, _VP, _VP, _VP, _VP, _I64, _I64,
+                                         _I, _VP, _VP, _VP]
+        L.fastar_branch_attention.argtypes = [_I, _VP, _I, _I, _VP, _VP, _VP, _F, _I, _VP, _VP, _VP, _SZ, _VP, _VP]
         for name in EXPORTS[7:]:
             getattr(L, name).restype = _I
         _lib = L
@@ -415,3 +444,188 @@ def fastar_annca_quant_attention(q, k_p, v_p, scale, topk, bits, out, sel_mask=N
     _check(lib().fastar_annca_quant_attention(_dt(q), _p(q), _p(k_p), _p(v_p), H, Nq, P, D, scale, topk, bits,
                                               _p(out), _p(sel_mask), _p(ws), nbytes, _p(status), _stream(stream)),
            "fastar_annca_quant_attention")
+
+
+# ---- branched rollouts: rotary positions, pages, attention over a shared prefix
+
+class RopePlan:
+    """Rotary positions with several axes: dims[a] channels turn by axis a
+    (e.g. (44, 42, 42) for time, height and width of a 128-channel head), the
+    channels behind their sum are copied.
+
+    pairing: "adjacent" (channels 2p, 2p+1) or "halves" (channels p, p + sum/2);
+    freqs: radians per position of each of the sum/2 pairs; by default pair i
+    of axis a has base**(-2 i / dims[a])."""
+
+    def __init__(self, D, dims, base=10000.0, pairing="adjacent", freqs=None):
+        dims = [int(d) for d in dims]
+        if pairing not in PAIRINGS:
+            raise ValueError(f"unknown pairing {pairing!r}")
+        if freqs is None:
+            freqs = [float(base) ** (-2.0 * i / d) for d in dims for i in range(d // 2)]
+        freqs = [float(f) for f in freqs]
+        if len(freqs) != sum(dims) // 2:
+            raise ValueError(f"{len(freqs)} frequencies for {sum(dims) // 2} pairs")
+        self.D, self.dims, self.pairing, self.axes = D, tuple(dims), pairing, len(dims)
+        self.struct = RopePlanStruct()
+        self.addr = ctypes.addressof(self.struct)
+        _check(lib().fastar_rope_plan_init(self.addr, D, len(dims), (_I * len(dims))(*dims), PAIRINGS[pairing],
+                                           (ctypes.c_double * len(freqs))(*freqs)), "fastar_rope_plan_init")
+
+
+def _dev(t):
+    """Pointer of a contiguous device tensor (None: NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    return _p(t)
+
+
+def _rows(t, what):
+    """Pointer and (head, token) strides of rows [H][N][D]."""
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{what} must be [heads][tokens][D] with contiguous rows")
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _positions(pos, N, plan):
+    if pos is None:
+        return None
+    if pos.dtype != torch.int32 or tuple(pos.shape) != (N, plan.axes):
+        raise ValueError(f"positions must be int32 [{N}][{plan.axes}]")
+    return _dev(pos)
+
+
+def _int32(t, n, what):
+    if t.dtype != torch.int32 or t.numel() != n:
+        raise ValueError(f"{what} must be int32 with {n} entries")
+    return _dev(t)
+
+
+def fastar_rope(x, pos, plan: RopePlan, out, inverse=False, status=None, stream=None):
+    """out = the rows of x [H][N][D] rotated by pos [N][axes] (int32).
+
+    x and out may have any head and token strides (the transpose of a
+    projection's [N][H][D] output, for one); out may be x itself.
+    inverse: turn back, which is also the gradient of the forward rotation."""
+    H, N, D = x.shape
+    if out.shape != x.shape or out.dtype != x.dtype or D != plan.D:
+        raise ValueError("x, out and the plan must agree in shape and dtype")
+    _check(lib().fastar_rope(_dt(x), *_rows(x, "x"), H, N, D, _positions(pos, N, plan), plan.addr,
+                             1 if inverse else 0, *_rows(out, "out"), _dev(status), _stream(stream)), "fastar_rope")
+
+
+class PagedKV:
+    """Keys and values of a layer's branches in pages (torch-owned):
+    K, V [n_pages][H][page][D], table [B][max_pages] int32 page ids, len [B]
+    int32 positions of each branch, the new tokens of a call included.  The
+    caller hands out the pages (table) and counts the positions (len)."""
+
+    def __init__(self, H, D, page, n_pages, B, max_pages, dtype=torch.bfloat16, device="cuda"):
+        dev = torch.device(device)
+        self._set(torch.zeros(n_pages, H, page, D, dtype=dtype, device=dev),
+                  torch.zeros(n_pages, H, page, D, dtype=dtype, device=dev),
+                  torch.zeros(B, max_pages, dtype=torch.int32, device=dev),
+                  torch.zeros(B, dtype=torch.int32, device=dev))
+
+    @classmethod
+    def view(cls, K, V, table, length):
+        """Pages over existing tensors (nothing is allocated)."""
+        p = cls.__new__(cls)
+        p._set(K, V, table, length)
+        return p
+
+    def _set(self, K, V, table, length):
+        if K.shape != V.shape or K.dtype != V.dtype or K.dim() != 4 or table.dim() != 2:
+            raise ValueError("K and V are [n_pages][H][page][D], the table [B][max_pages]")
+        self.K, self.V, self.table, self.len = K, V, table, length
+        self.n_pages, self.H, self.page, self.D = K.shape
+        self.B, self.max_pages = table.shape
+        self.dtype = K.dtype
+        _int32(length, self.B, "the lengths")
+        self.struct = PagesStruct(self.H, self.D, self.page, self.n_pages, self.B, self.max_pages, _dt(K), _dev(K),
+                                  _dev(V), _int32(table, table.numel(), "the table"), _dev(length))
+        self.addr = ctypes.addressof(self.struct)
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.K, self.V, self.table, self.len))
+
+
+class Prefix:
+    """The rows that every branch attends: K, V [H][C][D], optional counts m
+    [H][C] int32 (+ ln m) and live rows size [H] int32."""
+
+    def __init__(self, K, V, m=None, size=None):
+        if K.shape != V.shape or K.dtype != V.dtype or K.dim() != 3:
+            raise ValueError("K and V are [H][C][D]")
+        self.K, self.V, self.m, self.size = K, V, m, size
+        H, C, D = K.shape
+        self.struct = PrefixStruct(H, C, D, _dt(K), _dev(K), _dev(V), None if m is None else _int32(m, H * C, "m"),
+                                   None if size is None else _int32(size, H, "size"))
+        self.addr = ctypes.addressof(self.struct)
+
+    @classmethod
+    def of(cls, cache: Cache):
+        """The live groups of a merged cache, each with its + ln m."""
+        return cls(cache.K, cache.V, m=cache.m, size=cache.size)
+
+
+def fastar_page_append(pages: PagedKV, k, v, cu, pos=None, plan: RopePlan | None = None, q=None, q_out=None,
+                       status=None, stream=None):
+    """Put the keys and values of new tokens k, v [H][N][D] (any head and
+    token strides) into the pages: token cu[b] + i of branch b becomes
+    position len[b] - n_b + i.  The keys are rotated by pos and plan (none:
+    stored as they are); optional queries q [Hq][N][D] are rotated into q_out
+    [Hq][N][D] in the same pass."""
+    H, N, D = k.shape
+    if v.shape != k.shape or (H, D) != (pages.H, pages.D) or not k.dtype == v.dtype == pages.dtype:
+        raise ValueError("k and v do not fit the pages")
+    if (plan is None) != (pos is None):
+        raise ValueError("positions and their plan come together")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if plan is not None and plan.D != D:
+        raise ValueError("the plan has another head dimension")
+    qa, Hq = (None, 0, 0), 0
+    if q is not None:
+        if q.shape != q_out.shape or q.shape[1:] != k.shape[1:] or not q.dtype == q_out.dtype == k.dtype:
+            raise ValueError("q and q_out do not fit k")
+        qa, Hq = _rows(q, "q"), q.shape[0]
+    _check(lib().fastar_page_append(pages.addr, *_rows(k, "k"), *_rows(v, "v"), N, _int32(cu, pages.B + 1, "cu"),
+                                    _positions(pos, N, plan), None if plan is None else plan.addr, *qa, Hq,
+                                    _dev(q_out), _dev(status), _stream(stream)), "fastar_page_append")
+
+
+def branch_workspace_size(Hq: int, H: int, N: int, D: int) -> int:
+    """Bytes of workspace of fastar_branch_attention for N tokens."""
+    return fastar_workspace_size(OP_BRANCH, Hq, N, D, H, 0, 0)
+
+
+def fastar_branch_attention(q, cu, prefix: Prefix | None, pages: PagedKV, scale, out, lse=None, block=0, ws=None,
+                            status=None, stream=None):
+    """out [Hq][N][D] (and lse [Hq][N]): every branch's tokens over the shared
+    prefix and the branch's own pages.
+
+    cu [B + 1] int32: token cu[b] + i of q is new token i of branch b, whose
+    keys are already in the pages (fastar_page_append).  block 0: a token sees
+    every position of its branch; n: those of its own and earlier blocks of n
+    positions (1: causal).  ws: a uint8 device tensor of at least
+    branch_workspace_size(Hq, H, N, D) bytes; one is allocated for the call
+    when it is None."""
+    Hq, N, D = q.shape
+    if out.shape != q.shape or not out.dtype == q.dtype == pages.dtype or D != pages.D:
+        raise ValueError("q, out and the pages must agree in shape and dtype")
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != Hq * N):
+        raise ValueError("lse must be float32 [Hq][N]")
+    if ws is None:
+        ws = torch.empty(max(1, branch_workspace_size(Hq, pages.H, N, D)), dtype=torch.uint8, device=q.device)
+        if stream is not None:  # the allocator must not hand it out again before that stream is done with it
+            ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                             torch.cuda.ExternalStream(int(_stream(stream)), device=q.device))
+    _check(lib().fastar_branch_attention(pages.struct.dt, _dev(q), Hq, N, _int32(cu, pages.B + 1, "cu"),
+                                         None if prefix is None else prefix.addr, pages.addr, scale, block, _dev(out),
+                                         _dev(lse), _dev(ws), ws.numel() * ws.element_size(), _dev(status),
+                                         _stream(stream)), "fastar_branch_attention")

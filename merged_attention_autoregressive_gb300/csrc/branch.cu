@@ -1,0 +1,258 @@
+// fastar_branch_attention: the plan of its units, the join of its partials,
+// workspace layout and dispatch.
+#include <math.h>
+
+#include "branch.cuh"
+
+namespace fastar {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+__device__ __forceinline__ long long block_scan_ll(long long v, long long* sh, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) sh[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    long long w = sh[lane], wi = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, wi, o);
+      if (lane >= o) wi += x;
+    }
+    sh[lane] = wi - w;
+    if (lane == 31) sh[32] = wi;
+  }
+  __syncthreads();
+  const long long res = sh[warp] + inc - v;
+  *total = sh[32];
+  __syncthreads();
+  return res;
+}
+
+// Checks the lengths and writes the prefix sums of the units: one CTA, a warp
+// per branch and a lane per row tile that the branch touches.
+__global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a, int32_t* st) {
+  pdl_wait();
+  __shared__ long long sh[33];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (block_status_bad(st)) return;
+  for (int t = tid; t <= a.ntiles; t += kPlanThreads) a.tile[t] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int b = warp; b < a.B; b += kPlanThreads / 32) {
+    const int lo = a.cu[b], hi = a.cu[b + 1], len = a.len[b];
+    if (lo < 0 || hi < lo || hi > a.N || (b == 0 && lo != 0) || len < 0 ||
+        (long long)len > ((long long)a.max_pages << a.page_shift)) {
+      bad = true;
+      continue;
+    }
+    if (hi == lo) continue;
+    const int t0 = (int)((long long)lo * a.g / a.TM), t1 = (int)(((long long)hi * a.g - 1) / a.TM);
+    for (int t = t0 + lane; t <= t1; t += 32) {
+      const int T1 = (int)((((long long)t + 1) * a.TM + a.g - 1) / a.g);
+      const int keys = branch_limit(min(hi, T1) - 1 - lo, hi - lo, len, a.block);
+      atomicAdd((unsigned long long*)&a.tile[t], (unsigned long long)((keys + a.TN - 1) / a.TN));
+    }
+  }
+  for (int h = tid; h < a.H; h += kPlanThreads)
+    if (a.size && (a.size[h] < 0 || a.size[h] > a.C)) bad = true;
+  if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
+  if (__syncthreads_or(bad)) {
+    // nothing to do for the kernels behind, also without a status word
+    for (int h = tid; h <= a.H + 2; h += kPlanThreads) a.head[h] = 0;
+    return;
+  }
+  const long long rows = (long long)a.cu[a.B] * a.g;
+  const int nt = (int)((rows + a.TM - 1) / a.TM);
+  long long carry = 0, total;
+  for (int t0 = 0; t0 < nt; t0 += kPlanThreads) {
+    const int t = t0 + tid;
+    const long long v = t < nt ? __ldcg(&a.tile[t]) : 0;  // summed in L2
+    const long long x = block_scan_ll(v, sh, &total);
+    if (t < nt) a.tile[t] = carry + x;
+    carry += total;
+  }
+  if (tid == 0) a.tile[nt] = carry;
+  const long long pages = carry;
+  carry = 0;
+  for (int h0 = 0; h0 < a.H; h0 += kPlanThreads) {
+    const int h = h0 + tid;
+    const long long v = h < a.H ? (long long)nt * prefix_units(prefix_size(a, h), a.TN) + pages : 0;
+    const long long x = block_scan_ll(v, sh, &total);
+    if (h < a.H) a.head[h] = carry + x;
+    carry += total;
+  }
+  if (tid == 0) {
+    a.head[a.H] = nt > 0 ? carry : 0;
+    a.head[a.H + 1] = rows;
+    a.head[a.H + 2] = nt;
+  }
+  pdl_trigger();
+}
+
+// Joins the partials of every item that is cut: grid (cuts, row groups), a
+// warp per row.  The CTA of the item's first cut does the item.
+template <typename T>
+__global__ void __launch_bounds__(256) branch_combine_kernel(BranchArgs a, int32_t* st) {
+  pdl_wait();
+  if (status_bad(st)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x + 1;
+  const long long U = a.head[a.H];
+  const int nt = (int)a.head[a.H + 2];
+  const long long u = U * c / a.G, up = U * (c - 1) / a.G;
+  if (u == up || u >= U) return;
+  const int h = warp_count_le(a.head, a.H, u) - 1;
+  const int p = prefix_units(prefix_size(a, h), a.TN);
+  const long long off = u - a.head[h];
+  int l = 0, r = nt;
+  while (r - l > 1) {
+    const int step = (r - l + 31) / 32;
+    const int at = l + lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, at < r && (long long)at * p + a.tile[at] <= off);
+    const int k = max(1, __popc(m));
+    r = min(r, l + k * step);
+    l = l + (k - 1) * step;
+  }
+  const int t = l;
+  const long long start = a.head[h] + (long long)t * p + a.tile[t];
+  const long long end = start + p + a.tile[t + 1] - a.tile[t];
+  if (start < up || start == u) return;  // an earlier cut's, or the cut lies between two items
+  const long long rows = a.head[a.H + 1], r0 = (long long)t * a.TM;
+  const int nr = (int)min((long long)a.TM, rows - r0);
+  for (int i = blockIdx.y * 8 + warp; i < nr; i += gridDim.y * 8) {
+    // the first run's slot, then one per later run
+    float m = -INFINITY;
+    for (int j = c - 1; j < a.G; ++j) {
+      const long long b = U * j / a.G;
+      if (b >= end) break;
+      if (U * (j + 1) / a.G == b) continue;
+      const int slot = 2 * j + (j == c - 1 && start != b ? 1 : 0);
+      m = fmaxf(m, a.pml[(size_t)slot * a.slot_rows + i].x);
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+    float lsum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = c - 1; j < a.G; ++j) {
+      const long long b = U * j / a.G;
+      if (b >= end) break;
+      if (U * (j + 1) / a.G == b) continue;
+      const int slot = 2 * j + (j == c - 1 && start != b ? 1 : 0);
+      const float2 ml = a.pml[(size_t)slot * a.slot_rows + i];
+      if (ml.y == 0.f) continue;  // the row saw nothing in that run
+      const float w = exp2f(ml.x - base);
+      lsum += w * ml.y;
+      if (lane * 4 < a.D) {
+        const float4 x = *reinterpret_cast<const float4*>(a.po + ((size_t)slot * a.slot_rows + i) * a.D + lane * 4);
+        o[0] += w * x.x;
+        o[1] += w * x.y;
+        o[2] += w * x.z;
+        o[3] += w * x.w;
+      }
+    }
+    const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // a NaN sum stays one
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] *= inv;
+    const long long row = r0 + i;
+    const size_t at = (size_t)(h * a.g + (int)(row % a.g)) * a.N + (size_t)(row / a.g);
+    if (lane * 4 < a.D) st_vec<T, 4>((T*)a.out + at * a.D + lane * 4, o);
+    if (a.lse && lane == 0) a.lse[at] = lsum == 0.f ? -INFINITY : (base + log2f(lsum)) * 0.6931471805599453f;
+  }
+  pdl_trigger();
+}
+
+}  // namespace
+
+int launch_branch_plan(const BranchArgs& a, int32_t* st, cudaStream_t s) {
+  if (launch_pdl(branch_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, st) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FASTAR_ERR_CUDA;
+  }
+  FASTAR_LAUNCHED(s, "branch_plan");
+  return FASTAR_OK;
+}
+
+int launch_branch_combine(const BranchArgs& a, fastar_dtype dt, int32_t* st, cudaStream_t s) {
+  const int rows = (int)min((long long)a.TM, (long long)a.N * a.g);
+  const dim3 grid(a.G - 1, (rows + 7) / 8);
+  cudaError_t rc = dt == FASTAR_BF16 ? launch_pdl(branch_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a, st)
+                                     : launch_pdl(branch_combine_kernel<float>, grid, dim3(256), 0, s, a, st);
+  if (rc != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FASTAR_ERR_CUDA;
+  }
+  FASTAR_LAUNCHED(s, "branch_combine");
+  return FASTAR_OK;
+}
+
+namespace {
+// The launch geometry of a call: the SIMT kernel runs two CTAs per SM.
+constexpr int kSms = 152, kSimtG = 2 * kSms, kSimtTM = 64, kSimtTN = 64;
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+}  // namespace
+
+size_t branch_ws_bytes(int Hq, int H, int N, int D) {
+  if (Hq < 1 || H < 1 || N < 1 || D < 1 || Hq % H) return 0;
+  const long long rows = (long long)N * (Hq / H);
+  const long long slot_rows = rows < kSimtTM ? rows : kSimtTM;
+  const size_t lists = up256((size_t)(H + 3) * 8) + up256((size_t)(rows / kSimtTM + 2) * 8);
+  return lists + up256((size_t)2 * kSimtG * slot_rows * D * 4) + up256((size_t)2 * kSimtG * slot_rows * 8);
+}
+
+int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* cu, const fastar_prefix* px,
+                  const fastar_pages* pg, float scale, int block, void* out, float* lse, void* ws, int32_t* st,
+                  cudaStream_t s) {
+  BranchArgs a = {};
+  a.q = q;
+  a.cu = cu;
+  a.len = pg->len;
+  a.table = pg->table;
+  a.K = pg->K;
+  a.V = pg->V;
+  if (px) {
+    a.pK = px->K;
+    a.pV = px->V;
+    a.m = px->m;
+    a.size = px->size;
+    a.C = px->C;
+  }
+  a.N = N;
+  a.Hq = Hq;
+  a.H = pg->H;
+  a.g = Hq / pg->H;
+  a.B = pg->B;
+  a.D = pg->D;
+  a.max_pages = pg->max_pages;
+  a.n_pages = pg->n_pages;
+  while ((1 << a.page_shift) < pg->page) ++a.page_shift;
+  a.block = block;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.TM = kSimtTM;
+  a.TN = kSimtTN;
+  a.G = kSimtG;
+  const long long rows = (long long)N * a.g;
+  a.ntiles = (int)((rows + a.TM - 1) / a.TM);
+  a.slot_rows = (int)(rows < a.TM ? rows : a.TM);
+  char* w = (char*)ws;
+  a.head = (long long*)w;
+  w += up256((size_t)(a.H + 3) * 8);
+  a.tile = (long long*)w;
+  w += up256((size_t)(rows / kSimtTM + 2) * 8);
+  a.po = (float*)w;
+  w += up256((size_t)2 * a.G * a.slot_rows * a.D * 4);
+  a.pml = (float2*)w;
+  int rc = launch_branch_plan(a, st, s);
+  if (rc == FASTAR_OK) rc = launch_branch_simt(a, dt, st, s);
+  if (rc == FASTAR_OK) rc = launch_branch_combine(a, dt, st, s);
+  return rc;
+}
+
+}  // namespace fastar

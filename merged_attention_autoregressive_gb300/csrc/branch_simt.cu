@@ -1,0 +1,242 @@
+// fastar_branch_attention on the FP32 pipes.
+//
+// One CTA of 256 threads walks its run of units (branch.cuh), 64 query rows
+// by 64 keys at a time: the scores of a unit (4 x 4 per thread), one pass of
+// the running softmax, and the product with the values (4 rows x D/16
+// columns per thread, O in registers).  Scores, statistics, probabilities and
+// O are fp32; the row statistics of a thread's 4 rows are joined over the 16
+// threads of a row by shuffles.  Keys and probabilities share one buffer, so
+// two CTAs fit on an SM.
+#include <math.h>
+
+#include "branch.cuh"
+
+namespace fastar {
+namespace {
+
+constexpr int kTM = 64, kTN = 64, kThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int D>
+struct SimtSmem {
+  float Q[kTM][D + 4];
+  float K[kTN][D + 4];  // then the probabilities [kTM][kTN + 4]
+  float V[kTN][D];
+  float bias[kTN];
+  BranchUnit unit;
+  int more;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, int32_t* st) {
+  pdl_wait();
+  extern __shared__ uint4 raw[];
+  SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(raw);
+  float(*P)[kTN + 4] = reinterpret_cast<float(*)[kTN + 4]>(&sm.K[0][0]);
+  if (block_status_bad(st)) return;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  constexpr int VN = 16 / (int)sizeof(T), RV = D / VN;  // vectors per row
+  constexpr int OC = D / 16;                            // O columns per thread
+  const float scale2 = a.scale * kLog2e;
+  BranchWalk w;
+  const bool any = w.start(a, blockIdx.x);  // every warp walks; warp 0 publishes
+  if (!any) return;
+  const int rows = (int)a.head[a.H + 1];
+  float m[4], l[4], o[4][OC];
+  bool bad = false;
+  while (true) {
+    BranchUnit x;
+    if (!w.next(a, x)) break;
+    const int r0 = x.t * kTM;
+    __syncthreads();  // the previous unit's products are done with K, V, P and Q
+    if (x.flags & 1) {
+      for (int e = tid; e < kTM * RV; e += kThreads) {
+        const int r = e / RV, c = e % RV;
+        float v[VN];
+#pragma unroll
+        for (int i = 0; i < VN; ++i) v[i] = 0.f;
+        if (r0 + r < rows) {
+          const size_t at = (size_t)(x.h * a.g + (int)((r0 + r) % a.g)) * a.N + (size_t)((r0 + r) / a.g);
+          ld_vec<T, VN>((const T*)a.q + at * D + c * VN, v);
+        }
+#pragma unroll
+        for (int i = 0; i < VN; ++i) sm.Q[r][c * VN + i] = v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int d = 0; d < OC; ++d) o[i][d] = 0.f;
+      }
+    }
+    for (int e = tid; e < kTN * RV; e += kThreads) {
+      const int r = e / RV, c = e % RV;
+      float k[VN], v[VN];
+#pragma unroll
+      for (int i = 0; i < VN; ++i) k[i] = v[i] = 0.f;
+      if (r < x.nk) {
+        const T *kp, *vp;
+        bool ok = true;
+        size_t at;
+        if (x.branch < 0) {
+          at = (size_t)x.h * a.C + x.k0 + r;
+          kp = (const T*)a.pK;
+          vp = (const T*)a.pV;
+        } else {
+          const int pos = x.k0 + r;
+          const int id = a.table[(size_t)x.branch * a.max_pages + (pos >> a.page_shift)];
+          ok = id >= 0 && id < a.n_pages;
+          at = (((size_t)id * a.H + x.h) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+          kp = (const T*)a.K;
+          vp = (const T*)a.V;
+        }
+        if (ok) {
+          ld_vec<T, VN>(kp + at * D + c * VN, k);
+          ld_vec<T, VN>(vp + at * D + c * VN, v);
+        } else {
+          bad = true;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < VN; ++i) {
+        sm.K[r][c * VN + i] = k[i];
+        sm.V[r][c * VN + i] = v[i];
+      }
+    }
+    if (tid < kTN) {
+      float b = 0.f;
+      if (x.branch < 0 && a.m && tid < x.nk) {
+        const int c = a.m[(size_t)x.h * a.C + x.k0 + tid];
+        b = c > 0 ? log2f((float)c) : -INFINITY;
+      }
+      sm.bias[tid] = b;
+    }
+    __syncthreads();
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < D; k += 4) {
+      float4 qv[4], kv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sm.Q[ty * 4 + i][k]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.K[tx + 16 * j][k]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+          s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+          s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+          s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+        }
+    }
+    __syncthreads();  // K has been read: its buffer takes the probabilities
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + ty * 4 + i;
+      const int seen = r < rows ? branch_row_keys(a, x, r) : 0;
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = tx + 16 * j;
+        s[i][j] = c < seen ? fmaf(s[i][j], scale2, sm.bias[c]) : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float mn = fmaxf(m[i], top);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float alpha = exp2f(m[i] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(s[i][j] - base);
+        sum += p;
+        P[ty * 4 + i][tx + 16 * j] = p;
+      }
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      m[i] = mn;
+      l[i] = l[i] * alpha + sum;
+#pragma unroll
+      for (int d = 0; d < OC; ++d) o[i][d] *= alpha;
+    }
+    __syncthreads();
+#pragma unroll 2
+    for (int k = 0; k < kTN; k += 4) {
+      float4 pv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(&P[ty * 4 + i][k]);
+#pragma unroll
+      for (int c = 0; c < OC / 4; ++c) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const float4 v = *reinterpret_cast<const float4*>(&sm.V[k + kk][tx * 4 + 64 * c]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
+            o[i][4 * c] = fmaf(p, v.x, o[i][4 * c]);
+            o[i][4 * c + 1] = fmaf(p, v.y, o[i][4 * c + 1]);
+            o[i][4 * c + 2] = fmaf(p, v.z, o[i][4 * c + 2]);
+            o[i][4 * c + 3] = fmaf(p, v.w, o[i][4 * c + 3]);
+          }
+        }
+      }
+    }
+    if (x.flags & 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int lr = ty * 4 + i;
+        const int r = r0 + lr;
+        if (r >= rows) continue;
+        if (x.flags & 4) {
+          const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // a NaN sum stays one
+          const size_t at = (size_t)(x.h * a.g + (int)(r % a.g)) * a.N + (size_t)(r / a.g);
+#pragma unroll
+          for (int c = 0; c < OC / 4; ++c) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = o[i][4 * c + e] * inv;
+            st_vec<T, 4>((T*)a.out + at * D + tx * 4 + 64 * c, v);
+          }
+          if (a.lse && tx == 0) a.lse[at] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+        } else {
+          const size_t at = (size_t)x.slot * a.slot_rows + lr;
+#pragma unroll
+          for (int c = 0; c < OC / 4; ++c) st_vec<float, 4>(a.po + at * D + tx * 4 + 64 * c, &o[i][4 * c]);
+          if (tx == 0) a.pml[at] = make_float2(m[i], l[i]);
+        }
+      }
+    }
+  }
+  if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
+  pdl_trigger();
+}
+
+template <typename T, int D>
+int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
+  constexpr int smem = (int)sizeof(SimtSmem<D>);
+  auto kernel = branch_simt_kernel<T, D>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, a, st) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FASTAR_ERR_CUDA;
+  }
+  FASTAR_LAUNCHED(s, "branch_simt");
+  return FASTAR_OK;
+}
+
+}  // namespace
+
+int launch_branch_simt(const BranchArgs& a, fastar_dtype dt, int32_t* st, cudaStream_t s) {
+  if (dt == FASTAR_BF16)
+    return a.D == 128 ? launch_t<__nv_bfloat16, 128>(a, st, s) : launch_t<__nv_bfloat16, 64>(a, st, s);
+  return a.D == 128 ? launch_t<float, 128>(a, st, s) : launch_t<float, 64>(a, st, s);
+}
+
+}  // namespace fastar

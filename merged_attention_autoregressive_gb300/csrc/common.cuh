@@ -214,6 +214,16 @@ int launch_annsa_quant(const void* q, int Nq, const fastar_cache* c, float scale
                        float* lse, uint32_t* sel_mask, void* ws, int32_t* st, cudaStream_t s);
 int launch_annca_quant(const void* q, const void* k_p, const void* v_p, int H, int Nq, int P, float scale, int topk,
                        int bits, void* out, uint32_t* sel_mask, void* ws, int32_t* st, cudaStream_t s);
+int launch_rope(fastar_dtype dt, const void* x, int64_t xh, int64_t xt, int H, int N, int D, const int32_t* pos,
+                const fastar_rope_plan* plan, int inverse, void* out, int64_t oh, int64_t ot, int32_t* st,
+                cudaStream_t s);
+int launch_page_append(const fastar_pages* pg, const void* k, int64_t kh, int64_t kt, const void* v, int64_t vh,
+                       int64_t vt, int N, const int32_t* cu, const int32_t* pos, const fastar_rope_plan* plan,
+                       const void* q, int64_t qh, int64_t qt, int Hq, void* q_out, int32_t* st, cudaStream_t s);
+size_t branch_ws_bytes(int Hq, int H, int N, int D);
+int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* cu, const fastar_prefix* px,
+                  const fastar_pages* pg, float scale, int block, void* out, float* lse, void* ws, int32_t* st,
+                  cudaStream_t s);
 }  // namespace fastar
 
 namespace fastar {

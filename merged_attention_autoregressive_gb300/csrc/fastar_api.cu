@@ -1,6 +1,7 @@
 // C ABI of the FAST-AR per-chunk attention path: argument checks, workspace
 // sizing and dispatch to the kernels.  Nothing here allocates, frees or
 // synchronises; every launch goes to the caller's stream.
+#include <math.h>
 #include <string.h>
 
 #include <atomic>
@@ -150,6 +151,7 @@ size_t fastar_workspace_size(int op, int H, int N, int D, int T, int B, int C) {
     case FASTAR_OP_ANNCA: return annca_tc_ws_bytes(H, N, C, D);  // N = frames F, C = prompt tokens P
     case FASTAR_OP_ANNSA: return annsa_ws_bytes(H, N, D, T);
     case FASTAR_OP_ANNSA_PARTS: return annsa_parts_ws_bytes(H, N, D, T);  // T = part_total
+    case FASTAR_OP_BRANCH: return branch_ws_bytes(H, T, N, D);  // H = query heads, T = key/value heads
     case FASTAR_OP_QUANT: return quant_ws_bytes(H, N, C, D, T);  // N = Nq, T = bits, C = keys per head
     default: return 0;
   }
@@ -433,3 +435,123 @@ int fastar_annca_quant_attention(fastar_dtype dt, const void* q, const void* k_p
   if (!k_p || !v_p || !aligned16(k_p) || !aligned16(v_p)) return FASTAR_ERR_ARG;
   return launch_annca_quant(q, k_p, v_p, H, Nq, P, scale, topk, bits, out, sel_mask, ws, dev_status, stream);
 }
+
+// ---- branched rollouts
+
+// Rows of a strided tensor start on 16-byte boundaries (a stride counts only
+// where there is more than one row along it); rows that are written lie apart.
+static bool rows_ok(fastar_dtype dt, const void* x, int64_t head, int64_t token, int H, int N, int D,
+                    bool written = false) {
+  const int64_t v = dt == FASTAR_BF16 ? 8 : 4;
+  if (!x || !aligned16(x)) return false;
+  if (H > 1 && (head % v || (written && head < D && head > -D))) return false;
+  if (N > 1 && (token % v || (written && token < D && token > -D))) return false;
+  return true;
+}
+static bool plan_ok(const fastar_rope_plan* p, int D) {
+  if (!p || p->D != D || p->axes < 1 || p->axes > FASTAR_ROPE_MAX_AXES) return false;
+  if (p->pairs < 1 || p->pairs > D / 2 || (p->pairing != FASTAR_PAIRS_ADJACENT && p->pairing != FASTAR_PAIRS_HALVES))
+    return false;
+  if (p->pairing == FASTAR_PAIRS_HALVES && p->pairs % 8) return false;
+  for (int i = 0; i < p->pairs; ++i)
+    if (p->axis[i] >= p->axes) return false;
+  return true;
+}
+static int check_pages(const fastar_pages* p) {
+  if (!p) return FASTAR_ERR_ARG;
+  if (!dtype_ok(p->dt) || !dim_ok(p->D)) return FASTAR_ERR_UNSUPPORTED;
+  if (p->H < 1 || p->B < 0 || p->n_pages < 0 || p->max_pages < 0) return FASTAR_ERR_ARG;
+  if (p->page < 16 || p->page > 256 || (p->page & (p->page - 1))) return FASTAR_ERR_UNSUPPORTED;
+  if ((int64_t)p->max_pages * p->page > 0x7fffffff) return FASTAR_ERR_UNSUPPORTED;
+  if ((int64_t)p->n_pages * p->H > 0x7fffffff / p->page) return FASTAR_ERR_UNSUPPORTED;
+  if (p->B > 0 && !p->len) return FASTAR_ERR_ARG;
+  if (p->n_pages > 0 && (!p->K || !p->V || !aligned16(p->K) || !aligned16(p->V))) return FASTAR_ERR_ARG;
+  if (p->B > 0 && p->max_pages > 0 && (!p->table || p->n_pages == 0)) return FASTAR_ERR_ARG;
+  return FASTAR_OK;
+}
+
+extern "C" {
+
+int fastar_rope_plan_init(fastar_rope_plan* plan, int D, int axes, const int* dims, int pairing, const double* freq) {
+  if (!plan || !dims) return FASTAR_ERR_ARG;
+  if (!dim_ok(D)) return FASTAR_ERR_UNSUPPORTED;
+  if (axes < 1 || axes > FASTAR_ROPE_MAX_AXES) return FASTAR_ERR_ARG;
+  if (pairing != FASTAR_PAIRS_ADJACENT && pairing != FASTAR_PAIRS_HALVES) return FASTAR_ERR_ARG;
+  int64_t sum = 0;
+  for (int a = 0; a < axes; ++a) {
+    if (dims[a] < 0 || dims[a] % 2) return FASTAR_ERR_ARG;
+    sum += dims[a];
+  }
+  if (sum < 2 || sum > D || (pairing == FASTAR_PAIRS_HALVES && sum % 16)) return FASTAR_ERR_ARG;
+  for (int i = 0; freq && i < sum / 2; ++i)
+    if (!(freq[i] - freq[i] == 0.0)) return FASTAR_ERR_ARG;  // infinite or NaN
+  memset(plan, 0, sizeof(*plan));
+  plan->D = D;
+  plan->axes = axes;
+  plan->pairs = (int)(sum / 2);
+  plan->pairing = pairing;
+  for (int a = 0, p = 0; a < axes; ++a)
+    for (int i = 0; i < dims[a] / 2; ++i, ++p) {
+      const double f = freq ? freq[p] : pow(10000.0, -2.0 * i / dims[a]);
+      const double turns = f / 6.283185307179586476925286766559;
+      const double part = turns - floor(turns);  // 1.0 when a tiny negative one is rounded up
+      plan->turn[p] = part < 1.0 ? (uint64_t)ldexp(part, 64) : 0u;
+      plan->axis[p] = (uint8_t)a;
+    }
+  return FASTAR_OK;
+}
+
+int fastar_rope(fastar_dtype dt, const void* x, int64_t x_head, int64_t x_token, int H, int N, int D,
+                const int32_t* pos, const fastar_rope_plan* plan, int inverse, void* out, int64_t out_head,
+                int64_t out_token, int32_t* dev_status, cudaStream_t stream) {
+  CallRange range("fastar_rope");
+  if (!dtype_ok(dt) || !dim_ok(D)) return FASTAR_ERR_UNSUPPORTED;
+  if (H < 0 || N < 0 || !plan_ok(plan, D)) return FASTAR_ERR_ARG;
+  if (H == 0 || N == 0) return FASTAR_OK;
+  if (!pos || !rows_ok(dt, x, x_head, x_token, H, N, D) || !rows_ok(dt, out, out_head, out_token, H, N, D, true))
+    return FASTAR_ERR_ARG;
+  return launch_rope(dt, x, x_head, x_token, H, N, D, pos, plan, inverse, out, out_head, out_token, dev_status, stream);
+}
+
+int fastar_page_append(const fastar_pages* pages, const void* k, int64_t k_head, int64_t k_token, const void* v,
+                       int64_t v_head, int64_t v_token, int N, const int32_t* cu, const int32_t* pos,
+                       const fastar_rope_plan* plan, const void* q, int64_t q_head, int64_t q_token, int Hq,
+                       void* q_out, int32_t* dev_status, cudaStream_t stream) {
+  CallRange range("fastar_page_append");
+  int rc = check_pages(pages);
+  if (rc != FASTAR_OK) return rc;
+  if (N < 0 || Hq < 0 || (plan == nullptr) != (pos == nullptr)) return FASTAR_ERR_ARG;
+  if (plan && !plan_ok(plan, pages->D)) return FASTAR_ERR_ARG;
+  if (N == 0 || pages->B == 0) return FASTAR_OK;
+  if (!cu || !rows_ok(pages->dt, k, k_head, k_token, pages->H, N, pages->D) ||
+      !rows_ok(pages->dt, v, v_head, v_token, pages->H, N, pages->D))
+    return FASTAR_ERR_ARG;
+  if ((q == nullptr) != (Hq == 0) || (q == nullptr) != (q_out == nullptr)) return FASTAR_ERR_ARG;
+  if (q && (!rows_ok(pages->dt, q, q_head, q_token, Hq, N, pages->D) || !aligned16(q_out))) return FASTAR_ERR_ARG;
+  return launch_page_append(pages, k, k_head, k_token, v, v_head, v_token, N, cu, pos, plan, q, q_head, q_token, Hq,
+                            q_out, dev_status, stream);
+}
+
+int fastar_branch_attention(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* cu,
+                            const fastar_prefix* prefix, const fastar_pages* pages, float scale, int block, void* out,
+                            float* lse, void* ws, size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
+  CallRange range("fastar_branch_attention");
+  int rc = check_pages(pages);
+  if (rc != FASTAR_OK) return rc;
+  if (dt != pages->dt || N < 0 || Hq < 0 || Hq % pages->H || block < 0) return FASTAR_ERR_ARG;
+  if (!(scale > 0.f && scale < INFINITY)) return FASTAR_ERR_ARG;
+  if (N == 0 || Hq == 0 || pages->B == 0) return FASTAR_OK;
+  if ((int64_t)N * (Hq / pages->H) >= 0x7fffffff - 256) return FASTAR_ERR_UNSUPPORTED;
+  if (!q || !cu || !out || !aligned16(q) || !aligned16(out)) return FASTAR_ERR_ARG;
+  if (prefix && prefix->C == 0) prefix = nullptr;
+  if (prefix) {
+    if (prefix->H != pages->H || prefix->D != pages->D || prefix->dt != dt || prefix->C < 0) return FASTAR_ERR_ARG;
+    if (!prefix->K || !prefix->V || !aligned16(prefix->K) || !aligned16(prefix->V)) return FASTAR_ERR_ARG;
+    if ((int64_t)prefix->H * prefix->C > 0x7fffffff) return FASTAR_ERR_UNSUPPORTED;
+  }
+  const size_t need = branch_ws_bytes(Hq, pages->H, N, pages->D);
+  if (!ws || ws_bytes < need || ((uintptr_t)ws & 255)) return FASTAR_ERR_WORKSPACE;
+  return launch_branch(dt, q, Hq, N, cu, prefix, pages, scale, block, out, lse, ws, dev_status, stream);
+}
+
+}  // extern "C"

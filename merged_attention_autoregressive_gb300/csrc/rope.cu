@@ -1,0 +1,279 @@
+// Rotary positions with several axes, and the append of new keys and values
+// to a paged cache with the rotation applied on the way.
+//
+// Mathematics.  Pair p of a row turns by the angle pos[axis(p)] * freq(p):
+//   y0 = x0 cos - x1 sin,  y1 = x0 sin + x1 cos   (inverse: sin -> -sin).
+// The angle is needed modulo one turn only, so the plan holds freq / (2 pi)
+// as a 64-bit fixed-point fraction of a turn and the kernel multiplies it by
+// the integer position modulo 2^64: no position is too far for it (the error
+// of the fraction, 2^-53 from the caller's double, grows to 2^-22 of a turn
+// only at |pos| = 2^31), and no 64-bit floating point is used.
+//
+// What bounds it: memory, one read and one write of every row.  A thread owns
+// one token and the two 16-byte vectors of a row that hold whole pairs
+// (adjacent pairs: vectors i and i + D/2; halves: a vector and its partner),
+// keeps their sines and cosines in registers and walks the heads, so each
+// angle is taken once per token and head group, and every access of a warp is
+// 64 or 128 contiguous bytes per row on both sides whatever the strides.
+// Heads are split over grid y until the grid fills the GPU.
+#include <math.h>
+
+#include "common.cuh"
+
+namespace fastar {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // heads in flight per thread: 8 16-byte loads
+
+// One group of heads: rows x[h * xh + n * xt], written to out[h * oh + n * ot]
+// (pages: to slot `at` of the token's page).
+struct Rows {
+  const void* x;
+  int64_t xh, xt;
+  void* out;
+  int64_t oh, ot;
+  int H;
+};
+
+struct AppendArgs {
+  const int32_t* cu;
+  const int32_t* len;
+  const int32_t* table;
+  int B, max_pages, page_shift, n_pages, H;
+};
+
+struct RopeArgs {
+  Rows q, k, v;           // q: rotated; k: rotated (pages); v: copied (pages)
+  const int32_t* pos;     // [N][axes]; null: nothing is rotated
+  int N, heads_per_cta;
+  uint32_t flip;          // sign bit of the sine for the inverse
+};
+
+template <typename T> struct VecInfo { static constexpr int n = 16 / (int)sizeof(T); };
+
+// channels of vector a (0) and b (1) of item i, and the first pair of each;
+// pair < 0: copied unturned
+template <int V>
+__device__ __forceinline__ void item_channels(const fastar_rope_plan& p, int D, int i, int& ca, int& cb) {
+  if (p.pairing == FASTAR_PAIRS_HALVES) {
+    const int half = p.pairs;  // rotated channels / 2
+    if (i * V < half) {
+      ca = i * V;
+      cb = half + i * V;
+    } else {
+      ca = 2 * half + (i * V - half) * 2;
+      cb = ca + V;
+    }
+  } else {
+    ca = i * V;
+    cb = D / 2 + i * V;
+  }
+}
+
+// N pairs of a row turned by (c, s): (x, y) -> (x c - y s, x s + y c), each in
+// fp32 and rounded once to the row's type.
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+  const float a = x, b = y;
+  x = a * c - b * s;
+  y = a * s + b * c;
+}
+
+template <typename T, bool kHalves, bool kAppend>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ fastar_rope_plan plan, int D,
+                                                        const RopeArgs a, const AppendArgs ap, int32_t* st) {
+  constexpr int V = VecInfo<T>::n;     // elements of a 16-byte vector
+  pdl_wait();
+  const int items = D / (2 * V);       // threads per row
+  const int toks = kThreads / items;   // tokens per CTA
+  const int tid = threadIdx.x;
+  const int lt = tid / items, i = tid % items;
+  const int n0 = blockIdx.x * toks, n = n0 + lt;
+  bool bad = status_bad(st);
+  int page_row = -1;  // row of the token in its page, over all pages of head 0
+  bool live = n < a.N;
+  if constexpr (kAppend) {
+    // the branch of each token of the CTA: every branch marks its own tokens
+    __shared__ int s_branch[kThreads / 4], s_first[kThreads / 4], s_count[kThreads / 4];
+    for (int t = tid; t < toks; t += kThreads) s_branch[t] = -1;
+    __syncthreads();
+    bool bad_cu = false;
+    for (int b = tid; b < ap.B; b += kThreads) {
+      const int lo = ap.cu[b], hi = ap.cu[b + 1];
+      if (lo < 0 || hi < lo || hi > a.N || (b == 0 && lo != 0)) {
+        bad_cu = true;
+        continue;
+      }
+      for (int t = max(lo, n0); t < min(hi, n0 + toks); ++t) {
+        s_branch[t - n0] = b;
+        s_first[t - n0] = lo;
+        s_count[t - n0] = hi - lo;
+      }
+    }
+    if (bad_cu) status_set(st, FASTAR_ERR_DEVICE_ARG);
+    bad = __syncthreads_or(bad || bad_cu) != 0;
+    const int b = s_branch[lt];
+    live = live && b >= 0;
+    if (live) {
+      const int slot = ap.len[b] - s_count[lt] + (n - s_first[lt]);
+      const int pi = slot >> ap.page_shift;
+      bool ok = slot >= 0 && pi < ap.max_pages;
+      if (ok) {
+        const int id = ap.table[(size_t)b * ap.max_pages + pi];
+        ok = id >= 0 && id < ap.n_pages;
+        if (ok) page_row = ((id * ap.H) << ap.page_shift) + (slot & ((1 << ap.page_shift) - 1));
+      }
+      if (!ok) {
+        status_set(st, FASTAR_ERR_DEVICE_ARG);
+        live = false;
+      }
+    }
+  }
+  if (bad || !live) return;
+
+  // the item's channels and the sines and cosines of its pairs
+  int ca, cb;
+  item_channels<V>(plan, D, i, ca, cb);
+  constexpr int NP = V;  // pairs per item (V elements in each of two vectors)
+  float cs[NP], sn[NP];
+  const bool rotated = kHalves ? i * V < plan.pairs : true;
+  if (a.pos && rotated) {
+    // sines and cosines of the item's pairs (adjacent: V/2 from each vector)
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      const int p = kHalves ? ca + e : (e < V / 2 ? ca / 2 + e : cb / 2 + e - V / 2);
+      cs[e] = 1.f;
+      sn[e] = 0.f;
+      if (p < plan.pairs) {
+        const int64_t x = a.pos[(size_t)n * plan.axes + plan.axis[p]];
+        const uint64_t frac = plan.turn[p] * (uint64_t)x;  // of a turn, modulo 1
+        const float half_turns = (float)(int32_t)(frac >> 32) * 4.656612873077393e-10f;  // 2^-31
+        sincospif(half_turns, &sn[e], &cs[e]);
+        sn[e] = __uint_as_float(__float_as_uint(sn[e]) ^ a.flip);
+      }
+    }
+  }
+  const bool turns = a.pos != nullptr && rotated;
+
+  auto rotate = [&](uint4& u, uint4& w) {
+    float x[V], y[V];
+    raw_to_float<T, V>(u, x);
+    raw_to_float<T, V>(w, y);
+    if constexpr (kHalves) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) turn(x[e], y[e], cs[e], sn[e]);
+    } else {
+      // channels past the rotated ones are copied (not multiplied by 1 and 0)
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        if (ca / 2 + e < plan.pairs) turn(x[2 * e], x[2 * e + 1], cs[e], sn[e]);
+        if (cb / 2 + e < plan.pairs) turn(y[2 * e], y[2 * e + 1], cs[V / 2 + e], sn[V / 2 + e]);
+      }
+    }
+    T* p = reinterpret_cast<T*>(&u);
+    T* q = reinterpret_cast<T*>(&w);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      Elem<T>::st(p + e, x[e]);
+      Elem<T>::st(q + e, y[e]);
+    }
+  };
+
+  // the heads of this CTA: queries, then keys, then values
+  const int total = a.q.H + a.k.H + a.v.H;
+  const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(h0 + a.heads_per_cta, total);
+  auto source = [&](int h) -> const T* {
+    if (h < a.q.H) return (const T*)a.q.x + h * a.q.xh + n * a.q.xt;
+    h -= a.q.H;
+    if (h < a.k.H) return (const T*)a.k.x + h * a.k.xh + n * a.k.xt;
+    h -= a.k.H;
+    return (const T*)a.v.x + h * a.v.xh + n * a.v.xt;
+  };
+  auto target = [&](int h) -> T* {
+    if (h < a.q.H) return (T*)a.q.out + h * a.q.oh + n * a.q.ot;
+    h -= a.q.H;
+    T* base = (T*)(h < a.k.H ? a.k.out : a.v.out);
+    if (h >= a.k.H) h -= a.k.H;
+    return base + ((size_t)page_row + ((size_t)h << ap.page_shift)) * D;
+  };
+  for (int h = h0; h < h1; h += kUnroll) {
+    uint4 u[kUnroll], w[kUnroll];
+#pragma unroll
+    for (int e = 0; e < kUnroll; ++e)
+      if (h + e < h1) {
+        const T* s = source(h + e);
+        u[e] = *reinterpret_cast<const uint4*>(s + ca);
+        w[e] = *reinterpret_cast<const uint4*>(s + cb);
+      }
+#pragma unroll
+    for (int e = 0; e < kUnroll; ++e)
+      if (h + e < h1) {
+        if (turns && h + e < a.q.H + a.k.H) rotate(u[e], w[e]);
+        T* d = target(h + e);
+        *reinterpret_cast<uint4*>(d + ca) = u[e];
+        *reinterpret_cast<uint4*>(d + cb) = w[e];
+      }
+  }
+  pdl_trigger();
+}
+
+template <typename T, bool kAppend>
+int launch_rope_t(const fastar_rope_plan& plan, int D, RopeArgs a, const AppendArgs& ap, int32_t* st,
+                  cudaStream_t s) {
+  const int items = D / (2 * VecInfo<T>::n), toks = kThreads / items;
+  const int gx = (a.N + toks - 1) / toks;
+  const int total = a.q.H + a.k.H + a.v.H;
+  // split the heads until about 8 CTAs per SM are there (the angles are taken
+  // again by each part), in steps of the heads in flight
+  int parts = (152 * 8 + gx - 1) / gx;
+  int per = (total + parts - 1) / parts;
+  per = (per + kUnroll - 1) / kUnroll * kUnroll;
+  a.heads_per_cta = per;
+  const dim3 grid(gx, (total + per - 1) / per);
+  cudaError_t rc;
+  if (plan.pairing == FASTAR_PAIRS_HALVES)
+    rc = launch_pdl(rope_kernel<T, true, kAppend>, grid, dim3(kThreads), 0, s, plan, D, a, ap, st);
+  else
+    rc = launch_pdl(rope_kernel<T, false, kAppend>, grid, dim3(kThreads), 0, s, plan, D, a, ap, st);
+  if (rc != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FASTAR_ERR_CUDA;
+  }
+  FASTAR_LAUNCHED(s, kAppend ? "page_append" : "rope");
+  return FASTAR_OK;
+}
+
+}  // namespace
+
+int launch_rope(fastar_dtype dt, const void* x, int64_t xh, int64_t xt, int H, int N, int D, const int32_t* pos,
+                const fastar_rope_plan* plan, int inverse, void* out, int64_t oh, int64_t ot, int32_t* st,
+                cudaStream_t s) {
+  RopeArgs a = {};
+  a.q = {x, xh, xt, out, oh, ot, H};
+  a.pos = pos;
+  a.N = N;
+  a.flip = inverse ? 0x80000000u : 0u;
+  const AppendArgs ap = {};
+  return dt == FASTAR_BF16 ? launch_rope_t<__nv_bfloat16, false>(*plan, D, a, ap, st, s)
+                           : launch_rope_t<float, false>(*plan, D, a, ap, st, s);
+}
+
+int launch_page_append(const fastar_pages* pg, const void* k, int64_t kh, int64_t kt, const void* v, int64_t vh,
+                       int64_t vt, int N, const int32_t* cu, const int32_t* pos, const fastar_rope_plan* plan,
+                       const void* q, int64_t qh, int64_t qt, int Hq, void* q_out, int32_t* st, cudaStream_t s) {
+  RopeArgs a = {};
+  a.q = {q, qh, qt, q_out, (int64_t)N * pg->D, pg->D, q ? Hq : 0};
+  a.k = {k, kh, kt, pg->K, 0, 0, pg->H};
+  a.v = {v, vh, vt, pg->V, 0, 0, pg->H};
+  a.pos = pos;
+  a.N = N;
+  AppendArgs ap = {cu, pg->len, pg->table, pg->B, pg->max_pages, 0, pg->n_pages, pg->H};
+  while ((1 << ap.page_shift) < pg->page) ++ap.page_shift;
+  fastar_rope_plan none = {};
+  none.D = pg->D;
+  const fastar_rope_plan& p = plan ? *plan : none;
+  return pg->dt == FASTAR_BF16 ? launch_rope_t<__nv_bfloat16, true>(p, pg->D, a, ap, st, s)
+                               : launch_rope_t<float, true>(p, pg->D, a, ap, st, s);
+}
+
+}  // namespace fastar
