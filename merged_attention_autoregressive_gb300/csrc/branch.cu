@@ -192,17 +192,39 @@ int launch_branch_combine(const BranchArgs& a, fastar_dtype dt, int32_t* st, cud
 }
 
 namespace {
-// The launch geometry of a call: the SIMT kernel runs two CTAs per SM.
-constexpr int kSms = 152, kSimtG = 2 * kSms, kSimtTM = 64, kSimtTN = 64;
+// Units, runs and partials of a call.  bf16: one CTA per SM, 256 rows and 128
+// keys (128 rows where that is all there is); fp32: two CTAs per SM, 64 rows
+// and 64 keys.
+constexpr int kSms = 152;
+struct Geometry {
+  int TM, TN, G, ntiles, slot_rows;
+  size_t head, tile, po, pml;  // bytes of the workspace's parts
+};
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+Geometry geometry(fastar_dtype dt, int H, long long rows, int D) {
+  Geometry x;
+  x.TM = dt == FASTAR_F32 ? 64 : rows <= 128 ? 128 : 256;
+  x.TN = dt == FASTAR_F32 ? 64 : 128;
+  x.G = dt == FASTAR_F32 ? 2 * kSms : kSms;
+  x.ntiles = (int)((rows + x.TM - 1) / x.TM);
+  x.slot_rows = (int)(rows < x.TM ? rows : x.TM);
+  x.head = up256((size_t)(H + 3) * 8);
+  x.tile = up256((size_t)(x.ntiles + 1) * 8);
+  x.po = up256((size_t)2 * x.G * x.slot_rows * D * 4);
+  x.pml = up256((size_t)2 * x.G * x.slot_rows * 8);
+  return x;
+}
 }  // namespace
 
 size_t branch_ws_bytes(int Hq, int H, int N, int D) {
   if (Hq < 1 || H < 1 || N < 1 || D < 1 || Hq % H) return 0;
-  const long long rows = (long long)N * (Hq / H);
-  const long long slot_rows = rows < kSimtTM ? rows : kSimtTM;
-  const size_t lists = up256((size_t)(H + 3) * 8) + up256((size_t)(rows / kSimtTM + 2) * 8);
-  return lists + up256((size_t)2 * kSimtG * slot_rows * D * 4) + up256((size_t)2 * kSimtG * slot_rows * 8);
+  size_t most = 0;
+  for (fastar_dtype dt : {FASTAR_BF16, FASTAR_F32}) {
+    const Geometry x = geometry(dt, H, (long long)N * (Hq / H), D);
+    const size_t n = x.head + x.tile + x.po + x.pml;
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* cu, const fastar_prefix* px,
@@ -235,22 +257,19 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   a.scale = scale;
   a.out = out;
   a.lse = lse;
-  a.TM = kSimtTM;
-  a.TN = kSimtTN;
-  a.G = kSimtG;
-  const long long rows = (long long)N * a.g;
-  a.ntiles = (int)((rows + a.TM - 1) / a.TM);
-  a.slot_rows = (int)(rows < a.TM ? rows : a.TM);
+  const Geometry x = geometry(dt, a.H, (long long)N * a.g, a.D);
+  a.TM = x.TM;
+  a.TN = x.TN;
+  a.G = x.G;
+  a.ntiles = x.ntiles;
+  a.slot_rows = x.slot_rows;
   char* w = (char*)ws;
   a.head = (long long*)w;
-  w += up256((size_t)(a.H + 3) * 8);
-  a.tile = (long long*)w;
-  w += up256((size_t)(rows / kSimtTM + 2) * 8);
-  a.po = (float*)w;
-  w += up256((size_t)2 * a.G * a.slot_rows * a.D * 4);
-  a.pml = (float2*)w;
+  a.tile = (long long*)(w += x.head);
+  a.po = (float*)(w += x.tile);
+  a.pml = (float2*)(w + x.po);
   int rc = launch_branch_plan(a, st, s);
-  if (rc == FASTAR_OK) rc = launch_branch_simt(a, dt, st, s);
+  if (rc == FASTAR_OK) rc = dt == FASTAR_BF16 ? launch_branch_tc(a, st, s) : launch_branch_simt(a, st, s);
   if (rc == FASTAR_OK) rc = launch_branch_combine(a, dt, st, s);
   return rc;
 }

@@ -206,6 +206,7 @@ __device__ __forceinline__ int branch_row_keys(const BranchArgs& a, const Branch
 
 int launch_branch_plan(const BranchArgs& a, int32_t* st, cudaStream_t s);
 int launch_branch_combine(const BranchArgs& a, fastar_dtype dt, int32_t* st, cudaStream_t s);
-int launch_branch_simt(const BranchArgs& a, fastar_dtype dt, int32_t* st, cudaStream_t s);
+int launch_branch_simt(const BranchArgs& a, int32_t* st, cudaStream_t s);
+int launch_branch_tc(const BranchArgs& a, int32_t* st, cudaStream_t s);
 
 }  // namespace fastar

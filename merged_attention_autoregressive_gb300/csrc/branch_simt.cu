@@ -233,9 +233,7 @@ int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
 
 }  // namespace
 
-int launch_branch_simt(const BranchArgs& a, fastar_dtype dt, int32_t* st, cudaStream_t s) {
-  if (dt == FASTAR_BF16)
-    return a.D == 128 ? launch_t<__nv_bfloat16, 128>(a, st, s) : launch_t<__nv_bfloat16, 64>(a, st, s);
+int launch_branch_simt(const BranchArgs& a, int32_t* st, cudaStream_t s) {
   return a.D == 128 ? launch_t<float, 128>(a, st, s) : launch_t<float, 64>(a, st, s);
 }
 

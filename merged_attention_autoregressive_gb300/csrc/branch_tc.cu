@@ -1,0 +1,576 @@
+// fastar_branch_attention on the tensor cores (tcgen05 + TMEM, bf16).
+//
+// One persistent CTA per SM walks its run of units (branch.cuh; 128 keys per
+// unit) with three warpgroups:
+//   warps 0-3, 4-7  two softmax streams, one thread per query row;
+//   warp 8          loader: finds the units, describes each in a ring of
+//                   descriptors and fetches its key and value tiles by TMA
+//                   (prefix: two 128-row boxes a tile; pages: a box per page
+//                   and column half, one lane per page) into a ring of tiles;
+//   warp 9          MMA issuer (warps 10 and 11 only give their registers away): S_s = Q_s K^T (M 128, N 128, K D) and O_s +=
+//                   P_s V (M 128, N D, K 128; P_s read from TMEM, where the
+//                   softmax wrote it over S_s).
+// More than 128 rows of queries per key/value head: an item is 256 rows and
+// stream s owns rows 128 s .. 128 s + 127, so each tile that is fetched feeds
+// four products, and one stream's softmax runs under the other's products.
+// Up to 128 rows: both streams own the same rows and take the units in turn
+// (each with its own O, maximum and sum; joined in TMEM at the item's end),
+// which hides the softmax behind the loads of a memory-bound pass, and the
+// room of the second query tile holds one more key or value tile in flight.
+// A running maximum is only raised (and O in TMEM rescaled) when a unit's
+// exceeds it by more than 2^8, so P stays <= 256 and rescaling is rare.
+// S, maxima, sums and O are fp32; P is rounded to bf16 for the second product
+// (2^-8 of each weight at most, as the inputs themselves; the sums take the
+// unrounded weights).
+//
+// Waits are bounded: one that runs out sets the status word, and every warp
+// leaves its loop by its own bounded waits.
+#include <limits.h>
+#include <math.h>
+
+#include "branch.cuh"
+#include "tc.cuh"
+
+namespace fastar {
+namespace {
+
+constexpr int kM = 128, kN = 128, kThreads = 384, kLoader = 8, kIssuer = 9;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.f;  // raise the running max only when exceeded by more than this (log2)
+
+// What the consumers need of a unit.
+struct Desc {
+  BranchUnit x;
+  int act;  // streams that have rows in it
+};
+
+template <int D>
+struct Shape {
+  static constexpr int kTile = 128 * D * 2;              // bytes of a query, key or value tile
+  static constexpr int kRing = D == 128 ? 4 : 8;         // descriptors
+  static constexpr int kSlots1 = D == 128 ? 6 : 10;      // tiles in flight, one query tile
+  static constexpr int kSlots2 = D == 128 ? 5 : 10;      // two query tiles
+  static constexpr int kTiles = kSlots1 + 1 > kSlots2 + 2 ? kSlots1 + 1 : kSlots2 + 2;
+};
+
+template <int D>
+struct Smem {
+  using S = Shape<D>;
+  uint8_t tiles[S::kTiles * S::kTile];  // query tiles, then the ring
+  float bias[S::kRing][kN];             // log2 m of the unit's prefix rows
+  Desc desc[S::kRing];
+  uint64_t full[S::kSlots1], empty[S::kSlots1];
+  uint64_t dfull[S::kRing], dempty[S::kRing];
+  uint64_t sfull[2], pready[2], odone, qfull, fin;
+  uint32_t tmem;
+  int started1;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void bar_pair(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+
+// Registers: 384 threads launch with 168 each (64,512); the third warpgroup
+// gives 72 of its own up, so that the softmax rows (128 scores in registers)
+// get 200: 128 * 96 + 256 * 200 = 63,488.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_constant__ CUtensorMap mapPK,
+                                                               const __grid_constant__ CUtensorMap mapPV,
+                                                               const __grid_constant__ CUtensorMap mapK,
+                                                               const __grid_constant__ CUtensorMap mapV,
+                                                               const BranchArgs a, int split, int32_t* st) {
+  using S = Shape<D>;
+  pdl_wait();
+  extern __shared__ __align__(1024) uint8_t raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slots = split ? S::kSlots1 : S::kSlots2;
+  uint8_t* const ring = sm.tiles + (split ? 1 : 2) * S::kTile;
+  // CTA-uniform: the status word and the address of the tiles
+  if (tid == 0 && (tc::smem_u32(sm.tiles) & 1023u)) status_set(st, FASTAR_ERR_CUDA);
+  const int stop = __syncthreads_or(status_bad(st) || (tc::smem_u32(sm.tiles) & 1023u));
+  if (stop) return;
+  if (tid == 0) {
+    for (int i = 0; i < S::kSlots1; ++i) {
+      tc::mbar_init(&sm.full[i], 1);
+      tc::mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < S::kRing; ++i) {
+      tc::mbar_init(&sm.dfull[i], 1);
+      tc::mbar_init(&sm.dempty[i], 9);  // 8 softmax warps and the issuer
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&sm.sfull[s], 1);
+      tc::mbar_init(&sm.pready[s], 4);
+    }
+    tc::mbar_init(&sm.odone, 1);
+    tc::mbar_init(&sm.qfull, 8);
+    tc::mbar_init(&sm.fin, 1);
+    tc::fence_mbar_init();
+  }
+  if (warp == kIssuer) {
+    tc::tmem_alloc(&sm.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = sm.tmem;  // S_0 / P_0, S_1 / P_1 at columns 0 and 128, O_0, O_1 at 256 and 384
+  bool ok = true, bad = false;
+
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+  if (warp == kLoader) {
+    // ================================================= loader
+    BranchWalk w;
+    BranchUnit x, y;
+    const int rows = (int)a.head[a.H + 1];
+    const int box = min(1 << a.page_shift, kN);  // rows of a page box
+    if (lane == 0) {
+      tc::prefetch_tensormap(&mapK);
+      tc::prefetch_tensormap(&mapV);
+      tc::prefetch_tensormap(&mapPK);
+      tc::prefetch_tensormap(&mapPV);
+    }
+    // page id of box `lane` and the counts of rows lane + 32 e of a unit,
+    // fetched one unit ahead
+    auto fetch = [&](const BranchUnit& u, int& id, int* cnt) {
+      id = -1;
+      if (u.branch >= 0) {
+        if (lane * box < u.nk) id = a.table[(size_t)u.branch * a.max_pages + ((u.k0 + lane * box) >> a.page_shift)];
+      } else if (a.m) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          cnt[e] = lane + 32 * e < u.nk ? a.m[(size_t)u.h * a.C + u.k0 + lane + 32 * e] : 0;
+      }
+    };
+    int id = -1, idn = -1, cnt[4], cntn[4];
+    bool more = w.start(a, blockIdx.x) && w.next(a, x);
+    if (more) fetch(x, id, cnt);
+    uint32_t j = 0, t = 0;  // units described, tiles issued
+    while (more && ok) {
+      const bool another = w.next(a, y);
+      if (another) fetch(y, idn, cntn);
+      // rows of the item that the unit concerns, by stream
+      const int r0 = x.t * a.TM;
+      int lo = r0, hi = min(r0 + a.TM, rows);
+      if (x.branch >= 0) {
+        lo = max(lo, x.lo * a.g);
+        hi = min(hi, (x.lo + x.n) * a.g);
+      }
+      int act = 0;
+      if (x.nk > 0 && hi > lo) act = split ? 1 : ((lo < r0 + kM ? 1 : 0) | (hi > r0 + kM ? 2 : 0));
+      const int ds = j % S::kRing;
+      if (j >= S::kRing) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dempty[ds], (j / S::kRing - 1) & 1u));
+      if (!ok) break;
+      if (x.branch < 0 && a.m) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sm.bias[ds][lane + 32 * e] = cnt[e] > 0 ? log2f((float)cnt[e]) : -INFINITY;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sm.bias[ds][lane + 32 * e] = 0.f;
+      }
+      if (lane == 0) {
+        sm.desc[ds].x = x;
+        sm.desc[ds].act = act;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.dfull[ds]);
+      ++j;
+      if (act) {
+        int row = 0;
+        bool mine = false;
+        if (x.branch >= 0) {
+          mine = lane * box < x.nk;
+          if (mine && (id < 0 || id >= a.n_pages)) {
+            bad = true;
+            mine = false;
+          }
+          row = ((id * a.H + x.h) << a.page_shift) + (x.k0 & ((1 << a.page_shift) - 1));
+        } else {
+          mine = lane == 0;
+          row = x.h * a.C + x.k0;
+        }
+        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        const uint32_t bytes = (uint32_t)boxes * (x.branch >= 0 ? box : kN) * D * 2;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++t) {
+          const int s = t % slots;
+          if (t >= (uint32_t)slots) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[s], (t / slots - 1) & 1u));
+          if (!ok) break;
+          if (lane == 0) tc::mbar_arrive_expect_tx(&sm.full[s], bytes);
+          __syncwarp();
+          if (mine) {
+            uint8_t* dst = ring + (size_t)s * S::kTile + lane * box * 128;
+            const CUtensorMap* map = x.branch >= 0 ? (kv ? &mapV : &mapK) : (kv ? &mapPV : &mapPK);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) tc::tma_load_2d(dst + c * kN * 128, map, &sm.full[s], c * 64, row);
+          }
+        }
+      }
+      x = y;
+      id = idn;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) cnt[e] = cntn[e];
+      more = another;
+    }
+    // no unit: the end of the run
+    if (ok) {
+      const int ds = j % S::kRing;
+      if (j >= S::kRing) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dempty[ds], (j / S::kRing - 1) & 1u));
+      if (ok && lane == 0) {
+        sm.desc[ds].act = -1;
+        tc::mbar_arrive(&sm.dfull[ds]);
+      }
+    }
+    // the copies have landed before the CTA exits, also when somebody's wait
+    // ran out and nobody took the last tiles
+    if (lane == 0)
+      for (uint32_t i = t > (uint32_t)slots ? t - slots : 0; i < t; ++i)
+        if (!tc::mbar_wait(&sm.full[i % slots], (i / slots) & 1u)) ok = false;
+    ok = __all_sync(0xffffffffu, ok);
+  } else if (warp == kIssuer) {
+    // ================================================= MMA issuer
+    constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kM, kN, 0, 0);
+    constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kM, D, 0, 1);
+    uint32_t t = 0, items = 0, turn = 0;
+    uint32_t np[2] = {0, 0};               // P tiles consumed per stream
+    bool pend[2] = {false, false};         // S of the stream is out, its P V not yet
+    uint32_t vt[2] = {0, 0};               // its value tile (count of tiles)
+    int vk[2] = {0, 0}, left[2] = {0, 0};  // its keys; whether the tile is free afterwards
+    bool first[2] = {true, true};          // O of the stream starts anew
+    bool issued = false;
+    auto pv = [&](int s) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pready[s], np[s] & 1u) &&
+                                       tc::mbar_wait(&sm.full[vt[s] % slots], (vt[s] / slots) & 1u));
+      if (!ok) return;
+      ++np[s];
+      tc::tc_fence_after();
+      uint8_t* v = ring + (size_t)(vt[s] % slots) * S::kTile;
+      const int steps = (vk[s] + 15) / 16;
+      if (vk[s] & 15) {
+        // value rows behind the unit's keys take part in the last step with
+        // weight 0: they must not hold an infinity or NaN
+        for (int e = lane; e < (steps * 16 - vk[s]) * (D / 8); e += 32) {
+          const int r = vk[s] + e / (D / 8), c = e % (D / 8);
+          *reinterpret_cast<uint4*>(v + (c >> 3) * kN * 128 + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (tc::elect_one()) {
+        const uint64_t vd = tc::sdesc_mnmajor_sw128(tc::smem_u32(v), kN * 128);
+        for (int k = 0; k < steps; ++k)
+          tc::mma_bf16_tmem_a(tmem + 256 + s * 128, tmem + s * 128 + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv,
+                              (!first[s] || k > 0) ? 1u : 0u);
+        if (left[s]) tc::mma_commit(&sm.empty[vt[s] % slots]);
+      }
+      __syncwarp();
+      first[s] = false;
+      pend[s] = false;
+      issued = true;
+    };
+    for (uint32_t j = 0; ok; ++j) {
+      const int ds = j % S::kRing;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dfull[ds], (j / S::kRing) & 1u));
+      if (!ok) break;
+      const int act0 = sm.desc[ds].act;
+      const int flags = sm.desc[ds].x.flags, nk = sm.desc[ds].x.nk;
+      __syncwarp();
+      if (act0 < 0) break;
+      if (lane == 0) tc::mbar_arrive(&sm.dempty[ds]);
+      if (flags & 1) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.qfull, items & 1u));
+        if (!ok) break;
+        first[0] = first[1] = true;
+        turn = 0;
+      }
+      const int act = split && act0 ? 1 << (turn & 1) : act0;
+      if (act0) ++turn;
+      const int ks = t % slots;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (pend[s] && (!split || (act >> s & 1))) pv(s);
+        if (!ok) break;
+        if (act >> s & 1) {
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.full[ks], (t / slots) & 1u));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+            const uint64_t qd = tc::sdesc_kmajor_sw128(tc::smem_u32(sm.tiles + (split ? 0 : s) * S::kTile));
+            const uint64_t kd = tc::sdesc_kmajor_sw128(tc::smem_u32(ring + (size_t)ks * S::kTile));
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * kN * 128 + (k & 3) * 32;
+              tc::mma_bf16(tmem + s * 128, tc::sdesc_add(qd, off), tc::sdesc_add(kd, off), idesc_qk, k > 0 ? 1u : 0u);
+            }
+            tc::mma_commit(&sm.sfull[s]);
+            if ((act >> (s + 1)) == 0) tc::mma_commit(&sm.empty[ks]);
+          }
+          __syncwarp();
+          issued = true;
+          pend[s] = true;
+          vt[s] = t + 1;
+          vk[s] = nk;
+          left[s] = (act >> (s + 1)) == 0;
+        }
+      }
+      if (act) t += 2;
+      if (ok && (flags & 2)) {
+        // streams in the order of their units, so that tiles are freed in order
+        const int s0 = pend[0] && pend[1] && (int32_t)(vt[1] - vt[0]) < 0 ? 1 : 0;
+        if (pend[s0]) pv(s0);
+        if (ok && pend[s0 ^ 1]) pv(s0 ^ 1);
+        if (ok && tc::elect_one()) tc::mma_commit(&sm.odone);
+        __syncwarp();
+        ++items;
+      }
+    }
+    if (issued) {
+      // every product has finished before TMEM is freed
+      if (tc::elect_one()) tc::mma_commit(&sm.fin);
+      __syncwarp();
+      if (!tc::mbar_wait(&sm.fin, 0)) ok = false;
+    }
+  } else if (warp < 8) {
+    // ================================================= softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    const int s = warp >> 2, wr = (warp & 3) * 32 + lane;  // stream, row of its tile
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tS = tl + s * 128, tO = tl + 256 + s * 128;
+    const float scale2 = a.scale * kLog2e;
+    const int rows = (int)a.head[a.H + 1];
+    uint32_t ns = 0, items = 0, turn = 0;  // S tiles seen, items, active units of the item
+    float m = -INFINITY, l = 0.f;
+    bool started = false;
+    for (uint32_t j = 0; ok; ++j) {
+      const int ds = j % S::kRing;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dfull[ds], (j / S::kRing) & 1u));
+      if (!ok) break;
+      const int act0 = sm.desc[ds].act;
+      if (act0 < 0) break;
+      const BranchUnit x = sm.desc[ds].x;
+      const int r = x.t * a.TM + (split ? 0 : s * kM) + wr;
+      if (x.flags & 1) {
+        // gather the row's queries (the previous item's products are done:
+        // odone was waited for)
+        m = -INFINITY;
+        l = 0.f;
+        started = false;
+        turn = 0;
+        const uint32_t q0 = tc::smem_u32(sm.tiles + (split ? 0 : s) * S::kTile);
+        const char* src = (const char*)a.q;
+        const uint32_t n = r < rows ? 16u : 0u;
+        if (n) src += ((size_t)(x.h * a.g + r % a.g) * a.N + r / a.g) * (D * 2);
+        // both streams fetch half of the shared tile
+        const int c0 = split ? s * (D / 16) : 0, c1 = split ? c0 + D / 16 : D / 8;
+        for (int c = c0; c < c1; ++c) tc::cp_async16(q0 + tc::sw128_offset(wr, c, kM), src + (n ? c * 16 : 0), n);
+        tc::cp_async_wait_all();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.qfull);
+      }
+      const bool active = act0 && (split ? (turn & 1) == (uint32_t)s : (act0 >> s & 1));
+      if (act0) ++turn;
+      if (active) {
+        const int seen = r < rows ? branch_row_keys(a, x, r) : 0;
+        const bool any = __any_sync(0xffffffffu, seen > 0), all = __all_sync(0xffffffffu, seen >= kN);
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sfull[s], ns & 1u));
+        if (!ok) break;
+        ++ns;
+        tc::tc_fence_after();
+        uint32_t pk[64];
+        if (any) {
+          float v[kN];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tc::tmem_ld32(tS + q * 32, v + q * 32);
+          float mul = scale2;
+          const bool biased = x.branch < 0 && a.m != nullptr;
+          if (biased || !all) {
+            // log2 scores with their bias; what the row does not see: -inf
+            mul = 1.f;
+            const float* bias = sm.bias[ds];
+#pragma unroll
+            for (int i = 0; i < kN; i += 4) {
+              const float4 b = *reinterpret_cast<const float4*>(bias + i);
+              v[i] = fmaf(v[i], scale2, b.x);
+              v[i + 1] = fmaf(v[i + 1], scale2, b.y);
+              v[i + 2] = fmaf(v[i + 2], scale2, b.z);
+              v[i + 3] = fmaf(v[i + 3], scale2, b.w);
+            }
+            if (!all) {
+#pragma unroll
+              for (int i = 0; i < kN; ++i) v[i] = i < seen ? v[i] : -INFINITY;
+            }
+          }
+          float t4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int i = 4; i < kN; i += 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              t4[e] = i + 4 + e < kN ? tc::max3(t4[e], v[i + e], v[i + 4 + e]) : fmaxf(t4[e], v[i + e]);
+          }
+          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * mul;
+          const bool raise = top > m + kRescale;
+          const float mn = raise ? top : m;
+          const float alpha = (raise && m != -INFINITY) ? exp2f(m - mn) : 1.f;
+          if (started && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // S of this unit was issued behind the P V of the stream's last
+            // one, and products complete in issue order: O is at rest
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              float o[32];
+              tc::tmem_ld32(tO + q * 32, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tc::tmem_st32(tO + q * 32, o);
+            }
+          }
+          l *= alpha;
+          m = mn;
+          const float base = m == -INFINITY ? 0.f : m;
+          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < kN; i += 2) {
+            const float p0 = ex2(fmaf(v[i], mul, -base)), p1 = ex2(fmaf(v[i + 1], mul, -base));
+            ps[i & 3] += p0;
+            ps[(i & 3) + 1] += p1;
+            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+            pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        } else {
+          // no row of the warp is concerned: weights 0
+#pragma unroll
+          for (int i = 0; i < 64; ++i) pk[i] = 0u;
+        }
+        tc::tmem_st32u(tS, pk);
+        tc::tmem_st32u(tS + 32, pk + 32);
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.pready[s]);
+        started = true;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.dempty[ds]);
+      if (x.flags & 2) {
+        // ---- the item's end: O of the run
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.odone, items & 1u));
+        if (!ok) break;
+        ++items;
+        tc::tc_fence_after();
+        float w0 = 1.f, w1 = 0.f;
+        bool have1 = false;
+        if (split) {
+          // stream 1 hands its maxima and sums over; stream 0 reads both O
+          float2* ml = reinterpret_cast<float2*>(sm.tiles);  // the query tile is free
+          if (s == 1) {
+            ml[wr] = make_float2(m, l);
+            if (wr == 0) sm.started1 = started ? 1 : 0;
+          }
+          bar_pair(1);
+          if (s == 0) {
+            const float2 o = ml[wr];
+            have1 = sm.started1 != 0;
+            const float mn = fmaxf(m, o.x), base = mn == -INFINITY ? 0.f : mn;
+            w0 = m == -INFINITY && l == 0.f ? 0.f : exp2f(m - base);
+            w1 = o.x == -INFINITY && o.y == 0.f ? 0.f : exp2f(o.x - base);
+            l = (l == 0.f ? 0.f : l * w0) + (o.y == 0.f ? 0.f : o.y * w1);
+            m = mn;
+          }
+        }
+        if (!split || s == 0) {
+          const bool whole = x.flags & 4, live = r < rows;
+          const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a NaN sum stays one
+          w0 *= inv;
+          w1 *= inv;
+          const size_t at = live ? (size_t)(x.h * a.g + r % a.g) * a.N + r / a.g : 0;
+          const int slot_row = x.slot * a.slot_rows + (split ? 0 : s * kM) + wr;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            float o[32];
+            if (started) {
+              tc::tmem_ld32(tO + q * 32, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= w0;
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            }
+            if (have1) {
+              float o1[32];
+              tc::tmem_ld32(tO + 128 + q * 32, o1);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], w1, o[i]);
+            }
+            if (!live) continue;
+            if (whole) {
+              __nv_bfloat16* out = (__nv_bfloat16*)a.out + at * D + q * 32;
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) st_vec<__nv_bfloat16, 8>(out + i, o + i);
+            } else {
+              float* po = a.po + (size_t)slot_row * D + q * 32;
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) st_vec<float, 4>(po + i, o + i);
+            }
+          }
+          if (live) {
+            if (whole) {
+              if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+            } else {
+              a.pml[slot_row] = make_float2(m, l);
+            }
+          }
+        }
+        if (split) {
+          // stream 1 may overwrite its O (by its next P) only now
+          tc::tc_fence_before();
+          bar_pair(2);
+          tc::tc_fence_after();
+        }
+      }
+    }
+    tc::cp_async_wait_all();
+  }
+  if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
+  if (!ok) status_set(st, FASTAR_ERR_TIMEOUT);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == kIssuer) tc::tmem_dealloc(tmem, 512);
+  pdl_trigger();
+}
+
+template <int D>
+int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
+  CUtensorMap pk, pv, k, v;
+  const uint32_t box = (1u << a.page_shift) < (uint32_t)kN ? (1u << a.page_shift) : (uint32_t)kN;
+  const uint64_t rows = ((uint64_t)a.n_pages * a.H) << a.page_shift;
+  // a part that is absent is never loaded; its maps describe the queries
+  int rc = make_tmap_bf16_2d(&k, rows ? a.K : a.q, rows ? rows : 1, D, box, 64);
+  if (rc == FASTAR_OK) rc = make_tmap_bf16_2d(&v, rows ? a.V : a.q, rows ? rows : 1, D, box, 64);
+  if (rc == FASTAR_OK) rc = make_tmap_bf16_2d(&pk, a.C ? a.pK : a.q, a.C ? (uint64_t)a.H * a.C : 1, D, kN, 64);
+  if (rc == FASTAR_OK) rc = make_tmap_bf16_2d(&pv, a.C ? a.pV : a.q, a.C ? (uint64_t)a.H * a.C : 1, D, kN, 64);
+  if (rc != FASTAR_OK) return rc;
+  constexpr int smem = (int)sizeof(Smem<D>);
+  static_assert(smem <= 227 * 1024, "shared memory");
+  auto kernel = branch_tc_kernel<D>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, pk, pv, k, v, a, a.TM == kM ? 1 : 0, st) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FASTAR_ERR_CUDA;
+  }
+  FASTAR_LAUNCHED(s, "branch_tc");
+  return FASTAR_OK;
+}
+
+}  // namespace
+
+int launch_branch_tc(const BranchArgs& a, int32_t* st, cudaStream_t s) {
+  return a.D == 128 ? launch_t<128>(a, st, s) : launch_t<64>(a, st, s);
+}
+
+}  // namespace fastar
