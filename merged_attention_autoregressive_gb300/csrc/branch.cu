@@ -48,8 +48,7 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
   bool bad = false;
   for (int b = warp; b < a.B; b += kPlanThreads / 32) {
     const int lo = a.cu[b], hi = a.cu[b + 1], len = a.len[b];
-    if (lo < 0 || hi < lo || hi > a.N || (b == 0 && lo != 0) || len < 0 ||
-        (long long)len > ((long long)a.max_pages << a.page_shift)) {
+    if (!branch_ok(a, b, lo, hi, len)) {
       bad = true;
       continue;
     }
@@ -66,7 +65,7 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
   if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
   if (__syncthreads_or(bad)) {
     // nothing to do for the kernels behind, also without a status word
-    for (int h = tid; h <= a.H + 2; h += kPlanThreads) a.head[h] = 0;
+    for (int h = tid; h <= a.H + 1; h += kPlanThreads) a.head[h] = 0;
     return;
   }
   const long long rows = (long long)a.cu[a.B] * a.g;
@@ -91,78 +90,74 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
   }
   if (tid == 0) {
     a.head[a.H] = nt > 0 ? carry : 0;
-    a.head[a.H + 1] = rows;
-    a.head[a.H + 2] = nt;
+    a.head[a.H + 1] = nt;
   }
   pdl_trigger();
 }
 
-// Joins the partials of every item that is cut: grid (cuts, row groups), a
-// warp per row.  The CTA of the item's first cut does the item.
+// Joins the partials of every item that is cut: grid (runs, row groups), a
+// warp per row; the run that begins an item left a record of it.  The
+// maxima and sums of up to 32 partials are read at once, one per lane, then
+// the rows of O eight at a time, in the order of the runs.
+constexpr int kJoinRows = 16;  // rows per CTA, two per warp
+
 template <typename T>
 __global__ void __launch_bounds__(256) branch_combine_kernel(BranchArgs a, int32_t* st) {
   pdl_wait();
-  if (status_bad(st)) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x + 1;
-  const long long U = a.head[a.H];
-  const int nt = (int)a.head[a.H + 2];
-  const long long u = U * c / a.G, up = U * (c - 1) / a.G;
-  if (u == up || u >= U) return;
-  const int h = warp_count_le(a.head, a.H, u) - 1;
-  const int p = prefix_units(prefix_size(a, h), a.TN);
-  const long long off = u - a.head[h];
-  int l = 0, r = nt;
-  while (r - l > 1) {
-    const int step = (r - l + 31) / 32;
-    const int at = l + lane * step;
-    const unsigned m = __ballot_sync(0xffffffffu, at < r && (long long)at * p + a.tile[at] <= off);
-    const int k = max(1, __popc(m));
-    r = min(r, l + k * step);
-    l = l + (k - 1) * step;
-  }
-  const int t = l;
-  const long long start = a.head[h] + (long long)t * p + a.tile[t];
-  const long long end = start + p + a.tile[t + 1] - a.tile[t];
-  if (start < up || start == u) return;  // an earlier cut's, or the cut lies between two items
-  const long long rows = a.head[a.H + 1], r0 = (long long)t * a.TM;
-  const int nr = (int)min((long long)a.TM, rows - r0);
-  for (int i = blockIdx.y * 8 + warp; i < nr; i += gridDim.y * 8) {
-    // the first run's slot, then one per later run
-    float m = -INFINITY;
-    for (int j = c - 1; j < a.G; ++j) {
-      const long long b = U * j / a.G;
-      if (b >= end) break;
-      if (U * (j + 1) / a.G == b) continue;
-      const int slot = 2 * j + (j == c - 1 && start != b ? 1 : 0);
-      m = fmaxf(m, a.pml[(size_t)slot * a.slot_rows + i].x);
-    }
-    const float base = m == -INFINITY ? 0.f : m;
-    float lsum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = c - 1; j < a.G; ++j) {
-      const long long b = U * j / a.G;
-      if (b >= end) break;
-      if (U * (j + 1) / a.G == b) continue;
-      const int slot = 2 * j + (j == c - 1 && start != b ? 1 : 0);
-      const float2 ml = a.pml[(size_t)slot * a.slot_rows + i];
-      if (ml.y == 0.f) continue;  // the row saw nothing in that run
-      const float w = exp2f(ml.x - base);
-      lsum += w * ml.y;
-      if (lane * 4 < a.D) {
-        const float4 x = *reinterpret_cast<const float4*>(a.po + ((size_t)slot * a.slot_rows + i) * a.D + lane * 4);
-        o[0] += w * x.x;
-        o[1] += w * x.y;
-        o[2] += w * x.z;
-        o[3] += w * x.w;
+  const bool stop = status_bad(st);
+  const BranchCut x = a.cuts[blockIdx.x];
+  if (stop || x.h < 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
+  const int rows = a.cu[a.B] * a.g, r0 = x.t * a.TM;
+  const int nr = min(a.TM, rows - r0), n = x.last - c + 1;
+  for (int i = blockIdx.y * kJoinRows + warp; i < min(nr, (int)(blockIdx.y + 1) * kJoinRows); i += 8) {
+    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < n; j0 += 32) {
+      // run c + j0 + lane: its slot, or none where it is past the item or empty
+      const int j = c + j0 + lane;
+      int slot = j == c ? x.slot : 2 * j;
+      if (j0 + lane >= n || x.U * j / a.G == x.U * (j + 1) / a.G) slot = -1;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (slot >= 0) ml = a.pml[(size_t)slot * a.slot_rows + i];
+      if (ml.y == 0.f) slot = -1;  // the row saw nothing in that run
+      float top = slot >= 0 ? ml.x : -INFINITY;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
+      const float w = slot >= 0 ? exp2f(ml.x - base) : 0.f;
+      const float alpha = l == 0.f ? 0.f : exp2f(m - base);
+      l = l * alpha + warp_sum(slot >= 0 ? w * ml.y : 0.f);
+      m = mn;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] *= alpha;
+      for (int k0 = 0; k0 < min(32, n - j0); k0 += 8) {
+        float4 p[8];
+        float wk[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int sk = __shfl_sync(0xffffffffu, slot, k0 + k);
+          wk[k] = __shfl_sync(0xffffffffu, w, k0 + k);
+          p[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (sk >= 0 && lane * 4 < a.D)
+            p[k] = *reinterpret_cast<const float4*>(a.po + ((size_t)sk * a.slot_rows + i) * a.D + lane * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          o[0] = fmaf(wk[k], p[k].x, o[0]);
+          o[1] = fmaf(wk[k], p[k].y, o[1]);
+          o[2] = fmaf(wk[k], p[k].z, o[2]);
+          o[3] = fmaf(wk[k], p[k].w, o[3]);
+        }
       }
     }
-    const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // a NaN sum stays one
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN sum stays one
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] *= inv;
-    const long long row = r0 + i;
-    const size_t at = (size_t)(h * a.g + (int)(row % a.g)) * a.N + (size_t)(row / a.g);
+    const int row = r0 + i;
+    const size_t at = (size_t)(x.h * a.g + row % a.g) * a.N + row / a.g;
     if (lane * 4 < a.D) st_vec<T, 4>((T*)a.out + at * a.D + lane * 4, o);
-    if (a.lse && lane == 0) a.lse[at] = lsum == 0.f ? -INFINITY : (base + log2f(lsum)) * 0.6931471805599453f;
+    if (a.lse && lane == 0)
+      a.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.6931471805599453f;
   }
   pdl_trigger();
 }
@@ -180,7 +175,7 @@ int launch_branch_plan(const BranchArgs& a, int32_t* st, cudaStream_t s) {
 
 int launch_branch_combine(const BranchArgs& a, fastar_dtype dt, int32_t* st, cudaStream_t s) {
   const int rows = (int)min((long long)a.TM, (long long)a.N * a.g);
-  const dim3 grid(a.G - 1, (rows + 7) / 8);
+  const dim3 grid(a.G, (rows + kJoinRows - 1) / kJoinRows);
   cudaError_t rc = dt == FASTAR_BF16 ? launch_pdl(branch_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a, st)
                                      : launch_pdl(branch_combine_kernel<float>, grid, dim3(256), 0, s, a, st);
   if (rc != cudaSuccess) {
@@ -198,7 +193,7 @@ namespace {
 constexpr int kSms = 152;
 struct Geometry {
   int TM, TN, G, ntiles, slot_rows;
-  size_t head, tile, po, pml;  // bytes of the workspace's parts
+  size_t cuts, head, tile, po, pml;  // bytes of the workspace's parts
 };
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 Geometry geometry(fastar_dtype dt, int H, long long rows, int D) {
@@ -208,7 +203,8 @@ Geometry geometry(fastar_dtype dt, int H, long long rows, int D) {
   x.G = dt == FASTAR_F32 ? 2 * kSms : kSms;
   x.ntiles = (int)((rows + x.TM - 1) / x.TM);
   x.slot_rows = (int)(rows < x.TM ? rows : x.TM);
-  x.head = up256((size_t)(H + 3) * 8);
+  x.cuts = up256((size_t)x.G * sizeof(BranchCut));
+  x.head = up256((size_t)(H + 2) * 8);
   x.tile = up256((size_t)(x.ntiles + 1) * 8);
   x.po = up256((size_t)2 * x.G * x.slot_rows * D * 4);
   x.pml = up256((size_t)2 * x.G * x.slot_rows * 8);
@@ -221,7 +217,7 @@ size_t branch_ws_bytes(int Hq, int H, int N, int D) {
   size_t most = 0;
   for (fastar_dtype dt : {FASTAR_BF16, FASTAR_F32}) {
     const Geometry x = geometry(dt, H, (long long)N * (Hq / H), D);
-    const size_t n = x.head + x.tile + x.po + x.pml;
+    const size_t n = x.cuts + x.head + x.tile + x.po + x.pml;
     if (n > most) most = n;
   }
   return most;
@@ -264,11 +260,12 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   a.ntiles = x.ntiles;
   a.slot_rows = x.slot_rows;
   char* w = (char*)ws;
-  a.head = (long long*)w;
+  a.cuts = (BranchCut*)w;
+  a.head = (long long*)(w += x.cuts);
   a.tile = (long long*)(w += x.head);
   a.po = (float*)(w += x.tile);
   a.pml = (float2*)(w + x.po);
-  int rc = launch_branch_plan(a, st, s);
+  int rc = a.ntiles > 1 ? launch_branch_plan(a, st, s) : FASTAR_OK;
   if (rc == FASTAR_OK) rc = dt == FASTAR_BF16 ? launch_branch_tc(a, st, s) : launch_branch_simt(a, st, s);
   if (rc == FASTAR_OK) rc = launch_branch_combine(a, dt, st, s);
   return rc;

@@ -12,13 +12,16 @@
 // one run is finished there; one that is cut leaves a partial (O in fp32,
 // running max and sum) per run, and branch_combine joins them in order.
 //
-// The lengths live on the device, so branch_plan computes the prefix sums of
-// the units there; every consumer finds its place in them by searching.
+// The lengths live on the device.  With one row tile (single tokens) every
+// CTA sums the units itself; with more, branch_plan writes the prefix sums of
+// the units first and each CTA finds its place in them by searching.
 #pragma once
 
 #include "common.cuh"
 
 namespace fastar {
+
+struct BranchCut;
 
 struct BranchArgs {
   const void* q;
@@ -38,8 +41,9 @@ struct BranchArgs {
   // schedule
   int TM, TN, G, ntiles;  // ntiles: row tiles of all N tokens
   int slot_rows;          // rows of a partial
-  long long* head;        // [H + 1] first unit of each head; then [2] rows in use, tiles in use
-  long long* tile;        // [ntiles + 1] first page unit of each row tile
+  BranchCut* cuts;        // [G] what each run leaves unfinished
+  long long* head;        // more than one row tile: [H + 1] first unit of each head, then the tiles in use
+  long long* tile;        // the same: [ntiles + 1] first page unit of each row tile
   float* po;              // [2 G][slot_rows][D]
   float2* pml;            // [2 G][slot_rows]
 };
@@ -76,6 +80,95 @@ __device__ __forceinline__ int warp_count_le(const T* x, int n, T v) {
   return lo + __popc(m);
 }
 
+// Whether the lengths and offsets of a lane's branch hold.
+__device__ __forceinline__ bool branch_ok(const BranchArgs& a, int b, int lo, int hi, int len) {
+  return lo >= 0 && hi >= lo && hi <= a.N && (b != 0 || lo == 0) && len >= 0 &&
+         (long long)len <= ((long long)a.max_pages << a.page_shift);
+}
+
+// What a run starts from (whole warp).  One row tile: taken from the lengths
+// right here, so that single tokens need no plan kernel.  Otherwise from the
+// lists of branch_plan.
+struct BranchPlace {
+  long long U;      // units of the call; 0: nothing to do, or something does not hold
+  int nt, pages;    // row tiles in use; one row tile: its page units
+
+  __device__ __forceinline__ void load(const BranchArgs& a, int32_t* st) {
+    const int lane = threadIdx.x & 31;
+    nt = pages = 0;
+    if (a.ntiles > 1) {
+      U = a.head[a.H];
+      nt = (int)a.head[a.H + 1];
+      return;
+    }
+    bool ok = true;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + lane;
+      if (b < a.B) {
+        const int lo = a.cu[b], hi = a.cu[b + 1], len = a.len[b];
+        ok = ok && branch_ok(a, b, lo, hi, len);
+        if (ok && hi > lo) {
+          nt = 1;
+          pages += (branch_limit(hi - 1 - lo, hi - lo, len, a.block) + a.TN - 1) / a.TN;
+        }
+      }
+    }
+    nt = __reduce_max_sync(0xffffffffu, nt);
+    pages = __reduce_add_sync(0xffffffffu, pages);
+    U = 0;
+    for (int h0 = 0; h0 < a.H; h0 += 32) {
+      const int h = h0 + lane;
+      int v = 0;
+      if (h < a.H) {
+        const int size = a.size ? a.size[h] : a.C;
+        ok = ok && size >= 0 && size <= a.C;
+        v = prefix_units(prefix_size(a, h), a.TN);
+      }
+      U += __reduce_add_sync(0xffffffffu, v) + (long long)min(32, a.H - h0) * pages;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok && lane == 0) status_set(st, FASTAR_ERR_DEVICE_ARG);
+    if (!ok || nt == 0) U = 0;
+  }
+  // The item of unit u: head, row tile and first unit.
+  __device__ __forceinline__ void find(const BranchArgs& a, long long u, int& h, int& t, long long& first) const {
+    const int lane = threadIdx.x & 31;
+    if (a.ntiles > 1) {
+      h = warp_count_le(a.head, a.H, u) - 1;
+      const long long off = u - a.head[h];
+      const int p = prefix_units(prefix_size(a, h), a.TN);
+      int l = 0, r = nt;  // the row tile t with t p + tile[t] <= off < (t + 1) p + tile[t + 1]
+      while (r - l > 1) {
+        const int step = (r - l + 31) / 32;
+        const int at = l + lane * step;
+        const unsigned m = __ballot_sync(0xffffffffu, at < r && (long long)at * p + a.tile[at] <= off);
+        const int k = max(1, __popc(m));
+        r = min(r, l + k * step);
+        l = l + (k - 1) * step;
+      }
+      t = l;
+      first = a.head[h] + (long long)t * p + a.tile[t];
+      return;
+    }
+    t = 0;
+    h = 0;
+    first = 0;
+    for (int h0 = 0; h0 < a.H; h0 += 32) {
+      const int x = h0 + lane;
+      const int v = x < a.H ? prefix_units(prefix_size(a, x), a.TN) + pages : 0;
+      const int inc = warp_incl_scan(v);
+      const unsigned m = __ballot_sync(0xffffffffu, x < a.H && first + inc > u);
+      if (m) {
+        const int src = __ffs(m) - 1;
+        h = h0 + src;
+        first += __shfl_sync(0xffffffffu, inc - v, src);
+        return;
+      }
+      first += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+};
+
 // One unit of work, as the consumers see it.
 struct BranchUnit {
   int h, t;        // item
@@ -86,11 +179,22 @@ struct BranchUnit {
   int slot;        // partial slot of the item
 };
 
-// Walks the units of CTA run c, a whole warp in step.
+// What the join needs of the item that run c leaves unfinished (and began).
+struct BranchCut {
+  int h, t;        // h = -1: none
+  int last;        // the run that finishes it
+  int slot;        // the partial of run c; the later runs have slot 2 j
+  long long U;
+};
+
+// Walks the units of run c, a whole warp in step, a stretch of units of one
+// branch (or of the prefix) at a time.
 struct BranchWalk {
-  long long u, u_end, istart, iend, run0;
-  int h, t, c, nt, P, size;
+  int h, t, c, nt, left;           // item; run; units left in the run
+  int off, units, P, size, pages;  // next unit of the item, its units, those of the prefix
   int T0, T1;
+  bool head_item;                  // the run's first item
+  bool whole;
   // 32 branches at a time, one per lane: its tokens, length, visible keys and
   // the units up to and with it
   int bbase, before, total, lo, n, len, keys, nu, incl;
@@ -110,69 +214,84 @@ struct BranchWalk {
     incl = warp_incl_scan(nu);
     total = __shfl_sync(0xffffffffu, incl, 31);
   }
-  __device__ __forceinline__ void enter(const BranchArgs& a) {
-    const int rows = (int)a.head[a.H + 1];
+  __device__ __forceinline__ void enter(const BranchArgs& a, int from) {
+    const int rows = a.cu[a.B] * a.g;
     const int r0 = t * a.TM, r1 = min(r0 + a.TM, rows);
     T0 = r0 / a.g;
     T1 = (r1 + a.g - 1) / a.g;
-    const int hs = prefix_size(a, h);
-    size = hs;
-    P = prefix_units(hs, a.TN);
-    iend = istart + P + (a.tile[t + 1] - a.tile[t]);
+    size = prefix_size(a, h);
+    P = prefix_units(size, a.TN);
+    units = P + (a.ntiles > 1 ? (int)(a.tile[t + 1] - a.tile[t]) : pages);
+    off = from;
+    whole = from == 0 && units <= left;
     // first branch with tokens at or behind T0 (empty ones contribute nothing)
-    bbase = max(0, warp_count_le(a.cu, a.B, T0) - 1);
+    bbase = a.ntiles > 1 ? max(0, warp_count_le(a.cu, a.B, T0) - 1) : 0;
     before = 0;
     load_batch(a);
   }
-  // false: nothing to do for this CTA
-  __device__ __forceinline__ bool start(const BranchArgs& a, int cta) {
+  // Goes to the start of run cta; false: the run is empty.  The join's record
+  // of the run is left in *cut.
+  __device__ __forceinline__ bool start(const BranchArgs& a, int cta, int32_t* st, BranchCut* cut) {
+    BranchPlace p;
+    p.load(a, st);
     c = cta;
-    const long long U = a.head[a.H];
-    nt = (int)a.head[a.H + 2];
-    u = run0 = U * c / a.G;
-    u_end = U * (c + 1) / a.G;
-    if (u >= u_end) return false;
-    h = warp_count_le(a.head, a.H, u) - 1;
-    const long long off = u - a.head[h];
-    const int p = prefix_units(prefix_size(a, h), a.TN);
-    // the row tile t with t p + tile[t] <= off < (t + 1) p + tile[t + 1]
-    const int lane = threadIdx.x & 31;
-    int l = 0, r = nt;
-    while (r - l > 1) {
-      const int step = (r - l + 31) / 32;
-      const int at = l + lane * step;
-      const unsigned m = __ballot_sync(0xffffffffu, at < r && (long long)at * p + a.tile[at] <= off);
-      const int k = max(1, __popc(m));
-      r = min(r, l + k * step);
-      l = l + (k - 1) * step;
+    nt = p.nt;
+    pages = p.pages;
+    const long long u = p.U * c / a.G, end = p.U * (c + 1) / a.G;
+    left = (int)(end - u);
+    BranchCut x = {-1, 0, 0, 0, p.U};
+    if (left > 0) {
+      long long first;
+      p.find(a, u, h, t, first);
+      // the item of the run's last unit: begun here and not finished here?
+      const int h0 = h, t0 = t;
+      long long f1;
+      int h1, t1;
+      p.find(a, end - 1, h1, t1, f1);
+      h = h1;
+      t = t1;
+      enter(a, 0);
+      if (f1 >= u && f1 + units > end) {
+        x.h = h1;
+        x.t = t1;
+        x.slot = 2 * c + (f1 > u ? 1 : 0);
+        x.last = (int)(((f1 + units) * a.G - 1) / p.U);
+      }
+      h = h0;
+      t = t0;
+      head_item = true;
+      enter(a, (int)(u - first));
     }
-    t = l;
-    istart = a.head[h] + (long long)t * p + a.tile[t];
-    enter(a);
-    return true;
+    if ((threadIdx.x & 31) == 0) *cut = x;
+    return left > 0;
   }
-  // The next unit; false at the end of the run.
-  __device__ __forceinline__ bool next(const BranchArgs& a, BranchUnit& x) {
-    if (u >= u_end) return false;
-    if (u >= iend) {
-      istart = iend;
+  // The next stretch: x describes its first unit, `count` units follow one
+  // another, `keys_end` bounds their keys.  False at the end of the run.
+  // first / last: whether the stretch opens / closes the item in this run.
+  __device__ __forceinline__ bool next(const BranchArgs& a, BranchUnit& x, int& count, int& keys_end, bool& opens,
+                                       bool& closes, int opened) {
+    if (left == 0) return false;
+    if (off == units) {
       if (++t == nt) {
         t = 0;
         ++h;
       }
-      enter(a);
+      head_item = false;
+      enter(a, 0);
+      opened = 1;
     }
-    const int off = (int)(u - istart);
+    opens = opened != 0;
     x.h = h;
     x.t = t;
-    const bool whole = istart >= run0 && iend <= u_end;
-    x.flags = ((u == istart || u == run0) ? 1 : 0) | ((u + 1 == iend || u + 1 == u_end) ? 2 : 0) | (whole ? 4 : 0);
-    x.slot = 2 * c + (istart <= run0 ? 0 : 1);
+    x.flags = whole ? 4 : 0;
+    x.slot = 2 * c + (head_item ? 0 : 1);
+    int k;
     if (off < P) {
       x.branch = -1;
-      x.k0 = off * a.TN;
-      x.nk = max(0, min(a.TN, size - x.k0));
       x.lo = x.n = x.len = 0;
+      k = off;
+      count = P - off;
+      keys_end = size;
     } else {
       int s = off - P - before;
       while (s >= total && bbase < a.B) {
@@ -183,15 +302,21 @@ struct BranchWalk {
       }
       const unsigned m = __ballot_sync(0xffffffffu, incl > s);
       const int src = m ? __ffs(m) - 1 : 31;
-      const int k = s - (__shfl_sync(0xffffffffu, incl, src) - __shfl_sync(0xffffffffu, nu, src));
+      const int units_src = __shfl_sync(0xffffffffu, nu, src);
+      k = s - (__shfl_sync(0xffffffffu, incl, src) - units_src);
+      count = max(1, units_src - k);
       x.branch = bbase + src;
       x.lo = __shfl_sync(0xffffffffu, lo, src);
       x.n = __shfl_sync(0xffffffffu, n, src);
       x.len = __shfl_sync(0xffffffffu, len, src);
-      x.k0 = k * a.TN;
-      x.nk = max(0, min(a.TN, __shfl_sync(0xffffffffu, keys, src) - x.k0));
+      keys_end = __shfl_sync(0xffffffffu, keys, src);
     }
-    ++u;
+    count = min(count, left);
+    x.k0 = k * a.TN;
+    x.nk = 0;
+    off += count;
+    left -= count;
+    closes = left == 0 || off == units;
     return true;
   }
 };

@@ -23,8 +23,6 @@ struct SimtSmem {
   float K[kTN][D + 4];  // then the probabilities [kTM][kTN + 4]
   float V[kTN][D];
   float bias[kTN];
-  BranchUnit unit;
-  int more;
 };
 
 template <typename T, int D>
@@ -39,14 +37,26 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
   constexpr int OC = D / 16;                            // O columns per thread
   const float scale2 = a.scale * kLog2e;
   BranchWalk w;
-  const bool any = w.start(a, blockIdx.x);  // every warp walks; warp 0 publishes
-  if (!any) return;
-  const int rows = (int)a.head[a.H + 1];
+  // every warp walks for itself; what it writes is the same
+  int count = 0, keys_end = 0;
+  bool opens = false, closes = false;
+  BranchUnit x = {};
+  if (!w.start(a, blockIdx.x, st, a.cuts + blockIdx.x)) return;
+  const int rows = a.cu[a.B] * a.g;
   float m[4], l[4], o[4][OC];
   bool bad = false;
+  bool first_stretch = true;
   while (true) {
-    BranchUnit x;
-    if (!w.next(a, x)) break;
+    if (count == 0) {
+      if (!w.next(a, x, count, keys_end, opens, closes, first_stretch ? 1 : 0)) break;
+      first_stretch = false;
+    } else {
+      opens = false;
+      x.k0 += kTN;
+    }
+    --count;
+    x.nk = max(0, min(kTN, keys_end - x.k0));
+    x.flags = (x.flags & 4) | (opens ? 1 : 0) | (closes && count == 0 ? 2 : 0);
     const int r0 = x.t * kTM;
     __syncthreads();  // the previous unit's products are done with K, V, P and Q
     if (x.flags & 1) {

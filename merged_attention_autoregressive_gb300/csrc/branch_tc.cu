@@ -125,8 +125,6 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
   if (warp == kLoader) {
     // ================================================= loader
     BranchWalk w;
-    BranchUnit x, y;
-    const int rows = (int)a.head[a.H + 1];
     const int box = min(1 << a.page_shift, kN);  // rows of a page box
     if (lane == 0) {
       tc::prefetch_tensormap(&mapK);
@@ -134,88 +132,104 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       tc::prefetch_tensormap(&mapPK);
       tc::prefetch_tensormap(&mapPV);
     }
-    // page id of box `lane` and the counts of rows lane + 32 e of a unit,
-    // fetched one unit ahead
-    auto fetch = [&](const BranchUnit& u, int& id, int* cnt) {
-      id = -1;
-      if (u.branch >= 0) {
-        if (lane * box < u.nk) id = a.table[(size_t)u.branch * a.max_pages + ((u.k0 + lane * box) >> a.page_shift)];
-      } else if (a.m) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          cnt[e] = lane + 32 * e < u.nk ? a.m[(size_t)u.h * a.C + u.k0 + lane + 32 * e] : 0;
-      }
-    };
-    int id = -1, idn = -1, cnt[4], cntn[4];
-    bool more = w.start(a, blockIdx.x) && w.next(a, x);
-    if (more) fetch(x, id, cnt);
-    uint32_t j = 0, t = 0;  // units described, tiles issued
+    bool more = w.start(a, blockIdx.x, st, a.cuts + blockIdx.x);
+    const int rows = a.cu[a.B] * a.g;
+    uint32_t j = 0, t = 0;       // units described, tiles issued
+    uint32_t slot = 0, turn = 0; // of the ring: next tile, times round
+    int opened = 1;
     while (more && ok) {
-      const bool another = w.next(a, y);
-      if (another) fetch(y, idn, cntn);
-      // rows of the item that the unit concerns, by stream
+      // a stretch of units of one branch, or of the prefix
+      BranchUnit x;
+      int count, keys_end;
+      bool opens, closes;
+      more = w.next(a, x, count, keys_end, opens, closes, opened);
+      if (!more) break;
+      opened = 0;
+      const bool own = x.branch >= 0;
+      // rows of the item that it concerns, by stream
       const int r0 = x.t * a.TM;
       int lo = r0, hi = min(r0 + a.TM, rows);
-      if (x.branch >= 0) {
+      if (own) {
         lo = max(lo, x.lo * a.g);
         hi = min(hi, (x.lo + x.n) * a.g);
       }
-      int act = 0;
-      if (x.nk > 0 && hi > lo) act = split ? 1 : ((lo < r0 + kM ? 1 : 0) | (hi > r0 + kM ? 2 : 0));
-      const int ds = j % S::kRing;
-      if (j >= S::kRing) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dempty[ds], (j / S::kRing - 1) & 1u));
-      if (!ok) break;
-      if (x.branch < 0 && a.m) {
+      const int acts = hi <= lo ? 0 : split ? 1 : ((lo < r0 + kM ? 1 : 0) | (hi > r0 + kM ? 2 : 0));
+      // page id of box `lane` (or the counts of rows lane + 32 e) of the unit
+      // at k, fetched one unit ahead
+      const int32_t* table = a.table + (size_t)max(x.branch, 0) * a.max_pages;
+      const int32_t* counts = a.m ? a.m + (size_t)x.h * a.C : nullptr;
+      int id, cnt[4];
+      auto fetch = [&](int k, int* v) {
+        if (own) {
+          const int p = k + lane * box;
+          v[0] = p < keys_end && lane * box < kN ? table[p >> a.page_shift] : -1;
+        } else if (counts) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          sm.bias[ds][lane + 32 * e] = cnt[e] > 0 ? log2f((float)cnt[e]) : -INFINITY;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sm.bias[ds][lane + 32 * e] = 0.f;
-      }
-      if (lane == 0) {
-        sm.desc[ds].x = x;
-        sm.desc[ds].act = act;
-      }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.dfull[ds]);
-      ++j;
-      if (act) {
-        int row = 0;
-        bool mine = false;
-        if (x.branch >= 0) {
-          mine = lane * box < x.nk;
-          if (mine && (id < 0 || id >= a.n_pages)) {
-            bad = true;
-            mine = false;
-          }
-          row = ((id * a.H + x.h) << a.page_shift) + (x.k0 & ((1 << a.page_shift) - 1));
-        } else {
-          mine = lane == 0;
-          row = x.h * a.C + x.k0;
-        }
-        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        const uint32_t bytes = (uint32_t)boxes * (x.branch >= 0 ? box : kN) * D * 2;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++t) {
-          const int s = t % slots;
-          if (t >= (uint32_t)slots) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[s], (t / slots - 1) & 1u));
-          if (!ok) break;
-          if (lane == 0) tc::mbar_arrive_expect_tx(&sm.full[s], bytes);
-          __syncwarp();
-          if (mine) {
-            uint8_t* dst = ring + (size_t)s * S::kTile + lane * box * 128;
-            const CUtensorMap* map = x.branch >= 0 ? (kv ? &mapV : &mapK) : (kv ? &mapPV : &mapPK);
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) tc::tma_load_2d(dst + c * kN * 128, map, &sm.full[s], c * 64, row);
+          for (int e = 0; e < 4; ++e) {
+            const int p = k + lane + 32 * e;
+            v[e] = p < keys_end ? counts[p] : 0;
           }
         }
-      }
-      x = y;
-      id = idn;
+      };
+      int ahead[4] = {0, 0, 0, 0};
+      fetch(x.k0, ahead);
+      for (int i = 0; i < count && ok; ++i) {
+        id = ahead[0];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) cnt[e] = cntn[e];
-      more = another;
+        for (int e = 0; e < 4; ++e) cnt[e] = ahead[e];
+        if (i + 1 < count) fetch(x.k0 + kN, ahead);
+        x.nk = max(0, min(kN, keys_end - x.k0));
+        const int act = x.nk > 0 ? acts : 0;
+        const int ds = j % S::kRing;
+        if (j >= S::kRing) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dempty[ds], (j / S::kRing - 1) & 1u));
+        if (!ok) break;
+        if (!own && counts) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sm.bias[ds][lane + 32 * e] = cnt[e] > 0 ? __log2f((float)cnt[e]) : -INFINITY;
+        }
+        if (lane == 0) {
+          Desc& d = sm.desc[ds];
+          d.x = x;
+          d.x.flags = x.flags | (opens && i == 0 ? 1 : 0) | (closes && i == count - 1 ? 2 : 0);
+          d.act = act;
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.dfull[ds]);
+        ++j;
+        if (act) {
+          int row = x.h * a.C + x.k0;
+          bool mine = lane == 0;
+          uint32_t bytes = kN * D * 2;
+          if (own) {
+            mine = lane * box < x.nk;
+            if (mine && (id < 0 || id >= a.n_pages)) {
+              bad = true;
+              mine = false;
+            }
+            row = ((id * a.H + x.h) << a.page_shift) + (x.k0 & ((1 << a.page_shift) - 1));
+            bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box * D * 2;
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            if (turn > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[slot], (turn - 1) & 1u));
+            if (!ok) break;
+            if (lane == 0) tc::mbar_arrive_expect_tx(&sm.full[slot], bytes);
+            __syncwarp();
+            if (mine) {
+              uint8_t* dst = ring + (size_t)slot * S::kTile + (own ? lane * box * 128 : 0);
+              const CUtensorMap* map = own ? (kv ? &mapV : &mapK) : (kv ? &mapPV : &mapPK);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c) tc::tma_load_2d(dst + c * kN * 128, map, &sm.full[slot], c * 64, row);
+            }
+            ++t;
+            if (++slot == (uint32_t)slots) {
+              slot = 0;
+              ++turn;
+            }
+          }
+        }
+        x.k0 += kN;
+      }
     }
     // no unit: the end of the run
     if (ok) {
@@ -342,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = tl + s * 128, tO = tl + 256 + s * 128;
     const float scale2 = a.scale * kLog2e;
-    const int rows = (int)a.head[a.H + 1];
+    const int rows = a.cu[a.B] * a.g;
     uint32_t ns = 0, items = 0, turn = 0;  // S tiles seen, items, active units of the item
     float m = -INFINITY, l = 0.f;
     bool started = false;
@@ -393,8 +407,12 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
             // log2 scores with their bias; what the row does not see: -inf
             mul = 1.f;
             const float* bias = sm.bias[ds];
+            if (!biased) {
 #pragma unroll
-            for (int i = 0; i < kN; i += 4) {
+              for (int i = 0; i < kN; ++i) v[i] *= scale2;
+            } else
+#pragma unroll
+              for (int i = 0; i < kN; i += 4) {
               const float4 b = *reinterpret_cast<const float4*>(bias + i);
               v[i] = fmaf(v[i], scale2, b.x);
               v[i + 1] = fmaf(v[i + 1], scale2, b.y);
