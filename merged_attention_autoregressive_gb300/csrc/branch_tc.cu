@@ -248,44 +248,63 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     ok = __all_sync(0xffffffffu, ok);
   } else if (warp == kIssuer) {
     // ================================================= MMA issuer
+    // Descriptors are computed on every lane, outside the elected lane's
+    // branch, and the steps are unrolled: the issue of a product's MMAs then
+    // keeps up with the tensor core.
     constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kM, kN, 0, 0);
     constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kM, D, 0, 1);
-    uint32_t t = 0, items = 0, turn = 0;
-    uint32_t np[2] = {0, 0};               // P tiles consumed per stream
-    bool pend[2] = {false, false};         // S of the stream is out, its P V not yet
-    uint32_t vt[2] = {0, 0};               // its value tile (count of tiles)
-    int vk[2] = {0, 0}, left[2] = {0, 0};  // its keys; whether the tile is free afterwards
-    bool first[2] = {true, true};          // O of the stream starts anew
+    uint32_t slot = 0, phase = 0;  // of the ring: the next unit's key tile
+    uint32_t items = 0, turn = 0;
+    struct Stream {
+      uint32_t np = 0;       // P tiles consumed
+      bool pend = false;     // S is out, its P V not yet
+      uint32_t vslot = 0, vphase = 0, order = 0;  // its value tile
+      int vk = 0;            // its keys
+      bool free = false;     // whether the tile is free afterwards
+      uint32_t fresh = 0u;   // 0: O starts anew
+    } s0, s1;
+    uint32_t order = 0;
     bool issued = false;
-    auto pv = [&](int s) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pready[s], np[s] & 1u) &&
-                                       tc::mbar_wait(&sm.full[vt[s] % slots], (vt[s] / slots) & 1u));
+    const uint32_t ring_addr = tc::smem_u32(ring), q_addr = tc::smem_u32(sm.tiles);
+    auto pv = [&](Stream& x, const int s) {
+      ok = __all_sync(0xffffffffu,
+                      tc::mbar_wait(&sm.pready[s], x.np & 1u) && tc::mbar_wait(&sm.full[x.vslot], x.vphase));
       if (!ok) return;
-      ++np[s];
+      ++x.np;
       tc::tc_fence_after();
-      uint8_t* v = ring + (size_t)(vt[s] % slots) * S::kTile;
-      const int steps = (vk[s] + 15) / 16;
-      if (vk[s] & 15) {
-        // value rows behind the unit's keys take part in the last step with
-        // weight 0: they must not hold an infinity or NaN
-        for (int e = lane; e < (steps * 16 - vk[s]) * (D / 8); e += 32) {
-          const int r = vk[s] + e / (D / 8), c = e % (D / 8);
-          *reinterpret_cast<uint4*>(v + (c >> 3) * kN * 128 + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+      const uint64_t vd = tc::sdesc_mnmajor_sw128(ring_addr + x.vslot * S::kTile, kN * 128);
+      const uint32_t dO = tmem + 256 + s * 128, dP = tmem + s * 128;
+      const uint32_t acc = x.fresh;
+      uint64_t* const done = &sm.empty[x.vslot];
+      if (x.vk == kN) {
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kN / 16; ++k)
+            tc::mma_bf16_tmem_a(dO, dP + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : acc);
+          if (x.free) tc::mma_commit(done);
         }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (tc::elect_one()) {
-        const uint64_t vd = tc::sdesc_mnmajor_sw128(tc::smem_u32(v), kN * 128);
-        for (int k = 0; k < steps; ++k)
-          tc::mma_bf16_tmem_a(tmem + 256 + s * 128, tmem + s * 128 + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv,
-                              (!first[s] || k > 0) ? 1u : 0u);
-        if (left[s]) tc::mma_commit(&sm.empty[vt[s] % slots]);
+      } else {
+        const int steps = (x.vk + 15) / 16;
+        if (x.vk & 15) {
+          // value rows behind the unit's keys take part in the last step with
+          // weight 0: they must not hold an infinity or NaN
+          uint8_t* v = ring + (size_t)x.vslot * S::kTile;
+          for (int e = lane; e < (steps * 16 - x.vk) * (D / 8); e += 32) {
+            const int r = x.vk + e / (D / 8), c = e % (D / 8);
+            *reinterpret_cast<uint4*>(v + (c >> 3) * kN * 128 + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (tc::elect_one()) {
+          for (int k = 0; k < steps; ++k)
+            tc::mma_bf16_tmem_a(dO, dP + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : acc);
+          if (x.free) tc::mma_commit(done);
+        }
       }
       __syncwarp();
-      first[s] = false;
-      pend[s] = false;
-      issued = true;
+      x.fresh = 1u;
+      x.pend = false;
     };
     for (uint32_t j = 0; ok; ++j) {
       const int ds = j % S::kRing;
@@ -299,45 +318,56 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       if (flags & 1) {
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.qfull, items & 1u));
         if (!ok) break;
-        first[0] = first[1] = true;
+        s0.fresh = s1.fresh = 0u;
         turn = 0;
       }
       const int act = split && act0 ? 1 << (turn & 1) : act0;
       if (act0) ++turn;
-      const int ks = t % slots;
+      const uint32_t vslot = slot + 1 == (uint32_t)slots ? 0 : slot + 1;
+      const uint32_t vphase = slot + 1 == (uint32_t)slots ? phase ^ 1u : phase;
+      const uint64_t kd = tc::sdesc_kmajor_sw128(ring_addr + slot * S::kTile);
+      auto step = [&](Stream& x, const int s) {
+        if (x.pend && (!split || (act >> s & 1))) pv(x, s);
+        if (!ok || !(act >> s & 1)) return;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.full[slot], phase));
+        if (!ok) return;
+        tc::tc_fence_after();
+        const uint64_t qd = tc::sdesc_kmajor_sw128(q_addr + (split ? 0 : s) * S::kTile);
+        const uint32_t dS = tmem + s * 128;
+        const bool last = (act >> (s + 1)) == 0;
+        if (tc::elect_one()) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (pend[s] && (!split || (act >> s & 1))) pv(s);
-        if (!ok) break;
-        if (act >> s & 1) {
-          ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.full[ks], (t / slots) & 1u));
-          if (!ok) break;
-          tc::tc_fence_after();
-          if (tc::elect_one()) {
-            const uint64_t qd = tc::sdesc_kmajor_sw128(tc::smem_u32(sm.tiles + (split ? 0 : s) * S::kTile));
-            const uint64_t kd = tc::sdesc_kmajor_sw128(tc::smem_u32(ring + (size_t)ks * S::kTile));
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * kN * 128 + (k & 3) * 32;
-              tc::mma_bf16(tmem + s * 128, tc::sdesc_add(qd, off), tc::sdesc_add(kd, off), idesc_qk, k > 0 ? 1u : 0u);
-            }
-            tc::mma_commit(&sm.sfull[s]);
-            if ((act >> (s + 1)) == 0) tc::mma_commit(&sm.empty[ks]);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * kN * 128 + (k & 3) * 32;
+            tc::mma_bf16(dS, tc::sdesc_add(qd, off), tc::sdesc_add(kd, off), idesc_qk, k > 0 ? 1u : 0u);
           }
-          __syncwarp();
-          issued = true;
-          pend[s] = true;
-          vt[s] = t + 1;
-          vk[s] = nk;
-          left[s] = (act >> (s + 1)) == 0;
+          tc::mma_commit(&sm.sfull[s]);
+          if (last) tc::mma_commit(&sm.empty[slot]);
         }
+        __syncwarp();
+        issued = true;
+        x.pend = true;
+        x.vslot = vslot;
+        x.vphase = vphase;
+        x.order = order;
+        x.vk = nk;
+        x.free = last;
+      };
+      step(s0, 0);
+      if (!ok) break;
+      step(s1, 1);
+      if (!ok) break;
+      if (act) {
+        ++order;
+        slot = vslot + 1 == (uint32_t)slots ? 0 : vslot + 1;
+        phase = vslot + 1 == (uint32_t)slots ? vphase ^ 1u : vphase;
       }
-      if (act) t += 2;
-      if (ok && (flags & 2)) {
+      if (flags & 2) {
         // streams in the order of their units, so that tiles are freed in order
-        const int s0 = pend[0] && pend[1] && (int32_t)(vt[1] - vt[0]) < 0 ? 1 : 0;
-        if (pend[s0]) pv(s0);
-        if (ok && pend[s0 ^ 1]) pv(s0 ^ 1);
+        const bool swap = s0.pend && s1.pend && s1.order < s0.order;
+        if (!swap && s0.pend) pv(s0, 0);
+        if (ok && s1.pend) pv(s1, 1);
+        if (ok && swap) pv(s0, 0);
         if (ok && tc::elect_one()) tc::mma_commit(&sm.odone);
         __syncwarp();
         ++items;
