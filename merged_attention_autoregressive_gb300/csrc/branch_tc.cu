@@ -61,7 +61,7 @@ struct Smem {
   Desc desc[S::kRing];
   uint64_t full[S::kSlots1], empty[S::kSlots1];
   uint64_t dfull[S::kRing], dempty[S::kRing];
-  uint64_t sfull[2], pready[2], odone, qfull, fin;
+  uint64_t sfull[2], pready[2][2], odone, qfull, fin;  // pready: by stream and half of the keys
   uint32_t tmem;
   int started1;
 };
@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&sm.sfull[s], 1);
-      tc::mbar_init(&sm.pready[s], 4);
+      tc::mbar_init(&sm.pready[s][0], 4);
+      tc::mbar_init(&sm.pready[s][1], 4);
     }
     tc::mbar_init(&sm.odone, 1);
     tc::mbar_init(&sm.qfull, 8);
@@ -268,9 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     const uint32_t ring_addr = tc::smem_u32(ring), q_addr = tc::smem_u32(sm.tiles);
     auto pv = [&](Stream& x, const int s) {
       ok = __all_sync(0xffffffffu,
-                      tc::mbar_wait(&sm.pready[s], x.np & 1u) && tc::mbar_wait(&sm.full[x.vslot], x.vphase));
+                      tc::mbar_wait(&sm.pready[s][0], x.np & 1u) && tc::mbar_wait(&sm.full[x.vslot], x.vphase));
       if (!ok) return;
-      ++x.np;
       tc::tc_fence_after();
       const uint64_t vd = tc::sdesc_mnmajor_sw128(ring_addr + x.vslot * S::kTile, kN * 128);
       const uint32_t dO = tmem + 256 + s * 128, dP = tmem + s * 128;
@@ -279,8 +279,17 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       if (x.vk == kN) {
         if (tc::elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kN / 16; ++k)
+          for (int k = 0; k < kN / 32; ++k)
             tc::mma_bf16_tmem_a(dO, dP + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : acc);
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pready[s][1], x.np & 1u));
+        if (!ok) return;
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int k = kN / 32; k < kN / 16; ++k)
+            tc::mma_bf16_tmem_a(dO, dP + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, 1u);
           if (x.free) tc::mma_commit(done);
         }
       } else {
@@ -296,12 +305,16 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           tc::fence_proxy_async_smem();
           __syncwarp();
         }
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pready[s][1], x.np & 1u));
+        if (!ok) return;
+        tc::tc_fence_after();
         if (tc::elect_one()) {
           for (int k = 0; k < steps; ++k)
             tc::mma_bf16_tmem_a(dO, dP + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : acc);
           if (x.free) tc::mma_commit(done);
         }
       }
+      ++x.np;
       __syncwarp();
       x.fresh = 1u;
       x.pend = false;
@@ -420,55 +433,64 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       const bool active = act0 && (split ? (turn & 1) == (uint32_t)s : (act0 >> s & 1));
       if (act0) ++turn;
       if (active) {
-        const int seen = r < rows ? branch_row_keys(a, x, r) : 0;
-        const bool any = __any_sync(0xffffffffu, seen > 0), all = __all_sync(0xffffffffu, seen >= kN);
+        // rows behind the last token count as full: nobody reads their results
+        const int seen = r < rows ? branch_row_keys(a, x, r) : kN;
+        const bool any = __any_sync(0xffffffffu, r < rows && seen > 0), all = __all_sync(0xffffffffu, seen >= kN);
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sfull[s], ns & 1u));
         if (!ok) break;
         ++ns;
         tc::tc_fence_after();
-        uint32_t pk[64];
         if (any) {
-          float v[kN];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tc::tmem_ld32(tS + q * 32, v + q * 32);
-          float mul = scale2;
+          // log2 scores; without a bias or a mask the raw products, whose
+          // scale goes into the exponent's multiply-add
+          uint32_t raw0[64], raw1[64];
+          float* const v0 = reinterpret_cast<float*>(raw0);
+          float* const v1 = reinterpret_cast<float*>(raw1);
           const bool biased = x.branch < 0 && a.m != nullptr;
-          if (biased || !all) {
-            // log2 scores with their bias; what the row does not see: -inf
-            mul = 1.f;
-            const float* bias = sm.bias[ds];
-            if (!biased) {
+          const bool plain = !biased && all;
+          const float mul = plain ? scale2 : 1.f;
+          const float* bias = sm.bias[ds];
+          float tm[8];
+          auto scores = [&](float* v, const int c0) {
+            if (!plain) {
+              if (biased) {
 #pragma unroll
-              for (int i = 0; i < kN; ++i) v[i] *= scale2;
-            } else
+                for (int i = 0; i < 64; i += 4) {
+                  const float4 b = *reinterpret_cast<const float4*>(bias + c0 + i);
+                  tc::fma2(v[i], v[i + 1], scale2, scale2, b.x, b.y);
+                  tc::fma2(v[i + 2], v[i + 3], scale2, scale2, b.z, b.w);
+                }
+              } else {
 #pragma unroll
-              for (int i = 0; i < kN; i += 4) {
-              const float4 b = *reinterpret_cast<const float4*>(bias + i);
-              v[i] = fmaf(v[i], scale2, b.x);
-              v[i + 1] = fmaf(v[i + 1], scale2, b.y);
-              v[i + 2] = fmaf(v[i + 2], scale2, b.z);
-              v[i + 3] = fmaf(v[i + 3], scale2, b.w);
+                for (int i = 0; i < 64; i += 2) tc::mul2(v[i], v[i + 1], scale2, scale2);
+              }
+              if (!all) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) v[i] = c0 + i < seen ? v[i] : -INFINITY;
+              }
             }
-            if (!all) {
 #pragma unroll
-              for (int i = 0; i < kN; ++i) v[i] = i < seen ? v[i] : -INFINITY;
+            for (int i = 0; i < 64; i += 16) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                tm[e] = c0 + i == 0 ? fmaxf(v[i + e], v[i + 8 + e]) : tc::max3(tm[e], v[i + e], v[i + 8 + e]);
             }
-          }
-          float t4[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-          for (int i = 4; i < kN; i += 8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              t4[e] = i + 4 + e < kN ? tc::max3(t4[e], v[i + e], v[i + 4 + e]) : fmaxf(t4[e], v[i + e]);
-          }
-          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * mul;
+          };
+          tc::tmem_ld64_async(tS, raw0);
+          tc::tmem_wait64(raw0);
+          tc::tmem_ld64_async(tS + 64, raw1);  // lands under the first half's maxima
+          scores(v0, 0);
+          tc::tmem_wait64(raw1);
+          scores(v1, 64);
+          const float top =
+              fmaxf(tc::max3(tm[0], tm[1], tm[2]), tc::max3(tm[3], tm[4], tc::max3(tm[5], tm[6], tm[7]))) * mul;
           const bool raise = top > m + kRescale;
           const float mn = raise ? top : m;
           const float alpha = (raise && m != -INFINITY) ? exp2f(m - mn) : 1.f;
           if (started && __any_sync(0xffffffffu, alpha != 1.f)) {
             // S of this unit was issued behind the P V of the stream's last
             // one, and products complete in issue order: O is at rest
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               float o[32];
               tc::tmem_ld32(tO + q * 32, o);
@@ -479,27 +501,39 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           }
           l *= alpha;
           m = mn;
-          const float base = m == -INFINITY ? 0.f : m;
-          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+          const float base = m == -INFINITY ? 0.f : -m;
+          float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          // the weights of 64 keys, over the first columns of S in TMEM; the
+          // issuer may start their product with the values at once
+          auto weights = [&](float* v, const int half) {
+            uint32_t pk[32];
 #pragma unroll
-          for (int i = 0; i < kN; i += 2) {
-            const float p0 = ex2(fmaf(v[i], mul, -base)), p1 = ex2(fmaf(v[i + 1], mul, -base));
-            ps[i & 3] += p0;
-            ps[(i & 3) + 1] += p1;
-            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-            pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+            for (int i = 0; i < 64; i += 2) {
+              tc::fma2(v[i], v[i + 1], mul, mul, base, base);
+              const float p0 = ex2(v[i]), p1 = ex2(v[i + 1]);
+              tc::add2(ps[i & 7], ps[(i & 7) + 1], p0, p1);
+              const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+              pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            tc::tmem_st32u(tS + half * 32, pk);
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.pready[s][half]);
+          };
+          weights(v0, 0);
+          weights(v1, 1);
+          l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
         } else {
           // no row of the warp is concerned: weights 0
+          uint32_t pk[32];
 #pragma unroll
-          for (int i = 0; i < 64; ++i) pk[i] = 0u;
+          for (int i = 0; i < 32; ++i) pk[i] = 0u;
+          tc::tmem_st32u(tS, pk);
+          tc::tmem_st32u(tS + 32, pk);
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane < 2) tc::mbar_arrive(&sm.pready[s][lane]);
         }
-        tc::tmem_st32u(tS, pk);
-        tc::tmem_st32u(tS + 32, pk + 32);
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.pready[s]);
         started = true;
       }
       __syncwarp();
