@@ -7,9 +7,10 @@
 //                   descriptors and fetches its key and value tiles by TMA
 //                   (prefix: two 128-row boxes a tile; pages: a box per page
 //                   and column half, one lane per page) into a ring of tiles;
-//   warp 9          MMA issuer (warps 10 and 11 only give their registers away): S_s = Q_s K^T (M 128, N 128, K D) and O_s +=
+//   warps 9, 10     MMA issuers: S_s = Q_s K^T (M 128, N 128, K D) and O_s +=
 //                   P_s V (M 128, N D, K 128; P_s read from TMEM, where the
-//                   softmax wrote it over S_s).
+//                   softmax wrote it over S_s);
+//   warp 11         only gives its registers away.
 // More than 128 rows of queries per key/value head: an item is 256 rows and
 // stream s owns rows 128 s .. 128 s + 127, so each tile that is fetched feeds
 // four products, and one stream's softmax runs under the other's products.
@@ -61,7 +62,7 @@ struct Smem {
   Desc desc[S::kRing];
   uint64_t full[S::kSlots1], empty[S::kSlots1];
   uint64_t dfull[S::kRing], dempty[S::kRing];
-  uint64_t sfull[2], pready[2][2], odone, qfull, fin;  // pready: by stream and half of the keys
+  uint64_t sfull[2], pready[2][2], odone, qfull, fin[2];  // pready: by stream and half of the keys
   uint32_t tmem;
   int started1;
 };
@@ -76,18 +77,21 @@ __device__ __forceinline__ void bar_pair(int id) { asm volatile("bar.sync %0, 25
 // Registers: 384 threads launch with 168 each (64,512); the third warpgroup
 // gives 72 of its own up, so that the softmax rows (128 scores in registers)
 // get 200: 128 * 96 + 256 * 200 = 63,488.
-template <int D>
+template <int D, bool split>
 __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_constant__ CUtensorMap mapPK,
                                                                const __grid_constant__ CUtensorMap mapPV,
                                                                const __grid_constant__ CUtensorMap mapK,
                                                                const __grid_constant__ CUtensorMap mapV,
-                                                               const BranchArgs a, int split, int32_t* st) {
+                                                               const BranchArgs a, int32_t* st) {
   using S = Shape<D>;
   pdl_wait();
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slots = split ? S::kSlots1 : S::kSlots2;
+  // Tiles of a ring: one ring for both streams, or one each (a parity wait is
+  // sound only for who has seen every earlier use of the tile, and a stream
+  // that takes every other unit has not seen the other's).
+  constexpr int slots = split ? S::kSlots1 / 2 : S::kSlots2;
   uint8_t* const ring = sm.tiles + (split ? 1 : 2) * S::kTile;
   // CTA-uniform: the status word and the address of the tiles
   if (tid == 0 && (tc::smem_u32(sm.tiles) & 1023u)) status_set(st, FASTAR_ERR_CUDA);
@@ -100,16 +104,17 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     }
     for (int i = 0; i < S::kRing; ++i) {
       tc::mbar_init(&sm.dfull[i], 1);
-      tc::mbar_init(&sm.dempty[i], 9);  // 8 softmax warps and the issuer
+      tc::mbar_init(&sm.dempty[i], split ? 10 : 9);  // 8 softmax warps and the issuers
     }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&sm.sfull[s], 1);
       tc::mbar_init(&sm.pready[s][0], 4);
       tc::mbar_init(&sm.pready[s][1], 4);
     }
-    tc::mbar_init(&sm.odone, 1);
+    tc::mbar_init(&sm.odone, split ? 2 : 1);
     tc::mbar_init(&sm.qfull, 8);
-    tc::mbar_init(&sm.fin, 1);
+    tc::mbar_init(&sm.fin[0], 1);
+    tc::mbar_init(&sm.fin[1], 1);
     tc::fence_mbar_init();
   }
   if (warp == kIssuer) {
@@ -135,8 +140,10 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     }
     bool more = w.start(a, blockIdx.x, st, a.cuts + blockIdx.x);
     const int rows = a.cu[a.B] * a.g;
-    uint32_t j = 0, t = 0;       // units described, tiles issued
-    uint32_t slot = 0, turn = 0; // of the ring: next tile, times round
+    uint32_t j = 0;                   // units described
+    uint32_t slot0 = 0, round0 = 0;   // of the first ring: next tile, times round
+    uint32_t slot1 = 0, round1 = 0;   // of the second
+    uint32_t turn = 0;                // loaded units of the item
     int opened = 1;
     while (more && ok) {
       // a stretch of units of one branch, or of the prefix
@@ -146,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       more = w.next(a, x, count, keys_end, opens, closes, opened);
       if (!more) break;
       opened = 0;
+      if (opens) turn = 0;
       const bool own = x.branch >= 0;
       // rows of the item that it concerns, by stream
       const int r0 = x.t * a.TM;
@@ -210,23 +218,32 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
             row = ((id * a.H + x.h) << a.page_shift) + (x.k0 & ((1 << a.page_shift) - 1));
             bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box * D * 2;
           }
+          const bool second = split && (turn++ & 1);
+          uint32_t slot = second ? slot1 : slot0, round = second ? round1 : round0;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            if (turn > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[slot], (turn - 1) & 1u));
+            const uint32_t at = slot + (second ? slots : 0);
+            if (round > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.empty[at], (round - 1) & 1u));
             if (!ok) break;
-            if (lane == 0) tc::mbar_arrive_expect_tx(&sm.full[slot], bytes);
+            if (lane == 0) tc::mbar_arrive_expect_tx(&sm.full[at], bytes);
             __syncwarp();
             if (mine) {
-              uint8_t* dst = ring + (size_t)slot * S::kTile + (own ? lane * box * 128 : 0);
+              uint8_t* dst = ring + (size_t)at * S::kTile + (own ? lane * box * 128 : 0);
               const CUtensorMap* map = own ? (kv ? &mapV : &mapK) : (kv ? &mapPV : &mapPK);
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c) tc::tma_load_2d(dst + c * kN * 128, map, &sm.full[slot], c * 64, row);
+              for (int c = 0; c < D / 64; ++c) tc::tma_load_2d(dst + c * kN * 128, map, &sm.full[at], c * 64, row);
             }
-            ++t;
             if (++slot == (uint32_t)slots) {
               slot = 0;
-              ++turn;
+              ++round;
             }
+          }
+          if (second) {
+            slot1 = slot;
+            round1 = round;
+          } else {
+            slot0 = slot;
+            round0 = round;
           }
         }
         x.k0 += kN;
@@ -244,110 +261,108 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     // the copies have landed before the CTA exits, also when somebody's wait
     // ran out and nobody took the last tiles
     if (lane == 0)
-      for (uint32_t i = t > (uint32_t)slots ? t - slots : 0; i < t; ++i)
-        if (!tc::mbar_wait(&sm.full[i % slots], (i / slots) & 1u)) ok = false;
+      for (int i = 0; i < slots; ++i) {
+        const uint32_t n0 = round0 + (i < (int)slot0), n1 = round1 + (i < (int)slot1);
+        if (n0 && !tc::mbar_wait(&sm.full[i], (n0 - 1) & 1u)) ok = false;
+        if (n1 && !tc::mbar_wait(&sm.full[slots + i], (n1 - 1) & 1u)) ok = false;
+      }
     ok = __all_sync(0xffffffffu, ok);
-  } else if (warp == kIssuer) {
-    // ================================================= MMA issuer
+  } else if (split && (warp == kIssuer || warp == kIssuer + 1)) {
+    // ================================================= MMA issuers, one per stream
     // Descriptors are computed on every lane, outside the elected lane's
-    // branch, and the steps are unrolled: the issue of a product's MMAs then
-    // keeps up with the tensor core.
+    // branch, and the steps are unrolled.
     constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kM, kN, 0, 0);
     constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kM, D, 0, 1);
-    uint32_t slot = 0, phase = 0;  // of the ring: the next unit's key tile
+    const int s = warp - kIssuer;
+    const int base = s * slots;  // of the stream's ring
+    const uint32_t ring_addr = tc::smem_u32(ring + (size_t)base * S::kTile);
+    uint64_t *const full = sm.full + base, *const empty = sm.empty + base;
+    const uint64_t qd = tc::sdesc_kmajor_sw128(tc::smem_u32(sm.tiles));
+    const uint32_t dS = tmem + s * 128, dO = tmem + 256 + s * 128;
+    uint32_t slot = 0, phase = 0;    // of the ring: the next unit's key tile
     uint32_t items = 0, turn = 0;
-    struct Stream {
-      uint32_t np = 0;       // P tiles consumed
-      bool pend = false;     // S is out, its P V not yet
-      uint32_t vslot = 0, vphase = 0, order = 0;  // its value tile
-      int vk = 0;            // its keys
-      bool free = false;     // whether the tile is free afterwards
-      uint32_t fresh = 0u;   // 0: O starts anew
-    } s0, s1;
-    uint32_t order = 0;
+    uint32_t np = 0;                 // P tiles consumed
+    bool pend = false;               // S is out, its P V not yet
+    uint32_t pslot = 0, pphase = 0;  // its value tile
+    int pk = 0;                      // its keys
+    uint32_t acc = 0u;               // 0: O starts anew
     bool issued = false;
-    const uint32_t ring_addr = tc::smem_u32(ring), q_addr = tc::smem_u32(sm.tiles);
-    auto pv = [&](Stream& x, const int s) {
+    auto pv = [&]() {
       ok = __all_sync(0xffffffffu,
-                      tc::mbar_wait(&sm.pready[s][0], x.np & 1u) && tc::mbar_wait(&sm.full[x.vslot], x.vphase));
+                      tc::mbar_wait(&full[pslot], pphase) && tc::mbar_wait(&sm.pready[s][0], np & 1u));
       if (!ok) return;
       tc::tc_fence_after();
-      const uint64_t vd = tc::sdesc_mnmajor_sw128(ring_addr + x.vslot * S::kTile, kN * 128);
-      const uint32_t dO = tmem + 256 + s * 128, dP = tmem + s * 128;
-      const uint32_t acc = x.fresh;
-      uint64_t* const done = &sm.empty[x.vslot];
-      if (x.vk == kN) {
+      const uint64_t vd = tc::sdesc_mnmajor_sw128(ring_addr + pslot * S::kTile, kN * 128);
+      if (pk == kN) {
         if (tc::elect_one()) {
 #pragma unroll
           for (int k = 0; k < kN / 32; ++k)
-            tc::mma_bf16_tmem_a(dO, dP + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : acc);
+            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : acc);
         }
         __syncwarp();
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pready[s][1], x.np & 1u));
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pready[s][1], np & 1u));
         if (!ok) return;
         tc::tc_fence_after();
         if (tc::elect_one()) {
 #pragma unroll
           for (int k = kN / 32; k < kN / 16; ++k)
-            tc::mma_bf16_tmem_a(dO, dP + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, 1u);
-          if (x.free) tc::mma_commit(done);
+            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, 1u);
+          tc::mma_commit(&empty[pslot]);
         }
       } else {
-        const int steps = (x.vk + 15) / 16;
-        if (x.vk & 15) {
+        const int steps = (pk + 15) / 16;
+        if (pk & 15) {
           // value rows behind the unit's keys take part in the last step with
           // weight 0: they must not hold an infinity or NaN
-          uint8_t* v = ring + (size_t)x.vslot * S::kTile;
-          for (int e = lane; e < (steps * 16 - x.vk) * (D / 8); e += 32) {
-            const int r = x.vk + e / (D / 8), c = e % (D / 8);
+          uint8_t* v = ring + (size_t)(base + pslot) * S::kTile;
+          for (int e = lane; e < (steps * 16 - pk) * (D / 8); e += 32) {
+            const int r = pk + e / (D / 8), c = e % (D / 8);
             *reinterpret_cast<uint4*>(v + (c >> 3) * kN * 128 + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
           }
           tc::fence_proxy_async_smem();
           __syncwarp();
         }
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pready[s][1], x.np & 1u));
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pready[s][1], np & 1u));
         if (!ok) return;
         tc::tc_fence_after();
         if (tc::elect_one()) {
           for (int k = 0; k < steps; ++k)
-            tc::mma_bf16_tmem_a(dO, dP + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : acc);
-          if (x.free) tc::mma_commit(done);
+            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : acc);
+          tc::mma_commit(&empty[pslot]);
         }
       }
-      ++x.np;
       __syncwarp();
-      x.fresh = 1u;
-      x.pend = false;
+      ++np;
+      acc = 1u;
+      pend = false;
     };
     for (uint32_t j = 0; ok; ++j) {
       const int ds = j % S::kRing;
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dfull[ds], (j / S::kRing) & 1u));
       if (!ok) break;
-      const int act0 = sm.desc[ds].act;
+      const int act = sm.desc[ds].act;
       const int flags = sm.desc[ds].x.flags, nk = sm.desc[ds].x.nk;
       __syncwarp();
-      if (act0 < 0) break;
+      if (act < 0) break;
       if (lane == 0) tc::mbar_arrive(&sm.dempty[ds]);
       if (flags & 1) {
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.qfull, items & 1u));
         if (!ok) break;
-        s0.fresh = s1.fresh = 0u;
+        acc = 0u;
         turn = 0;
       }
-      const int act = split && act0 ? 1 << (turn & 1) : act0;
-      if (act0) ++turn;
+      const bool mine = act && (int)(turn & 1) == s;
       const uint32_t vslot = slot + 1 == (uint32_t)slots ? 0 : slot + 1;
       const uint32_t vphase = slot + 1 == (uint32_t)slots ? phase ^ 1u : phase;
-      const uint64_t kd = tc::sdesc_kmajor_sw128(ring_addr + slot * S::kTile);
-      auto step = [&](Stream& x, const int s) {
-        if (x.pend && (!split || (act >> s & 1))) pv(x, s);
-        if (!ok || !(act >> s & 1)) return;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.full[slot], phase));
-        if (!ok) return;
+      if (mine && pend) {
+        pv();
+        if (!ok) break;
+      }
+      if (mine) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[slot], phase));
+        if (!ok) break;
         tc::tc_fence_after();
-        const uint64_t qd = tc::sdesc_kmajor_sw128(q_addr + (split ? 0 : s) * S::kTile);
-        const uint32_t dS = tmem + s * 128;
-        const bool last = (act >> (s + 1)) == 0;
+        const uint64_t kd = tc::sdesc_kmajor_sw128(ring_addr + slot * S::kTile);
         if (tc::elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -355,32 +370,22 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
             tc::mma_bf16(dS, tc::sdesc_add(qd, off), tc::sdesc_add(kd, off), idesc_qk, k > 0 ? 1u : 0u);
           }
           tc::mma_commit(&sm.sfull[s]);
-          if (last) tc::mma_commit(&sm.empty[slot]);
+          tc::mma_commit(&empty[slot]);
         }
         __syncwarp();
         issued = true;
-        x.pend = true;
-        x.vslot = vslot;
-        x.vphase = vphase;
-        x.order = order;
-        x.vk = nk;
-        x.free = last;
-      };
-      step(s0, 0);
-      if (!ok) break;
-      step(s1, 1);
-      if (!ok) break;
-      if (act) {
-        ++order;
+        pend = true;
+        pslot = vslot;
+        pphase = vphase;
+        pk = nk;
+      }
+      if (act) ++turn;
+      if (mine) {
         slot = vslot + 1 == (uint32_t)slots ? 0 : vslot + 1;
         phase = vslot + 1 == (uint32_t)slots ? vphase ^ 1u : vphase;
       }
       if (flags & 2) {
-        // streams in the order of their units, so that tiles are freed in order
-        const bool swap = s0.pend && s1.pend && s1.order < s0.order;
-        if (!swap && s0.pend) pv(s0, 0);
-        if (ok && s1.pend) pv(s1, 1);
-        if (ok && swap) pv(s0, 0);
+        if (pend) pv();
         if (ok && tc::elect_one()) tc::mma_commit(&sm.odone);
         __syncwarp();
         ++items;
@@ -388,9 +393,152 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     }
     if (issued) {
       // every product has finished before TMEM is freed
-      if (tc::elect_one()) tc::mma_commit(&sm.fin);
+      if (tc::elect_one()) tc::mma_commit(&sm.fin[s]);
       __syncwarp();
-      if (!tc::mbar_wait(&sm.fin, 0)) ok = false;
+      if (!tc::mbar_wait(&sm.fin[s], 0)) ok = false;
+    }
+  } else if (!split && warp == kIssuer) {
+    // ================================================= MMA issuer of both streams
+    // In turn P_0 V, Q_0 K^T, P_1 V, Q_1 K^T: each softmax has the other
+    // stream's two products to itself (with an issuer per stream both fell
+    // into step, and the tensor core idled through both softmaxes).  The
+    // queue of the tensor core holds a few MMAs only, so that what lies
+    // between two products is kept short: a tile is waited for once, the
+    // next unit's descriptor is read under the queued products.
+    constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kM, kN, 0, 0);
+    constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kM, D, 0, 1);
+    const uint32_t ring_addr = tc::smem_u32(ring), q_addr = tc::smem_u32(sm.tiles);
+    const bool leader = tc::elect_one();
+    uint32_t slot = 0, phase = 0, items = 0;
+    // the streams whose S is out and whose P V is not yet, their value tile
+    // (one for both), its keys, and whether O starts anew
+    int pend = 0, pk = 0;
+    uint32_t pslot = 0, pphase = 0, np[2] = {0u, 0u}, acc[2] = {0u, 0u};
+    bool issued = false, vthere = false;
+    auto pv = [&](auto stream) {
+      constexpr int s = decltype(stream)::value;
+      if (!vthere) {
+        ok = ok && tc::mbar_wait(&sm.full[pslot], pphase);
+        vthere = true;
+        if (pk & 15) {
+          // value rows behind the unit's keys take part in the last step with
+          // weight 0: they must not hold an infinity or NaN
+          uint8_t* v = ring + (size_t)pslot * S::kTile;
+          for (int e = lane; e < (16 - (pk & 15)) * (D / 8); e += 32) {
+            const int r = pk + e / (D / 8), c = e % (D / 8);
+            *reinterpret_cast<uint4*>(v + (c >> 3) * kN * 128 + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
+      const uint64_t vd = tc::sdesc_mnmajor_sw128(ring_addr + pslot * S::kTile, kN * 128);
+      const uint32_t dS = tmem + s * 128, dO = tmem + 256 + s * 128;
+      const uint32_t ac = acc[s];
+      ok = ok && tc::mbar_wait(&sm.pready[s][0], np[s] & 1u);
+      tc::tc_fence_after();
+      if (pk == kN) {
+        if (leader && ok) {
+#pragma unroll
+          for (int k = 0; k < kN / 32; ++k)
+            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : ac);
+        }
+        __syncwarp();
+        ok = ok && tc::mbar_wait(&sm.pready[s][1], np[s] & 1u);
+        tc::tc_fence_after();
+        if (leader && ok) {
+#pragma unroll
+          for (int k = kN / 32; k < kN / 16; ++k)
+            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, 1u);
+        }
+      } else {
+        ok = ok && tc::mbar_wait(&sm.pready[s][1], np[s] & 1u);
+        tc::tc_fence_after();
+        const int steps = (pk + 15) / 16;
+        if (leader && ok)
+          for (int k = 0; k < steps; ++k)
+            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : ac);
+      }
+      pend &= ~(1 << s);
+      if (pend == 0 && leader && ok) tc::mma_commit(&sm.empty[pslot]);  // no stream wants the tile any more
+      __syncwarp();
+      ++np[s];
+      acc[s] = 1u;
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    int act = 0, flags = 0, nk = 0;
+    bool read = false;  // the unit's descriptor has been read
+    auto take = [&](uint32_t j, bool wait) {
+      const int ds = j % S::kRing;
+      if (wait)
+        ok = ok && tc::mbar_wait(&sm.dfull[ds], (j / S::kRing) & 1u);
+      else if (!__all_sync(0xffffffffu, tc::mbar_test_wait(&sm.dfull[ds], (j / S::kRing) & 1u)))
+        return;
+      act = sm.desc[ds].act;
+      flags = sm.desc[ds].x.flags;
+      nk = sm.desc[ds].x.nk;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sm.dempty[ds]);
+      read = true;
+    };
+    for (uint32_t j = 0;; ++j) {
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (!read) take(j, true);
+      read = false;
+      if (!ok || act < 0) break;
+      const int uact = act, uflags = flags, unk = nk;
+      if (uflags & 1) {
+        ok = ok && tc::mbar_wait(&sm.qfull, items & 1u);
+        acc[0] = acc[1] = 0u;
+      }
+      const uint64_t kd = tc::sdesc_kmajor_sw128(ring_addr + slot * S::kTile);
+      auto qk = [&](auto stream) {
+        constexpr int s = decltype(stream)::value;
+        tc::tc_fence_after();
+        const uint64_t qd = tc::sdesc_kmajor_sw128(q_addr + s * S::kTile);
+        const uint32_t dS = tmem + s * 128;
+        if (leader && ok) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * kN * 128 + (k & 3) * 32;
+            tc::mma_bf16(dS, tc::sdesc_add(qd, off), tc::sdesc_add(kd, off), idesc_qk, k > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(&sm.sfull[s]);
+          if ((uact >> (s + 1)) == 0) tc::mma_commit(&sm.empty[slot]);
+        }
+        __syncwarp();
+      };
+      if (uact) {
+        if (pend & 1) pv(S0());
+        ok = ok && tc::mbar_wait(&sm.full[slot], phase);
+        if (uact & 1) qk(S0());
+        take(j + 1, false);
+        if (pend & 2) pv(S1());
+        if (uact & 2) qk(S1());
+        issued = true;
+        pend = uact;
+        pk = unk;
+        vthere = false;
+        pslot = slot + 1 == slots ? 0 : slot + 1;
+        pphase = slot + 1 == slots ? phase ^ 1u : phase;
+        slot = pslot + 1 == slots ? 0 : pslot + 1;
+        phase = pslot + 1 == slots ? pphase ^ 1u : pphase;
+      }
+      if (uflags & 2) {
+        if (pend & 1) pv(S0());
+        if (pend & 2) pv(S1());
+        if (leader && ok) tc::mma_commit(&sm.odone);
+        __syncwarp();
+        ++items;
+      }
+    }
+    if (issued) {
+      // every product has finished before TMEM is freed
+      if (leader) tc::mma_commit(&sm.fin[0]);
+      __syncwarp();
+      if (!tc::mbar_wait(&sm.fin[0], 0)) ok = false;
     }
   } else if (warp < 8) {
     // ================================================= softmax
@@ -626,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
   pdl_trigger();
 }
 
-template <int D>
+template <int D, bool split>
 int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
   CUtensorMap pk, pv, k, v;
   const uint32_t box = (1u << a.page_shift) < (uint32_t)kN ? (1u << a.page_shift) : (uint32_t)kN;
@@ -639,9 +787,9 @@ int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
   if (rc != FASTAR_OK) return rc;
   constexpr int smem = (int)sizeof(Smem<D>);
   static_assert(smem <= 227 * 1024, "shared memory");
-  auto kernel = branch_tc_kernel<D>;
+  auto kernel = branch_tc_kernel<D, split>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-      launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, pk, pv, k, v, a, a.TM == kM ? 1 : 0, st) != cudaSuccess) {
+      launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, pk, pv, k, v, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
   }
@@ -652,7 +800,8 @@ int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
 }  // namespace
 
 int launch_branch_tc(const BranchArgs& a, int32_t* st, cudaStream_t s) {
-  return a.D == 128 ? launch_t<128>(a, st, s) : launch_t<64>(a, st, s);
+  if (a.TM == kM) return a.D == 128 ? launch_t<128, true>(a, st, s) : launch_t<64, true>(a, st, s);
+  return a.D == 128 ? launch_t<128, false>(a, st, s) : launch_t<64, false>(a, st, s);
 }
 
 }  // namespace fastar
