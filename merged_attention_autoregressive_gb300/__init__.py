@@ -473,36 +473,59 @@ class RopePlan:
                                            (ctypes.c_double * len(freqs))(*freqs)), "fastar_rope_plan_init")
 
 
-def _dev(t):
-    """Pointer of a contiguous device tensor (None: NULL)."""
+def _at(t, dev):
+    """Pointer of a contiguous tensor of GPU `dev` (None: NULL)."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("tensors must be on the GPU")
-    return _p(t)
+    if t.get_device() != dev:
+        raise ValueError("tensors must be on one GPU")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
-def _rows(t, what):
-    """Pointer and (head, token) strides of rows [H][N][D]."""
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+def _rows(t, dev, what):
+    """Pointer and (head, token) strides of rows [H][N][D] on GPU `dev`."""
+    if t.get_device() != dev:
+        raise ValueError("tensors must be on one GPU")
+    st = t.stride()
+    if len(st) != 3 or st[2] != 1:
         raise ValueError(f"{what} must be [heads][tokens][D] with contiguous rows")
-    if not t.is_cuda:
-        raise ValueError("tensors must be on the GPU")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return t.data_ptr(), st[0], st[1]
 
 
-def _positions(pos, N, plan):
+def _positions(pos, N, plan, dev):
     if pos is None:
         return None
     if pos.dtype != torch.int32 or tuple(pos.shape) != (N, plan.axes):
         raise ValueError(f"positions must be int32 [{N}][{plan.axes}]")
-    return _dev(pos)
+    return _at(pos, dev)
 
 
-def _int32(t, n, what):
+def _int32(t, n, dev, what):
     if t.dtype != torch.int32 or t.numel() != n:
         raise ValueError(f"{what} must be int32 with {n} entries")
-    return _dev(t)
+    return _at(t, dev)
+
+
+def _gpu(t):
+    """The GPU that holds t."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU")
+    return dev
+
+
+def _on(dev, stream, call, *args):
+    """call(*args, stream) on GPU `dev`: on its current stream by default."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        stream = _stream(stream)
+    if dev == torch.cuda.current_device():
+        return call(*args, stream)
+    with torch.cuda.device(dev):
+        return call(*args, stream)
 
 
 def fastar_rope(x, pos, plan: RopePlan, out, inverse=False, status=None, stream=None):
@@ -511,11 +534,14 @@ def fastar_rope(x, pos, plan: RopePlan, out, inverse=False, status=None, stream=
     x and out may have any head and token strides (the transpose of a
     projection's [N][H][D] output, for one); out may be x itself.
     inverse: turn back, which is also the gradient of the forward rotation."""
-    H, N, D = x.shape
-    if out.shape != x.shape or out.dtype != x.dtype or D != plan.D:
+    shape = H, N, D = x.shape
+    dev = _gpu(x)
+    if out.shape != shape or out.dtype != x.dtype or D != plan.D:
         raise ValueError("x, out and the plan must agree in shape and dtype")
-    _check(lib().fastar_rope(_dt(x), *_rows(x, "x"), H, N, D, _positions(pos, N, plan), plan.addr,
-                             1 if inverse else 0, *_rows(out, "out"), _dev(status), _stream(stream)), "fastar_rope")
+    rc = _on(dev, stream, lib().fastar_rope, _dt(x), *_rows(x, dev, "x"), H, N, D, _positions(pos, N, plan, dev),
+             plan.addr, 1 if inverse else 0, *_rows(out, dev, "out"), _at(status, dev))
+    if rc:
+        raise FastarError(rc, "fastar_rope")
 
 
 class PagedKV:
@@ -545,9 +571,11 @@ class PagedKV:
         self.n_pages, self.H, self.page, self.D = K.shape
         self.B, self.max_pages = table.shape
         self.dtype = K.dtype
-        _int32(length, self.B, "the lengths")
-        self.struct = PagesStruct(self.H, self.D, self.page, self.n_pages, self.B, self.max_pages, _dt(K), _dev(K),
-                                  _dev(V), _int32(table, table.numel(), "the table"), _dev(length))
+        self.device = _gpu(K)
+        self.struct = PagesStruct(self.H, self.D, self.page, self.n_pages, self.B, self.max_pages, _dt(K),
+                                  _at(K, self.device), _at(V, self.device),
+                                  _int32(table, table.numel(), self.device, "the table"),
+                                  _int32(length, self.B, self.device, "the lengths"))
         self.addr = ctypes.addressof(self.struct)
 
     def nbytes(self) -> int:
@@ -563,8 +591,10 @@ class Prefix:
             raise ValueError("K and V are [H][C][D]")
         self.K, self.V, self.m, self.size = K, V, m, size
         H, C, D = K.shape
-        self.struct = PrefixStruct(H, C, D, _dt(K), _dev(K), _dev(V), None if m is None else _int32(m, H * C, "m"),
-                                   None if size is None else _int32(size, H, "size"))
+        self.device = dev = _gpu(K)
+        self.struct = PrefixStruct(H, C, D, _dt(K), _at(K, dev), _at(V, dev),
+                                   None if m is None else _int32(m, H * C, dev, "m"),
+                                   None if size is None else _int32(size, H, dev, "size"))
         self.addr = ctypes.addressof(self.struct)
 
     @classmethod
@@ -589,14 +619,17 @@ def fastar_page_append(pages: PagedKV, k, v, cu, pos=None, plan: RopePlan | None
         raise ValueError("q and q_out come together")
     if plan is not None and plan.D != D:
         raise ValueError("the plan has another head dimension")
+    dev = pages.device
     qa, Hq = (None, 0, 0), 0
     if q is not None:
         if q.shape != q_out.shape or q.shape[1:] != k.shape[1:] or not q.dtype == q_out.dtype == k.dtype:
             raise ValueError("q and q_out do not fit k")
-        qa, Hq = _rows(q, "q"), q.shape[0]
-    _check(lib().fastar_page_append(pages.addr, *_rows(k, "k"), *_rows(v, "v"), N, _int32(cu, pages.B + 1, "cu"),
-                                    _positions(pos, N, plan), None if plan is None else plan.addr, *qa, Hq,
-                                    _dev(q_out), _dev(status), _stream(stream)), "fastar_page_append")
+        qa, Hq = _rows(q, dev, "q"), q.shape[0]
+    rc = _on(dev, stream, lib().fastar_page_append, pages.addr, *_rows(k, dev, "k"), *_rows(v, dev, "v"), N,
+             _int32(cu, pages.B + 1, dev, "cu"), _positions(pos, N, plan, dev), None if plan is None else plan.addr,
+             *qa, Hq, _at(q_out, dev), _at(status, dev))
+    if rc:
+        raise FastarError(rc, "fastar_page_append")
 
 
 def branch_workspace_size(Hq: int, H: int, N: int, D: int) -> int:
@@ -620,12 +653,16 @@ def fastar_branch_attention(q, cu, prefix: Prefix | None, pages: PagedKV, scale,
         raise ValueError("q, out and the pages must agree in shape and dtype")
     if lse is not None and (lse.dtype != torch.float32 or lse.numel() != Hq * N):
         raise ValueError("lse must be float32 [Hq][N]")
+    dev = pages.device
+    if prefix is not None and prefix.device != dev:
+        raise ValueError("tensors must be on one GPU")
     if ws is None:
         ws = torch.empty(max(1, branch_workspace_size(Hq, pages.H, N, D)), dtype=torch.uint8, device=q.device)
         if stream is not None:  # the allocator must not hand it out again before that stream is done with it
             ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
                              torch.cuda.ExternalStream(int(_stream(stream)), device=q.device))
-    _check(lib().fastar_branch_attention(pages.struct.dt, _dev(q), Hq, N, _int32(cu, pages.B + 1, "cu"),
-                                         None if prefix is None else prefix.addr, pages.addr, scale, block, _dev(out),
-                                         _dev(lse), _dev(ws), ws.numel() * ws.element_size(), _dev(status),
-                                         _stream(stream)), "fastar_branch_attention")
+    rc = _on(dev, stream, lib().fastar_branch_attention, pages.struct.dt, _at(q, dev), Hq, N,
+             _int32(cu, pages.B + 1, dev, "cu"), None if prefix is None else prefix.addr, pages.addr, scale, block,
+             _at(out, dev), _at(lse, dev), _at(ws, dev), ws.numel() * ws.element_size(), _at(status, dev))
+    if rc:
+        raise FastarError(rc, "fastar_branch_attention")

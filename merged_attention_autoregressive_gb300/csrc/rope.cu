@@ -23,7 +23,7 @@
 namespace fastar {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kUnroll = 4;  // heads in flight per thread: 8 16-byte loads
 
 // One group of heads: rows x[h * xh + n * xt], written to out[h * oh + n * ot]
@@ -80,7 +80,7 @@ __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
 }
 
 template <typename T, bool kHalves, bool kAppend>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ fastar_rope_plan plan, int D,
+__global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant__ fastar_rope_plan plan, int D,
                                                         const RopeArgs a, const AppendArgs ap, int32_t* st) {
   constexpr int V = VecInfo<T>::n;     // elements of a 16-byte vector
   pdl_wait();
@@ -223,9 +223,11 @@ int launch_rope_t(const fastar_rope_plan& plan, int D, RopeArgs a, const AppendA
   const int items = D / (2 * VecInfo<T>::n), toks = kThreads / items;
   const int gx = (a.N + toks - 1) / toks;
   const int total = a.q.H + a.k.H + a.v.H;
-  // split the heads until about 8 CTAs per SM are there (the angles are taken
-  // again by each part), in steps of the heads in flight
-  int parts = (152 * 8 + gx - 1) / gx;
+  // split the heads until about 32 CTAs per SM are there (the angles are taken
+  // again by each part), in steps of the heads in flight: 10800 tokens of 40
+  // bf16 heads took 39.6 us so, 51 us at half the parts (the last of few waves
+  // runs alone) and 48 us at twice (the angles)
+  int parts = (152 * 32 + gx - 1) / gx;
   int per = (total + parts - 1) / parts;
   per = (per + kUnroll - 1) / kUnroll * kUnroll;
   a.heads_per_cta = per;
