@@ -35,7 +35,7 @@
 namespace fastar {
 namespace {
 
-constexpr int kM = 128, kN = 128, kThreads = 384, kLoader = 8, kIssuer = 9;
+constexpr int kM = 128, kN = 128, kThreads = 640, kSoftmax = 16, kLoader = 16, kIssuer = 17;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;  // raise the running max only when exceeded by more than this (log2)
 
@@ -48,7 +48,7 @@ struct Desc {
 template <int D>
 struct Shape {
   static constexpr int kTile = 128 * D * 2;              // bytes of a query, key or value tile
-  static constexpr int kRing = D == 128 ? 4 : 8;         // descriptors
+  static constexpr int kRing = D == 128 ? 3 : 6;         // descriptors
   static constexpr int kSlots1 = D == 128 ? 6 : 10;      // tiles in flight, one query tile
   static constexpr int kSlots2 = D == 128 ? 5 : 10;      // two query tiles
   static constexpr int kTiles = kSlots1 + 1 > kSlots2 + 2 ? kSlots1 + 1 : kSlots2 + 2;
@@ -65,6 +65,8 @@ struct Smem {
   uint64_t sfull[2], pready[2][2], odone, qfull, fin[2];  // pready: by stream and half of the keys
   uint32_t tmem;
   int started1;
+  uint32_t gone;                        // a bit per pair of softmax warps one of which has given up
+  float row[2][kM];                     // a value per row, by stream, from one half of it to the other
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -72,11 +74,23 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void bar_pair(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void bar_all(int id) { asm volatile("bar.sync %0, 512;" ::"r"(id) : "memory"); }
+// `threads` threads meet; whether any of them holds p.
+template <int threads>
+__device__ __forceinline__ bool bar_or(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.red.or.pred q, %1, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)p), "n"(threads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bar_two(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
-// Registers: 384 threads launch with 168 each (64,512); the third warpgroup
-// gives 72 of its own up, so that the softmax rows (128 scores in registers)
-// get 200: 128 * 96 + 256 * 200 = 63,488.
 template <int D, bool split>
 __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_constant__ CUtensorMap mapPK,
                                                                const __grid_constant__ CUtensorMap mapPV,
@@ -104,15 +118,16 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     }
     for (int i = 0; i < S::kRing; ++i) {
       tc::mbar_init(&sm.dfull[i], 1);
-      tc::mbar_init(&sm.dempty[i], split ? 10 : 9);  // 8 softmax warps and the issuers
+      tc::mbar_init(&sm.dempty[i], kSoftmax + (split ? 2 : 1));  // the softmax warps and the issuers
     }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&sm.sfull[s], 1);
       tc::mbar_init(&sm.pready[s][0], 4);
       tc::mbar_init(&sm.pready[s][1], 4);
     }
+    sm.gone = 0u;
     tc::mbar_init(&sm.odone, split ? 2 : 1);
-    tc::mbar_init(&sm.qfull, 8);
+    tc::mbar_init(&sm.qfull, kSoftmax);
     tc::mbar_init(&sm.fin[0], 1);
     tc::mbar_init(&sm.fin[1], 1);
     tc::fence_mbar_init();
@@ -127,7 +142,6 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
   const uint32_t tmem = sm.tmem;  // S_0 / P_0, S_1 / P_1 at columns 0 and 128, O_0, O_1 at 256 and 384
   bool ok = true, bad = false;
 
-  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
   if (warp == kLoader) {
     // ================================================= loader
     BranchWalk w;
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     const int base = s * slots;  // of the stream's ring
     const uint32_t ring_addr = tc::smem_u32(ring + (size_t)base * S::kTile);
     uint64_t *const full = sm.full + base, *const empty = sm.empty + base;
-    const uint64_t qd = tc::sdesc_kmajor_sw128(tc::smem_u32(sm.tiles));
+    const uint32_t qd = tc::desc_low(tc::smem_u32(sm.tiles), 16);
     const uint32_t dS = tmem + s * 128, dO = tmem + 256 + s * 128;
     uint32_t slot = 0, phase = 0;    // of the ring: the next unit's key tile
     uint32_t items = 0, turn = 0;
@@ -288,25 +302,16 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     uint32_t acc = 0u;               // 0: O starts anew
     bool issued = false;
     auto pv = [&]() {
-      ok = __all_sync(0xffffffffu,
-                      tc::mbar_wait(&full[pslot], pphase) && tc::mbar_wait(&sm.pready[s][0], np & 1u));
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[pslot], pphase) && tc::mbar_wait(&sm.pready[s][0], np & 1u) &&
+                                       tc::mbar_wait(&sm.pready[s][1], np & 1u));
       if (!ok) return;
       tc::tc_fence_after();
-      const uint64_t vd = tc::sdesc_mnmajor_sw128(ring_addr + pslot * S::kTile, kN * 128);
+      const uint32_t vd = tc::desc_low(ring_addr + pslot * S::kTile, kN * 128);
       if (pk == kN) {
         if (tc::elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kN / 32; ++k)
-            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : acc);
-        }
-        __syncwarp();
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pready[s][1], np & 1u));
-        if (!ok) return;
-        tc::tc_fence_after();
-        if (tc::elect_one()) {
-#pragma unroll
-          for (int k = kN / 32; k < kN / 16; ++k)
-            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, 1u);
+          for (int k = 0; k < kN / 16; ++k)
+            tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv, k > 0 ? 1u : acc);
           tc::mma_commit(&empty[pslot]);
         }
       } else {
@@ -322,12 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           tc::fence_proxy_async_smem();
           __syncwarp();
         }
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pready[s][1], np & 1u));
-        if (!ok) return;
-        tc::tc_fence_after();
         if (tc::elect_one()) {
           for (int k = 0; k < steps; ++k)
-            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : acc);
+            tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv, k > 0 ? 1u : acc);
           tc::mma_commit(&empty[pslot]);
         }
       }
@@ -362,12 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[slot], phase));
         if (!ok) break;
         tc::tc_fence_after();
-        const uint64_t kd = tc::sdesc_kmajor_sw128(ring_addr + slot * S::kTile);
+        const uint32_t kd = tc::desc_low(ring_addr + slot * S::kTile, 16);
         if (tc::elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * kN * 128 + (k & 3) * 32;
-            tc::mma_bf16(dS, tc::sdesc_add(qd, off), tc::sdesc_add(kd, off), idesc_qk, k > 0 ? 1u : 0u);
+            const uint32_t off = ((k >> 2) * kN * 128 + (k & 3) * 32) / 16;
+            tc::mma_bf16_low(dS, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
           }
           tc::mma_commit(&sm.sfull[s]);
           tc::mma_commit(&empty[slot]);
@@ -413,10 +415,9 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     // the streams whose S is out and whose P V is not yet, their value tile
     // (one for both), its keys, and whether O starts anew
     int pend = 0, pk = 0;
-    uint32_t pslot = 0, pphase = 0, np[2] = {0u, 0u}, acc[2] = {0u, 0u};
+    uint32_t pslot = 0, pphase = 0, np = 0u, acc = 0u;  // np, acc: a bit per stream
     bool issued = false, vthere = false;
-    auto pv = [&](auto stream) {
-      constexpr int s = decltype(stream)::value;
+    auto pv = [&](const int s) {
       if (!vthere) {
         ok = ok && tc::mbar_wait(&sm.full[pslot], pphase);
         vthere = true;
@@ -432,41 +433,29 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           __syncwarp();
         }
       }
-      const uint64_t vd = tc::sdesc_mnmajor_sw128(ring_addr + pslot * S::kTile, kN * 128);
+      const uint32_t vd = tc::desc_low(ring_addr + pslot * S::kTile, kN * 128);
+      // weights: keys 0-63 over S columns 0-31, keys 64-127 over columns 64-95
       const uint32_t dS = tmem + s * 128, dO = tmem + 256 + s * 128;
-      const uint32_t ac = acc[s];
-      ok = ok && tc::mbar_wait(&sm.pready[s][0], np[s] & 1u);
+      const uint32_t ac = acc >> s & 1u, par = np >> s & 1u;
+      ok = ok && tc::mbar_wait(&sm.pready[s][0], par) && tc::mbar_wait(&sm.pready[s][1], par);
       tc::tc_fence_after();
-      if (pk == kN) {
-        if (leader && ok) {
-#pragma unroll
-          for (int k = 0; k < kN / 32; ++k)
-            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : ac);
-        }
-        __syncwarp();
-        ok = ok && tc::mbar_wait(&sm.pready[s][1], np[s] & 1u);
-        tc::tc_fence_after();
-        if (leader && ok) {
-#pragma unroll
-          for (int k = kN / 32; k < kN / 16; ++k)
-            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, 1u);
-        }
-      } else {
-        ok = ok && tc::mbar_wait(&sm.pready[s][1], np[s] & 1u);
-        tc::tc_fence_after();
-        const int steps = (pk + 15) / 16;
-        if (leader && ok)
-          for (int k = 0; k < steps; ++k)
-            tc::mma_bf16_tmem_a(dO, dS + k * 8, tc::sdesc_add(vd, k * 16 * 128), idesc_pv, k > 0 ? 1u : ac);
-      }
       pend &= ~(1 << s);
-      if (pend == 0 && leader && ok) tc::mma_commit(&sm.empty[pslot]);  // no stream wants the tile any more
+      if (leader && ok) {
+        if (pk == kN) {
+#pragma unroll
+          for (int k = 0; k < kN / 16; ++k)
+            tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv, k > 0 ? 1u : ac);
+        } else {
+          const int steps = (pk + 15) / 16;
+          for (int k = 0; k < steps; ++k)
+            tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv, k > 0 ? 1u : ac);
+        }
+        if (pend == 0) tc::mma_commit(&sm.empty[pslot]);  // no stream wants the tile any more
+      }
       __syncwarp();
-      ++np[s];
-      acc[s] = 1u;
+      np ^= 1u << s;
+      acc |= 1u << s;
     };
-    using S0 = std::integral_constant<int, 0>;
-    using S1 = std::integral_constant<int, 1>;
     int act = 0, flags = 0, nk = 0;
     bool read = false;  // the unit's descriptor has been read
     auto take = [&](uint32_t j, bool wait) {
@@ -491,32 +480,31 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       const int uact = act, uflags = flags, unk = nk;
       if (uflags & 1) {
         ok = ok && tc::mbar_wait(&sm.qfull, items & 1u);
-        acc[0] = acc[1] = 0u;
+        acc = 0u;
       }
-      const uint64_t kd = tc::sdesc_kmajor_sw128(ring_addr + slot * S::kTile);
-      auto qk = [&](auto stream) {
-        constexpr int s = decltype(stream)::value;
-        tc::tc_fence_after();
-        const uint64_t qd = tc::sdesc_kmajor_sw128(q_addr + s * S::kTile);
-        const uint32_t dS = tmem + s * 128;
-        if (leader && ok) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * kN * 128 + (k & 3) * 32;
-            tc::mma_bf16(dS, tc::sdesc_add(qd, off), tc::sdesc_add(kd, off), idesc_qk, k > 0 ? 1u : 0u);
-          }
-          tc::mma_commit(&sm.sfull[s]);
-          if ((uact >> (s + 1)) == 0) tc::mma_commit(&sm.empty[slot]);
-        }
-        __syncwarp();
-      };
+      const uint32_t kd = tc::desc_low(ring_addr + slot * S::kTile, 16);
       if (uact) {
-        if (pend & 1) pv(S0());
-        ok = ok && tc::mbar_wait(&sm.full[slot], phase);
-        if (uact & 1) qk(S0());
-        take(j + 1, false);
-        if (pend & 2) pv(S1());
-        if (uact & 2) qk(S1());
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          if (pend >> s & 1) pv(s);
+          if (s == 0) ok = ok && tc::mbar_wait(&sm.full[slot], phase);
+          if (uact >> s & 1) {
+            tc::tc_fence_after();
+            const uint32_t qd = tc::desc_low(q_addr + s * S::kTile, 16);
+            const uint32_t dS = tmem + s * 128;
+            if (leader && ok) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k >> 2) * kN * 128 + (k & 3) * 32) / 16;
+                tc::mma_bf16_low(dS, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
+              }
+              tc::mma_commit(&sm.sfull[s]);
+              if ((uact >> (s + 1)) == 0) tc::mma_commit(&sm.empty[slot]);
+            }
+            __syncwarp();
+          }
+          if (s == 0) take(j + 1, false);
+        }
         issued = true;
         pend = uact;
         pk = unk;
@@ -527,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         phase = pslot + 1 == slots ? pphase ^ 1u : pphase;
       }
       if (uflags & 2) {
-        if (pend & 1) pv(S0());
-        if (pend & 2) pv(S1());
+        for (int s = 0; s < 2; ++s)
+          if (pend >> s & 1) pv(s);
         if (leader && ok) tc::mma_commit(&sm.odone);
         __syncwarp();
         ++items;
@@ -540,17 +528,23 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       __syncwarp();
       if (!tc::mbar_wait(&sm.fin[0], 0)) ok = false;
     }
-  } else if (warp < 8) {
+  } else if (warp < kSoftmax) {
     // ================================================= softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    const int s = warp >> 2, wr = (warp & 3) * 32 + lane;  // stream, row of its tile
+    const int s = warp >> 3, half = (warp >> 2) & 1;  // stream, half of the unit's keys
+    const int wr = (warp & 3) * 32 + lane;            // row of the stream's tile
+    const int pair = 3 + s * 4 + (warp & 3);          // barrier of the two warps of these rows
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = tl + s * 128, tO = tl + 256 + s * 128;
+    const uint32_t tS = tl + s * 128, tO = tl + 256 + s * 128 + half * (D / 2);
     const float scale2 = a.scale * kLog2e;
     const int rows = a.cu[a.B] * a.g;
     uint32_t ns = 0, items = 0, turn = 0;  // S tiles seen, items, active units of the item
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f;          // of the row; of this half's keys
     bool started = false;
+    // Warps meet at named barriers, which have no limit of their own.  So a
+    // warp whose bounded wait ran out does not just leave: the barrier that
+    // its partners come to next is always one that carries a flag, and there
+    // it says so (met: how many of these meetings it has had on its way out).
+    int met = 0;
     for (uint32_t j = 0; ok; ++j) {
       const int ds = j % S::kRing;
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dfull[ds], (j / S::kRing) & 1u));
@@ -570,9 +564,12 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         const char* src = (const char*)a.q;
         const uint32_t n = r < rows ? 16u : 0u;
         if (n) src += ((size_t)(x.h * a.g + r % a.g) * a.N + r / a.g) * (D * 2);
-        // both streams fetch half of the shared tile
-        const int c0 = split ? s * (D / 16) : 0, c1 = split ? c0 + D / 16 : D / 8;
-        for (int c = c0; c < c1; ++c) tc::cp_async16(q0 + tc::sw128_offset(wr, c, kM), src + (n ? c * 16 : 0), n);
+        // the warps of a tile's rows share its 16-byte columns
+        constexpr int per = D / (split ? 32 : 16);
+        const int c0 = (split ? s * 2 + half : half) * per;
+#pragma unroll
+        for (int c = 0; c < per; ++c)
+          tc::cp_async16(q0 + tc::sw128_offset(wr, c0 + c, kM), src + (n ? (c0 + c) * 16 : 0), n);
         tc::cp_async_wait_all();
         tc::fence_proxy_async_smem();
         __syncwarp();
@@ -582,106 +579,107 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       if (act0) ++turn;
       if (active) {
         // rows behind the last token count as full: nobody reads their results
-        const int seen = r < rows ? branch_row_keys(a, x, r) : kN;
-        const bool any = __any_sync(0xffffffffu, r < rows && seen > 0), all = __all_sync(0xffffffffu, seen >= kN);
+        const int seen = (r < rows ? branch_row_keys(a, x, r) : kN) - half * 64;
+        const bool any = __any_sync(0xffffffffu, r < rows && seen + half * 64 > 0);  // alike in both halves
+        const bool all = __all_sync(0xffffffffu, seen >= 64);
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sfull[s], ns & 1u));
         if (!ok) break;
         ++ns;
         tc::tc_fence_after();
+        uint32_t pk[32];
         if (any) {
           // log2 scores; without a bias or a mask the raw products, whose
           // scale goes into the exponent's multiply-add
-          uint32_t raw0[64], raw1[64];
-          float* const v0 = reinterpret_cast<float*>(raw0);
-          float* const v1 = reinterpret_cast<float*>(raw1);
+          uint32_t raw[64];
+          float* const v = reinterpret_cast<float*>(raw);
+          tc::tmem_ld64_async(tS + half * 64, raw);
           const bool biased = x.branch < 0 && a.m != nullptr;
           const bool plain = !biased && all;
           const float mul = plain ? scale2 : 1.f;
-          const float* bias = sm.bias[ds];
-          float tm[8];
-          auto scores = [&](float* v, const int c0) {
-            if (!plain) {
-              if (biased) {
+          tc::tmem_wait64(raw);
+          if (!plain) {
+            if (biased) {
+              const float* bias = sm.bias[ds] + half * 64;
 #pragma unroll
-                for (int i = 0; i < 64; i += 4) {
-                  const float4 b = *reinterpret_cast<const float4*>(bias + c0 + i);
-                  tc::fma2(v[i], v[i + 1], scale2, scale2, b.x, b.y);
-                  tc::fma2(v[i + 2], v[i + 3], scale2, scale2, b.z, b.w);
-                }
-              } else {
-#pragma unroll
-                for (int i = 0; i < 64; i += 2) tc::mul2(v[i], v[i + 1], scale2, scale2);
+              for (int i = 0; i < 64; i += 4) {
+                const float4 b = *reinterpret_cast<const float4*>(bias + i);
+                tc::fma2(v[i], v[i + 1], scale2, scale2, b.x, b.y);
+                tc::fma2(v[i + 2], v[i + 3], scale2, scale2, b.z, b.w);
               }
-              if (!all) {
+            } else {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) v[i] = c0 + i < seen ? v[i] : -INFINITY;
-              }
+              for (int i = 0; i < 64; i += 2) tc::mul2(v[i], v[i + 1], scale2, scale2);
             }
+            if (!all) {
 #pragma unroll
-            for (int i = 0; i < 64; i += 16) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                tm[e] = c0 + i == 0 ? fmaxf(v[i + e], v[i + 8 + e]) : tc::max3(tm[e], v[i + e], v[i + 8 + e]);
-            }
-          };
-          tc::tmem_ld64_async(tS, raw0);
-          tc::tmem_wait64(raw0);
-          tc::tmem_ld64_async(tS + 64, raw1);  // lands under the first half's maxima
-          scores(v0, 0);
-          tc::tmem_wait64(raw1);
-          scores(v1, 64);
-          const float top =
-              fmaxf(tc::max3(tm[0], tm[1], tm[2]), tc::max3(tm[3], tm[4], tc::max3(tm[5], tm[6], tm[7]))) * mul;
-          const bool raise = top > m + kRescale;
-          const float mn = raise ? top : m;
-          const float alpha = (raise && m != -INFINITY) ? exp2f(m - mn) : 1.f;
-          if (started && __any_sync(0xffffffffu, alpha != 1.f)) {
-            // S of this unit was issued behind the P V of the stream's last
-            // one, and products complete in issue order: O is at rest
-#pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              float o[32];
-              tc::tmem_ld32(tO + q * 32, o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= alpha;
-              tc::tmem_st32(tO + q * 32, o);
+              for (int i = 0; i < 64; ++i) v[i] = i < seen ? v[i] : -INFINITY;
             }
           }
-          l *= alpha;
-          m = mn;
+          float tm[8];
+#pragma unroll
+          for (int i = 0; i < 64; i += 16) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) tm[e] = i == 0 ? fmaxf(v[e], v[8 + e]) : tc::max3(tm[e], v[i + e], v[i + 8 + e]);
+          }
+          float top =
+              fmaxf(tc::max3(tm[0], tm[1], tm[2]), tc::max3(tm[3], tm[4], tc::max3(tm[5], tm[6], tm[7]))) * mul;
+          // both halves of a row keep one maximum: while neither exceeds it by
+          // more than 2^8 they only meet here
+          tc::tc_fence_before();
+          const bool meet = bar_or<64>(pair, top > m + kRescale);
+          tc::tc_fence_after();
+          if (meet) {
+            if (*(volatile uint32_t*)&sm.gone >> pair & 1u) {
+              ok = false;
+              met = 1;
+              break;
+            }
+            float* const shared_top = &sm.row[s][wr];
+            if (half == 0) *shared_top = top;
+            bar_two(pair);
+            if (half == 1) *shared_top = top = fmaxf(top, *shared_top);
+            bar_two(pair);
+            top = *shared_top;
+            const bool raise = top > m + kRescale;
+            const float mn = raise ? top : m;
+            const float alpha = (raise && m != -INFINITY) ? exp2f(m - mn) : 1.f;
+            if (started && __any_sync(0xffffffffu, alpha != 1.f)) {
+              // S of this unit was issued behind the P V of the stream's last
+              // one, and products complete in issue order: O is at rest
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                float o[8];
+                tc::tmem_ld8(tO + q * 8, o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] *= alpha;
+                tc::tmem_st8(tO + q * 8, o);
+              }
+            }
+            l *= alpha;
+            m = mn;
+            tc::tc_fence_before();
+            bar_two(pair);  // O is rescaled before either half's weights are taken
+          }
           const float base = m == -INFINITY ? 0.f : -m;
           float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          // the weights of 64 keys, over the first columns of S in TMEM; the
-          // issuer may start their product with the values at once
-          auto weights = [&](float* v, const int half) {
-            uint32_t pk[32];
 #pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              tc::fma2(v[i], v[i + 1], mul, mul, base, base);
-              const float p0 = ex2(v[i]), p1 = ex2(v[i + 1]);
-              tc::add2(ps[i & 7], ps[(i & 7) + 1], p0, p1);
-              const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-              pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            tc::tmem_st32u(tS + half * 32, pk);
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sm.pready[s][half]);
-          };
-          weights(v0, 0);
-          weights(v1, 1);
+          for (int i = 0; i < 64; i += 2) {
+            tc::fma2(v[i], v[i + 1], mul, mul, base, base);
+            const float p0 = ex2(v[i]), p1 = ex2(v[i + 1]);
+            tc::add2(ps[i & 7], ps[(i & 7) + 1], p0, p1);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+            pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+          }
           l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
         } else {
           // no row of the warp is concerned: weights 0
-          uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) pk[i] = 0u;
-          tc::tmem_st32u(tS, pk);
-          tc::tmem_st32u(tS + 32, pk);
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane < 2) tc::mbar_arrive(&sm.pready[s][lane]);
         }
+        tc::tmem_st32u(tS + half * 64, pk);
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.pready[s][half]);
         started = true;
       }
       __syncwarp();
@@ -690,18 +688,33 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         // ---- the item's end: O of the run
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.odone, items & 1u));
         if (!ok) break;
+        if (bar_or<64>(pair, false)) {
+          ok = false;
+          met = 1;
+          break;
+        }
         ++items;
         tc::tc_fence_after();
+        // the sums of both halves; O is split by columns from here on
+        if (half == 0) sm.row[s][wr] = l;
+        bar_two(pair);
+        if (half == 1) sm.row[s][wr] = l = sm.row[s][wr] + l;
+        bar_two(pair);
+        l = sm.row[s][wr];
         float w0 = 1.f, w1 = 0.f;
         bool have1 = false;
         if (split) {
           // stream 1 hands its maxima and sums over; stream 0 reads both O
           float2* ml = reinterpret_cast<float2*>(sm.tiles);  // the query tile is free
-          if (s == 1) {
+          if (s == 1 && half == 0) {
             ml[wr] = make_float2(m, l);
             if (wr == 0) sm.started1 = started ? 1 : 0;
           }
-          bar_pair(1);
+          if (bar_or<512>(1, false)) {
+            ok = false;
+            met = 2;
+            break;
+          }
           if (s == 0) {
             const float2 o = ml[wr];
             have1 = sm.started1 != 0;
@@ -719,8 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           w1 *= inv;
           const size_t at = live ? (size_t)(x.h * a.g + r % a.g) * a.N + r / a.g : 0;
           const int slot_row = x.slot * a.slot_rows + (split ? 0 : s * kM) + wr;
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
+#pragma unroll 1
+          for (int q = 0; q < D / 64; ++q) {
             float o[32];
             if (started) {
               tc::tmem_ld32(tO + q * 32, o);
@@ -737,17 +750,18 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
               for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], w1, o[i]);
             }
             if (!live) continue;
+            const int col = half * (D / 2) + q * 32;
             if (whole) {
-              __nv_bfloat16* out = (__nv_bfloat16*)a.out + at * D + q * 32;
+              __nv_bfloat16* out = (__nv_bfloat16*)a.out + at * D + col;
 #pragma unroll
               for (int i = 0; i < 32; i += 8) st_vec<__nv_bfloat16, 8>(out + i, o + i);
             } else {
-              float* po = a.po + (size_t)slot_row * D + q * 32;
+              float* po = a.po + (size_t)slot_row * D + col;
 #pragma unroll
               for (int i = 0; i < 32; i += 4) st_vec<float, 4>(po + i, o + i);
             }
           }
-          if (live) {
+          if (live && half == 0) {
             if (whole) {
               if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
             } else {
@@ -758,11 +772,24 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         if (split) {
           // stream 1 may overwrite its O (by its next P) only now
           tc::tc_fence_before();
-          bar_pair(2);
+          bar_all(2);
+          tc::tc_fence_after();
+        } else {
+          tc::tc_fence_before();
+          bar_two(pair);  // the sums have been read
           tc::tc_fence_after();
         }
       }
     }
+    if (met == 0) {
+      if (!ok && lane == 0) {
+        atomicOr(&sm.gone, 1u << pair);
+        __threadfence_block();
+      }
+      __syncwarp();
+      if (bar_or<64>(pair, !ok)) ok = false;
+    }
+    if (split && met < 2) (void)bar_or<512>(1, !ok);
     tc::cp_async_wait_all();
   }
   if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
