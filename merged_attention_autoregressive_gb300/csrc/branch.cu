@@ -95,69 +95,100 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
   pdl_trigger();
 }
 
-// Joins the partials of every item that is cut: grid (runs, row groups), a
-// warp per row; the run that begins an item left a record of it.  The
-// maxima and sums of up to 32 partials are read at once, one per lane, then
-// the rows of O eight at a time, in the order of the runs.
-constexpr int kJoinRows = 16;  // rows per CTA, two per warp
-
+// Joins the partials of every item that is cut: grid (runs, row groups); the
+// run that begins an item left a record of it.  A warp takes 8 rows by 16
+// columns: lane = row + 8 sub, and sub-group `sub` adds the partials of every
+// fourth run, so that a few rows over many runs still keep four loads of each
+// lane in flight; the four sums are joined by shuffles (a fixed order).
 template <typename T>
 __global__ void __launch_bounds__(256) branch_combine_kernel(BranchArgs a, int32_t* st) {
   pdl_wait();
   const bool stop = status_bad(st);
   const BranchCut x = a.cuts[blockIdx.x];
   if (stop || x.h < 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
+  const int lane = threadIdx.x & 31, c = blockIdx.x;
+  const int w = blockIdx.y * 8 + (threadIdx.x >> 5), groups = a.D / 16;
+  const int i = w / groups * 8 + (lane & 7), col = w % groups * 16, sub = lane >> 3;
   const int rows = a.cu[a.B] * a.g, r0 = x.t * a.TM;
   const int nr = min(a.TM, rows - r0), n = x.last - c + 1;
-  for (int i = blockIdx.y * kJoinRows + warp; i < min(nr, (int)(blockIdx.y + 1) * kJoinRows); i += 8) {
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < n; j0 += 32) {
-      // run c + j0 + lane: its slot, or none where it is past the item or empty
-      const int j = c + j0 + lane;
-      int slot = j == c ? x.slot : 2 * j;
-      if (j0 + lane >= n || x.U * j / a.G == x.U * (j + 1) / a.G) slot = -1;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (slot >= 0) ml = a.pml[(size_t)slot * a.slot_rows + i];
-      if (ml.y == 0.f) slot = -1;  // the row saw nothing in that run
-      float top = slot >= 0 ? ml.x : -INFINITY;
+  if (w / groups * 8 >= nr) return;
+  const bool live = i < nr;
+  // the slot of the item's k-th run, -1 where that run is empty
+  auto slot_of = [&](int k) {
+    const int j = c + k;
+    if (x.U < a.G && branch_cut(x.U, j, a.G) == branch_cut(x.U, j + 1, a.G)) return -1;
+    return j == c ? x.slot : 2 * j;
+  };
+  float m = -INFINITY;
+  for (int k0 = sub; k0 < n; k0 += 16) {
+    float2 ml[4];
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
-      const float w = slot >= 0 ? exp2f(ml.x - base) : 0.f;
-      const float alpha = l == 0.f ? 0.f : exp2f(m - base);
-      l = l * alpha + warp_sum(slot >= 0 ? w * ml.y : 0.f);
-      m = mn;
+    for (int e = 0; e < 4; ++e) {
+      const int k = k0 + 4 * e, slot = live && k < n ? slot_of(k) : -1;
+      ml[e] = slot >= 0 ? a.pml[(size_t)slot * a.slot_rows + i] : make_float2(-INFINITY, 0.f);
+    }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] *= alpha;
-      for (int k0 = 0; k0 < min(32, n - j0); k0 += 8) {
-        float4 p[8];
-        float wk[8];
+    for (int e = 0; e < 4; ++e)
+      if (ml[e].y != 0.f) m = fmaxf(m, ml[e].x);  // a run in which the row saw nothing has sum 0
+  }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int sk = __shfl_sync(0xffffffffu, slot, k0 + k);
-          wk[k] = __shfl_sync(0xffffffffu, w, k0 + k);
-          p[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (sk >= 0 && lane * 4 < a.D)
-            p[k] = *reinterpret_cast<const float4*>(a.po + ((size_t)sk * a.slot_rows + i) * a.D + lane * 4);
-        }
+  for (int e = 0; e < 16; ++e) o[e] = 0.f;
+  for (int k0 = sub; k0 < n; k0 += 8) {
+    float wk[2];
+    float4 p[2][4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          o[0] = fmaf(wk[k], p[k].x, o[0]);
-          o[1] = fmaf(wk[k], p[k].y, o[1]);
-          o[2] = fmaf(wk[k], p[k].z, o[2]);
-          o[3] = fmaf(wk[k], p[k].w, o[3]);
+    for (int q = 0; q < 2; ++q) {
+      const int k = k0 + 4 * q, slot = live && k < n ? slot_of(k) : -1;
+      wk[q] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[q][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (slot >= 0) {
+        const float2 ml = a.pml[(size_t)slot * a.slot_rows + i];
+        const float4* po =
+            reinterpret_cast<const float4*>(a.po + (size_t)slot * a.slot_rows * a.D) + (size_t)(col / 4) * a.slot_rows + i;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[q][e] = po[(size_t)e * a.slot_rows];
+        if (ml.y != 0.f) {
+          wk[q] = exp2f(ml.x - base);
+          l += wk[q] * ml.y;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[q][e] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
     }
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[4 * e] = fmaf(wk[q], p[q][e].x, o[4 * e]);
+        o[4 * e + 1] = fmaf(wk[q], p[q][e].y, o[4 * e + 1]);
+        o[4 * e + 2] = fmaf(wk[q], p[q][e].z, o[4 * e + 2]);
+        o[4 * e + 3] = fmaf(wk[q], p[q][e].w, o[4 * e + 3]);
+      }
+  }
+  l += __shfl_xor_sync(0xffffffffu, l, 8);
+  l += __shfl_xor_sync(0xffffffffu, l, 16);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    o[e] += __shfl_xor_sync(0xffffffffu, o[e], 8);
+    o[e] += __shfl_xor_sync(0xffffffffu, o[e], 16);
+  }
+  if (live && sub == 0) {
     const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN sum stays one
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] *= inv;
+    for (int e = 0; e < 16; ++e) o[e] *= inv;
     const int row = r0 + i;
     const size_t at = (size_t)(x.h * a.g + row % a.g) * a.N + row / a.g;
-    if (lane * 4 < a.D) st_vec<T, 4>((T*)a.out + at * a.D + lane * 4, o);
-    if (a.lse && lane == 0)
-      a.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.6931471805599453f;
+    T* out = (T*)a.out + at * a.D + col;
+    constexpr int V = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int e = 0; e < 16; e += V) st_vec<T, V>(out + e, o + e);
+    if (a.lse && col == 0) a.lse[at] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
   }
   pdl_trigger();
 }
@@ -175,7 +206,7 @@ int launch_branch_plan(const BranchArgs& a, int32_t* st, cudaStream_t s) {
 
 int launch_branch_combine(const BranchArgs& a, fastar_dtype dt, int32_t* st, cudaStream_t s) {
   const int rows = (int)min((long long)a.TM, (long long)a.N * a.g);
-  const dim3 grid(a.G, (rows + kJoinRows - 1) / kJoinRows);
+  const dim3 grid(a.G, ((rows + 7) / 8 * (a.D / 16) + 7) / 8);
   cudaError_t rc = dt == FASTAR_BF16 ? launch_pdl(branch_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a, st)
                                      : launch_pdl(branch_combine_kernel<float>, grid, dim3(256), 0, s, a, st);
   if (rc != cudaSuccess) {
@@ -187,18 +218,17 @@ int launch_branch_combine(const BranchArgs& a, fastar_dtype dt, int32_t* st, cud
 }
 
 namespace {
-// Units, runs and partials of a call.  bf16: one CTA per SM, 256 rows and 128
-// keys (128 rows where that is all there is); fp32: two CTAs per SM, 64 rows
-// and 64 keys.
+// Units, runs and partials of a call.  bf16: one CTA per SM, 256 (wide) or
+// 128 rows and 128 keys; fp32: two CTAs per SM, 64 rows and 64 keys.
 constexpr int kSms = 152;
 struct Geometry {
   int TM, TN, G, ntiles, slot_rows;
   size_t cuts, head, tile, po, pml;  // bytes of the workspace's parts
 };
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-Geometry geometry(fastar_dtype dt, int H, long long rows, int D) {
+Geometry geometry(fastar_dtype dt, bool wide, int H, long long rows, int D) {
   Geometry x;
-  x.TM = dt == FASTAR_F32 ? 64 : rows <= 128 ? 128 : 256;
+  x.TM = dt == FASTAR_F32 ? 64 : wide ? 256 : 128;
   x.TN = dt == FASTAR_F32 ? 64 : 128;
   x.G = dt == FASTAR_F32 ? 2 * kSms : kSms;
   x.ntiles = (int)((rows + x.TM - 1) / x.TM);
@@ -215,8 +245,8 @@ Geometry geometry(fastar_dtype dt, int H, long long rows, int D) {
 size_t branch_ws_bytes(int Hq, int H, int N, int D) {
   if (Hq < 1 || H < 1 || N < 1 || D < 1 || Hq % H) return 0;
   size_t most = 0;
-  for (fastar_dtype dt : {FASTAR_BF16, FASTAR_F32}) {
-    const Geometry x = geometry(dt, H, (long long)N * (Hq / H), D);
+  for (int k = 0; k < 3; ++k) {
+    const Geometry x = geometry(k == 2 ? FASTAR_F32 : FASTAR_BF16, k == 1, H, (long long)N * (Hq / H), D);
     const size_t n = x.cuts + x.head + x.tile + x.po + x.pml;
     if (n > most) most = n;
   }
@@ -253,7 +283,17 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   a.scale = scale;
   a.out = out;
   a.lse = lse;
-  const Geometry x = geometry(dt, a.H, (long long)N * a.g, a.D);
+  // 256 rows per item pay where a branch fills them and the runs are long:
+  // every tile that is loaded then feeds four products (two branches of 4680
+  // tokens, 12 heads, 42,000 keys: 1.87 ms, against 2.26 ms at 128 rows).  A
+  // branch of few rows leaves most of a wide item idle while its pages pass
+  // (64 single tokens of 5 heads a group over 32,768 + 1,000 keys: 142 us
+  // against 119 us), and short runs are latency alone (9 ragged prompts of up
+  // to 858 keys: 53 us against 47 us).
+  const long long rows = (long long)N * a.g;
+  const long long keys = (long long)a.C + ((long long)a.max_pages << a.page_shift);
+  const bool wide = rows / a.B >= 256 && a.H * ((rows + 255) / 256) * ((keys + 127) / 128) >= 16 * kSms;
+  const Geometry x = geometry(dt, wide, a.H, rows, a.D);
   a.TM = x.TM;
   a.TN = x.TN;
   a.G = x.G;

@@ -44,7 +44,7 @@ struct BranchArgs {
   BranchCut* cuts;        // [G] what each run leaves unfinished
   long long* head;        // more than one row tile: [H + 1] first unit of each head, then the tiles in use
   long long* tile;        // the same: [ntiles + 1] first page unit of each row tile
-  float* po;              // [2 G][slot_rows][D]
+  float* po;              // [2 G][D / 4][slot_rows][4]: neighbouring rows lie side by side
   float2* pml;            // [2 G][slot_rows]
 };
 
@@ -102,6 +102,7 @@ struct BranchPlace {
       return;
     }
     bool ok = true;
+    const int size0 = a.size && lane < a.H ? a.size[lane] : a.C;  // on its way with the lengths
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
       if (b < a.B) {
@@ -120,9 +121,9 @@ struct BranchPlace {
       const int h = h0 + lane;
       int v = 0;
       if (h < a.H) {
-        const int size = a.size ? a.size[h] : a.C;
+        const int size = h0 == 0 ? size0 : a.size ? a.size[h] : a.C;
         ok = ok && size >= 0 && size <= a.C;
-        v = prefix_units(prefix_size(a, h), a.TN);
+        v = prefix_units(min(max(size, 0), a.C), a.TN);
       }
       U += __reduce_add_sync(0xffffffffu, v) + (long long)min(32, a.H - h0) * pages;
     }
@@ -179,6 +180,11 @@ struct BranchUnit {
   int slot;        // partial slot of the item
 };
 
+// First unit of run c of G.
+__device__ __forceinline__ long long branch_cut(long long U, int c, int G) {
+  return U < (1 << 23) ? (long long)((unsigned)U * (unsigned)c / (unsigned)G) : U * c / G;
+}
+
 // What the join needs of the item that run c leaves unfinished (and began).
 struct BranchCut {
   int h, t;        // h = -1: none
@@ -191,7 +197,9 @@ struct BranchCut {
 // branch (or of the prefix) at a time.
 struct BranchWalk {
   int h, t, c, nt, left;           // item; run; units left in the run
-  int off, units, P, size, pages;  // next unit of the item, its units, those of the prefix
+  int off, units, from;            // next unit of the item, its units, the first one in this run
+  int P, size, pages;              // units and rows of the prefix; one row tile: page units
+  long long U, end;                // units of the call; end of the run
   int T0, T1;
   bool head_item;                  // the run's first item
   bool whole;
@@ -214,7 +222,7 @@ struct BranchWalk {
     incl = warp_incl_scan(nu);
     total = __shfl_sync(0xffffffffu, incl, 31);
   }
-  __device__ __forceinline__ void enter(const BranchArgs& a, int from) {
+  __device__ __forceinline__ void enter(const BranchArgs& a, int at) {
     const int rows = a.cu[a.B] * a.g;
     const int r0 = t * a.TM, r1 = min(r0 + a.TM, rows);
     T0 = r0 / a.g;
@@ -222,48 +230,45 @@ struct BranchWalk {
     size = prefix_size(a, h);
     P = prefix_units(size, a.TN);
     units = P + (a.ntiles > 1 ? (int)(a.tile[t + 1] - a.tile[t]) : pages);
-    off = from;
-    whole = from == 0 && units <= left;
+    off = from = at;
+    whole = at == 0 && units <= left;
     // first branch with tokens at or behind T0 (empty ones contribute nothing)
     bbase = a.ntiles > 1 ? max(0, warp_count_le(a.cu, a.B, T0) - 1) : 0;
     before = 0;
     load_batch(a);
   }
-  // Goes to the start of run cta; false: the run is empty.  The join's record
-  // of the run is left in *cut.
-  __device__ __forceinline__ bool start(const BranchArgs& a, int cta, int32_t* st, BranchCut* cut) {
+  // Goes to the start of run cta; false: the run is empty.
+  __device__ __forceinline__ bool start(const BranchArgs& a, int cta, int32_t* st) {
     BranchPlace p;
     p.load(a, st);
     c = cta;
     nt = p.nt;
     pages = p.pages;
-    const long long u = p.U * c / a.G, end = p.U * (c + 1) / a.G;
+    U = p.U;
+    const long long u = branch_cut(U, c, a.G);
+    end = branch_cut(U, c + 1, a.G);
     left = (int)(end - u);
-    BranchCut x = {-1, 0, 0, 0, p.U};
+    off = units = from = 0;
+    head_item = true;
     if (left > 0) {
       long long first;
       p.find(a, u, h, t, first);
-      // the item of the run's last unit: begun here and not finished here?
-      const int h0 = h, t0 = t;
-      long long f1;
-      int h1, t1;
-      p.find(a, end - 1, h1, t1, f1);
-      h = h1;
-      t = t1;
-      enter(a, 0);
-      if (f1 >= u && f1 + units > end) {
-        x.h = h1;
-        x.t = t1;
-        x.slot = 2 * c + (f1 > u ? 1 : 0);
-        x.last = (int)(((f1 + units) * a.G - 1) / p.U);
-      }
-      h = h0;
-      t = t0;
-      head_item = true;
       enter(a, (int)(u - first));
     }
-    if ((threadIdx.x & 31) == 0) *cut = x;
     return left > 0;
+  }
+  // At the end of the run: the join's record of the item that it began and
+  // left unfinished.
+  __device__ __forceinline__ BranchCut cut(const BranchArgs& a) const {
+    BranchCut x = {-1, 0, 0, 0, U};
+    if (off < units && from == 0) {
+      x.h = h;
+      x.t = t;
+      x.slot = 2 * c + (head_item ? 0 : 1);
+      const long long last = end - off + units;  // one behind the item's last unit
+      x.last = U < (1 << 23) ? (int)(((unsigned)last * (unsigned)a.G - 1) / (unsigned)U) : (int)((last * a.G - 1) / U);
+    }
+    return x;
   }
   // The next stretch: x describes its first unit, `count` units follow one
   // another, `keys_end` bounds their keys.  False at the end of the run.

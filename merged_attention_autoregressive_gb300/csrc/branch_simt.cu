@@ -41,7 +41,10 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
   int count = 0, keys_end = 0;
   bool opens = false, closes = false;
   BranchUnit x = {};
-  if (!w.start(a, blockIdx.x, st, a.cuts + blockIdx.x)) return;
+  if (!w.start(a, blockIdx.x, st)) {
+    if (tid == 0) a.cuts[blockIdx.x] = w.cut(a);
+    return;
+  }
   const int rows = a.cu[a.B] * a.g;
   float m[4], l[4], o[4][OC];
   bool bad = false;
@@ -218,12 +221,14 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
         } else {
           const size_t at = (size_t)x.slot * a.slot_rows + lr;
 #pragma unroll
-          for (int c = 0; c < OC / 4; ++c) st_vec<float, 4>(a.po + at * D + tx * 4 + 64 * c, &o[i][4 * c]);
+          for (int c = 0; c < OC / 4; ++c)
+            st_vec<float, 4>(a.po + ((size_t)x.slot * D + 4 * (tx + 16 * c)) * a.slot_rows + 4 * lr, &o[i][4 * c]);
           if (tx == 0) a.pml[at] = make_float2(m[i], l[i]);
         }
       }
     }
   }
+  if (tid == 0) a.cuts[blockIdx.x] = w.cut(a);
   if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
   pdl_trigger();
 }

@@ -74,6 +74,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ void bar_stream(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void bar_all(int id) { asm volatile("bar.sync %0, 512;" ::"r"(id) : "memory"); }
 // `threads` threads meet; whether any of them holds p.
 template <int threads>
@@ -109,8 +110,10 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
   uint8_t* const ring = sm.tiles + (split ? 1 : 2) * S::kTile;
   // CTA-uniform: the status word and the address of the tiles
   if (tid == 0 && (tc::smem_u32(sm.tiles) & 1023u)) status_set(st, FASTAR_ERR_CUDA);
-  const int stop = __syncthreads_or(status_bad(st) || (tc::smem_u32(sm.tiles) & 1023u));
-  if (stop) return;
+  // the loader finds the run's place while the others set the CTA up
+  BranchWalk w;
+  bool more = false;
+  if (warp == kLoader) more = w.start(a, blockIdx.x, st);
   if (tid == 0) {
     for (int i = 0; i < S::kSlots1; ++i) {
       tc::mbar_init(&sm.full[i], 1);
@@ -137,14 +140,17 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     tc::tmem_relinquish();
   }
   tc::tc_fence_before();
-  __syncthreads();
+  const int stop = __syncthreads_or(status_bad(st) || (tc::smem_u32(sm.tiles) & 1023u));
   tc::tc_fence_after();
+  if (stop) {
+    if (warp == kIssuer) tc::tmem_dealloc(sm.tmem, 512);
+    return;
+  }
   const uint32_t tmem = sm.tmem;  // S_0 / P_0, S_1 / P_1 at columns 0 and 128, O_0, O_1 at 256 and 384
   bool ok = true, bad = false;
 
   if (warp == kLoader) {
     // ================================================= loader
-    BranchWalk w;
     const int box = min(1 << a.page_shift, kN);  // rows of a page box
     if (lane == 0) {
       tc::prefetch_tensormap(&mapK);
@@ -152,7 +158,6 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       tc::prefetch_tensormap(&mapPK);
       tc::prefetch_tensormap(&mapPV);
     }
-    bool more = w.start(a, blockIdx.x, st, a.cuts + blockIdx.x);
     const int rows = a.cu[a.B] * a.g;
     uint32_t j = 0;                   // units described
     uint32_t slot0 = 0, round0 = 0;   // of the first ring: next tile, times round
@@ -263,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         x.k0 += kN;
       }
     }
+    if (lane == 0) a.cuts[blockIdx.x] = w.cut(a);
     // no unit: the end of the run
     if (ok) {
       const int ds = j % S::kRing;
@@ -731,7 +737,12 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           w0 *= inv;
           w1 *= inv;
           const size_t at = live ? (size_t)(x.h * a.g + r % a.g) * a.N + r / a.g : 0;
-          const int slot_row = x.slot * a.slot_rows + (split ? 0 : s * kM) + wr;
+          const int slot_row = (split ? 0 : s * kM) + wr;
+          // a finished row goes through the query tile (free by now; 16-byte
+          // piece c of row r at place c ^ r % 8) and leaves in whole lines; a
+          // partial is laid out so that the rows of a warp are neighbours
+          uint8_t* const stage = sm.tiles + (split ? 0 : s) * S::kTile;
+          if (split && whole) bar_stream(2);  // the maxima and sums in it have been read
 #pragma unroll 1
           for (int q = 0; q < D / 64; ++q) {
             float o[32];
@@ -749,34 +760,47 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], w1, o[i]);
             }
-            if (!live) continue;
             const int col = half * (D / 2) + q * 32;
             if (whole) {
-              __nv_bfloat16* out = (__nv_bfloat16*)a.out + at * D + col;
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) st_vec<__nv_bfloat16, 8>(out + i, o + i);
-            } else {
-              float* po = a.po + (size_t)slot_row * D + col;
+              for (int i = 0; i < 4; ++i)
+                st_vec<__nv_bfloat16, 8>(
+                    reinterpret_cast<__nv_bfloat16*>(stage + wr * (D * 2) + (((col / 8 + i) ^ (wr & 7)) << 4)), o + i * 8);
+            } else if (live) {
+              float* po = a.po + (size_t)x.slot * a.slot_rows * D + ((size_t)(col / 4) * a.slot_rows + slot_row) * 4;
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) st_vec<float, 4>(po + i, o + i);
+              for (int i = 0; i < 8; ++i) st_vec<float, 4>(po + (size_t)i * a.slot_rows * 4, o + i * 4);
             }
           }
           if (live && half == 0) {
             if (whole) {
               if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
             } else {
-              a.pml[slot_row] = make_float2(m, l);
+              a.pml[(size_t)x.slot * a.slot_rows + slot_row] = make_float2(m, l);
+            }
+          }
+          if (whole) {
+            bar_two(pair);
+            constexpr int per = D / 8, step = 32 / per;  // pieces of a row, rows per warp access
+            const int c = lane % per;
+#pragma unroll
+            for (int k = 0; k < 16; k += step) {
+              const int y = half * 16 + k + lane / per;  // row of the warp's 32
+              const size_t to = __shfl_sync(0xffffffffu, at, y);
+              const int yr = (warp & 3) * 32 + y;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + yr * (D * 2) + ((c ^ (yr & 7)) << 4));
+              if (r - lane + y < rows) *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + to * D + c * 8) = v;
             }
           }
         }
         if (split) {
           // stream 1 may overwrite its O (by its next P) only now
           tc::tc_fence_before();
-          bar_all(2);
+          bar_all(11);
           tc::tc_fence_after();
         } else {
           tc::tc_fence_before();
-          bar_two(pair);  // the sums have been read
+          bar_two(pair);  // the sums and the staged rows have been read
           tc::tc_fence_after();
         }
       }
