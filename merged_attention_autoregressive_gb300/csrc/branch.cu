@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
       continue;
     }
     if (hi == lo) continue;
-    const int t0 = (int)((long long)lo * a.g / a.TM), t1 = (int)(((long long)hi * a.g - 1) / a.TM);
+    const int t0 = lo * a.g / a.TM, t1 = (hi * a.g - 1) / a.TM;
     for (int t = t0 + lane; t <= t1; t += 32) {
       const int T1 = (int)((((long long)t + 1) * a.TM + a.g - 1) / a.g);
       const int keys = branch_limit(min(hi, T1) - 1 - lo, hi - lo, len, a.block);
@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
   long long carry = 0, total;
   for (int t0 = 0; t0 < nt; t0 += kPlanThreads) {
     const int t = t0 + tid;
-    const long long v = t < nt ? __ldcg(&a.tile[t]) : 0;  // summed in L2
+    // (summed in L2; an item over nothing still has a unit, to be written)
+    const long long v = t < nt ? max(1ll, __ldcg(&a.tile[t])) : 0;
     const long long x = block_scan_ll(v, sh, &total);
     if (t < nt) a.tile[t] = carry + x;
     carry += total;
@@ -95,21 +96,25 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
   pdl_trigger();
 }
 
-// Joins the partials of every item that is cut: grid (runs, row groups); the
+// Joins the partials of every item that is cut: grid (records, row groups); the
 // run that begins an item left a record of it.  A warp takes 8 rows by 16
 // columns: lane = row + 8 sub, and sub-group `sub` adds the partials of every
 // fourth run, so that a few rows over many runs still keep four loads of each
 // lane in flight; the four sums are joined by shuffles (a fixed order).
+constexpr int kJoinThreads = 256;
+
 template <typename T>
-__global__ void __launch_bounds__(256) branch_combine_kernel(BranchArgs a, int32_t* st) {
+__global__ void __launch_bounds__(kJoinThreads) branch_combine_kernel(BranchArgs a, int32_t* st) {
   pdl_wait();
   const bool stop = status_bad(st);
   const BranchCut x = a.cuts[blockIdx.x];
-  if (stop || x.h < 0) return;
-  const int lane = threadIdx.x & 31, c = blockIdx.x;
-  const int w = blockIdx.y * 8 + (threadIdx.x >> 5), groups = a.D / 16;
+  const int rows = a.cu[a.B] * a.g;
+  // an item of padding alone has no record
+  if (stop || (a.by_item && (int)(blockIdx.x % a.ntiles) * a.TM >= rows) || x.h < 0) return;
+  const int lane = threadIdx.x & 31, c = x.run;
+  const int w = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), groups = a.D / 16;
   const int i = w / groups * 8 + (lane & 7), col = w % groups * 16, sub = lane >> 3;
-  const int rows = a.cu[a.B] * a.g, r0 = x.t * a.TM;
+  const int r0 = x.t * a.TM;
   const int nr = min(a.TM, rows - r0), n = x.last - c + 1;
   if (w / groups * 8 >= nr) return;
   const bool live = i < nr;
@@ -206,9 +211,10 @@ int launch_branch_plan(const BranchArgs& a, int32_t* st, cudaStream_t s) {
 
 int launch_branch_combine(const BranchArgs& a, fastar_dtype dt, int32_t* st, cudaStream_t s) {
   const int rows = (int)min((long long)a.TM, (long long)a.N * a.g);
-  const dim3 grid(a.G, ((rows + 7) / 8 * (a.D / 16) + 7) / 8);
-  cudaError_t rc = dt == FASTAR_BF16 ? launch_pdl(branch_combine_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a, st)
-                                     : launch_pdl(branch_combine_kernel<float>, grid, dim3(256), 0, s, a, st);
+  const int warps = kJoinThreads / 32;
+  const dim3 grid(a.by_item ? a.H * a.ntiles : a.G, ((rows + 7) / 8 * (a.D / 16) + warps - 1) / warps);
+  cudaError_t rc = dt == FASTAR_BF16 ? launch_pdl(branch_combine_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0, s, a, st)
+                                     : launch_pdl(branch_combine_kernel<float>, grid, dim3(kJoinThreads), 0, s, a, st);
   if (rc != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
@@ -299,15 +305,22 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   a.G = x.G;
   a.ntiles = x.ntiles;
   a.slot_rows = x.slot_rows;
+  a.planned = a.ntiles > kMaxTiles || (a.ntiles > kFewTiles && a.B > kMaxBranches);
+  // Short items (a few microseconds each) are not cut where there are enough
+  // of them: the join costs as much as the imbalance (9 ragged prompts of up
+  // to 858 keys, 256 items: 24 us, 32 us when cut).
+  const long long items = (long long)a.H * a.ntiles;
+  a.whole = items >= a.G && (keys + a.TN - 1) / a.TN <= 8;
+  a.by_item = items <= a.G;
   char* w = (char*)ws;
   a.cuts = (BranchCut*)w;
   a.head = (long long*)(w += x.cuts);
   a.tile = (long long*)(w += x.head);
   a.po = (float*)(w += x.tile);
   a.pml = (float2*)(w + x.po);
-  int rc = a.ntiles > 1 ? launch_branch_plan(a, st, s) : FASTAR_OK;
+  int rc = a.planned ? launch_branch_plan(a, st, s) : FASTAR_OK;
   if (rc == FASTAR_OK) rc = dt == FASTAR_BF16 ? launch_branch_tc(a, st, s) : launch_branch_simt(a, st, s);
-  if (rc == FASTAR_OK) rc = launch_branch_combine(a, dt, st, s);
+  if (rc == FASTAR_OK && !a.whole) rc = launch_branch_combine(a, dt, st, s);
   return rc;
 }
 

@@ -41,9 +41,12 @@ struct BranchArgs {
   // schedule
   int TM, TN, G, ntiles;  // ntiles: row tiles of all N tokens
   int slot_rows;          // rows of a partial
-  BranchCut* cuts;        // [G] what each run leaves unfinished
-  long long* head;        // more than one row tile: [H + 1] first unit of each head, then the tiles in use
-  long long* tile;        // the same: [ntiles + 1] first page unit of each row tile
+  int planned;            // branch_plan has written head and tile
+  int whole;              // items are not cut: a run ends where an item begins
+  int by_item;            // cuts has an entry per item (there are at most G), else per run
+  BranchCut* cuts;        // [G] the items that are cut
+  long long* head;        // planned: [H + 1] first unit of each head, then the tiles in use
+  long long* tile;        // planned: [ntiles + 1] first page unit of each row tile
   float* po;              // [2 G][D / 4][slot_rows][4]: neighbouring rows lie side by side
   float2* pml;            // [2 G][slot_rows]
 };
@@ -59,7 +62,7 @@ __device__ __forceinline__ int branch_limit(int i, int n, int len, int block) {
 __device__ __forceinline__ int prefix_size(const BranchArgs& a, int h) {
   return a.size ? min(max(a.size[h], 0), a.C) : a.C;
 }
-__device__ __forceinline__ int prefix_units(int size, int TN) { return max(1, (size + TN - 1) / TN); }
+__device__ __forceinline__ int prefix_units(int size, int TN) { return (size + TN - 1) / TN; }
 
 // Entries of the ascending list x[0..n) that are <= v (whole warp).
 template <typename T>
@@ -86,36 +89,82 @@ __device__ __forceinline__ bool branch_ok(const BranchArgs& a, int b, int lo, in
          (long long)len <= ((long long)a.max_pages << a.page_shift);
 }
 
-// What a run starts from (whole warp).  One row tile: taken from the lengths
-// right here, so that single tokens need no plan kernel.  Otherwise from the
-// lists of branch_plan.
+constexpr int kLaneTiles = 2;               // row tiles per lane of an unplanned call
+constexpr int kMaxTiles = 32 * kLaneTiles;  // row tiles, and above kFewTiles of them
+constexpr int kMaxBranches = 32;            // branches, of a call that goes without a plan
+constexpr int kFewTiles = 8;
+
+// First token of row tile t, and one behind its last.
+__device__ __forceinline__ int tile_begin(const BranchArgs& a, int t) { return t * a.TM / a.g; }
+__device__ __forceinline__ int tile_end(const BranchArgs& a, int t) { return ((t + 1) * a.TM + a.g - 1) / a.g; }
+
+// What a run starts from (whole warp).  Few row tiles: summed from the
+// lengths right here, so that single tokens and short prompts need no plan
+// kernel; lane l holds tiles l and l + 32.  Otherwise from branch_plan's lists.
 struct BranchPlace {
-  long long U;      // units of the call; 0: nothing to do, or something does not hold
-  int nt, pages;    // row tiles in use; one row tile: its page units
+  long long U;            // units of the call; 0: nothing to do, or something does not hold
+  int nt, sum;            // row tiles in use; page units of one head's tiles (unplanned)
+  int pages[kLaneTiles];  // page units of the lane's tiles (unplanned)
 
   __device__ __forceinline__ void load(const BranchArgs& a, int32_t* st) {
     const int lane = threadIdx.x & 31;
-    nt = pages = 0;
-    if (a.ntiles > 1) {
+    if (a.planned) {
       U = a.head[a.H];
       nt = (int)a.head[a.H + 1];
       return;
     }
     bool ok = true;
     const int size0 = a.size && lane < a.H ? a.size[lane] : a.C;  // on its way with the lengths
+    int used = 0, t0[kLaneTiles], t1[kLaneTiles];
+#pragma unroll
+    for (int e = 0; e < kLaneTiles; ++e) {
+      const int t = lane + 32 * e;
+      pages[e] = 0;
+      t0[e] = t < a.ntiles ? tile_begin(a, t) : 0x7fffffff;
+      t1[e] = t < a.ntiles ? tile_end(a, t) : 0;
+    }
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
+      int lo = 0, hi = 0, len = 0;
       if (b < a.B) {
-        const int lo = a.cu[b], hi = a.cu[b + 1], len = a.len[b];
+        lo = a.cu[b];
+        hi = a.cu[b + 1];
+        len = a.len[b];
         ok = ok && branch_ok(a, b, lo, hi, len);
-        if (ok && hi > lo) {
-          nt = 1;
-          pages += (branch_limit(hi - 1 - lo, hi - lo, len, a.block) + a.TN - 1) / a.TN;
+        if (!ok) hi = lo = 0;
+      }
+      used = max(used, hi);
+      if (a.ntiles <= kFewTiles) {
+        // a branch per lane, the tiles one after the other
+        for (int t = 0; t < a.ntiles; ++t) {
+          const int last = min(hi, tile_end(a, t)) - 1;
+          int v = 0;
+          if (last >= max(lo, tile_begin(a, t))) v = (branch_limit(last - lo, hi - lo, len, a.block) + a.TN - 1) / a.TN;
+          v = __reduce_add_sync(0xffffffffu, v);
+          if (lane == t) pages[0] += v;
+        }
+      } else {
+        // a tile per lane, the branches one after the other
+        for (int k = 0; k < min(32, a.B - b0); ++k) {
+          const int l = __shfl_sync(0xffffffffu, lo, k), r = __shfl_sync(0xffffffffu, hi, k);
+          const int n = __shfl_sync(0xffffffffu, len, k);
+#pragma unroll
+          for (int e = 0; e < kLaneTiles; ++e) {
+            const int last = min(r, t1[e]) - 1;
+            if (last >= max(l, t0[e])) pages[e] += (branch_limit(last - l, r - l, n, a.block) + a.TN - 1) / a.TN;
+          }
         }
       }
     }
-    nt = __reduce_max_sync(0xffffffffu, nt);
-    pages = __reduce_add_sync(0xffffffffu, pages);
+    nt = (__reduce_max_sync(0xffffffffu, used) * a.g + a.TM - 1) / a.TM;
+    sum = 0;
+#pragma unroll
+    for (int e = 0; e < kLaneTiles; ++e) {
+      // an item over nothing still has a unit, to be written
+      pages[e] = lane + 32 * e < nt ? max(1, pages[e]) : 0;
+      sum += pages[e];
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
     U = 0;
     for (int h0 = 0; h0 < a.H; h0 += 32) {
       const int h = h0 + lane;
@@ -125,16 +174,27 @@ struct BranchPlace {
         ok = ok && size >= 0 && size <= a.C;
         v = prefix_units(min(max(size, 0), a.C), a.TN);
       }
-      U += __reduce_add_sync(0xffffffffu, v) + (long long)min(32, a.H - h0) * pages;
+      U += (long long)__reduce_add_sync(0xffffffffu, v) * nt + (long long)min(32, a.H - h0) * sum;
     }
     ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) status_set(st, FASTAR_ERR_DEVICE_ARG);
     if (!ok || nt == 0) U = 0;
   }
+  // Page units of row tile t.
+  __device__ __forceinline__ int pages_of(const BranchArgs& a, int t) const {
+    if (a.planned) return (int)(a.tile[t + 1] - a.tile[t]);
+    int v = 0;
+#pragma unroll
+    for (int e = 0; e < kLaneTiles; ++e) {
+      const int x = __shfl_sync(0xffffffffu, pages[e], t & 31);
+      if (t >> 5 == e) v = x;
+    }
+    return v;
+  }
   // The item of unit u: head, row tile and first unit.
   __device__ __forceinline__ void find(const BranchArgs& a, long long u, int& h, int& t, long long& first) const {
     const int lane = threadIdx.x & 31;
-    if (a.ntiles > 1) {
+    if (a.planned) {
       h = warp_count_le(a.head, a.H, u) - 1;
       const long long off = u - a.head[h];
       const int p = prefix_units(prefix_size(a, h), a.TN);
@@ -151,17 +211,33 @@ struct BranchPlace {
       first = a.head[h] + (long long)t * p + a.tile[t];
       return;
     }
-    t = 0;
-    h = 0;
+    h = t = 0;
     first = 0;
+    int p = 0;
     for (int h0 = 0; h0 < a.H; h0 += 32) {
       const int x = h0 + lane;
-      const int v = x < a.H ? prefix_units(prefix_size(a, x), a.TN) + pages : 0;
+      const int pu = x < a.H ? prefix_units(prefix_size(a, x), a.TN) : 0;
+      const int v = x < a.H ? pu * nt + sum : 0;  // an unplanned head has far fewer than 2^31 / 32 units
       const int inc = warp_incl_scan(v);
       const unsigned m = __ballot_sync(0xffffffffu, x < a.H && first + inc > u);
       if (m) {
         const int src = __ffs(m) - 1;
         h = h0 + src;
+        p = __shfl_sync(0xffffffffu, pu, src);
+        first += __shfl_sync(0xffffffffu, inc - v, src);
+        break;
+      }
+      first += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (nt == 1) return;
+#pragma unroll
+    for (int e = 0; e < kLaneTiles; ++e) {
+      const int x = lane + 32 * e, v = x < nt ? p + pages[e] : 0;
+      const int inc = warp_incl_scan(v);
+      const unsigned m = __ballot_sync(0xffffffffu, x < nt && first + inc > u);
+      if (m) {
+        const int src = __ffs(m) - 1;
+        t = 32 * e + src;
         first += __shfl_sync(0xffffffffu, inc - v, src);
         return;
       }
@@ -185,21 +261,22 @@ __device__ __forceinline__ long long branch_cut(long long U, int c, int G) {
   return U < (1 << 23) ? (long long)((unsigned)U * (unsigned)c / (unsigned)G) : U * c / G;
 }
 
-// What the join needs of the item that run c leaves unfinished (and began).
+// What the join needs of an item that is cut.
 struct BranchCut {
   int h, t;        // h = -1: none
-  int last;        // the run that finishes it
-  int slot;        // the partial of run c; the later runs have slot 2 j
+  int run, last;   // the runs that begin and finish it
+  int slot;        // the partial of the first; the later runs have slot 2 j
   long long U;
 };
 
 // Walks the units of run c, a whole warp in step, a stretch of units of one
 // branch (or of the prefix) at a time.
 struct BranchWalk {
-  int h, t, c, nt, left;           // item; run; units left in the run
+  BranchPlace place;
+  int h, t, c, left;               // item; run; units left in the run
   int off, units, from;            // next unit of the item, its units, the first one in this run
-  int P, size, pages;              // units and rows of the prefix; one row tile: page units
-  long long U, end;                // units of the call; end of the run
+  int P, size;                     // units and rows of the prefix
+  long long end;                   // end of the run
   int T0, T1;
   bool head_item;                  // the run's first item
   bool whole;
@@ -229,9 +306,11 @@ struct BranchWalk {
     T1 = (r1 + a.g - 1) / a.g;
     size = prefix_size(a, h);
     P = prefix_units(size, a.TN);
-    units = P + (a.ntiles > 1 ? (int)(a.tile[t + 1] - a.tile[t]) : pages);
+    units = P + place.pages_of(a, t);
     off = from = at;
     whole = at == 0 && units <= left;
+    // the join's record of an item that this run begins
+    if (at == 0 && a.by_item && (threadIdx.x & 31) == 0) a.cuts[h * a.ntiles + t] = cut(a);
     // first branch with tokens at or behind T0 (empty ones contribute nothing)
     bbase = a.ntiles > 1 ? max(0, warp_count_le(a.cu, a.B, T0) - 1) : 0;
     before = 0;
@@ -239,33 +318,39 @@ struct BranchWalk {
   }
   // Goes to the start of run cta; false: the run is empty.
   __device__ __forceinline__ bool start(const BranchArgs& a, int cta, int32_t* st) {
-    BranchPlace p;
-    p.load(a, st);
+    place.load(a, st);
     c = cta;
-    nt = p.nt;
-    pages = p.pages;
-    U = p.U;
-    const long long u = branch_cut(U, c, a.G);
-    end = branch_cut(U, c + 1, a.G);
-    left = (int)(end - u);
-    off = units = from = 0;
+    off = units = from = left = 0;
     head_item = true;
-    if (left > 0) {
-      long long first;
-      p.find(a, u, h, t, first);
-      enter(a, (int)(u - first));
+    const long long U = place.U;
+    if (U == 0) {
+      // no item: nothing for the join
+      if (a.by_item && c == 0)
+        for (int i = threadIdx.x & 31; i < a.H * a.ntiles; i += 32) a.cuts[i].h = -1;
+      return false;
     }
+    long long u = branch_cut(U, c, a.G), first = u;
+    end = branch_cut(U, c + 1, a.G);
+    if (a.whole && end < U) {
+      place.find(a, end, h, t, first);
+      end = first;
+    }
+    if (u < U) place.find(a, u, h, t, first);
+    if (a.whole) u = u < U ? first : U;
+    left = (int)(end - u);
+    if (left > 0) enter(a, (int)(u - first));
     return left > 0;
   }
-  // At the end of the run: the join's record of the item that it began and
-  // left unfinished.
+  // The join's record of the present item: a run that begins an item and does
+  // not finish it names the run that does.
   __device__ __forceinline__ BranchCut cut(const BranchArgs& a) const {
-    BranchCut x = {-1, 0, 0, 0, U};
-    if (off < units && from == 0) {
+    BranchCut x = {-1, 0, 0, 0, 0, place.U};
+    if (from == 0 && units - off > left) {
       x.h = h;
       x.t = t;
+      x.run = c;
       x.slot = 2 * c + (head_item ? 0 : 1);
-      const long long last = end - off + units;  // one behind the item's last unit
+      const long long last = end - left - off + units, U = place.U;  // one behind the item's last unit
       x.last = U < (1 << 23) ? (int)(((unsigned)last * (unsigned)a.G - 1) / (unsigned)U) : (int)((last * a.G - 1) / U);
     }
     return x;
@@ -277,7 +362,7 @@ struct BranchWalk {
                                        bool& closes, int opened) {
     if (left == 0) return false;
     if (off == units) {
-      if (++t == nt) {
+      if (++t == place.nt) {
         t = 0;
         ++h;
       }

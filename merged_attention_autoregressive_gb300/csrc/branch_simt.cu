@@ -41,15 +41,12 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
   int count = 0, keys_end = 0;
   bool opens = false, closes = false;
   BranchUnit x = {};
-  if (!w.start(a, blockIdx.x, st)) {
-    if (tid == 0) a.cuts[blockIdx.x] = w.cut(a);
-    return;
-  }
+  const bool any = w.start(a, blockIdx.x, st);
   const int rows = a.cu[a.B] * a.g;
   float m[4], l[4], o[4][OC];
   bool bad = false;
   bool first_stretch = true;
-  while (true) {
+  while (any) {
     if (count == 0) {
       if (!w.next(a, x, count, keys_end, opens, closes, first_stretch ? 1 : 0)) break;
       first_stretch = false;
@@ -228,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
       }
     }
   }
-  if (tid == 0) a.cuts[blockIdx.x] = w.cut(a);
+  if (tid == 0 && !a.by_item) a.cuts[blockIdx.x] = w.cut(a);
   if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
   pdl_trigger();
 }

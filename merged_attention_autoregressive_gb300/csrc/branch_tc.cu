@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
                                                                const BranchArgs a, int32_t* st) {
   using S = Shape<D>;
   pdl_wait();
+  const bool stopped = status_bad(st);  // on its way while the CTA is set up
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     tc::tmem_relinquish();
   }
   tc::tc_fence_before();
-  const int stop = __syncthreads_or(status_bad(st) || (tc::smem_u32(sm.tiles) & 1023u));
+  const int stop = __syncthreads_or(stopped || (tc::smem_u32(sm.tiles) & 1023u));
   tc::tc_fence_after();
   if (stop) {
     if (warp == kIssuer) tc::tmem_dealloc(sm.tmem, 512);
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         x.k0 += kN;
       }
     }
-    if (lane == 0) a.cuts[blockIdx.x] = w.cut(a);
+    if (lane == 0 && !a.by_item) a.cuts[blockIdx.x] = w.cut(a);
     // no unit: the end of the run
     if (ok) {
       const int ds = j % S::kRing;
