@@ -105,6 +105,7 @@ constexpr int kJoinThreads = 256;
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) branch_combine_kernel(BranchArgs a, int32_t* st) {
+  branch_touch(a, st);
   pdl_wait();
   const bool stop = status_bad(st);
   const BranchCut x = a.cuts[blockIdx.x];

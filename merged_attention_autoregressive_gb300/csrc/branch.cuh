@@ -51,6 +51,13 @@ struct BranchArgs {
   float2* pml;            // [2 G][slot_rows]
 };
 
+// Brings the call's arguments into the constant cache; before pdl_wait, so
+// that their misses (one per 64 bytes) pass while the previous kernel ends.
+__device__ __forceinline__ void branch_touch(const BranchArgs& a, const int32_t* st) {
+  asm volatile("" ::"l"(a.q), "l"(a.size), "r"(a.N), "r"(a.max_pages), "l"(a.lse), "r"(a.G), "l"(a.head), "l"(a.pml),
+               "l"(st));
+}
+
 // Keys of its branch that token i of n (branch length len) sees.
 __device__ __forceinline__ int branch_limit(int i, int n, int len, int block) {
   if (block <= 0) return len;

@@ -27,6 +27,7 @@ struct SimtSmem {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, int32_t* st) {
+  branch_touch(a, st);
   pdl_wait();
   extern __shared__ uint4 raw[];
   SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(raw);

@@ -99,8 +99,6 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
                                                                const __grid_constant__ CUtensorMap mapV,
                                                                const BranchArgs a, int32_t* st) {
   using S = Shape<D>;
-  pdl_wait();
-  const bool stopped = status_bad(st);  // on its way while the CTA is set up
   extern __shared__ __align__(1024) uint8_t raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -109,12 +107,8 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
   // that takes every other unit has not seen the other's).
   constexpr int slots = split ? S::kSlots1 / 2 : S::kSlots2;
   uint8_t* const ring = sm.tiles + (split ? 1 : 2) * S::kTile;
-  // CTA-uniform: the status word and the address of the tiles
-  if (tid == 0 && (tc::smem_u32(sm.tiles) & 1023u)) status_set(st, FASTAR_ERR_CUDA);
-  // the loader finds the run's place while the others set the CTA up
-  BranchWalk w;
-  bool more = false;
-  if (warp == kLoader) more = w.start(a, blockIdx.x, st);
+  // what needs nothing of the previous kernel
+  branch_touch(a, st);
   if (tid == 0) {
     for (int i = 0; i < S::kSlots1; ++i) {
       tc::mbar_init(&sm.full[i], 1);
@@ -136,6 +130,19 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     tc::mbar_init(&sm.fin[1], 1);
     tc::fence_mbar_init();
   }
+  if (warp == kIssuer + 1 && lane == 0) {
+    tc::prefetch_tensormap(&mapK);
+    tc::prefetch_tensormap(&mapV);
+    tc::prefetch_tensormap(&mapPK);
+    tc::prefetch_tensormap(&mapPV);
+  }
+  pdl_wait();
+  const bool stopped = status_bad(st);  // on its way while the CTA is set up
+  if (tid == 0 && (tc::smem_u32(sm.tiles) & 1023u)) status_set(st, FASTAR_ERR_CUDA);
+  // the loader finds the run's place while the others set the CTA up
+  BranchWalk w;
+  bool more = false;
+  if (warp == kLoader) more = w.start(a, blockIdx.x, st);
   if (warp == kIssuer) {
     tc::tmem_alloc(&sm.tmem, 512);
     tc::tmem_relinquish();
@@ -153,12 +160,6 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
   if (warp == kLoader) {
     // ================================================= loader
     const int box = min(1 << a.page_shift, kN);  // rows of a page box
-    if (lane == 0) {
-      tc::prefetch_tensormap(&mapK);
-      tc::prefetch_tensormap(&mapV);
-      tc::prefetch_tensormap(&mapPK);
-      tc::prefetch_tensormap(&mapPV);
-    }
     const int rows = a.cu[a.B] * a.g;
     uint32_t j = 0;                   // units described
     uint32_t slot0 = 0, round0 = 0;   // of the first ring: next tile, times round
