@@ -39,11 +39,17 @@ constexpr int kM = 128, kN = 128, kThreads = 640, kSoftmax = 16, kLoader = 16, k
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;  // raise the running max only when exceeded by more than this (log2)
 
-// What the consumers need of a unit.
+// What the consumers need of a unit: all of it in one word, but for the ends
+// of items and units that some row does not see whole.
 struct Desc {
   BranchUnit x;
-  int act;  // streams that have rows in it
+  int bits;
 };
+constexpr int kAct = 3;        // streams that have rows in it
+constexpr int kFull = 4;       // every row of the item sees every one of the 128 keys
+constexpr int kBiased = 8;     // the keys have biases
+constexpr int kFirst = 16, kLast = 32;  // of the item, in this run
+constexpr int kEnd = 64;       // no unit: the run is over
 
 template <int D>
 struct Shape {
@@ -183,6 +189,13 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         lo = max(lo, x.lo * a.g);
         hi = min(hi, (x.lo + x.n) * a.g);
       }
+      // keys that every row of the item sees: those of its first token, where
+      // the item belongs to one branch
+      int full_keys = keys_end;
+      if (own)
+        full_keys = x.lo * a.g <= r0 && (x.lo + x.n) * a.g >= min(r0 + a.TM, rows)
+                        ? branch_limit(r0 / a.g - x.lo, x.n, x.len, a.block)
+                        : 0;
       const int acts = hi <= lo ? 0 : split ? 1 : ((lo < r0 + kM ? 1 : 0) | (hi > r0 + kM ? 2 : 0));
       // page id of box `lane` (or the counts of rows lane + 32 e) of the unit
       // at k, fetched one unit ahead
@@ -220,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         if (lane == 0) {
           Desc& d = sm.desc[ds];
           d.x = x;
-          d.x.flags = x.flags | (opens && i == 0 ? 1 : 0) | (closes && i == count - 1 ? 2 : 0);
-          d.act = act;
+          d.bits = act | (x.nk == kN && x.k0 + kN <= full_keys ? kFull : 0) | (!own && counts ? kBiased : 0) |
+                   (opens && i == 0 ? kFirst : 0) | (closes && i == count - 1 ? kLast : 0);
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.dfull[ds]);
@@ -276,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       const int ds = j % S::kRing;
       if (j >= S::kRing) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dempty[ds], (j / S::kRing - 1) & 1u));
       if (ok && lane == 0) {
-        sm.desc[ds].act = -1;
+        sm.desc[ds].bits = kEnd;
         tc::mbar_arrive(&sm.dfull[ds]);
       }
     }
@@ -350,12 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       const int ds = j % S::kRing;
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dfull[ds], (j / S::kRing) & 1u));
       if (!ok) break;
-      const int act = sm.desc[ds].act;
-      const int flags = sm.desc[ds].x.flags, nk = sm.desc[ds].x.nk;
+      const int bits = sm.desc[ds].bits, nk = sm.desc[ds].x.nk;
       __syncwarp();
-      if (act < 0) break;
+      if (bits & kEnd) break;
       if (lane == 0) tc::mbar_arrive(&sm.dempty[ds]);
-      if (flags & 1) {
+      const int act = bits & kAct;
+      if (bits & kFirst) {
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.qfull, items & 1u));
         if (!ok) break;
         acc = 0u;
@@ -394,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         slot = vslot + 1 == (uint32_t)slots ? 0 : vslot + 1;
         phase = vslot + 1 == (uint32_t)slots ? vphase ^ 1u : vphase;
       }
-      if (flags & 2) {
+      if (bits & kLast) {
         if (pend) pv();
         if (ok && tc::elect_one()) tc::mma_commit(&sm.odone);
         __syncwarp();
@@ -464,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       np ^= 1u << s;
       acc |= 1u << s;
     };
-    int act = 0, flags = 0, nk = 0;
+    int bits = 0, nk = 0;
     bool read = false;  // the unit's descriptor has been read
     auto take = [&](uint32_t j, bool wait) {
       const int ds = j % S::kRing;
@@ -472,8 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         ok = ok && tc::mbar_wait(&sm.dfull[ds], (j / S::kRing) & 1u);
       else if (!__all_sync(0xffffffffu, tc::mbar_test_wait(&sm.dfull[ds], (j / S::kRing) & 1u)))
         return;
-      act = sm.desc[ds].act;
-      flags = sm.desc[ds].x.flags;
+      bits = sm.desc[ds].bits;
       nk = sm.desc[ds].x.nk;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.dempty[ds]);
@@ -484,9 +496,9 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       if (!ok) break;
       if (!read) take(j, true);
       read = false;
-      if (!ok || act < 0) break;
-      const int uact = act, uflags = flags, unk = nk;
-      if (uflags & 1) {
+      if (!ok || (bits & kEnd)) break;
+      const int uact = bits & kAct, ubits = bits, unk = nk;
+      if (ubits & kFirst) {
         ok = ok && tc::mbar_wait(&sm.qfull, items & 1u);
         acc = 0u;
       }
@@ -522,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         slot = pslot + 1 == slots ? 0 : pslot + 1;
         phase = pslot + 1 == slots ? pphase ^ 1u : pphase;
       }
-      if (uflags & 2) {
+      if (ubits & kLast) {
         for (int s = 0; s < 2; ++s)
           if (pend >> s & 1) pv(s);
         if (leader && ok) tc::mma_commit(&sm.odone);
@@ -546,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     const float scale2 = a.scale * kLog2e;
     const int rows = a.cu[a.B] * a.g;
     uint32_t ns = 0, items = 0, turn = 0;  // S tiles seen, items, active units of the item
+    int r = 0;                             // the row, counted over the items of the head
     float m = -INFINITY, l = 0.f;          // of the row; of this half's keys
     bool started = false;
     // Warps meet at named barriers, which have no limit of their own.  So a
@@ -557,11 +570,12 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       const int ds = j % S::kRing;
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dfull[ds], (j / S::kRing) & 1u));
       if (!ok) break;
-      const int act0 = sm.desc[ds].act;
-      if (act0 < 0) break;
-      const BranchUnit x = sm.desc[ds].x;
-      const int r = x.t * a.TM + (split ? 0 : s * kM) + wr;
-      if (x.flags & 1) {
+      const int bits = sm.desc[ds].bits;
+      if (bits & kEnd) break;
+      const int act0 = bits & kAct;
+      if (bits & kFirst) {
+        const BranchUnit x = sm.desc[ds].x;
+        r = x.t * a.TM + (split ? 0 : s * kM) + wr;
         // gather the row's queries (the previous item's products are done:
         // odone was waited for)
         m = -INFINITY;
@@ -586,10 +600,14 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       const bool active = act0 && (split ? (turn & 1) == (uint32_t)s : (act0 >> s & 1));
       if (act0) ++turn;
       if (active) {
-        // rows behind the last token count as full: nobody reads their results
-        const int seen = (r < rows ? branch_row_keys(a, x, r) : kN) - half * 64;
-        const bool any = __any_sync(0xffffffffu, r < rows && seen + half * 64 > 0);  // alike in both halves
-        const bool all = __all_sync(0xffffffffu, seen >= 64);
+        int seen = 64;  // keys of this half that the row sees
+        bool any = true, all = true;
+        if (!(bits & kFull)) {
+          // rows behind the last token count as full: nobody reads their results
+          seen = (r < rows ? branch_row_keys(a, sm.desc[ds].x, r) : kN) - half * 64;
+          any = __any_sync(0xffffffffu, r < rows && seen + half * 64 > 0);  // alike in both halves
+          all = __all_sync(0xffffffffu, seen >= 64);
+        }
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sfull[s], ns & 1u));
         if (!ok) break;
         ++ns;
@@ -601,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           uint32_t raw[64];
           float* const v = reinterpret_cast<float*>(raw);
           tc::tmem_ld64_async(tS + half * 64, raw);
-          const bool biased = x.branch < 0 && a.m != nullptr;
+          const bool biased = bits & kBiased;
           const bool plain = !biased && all;
           const float mul = plain ? scale2 : 1.f;
           tc::tmem_wait64(raw);
@@ -691,8 +709,11 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         started = true;
       }
       __syncwarp();
+      BranchUnit x;
+      if (bits & kLast) x = sm.desc[ds].x;
+      __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.dempty[ds]);
-      if (x.flags & 2) {
+      if (bits & kLast) {
         // ---- the item's end: O of the run
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.odone, items & 1u));
         if (!ok) break;
