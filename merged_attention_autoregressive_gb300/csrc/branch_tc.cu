@@ -68,7 +68,7 @@ struct Smem {
   Desc desc[S::kRing];
   uint64_t full[S::kSlots1], empty[S::kSlots1];
   uint64_t dfull[S::kRing], dempty[S::kRing];
-  uint64_t sfull[2], pready[2][2], odone, qfull, fin[2];  // pready: by stream and half of the keys
+  uint64_t sfull[2], pready[2], odone, qfull, fin[2];
   uint32_t tmem;
   int started1;
   uint32_t gone;                        // a bit per pair of softmax warps one of which has given up
@@ -126,8 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&sm.sfull[s], 1);
-      tc::mbar_init(&sm.pready[s][0], 4);
-      tc::mbar_init(&sm.pready[s][1], 4);
+      tc::mbar_init(&sm.pready[s], kSoftmax / 2);
     }
     sm.gone = 0u;
     tc::mbar_init(&sm.odone, split ? 2 : 1);
@@ -323,8 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     uint32_t acc = 0u;               // 0: O starts anew
     bool issued = false;
     auto pv = [&]() {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[pslot], pphase) && tc::mbar_wait(&sm.pready[s][0], np & 1u) &&
-                                       tc::mbar_wait(&sm.pready[s][1], np & 1u));
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[pslot], pphase) && tc::mbar_wait(&sm.pready[s], np & 1u));
       if (!ok) return;
       tc::tc_fence_after();
       const uint32_t vd = tc::desc_low(ring_addr + pslot * S::kTile, kN * 128);
@@ -422,12 +420,12 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     }
   } else if (!split && warp == kIssuer) {
     // ================================================= MMA issuer of both streams
-    // In turn P_0 V, Q_0 K^T, P_1 V, Q_1 K^T: each softmax has the other
-    // stream's two products to itself (with an issuer per stream both fell
-    // into step, and the tensor core idled through both softmaxes).  The
-    // queue of the tensor core holds a few MMAs only, so that what lies
-    // between two products is kept short: a tile is waited for once, the
-    // next unit's descriptor is read under the queued products.
+    // In turn P_0 V and Q_0 K^T, then P_1 V and Q_1 K^T: each softmax has the
+    // other stream's two products to itself (with an issuer per stream both
+    // fell into step, and the tensor core idled through both softmaxes).  The
+    // queue of the tensor core holds a few MMAs only, so a stream's two
+    // products go out without a wait between them: both tiles are waited for
+    // first, and the next unit's descriptor is read under the queued products.
     constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kM, kN, 0, 0);
     constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kM, D, 0, 1);
     const uint32_t ring_addr = tc::smem_u32(ring), q_addr = tc::smem_u32(sm.tiles);
@@ -437,45 +435,62 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     // (one for both), its keys, and whether O starts anew
     int pend = 0, pk = 0;
     uint32_t pslot = 0, pphase = 0, np = 0u, acc = 0u;  // np, acc: a bit per stream
-    bool issued = false, vthere = false;
-    auto pv = [&](const int s) {
-      if (!vthere) {
-        ok = ok && tc::mbar_wait(&sm.full[pslot], pphase);
-        vthere = true;
-        if (pk & 15) {
-          // value rows behind the unit's keys take part in the last step with
-          // weight 0: they must not hold an infinity or NaN
-          uint8_t* v = ring + (size_t)pslot * S::kTile;
-          for (int e = lane; e < (16 - (pk & 15)) * (D / 8); e += 32) {
-            const int r = pk + e / (D / 8), c = e % (D / 8);
-            *reinterpret_cast<uint4*>(v + (c >> 3) * kN * 128 + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
+    bool issued = false;
+    auto values = [&]() {
+      ok = ok && tc::mbar_wait(&sm.full[pslot], pphase);
+      if (pk & 15) {
+        // value rows behind the unit's keys take part in the last step with
+        // weight 0: they must not hold an infinity or NaN
+        uint8_t* v = ring + (size_t)pslot * S::kTile;
+        for (int e = lane; e < (16 - (pk & 15)) * (D / 8); e += 32) {
+          const int r = pk + e / (D / 8), c = e % (D / 8);
+          *reinterpret_cast<uint4*>(v + (c >> 3) * kN * 128 + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
         }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
       }
+    };
+    auto products = [&](const int s, const bool next, const bool next_last) {
+      const bool old = pend >> s & 1;
+      if (!old && !next) return;
       const uint32_t vd = tc::desc_low(ring_addr + pslot * S::kTile, kN * 128);
+      const uint32_t kd = tc::desc_low(ring_addr + slot * S::kTile, 16);
+      const uint32_t qd = tc::desc_low(q_addr + s * S::kTile, 16);
       // weights: keys 0-63 over S columns 0-31, keys 64-127 over columns 64-95
-      const uint32_t dS = tmem + s * 128, dO = tmem + 256 + s * 128;
-      const uint32_t ac = acc >> s & 1u, par = np >> s & 1u;
-      ok = ok && tc::mbar_wait(&sm.pready[s][0], par) && tc::mbar_wait(&sm.pready[s][1], par);
+      const uint32_t dS = tmem + s * 128, dO = tmem + 256 + s * 128, ac = acc >> s & 1u;
+      if (old) {
+        ok = ok && tc::mbar_wait(&sm.pready[s], np >> s & 1u);
+        np ^= 1u << s;
+        acc |= 1u << s;
+        pend &= ~(1 << s);
+      }
       tc::tc_fence_after();
-      pend &= ~(1 << s);
       if (leader && ok) {
-        if (pk == kN) {
+        if (old) {
+          if (pk == kN) {
 #pragma unroll
-          for (int k = 0; k < kN / 16; ++k)
-            tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv, k > 0 ? 1u : ac);
-        } else {
-          const int steps = (pk + 15) / 16;
-          for (int k = 0; k < steps; ++k)
-            tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv, k > 0 ? 1u : ac);
+            for (int k = 0; k < kN / 16; ++k)
+              tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv,
+                                      k > 0 ? 1u : ac);
+          } else {
+            const int steps = (pk + 15) / 16;
+            for (int k = 0; k < steps; ++k)
+              tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv,
+                                      k > 0 ? 1u : ac);
+          }
+          if (pend == 0) tc::mma_commit(&sm.empty[pslot]);  // no stream wants the tile any more
         }
-        if (pend == 0) tc::mma_commit(&sm.empty[pslot]);  // no stream wants the tile any more
+        if (next) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * kN * 128 + (k & 3) * 32) / 16;
+            tc::mma_bf16_low(dS, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(&sm.sfull[s]);
+          if (next_last) tc::mma_commit(&sm.empty[slot]);
+        }
       }
       __syncwarp();
-      np ^= 1u << s;
-      acc |= 1u << s;
     };
     int bits = 0, nk = 0;
     bool read = false;  // the unit's descriptor has been read
@@ -502,41 +517,25 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         ok = ok && tc::mbar_wait(&sm.qfull, items & 1u);
         acc = 0u;
       }
-      const uint32_t kd = tc::desc_low(ring_addr + slot * S::kTile, 16);
       if (uact) {
+        if (pend) values();
+        ok = ok && tc::mbar_wait(&sm.full[slot], phase);
 #pragma unroll 1
         for (int s = 0; s < 2; ++s) {
-          if (pend >> s & 1) pv(s);
-          if (s == 0) ok = ok && tc::mbar_wait(&sm.full[slot], phase);
-          if (uact >> s & 1) {
-            tc::tc_fence_after();
-            const uint32_t qd = tc::desc_low(q_addr + s * S::kTile, 16);
-            const uint32_t dS = tmem + s * 128;
-            if (leader && ok) {
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = ((k >> 2) * kN * 128 + (k & 3) * 32) / 16;
-                tc::mma_bf16_low(dS, qd + off, kd + off, idesc_qk, k > 0 ? 1u : 0u);
-              }
-              tc::mma_commit(&sm.sfull[s]);
-              if ((uact >> (s + 1)) == 0) tc::mma_commit(&sm.empty[slot]);
-            }
-            __syncwarp();
-          }
+          products(s, uact >> s & 1, (uact >> (s + 1)) == 0);
           if (s == 0) take(j + 1, false);
         }
         issued = true;
         pend = uact;
         pk = unk;
-        vthere = false;
         pslot = slot + 1 == slots ? 0 : slot + 1;
         pphase = slot + 1 == slots ? phase ^ 1u : phase;
         slot = pslot + 1 == slots ? 0 : pslot + 1;
         phase = pslot + 1 == slots ? pphase ^ 1u : pphase;
       }
       if (ubits & kLast) {
-        for (int s = 0; s < 2; ++s)
-          if (pend >> s & 1) pv(s);
+        if (pend) values();
+        for (int s = 0; s < 2; ++s) products(s, false, false);
         if (leader && ok) tc::mma_commit(&sm.odone);
         __syncwarp();
         ++items;
@@ -705,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         tc::tmem_st32u(tS + half * 64, pk);
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.pready[s][half]);
+        if (lane == 0) tc::mbar_arrive(&sm.pready[s]);
         started = true;
       }
       __syncwarp();
