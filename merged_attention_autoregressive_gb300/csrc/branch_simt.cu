@@ -1,6 +1,6 @@
 // fastar_branch_attention on the FP32 pipes.
 //
-// One CTA of 256 threads walks its run of units (branch.cuh), 64 query rows
+// One CTA of 256 threads (and a warp that walks) takes its run of units (branch.cuh), 64 query rows
 // by 64 keys at a time: the scores of a unit (4 x 4 per thread), one pass of
 // the running softmax, and the product with the values (4 rows x D/16
 // columns per thread, O in registers).  Scores, statistics, probabilities and
@@ -17,16 +17,34 @@ namespace {
 constexpr int kTM = 64, kTN = 64, kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// (a0, a1) += (x0 y0, x1 y1), one instruction, each as fmaf rounds it.
+__device__ __forceinline__ void fma_pair(float& a0, float& a1, float x0, float x1, float y0, float y1) {
+  asm("{\n\t.reg .b64 a, x, y;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "fma.rn.f32x2 a, x, y, a;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // relative error about 2^-22
+  return y;
+}
+
 template <int D>
 struct SimtSmem {
   float Q[kTM][D + 4];
   float K[kTN][D + 4];  // then the probabilities [kTM][kTN + 4]
   float V[kTN][D];
   float bias[kTN];
+  BranchUnit unit;  // flag 8: none, the run is over
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, int32_t* st) {
+__global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArgs a, int32_t* st) {
   branch_touch(a, st);
   pdl_wait();
   extern __shared__ uint4 raw[];
@@ -37,29 +55,44 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
   constexpr int VN = 16 / (int)sizeof(T), RV = D / VN;  // vectors per row
   constexpr int OC = D / 16;                            // O columns per thread
   const float scale2 = a.scale * kLog2e;
-  BranchWalk w;
-  // every warp walks for itself; what it writes is the same
-  int count = 0, keys_end = 0;
-  bool opens = false, closes = false;
-  BranchUnit x = {};
-  const bool any = w.start(a, blockIdx.x, st);
+  if (tid >= kThreads) {
+    // the last warp walks the run and describes each unit while the others
+    // finish the one before; it meets them at their four barriers a unit
+    BranchWalk w;
+    int count = 0, keys_end = 0;
+    bool opens = false, closes = false;
+    BranchUnit y = {};
+    bool more = w.start(a, blockIdx.x, st);
+    for (bool begun = false; more; begun = true) {
+      if (count == 0) {
+        more = w.next(a, y, count, keys_end, opens, closes, begun ? 0 : 1);
+        if (!more) break;
+      } else {
+        opens = false;
+        y.k0 += kTN;
+      }
+      --count;
+      y.nk = max(0, min(kTN, keys_end - y.k0));
+      y.flags = (y.flags & 4) | (opens ? 1 : 0) | (closes && count == 0 ? 2 : 0);
+      if (tid == kThreads) sm.unit = y;
+      for (int i = 0; i < 4; ++i) __syncthreads();
+    }
+    if (tid == kThreads) {
+      sm.unit.flags = 8;
+      if (!a.by_item) a.cuts[blockIdx.x] = w.cut(a);
+    }
+    __syncthreads();
+    pdl_trigger();
+    return;
+  }
   const int rows = a.cu[a.B] * a.g;
   float m[4], l[4], o[4][OC];
   bool bad = false;
-  bool first_stretch = true;
-  while (any) {
-    if (count == 0) {
-      if (!w.next(a, x, count, keys_end, opens, closes, first_stretch ? 1 : 0)) break;
-      first_stretch = false;
-    } else {
-      opens = false;
-      x.k0 += kTN;
-    }
-    --count;
-    x.nk = max(0, min(kTN, keys_end - x.k0));
-    x.flags = (x.flags & 4) | (opens ? 1 : 0) | (closes && count == 0 ? 2 : 0);
+  while (true) {
+    __syncthreads();  // the unit is described; the previous one's products are done with K, V, P and Q
+    const BranchUnit x = sm.unit;
+    if (x.flags & 8) break;
     const int r0 = x.t * kTM;
-    __syncthreads();  // the previous unit's products are done with K, V, P and Q
     if (x.flags & 1) {
       for (int e = tid; e < kTM * RV; e += kThreads) {
         const int r = e / RV, c = e % RV;
@@ -129,6 +162,12 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+    // two channels at a time: even and odd channels have a sum each
+    float s1[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s1[i][j] = 0.f;
 #pragma unroll 4
     for (int k = 0; k < D; k += 4) {
       float4 qv[4], kv[4];
@@ -140,10 +179,8 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
-          s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
-          s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
-          s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+          fma_pair(s[i][j], s1[i][j], qv[i].x, qv[i].y, kv[j].x, kv[j].y);
+          fma_pair(s[i][j], s1[i][j], qv[i].z, qv[i].w, kv[j].z, kv[j].w);
         }
     }
     __syncthreads();  // K has been read: its buffer takes the probabilities
@@ -155,18 +192,18 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = tx + 16 * j;
-        s[i][j] = c < seen ? fmaf(s[i][j], scale2, sm.bias[c]) : -INFINITY;
+        s[i][j] = c < seen ? fmaf(s[i][j] + s1[i][j], scale2, sm.bias[c]) : -INFINITY;
         top = fmaxf(top, s[i][j]);
       }
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       const float mn = fmaxf(m[i], top);
       const float base = mn == -INFINITY ? 0.f : mn;
-      const float alpha = exp2f(m[i] - base);
+      const float alpha = ex2(m[i] - base);
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float p = exp2f(s[i][j] - base);
+        const float p = ex2(s[i][j] - base);
         sum += p;
         P[ty * 4 + i][tx + 16 * j] = p;
       }
@@ -191,10 +228,8 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
-            o[i][4 * c] = fmaf(p, v.x, o[i][4 * c]);
-            o[i][4 * c + 1] = fmaf(p, v.y, o[i][4 * c + 1]);
-            o[i][4 * c + 2] = fmaf(p, v.z, o[i][4 * c + 2]);
-            o[i][4 * c + 3] = fmaf(p, v.w, o[i][4 * c + 3]);
+            fma_pair(o[i][4 * c], o[i][4 * c + 1], p, p, v.x, v.y);
+            fma_pair(o[i][4 * c + 2], o[i][4 * c + 3], p, p, v.z, v.w);
           }
         }
       }
@@ -226,7 +261,6 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
       }
     }
   }
-  if (tid == 0 && !a.by_item) a.cuts[blockIdx.x] = w.cut(a);
   if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
   pdl_trigger();
 }
@@ -236,7 +270,7 @@ int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
   constexpr int smem = (int)sizeof(SimtSmem<D>);
   auto kernel = branch_simt_kernel<T, D>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-      launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, a, st) != cudaSuccess) {
+      launch_pdl(kernel, dim3(a.G), dim3(kThreads + 32), smem, s, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
   }
