@@ -10,6 +10,7 @@
 #include <math.h>
 
 #include "branch.cuh"
+#include "tc.cuh"
 
 namespace fastar {
 namespace {
@@ -34,77 +35,133 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 64 channels leave room for a second stage of keys and values, filled while
+// the unit before is computed.
 template <int D>
 struct SimtSmem {
+  static constexpr int kStages = D == 64 ? 2 : 1;
   float Q[kTM][D + 4];
-  float K[kTN][D + 4];  // then the probabilities [kTM][kTN + 4]
-  float V[kTN][D];
-  float bias[kTN];
-  BranchUnit unit;  // flag 8: none, the run is over
+  float K[kStages][kTN][D + 4];  // a stage's keys, then its unit's probabilities [kTM][kTN + 4]
+  float V[kStages][kTN][D];
+  float bias[kStages][kTN];
+  BranchUnit unit[2];  // flag 8: none, the run is over; flag 16: every row sees every one of the 64 keys
 };
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArgs a, int32_t* st) {
   branch_touch(a, st);
   pdl_wait();
   extern __shared__ uint4 raw[];
   SimtSmem<D>& sm = *reinterpret_cast<SimtSmem<D>*>(raw);
-  float(*P)[kTN + 4] = reinterpret_cast<float(*)[kTN + 4]>(&sm.K[0][0]);
   if (block_status_bad(st)) return;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  constexpr int VN = 16 / (int)sizeof(T), RV = D / VN;  // vectors per row
+  constexpr int VN = 4, RV = D / VN;  // vectors per row
+  constexpr int kStages = SimtSmem<D>::kStages;
   constexpr int OC = D / 16;                            // O columns per thread
   const float scale2 = a.scale * kLog2e;
   if (tid >= kThreads) {
-    // the last warp walks the run and describes each unit while the others
-    // finish the one before; it meets them at their four barriers a unit
+    // the last warp walks the run and describes each unit one ahead of its
+    // use; it meets the others at their four barriers a unit
     BranchWalk w;
-    int count = 0, keys_end = 0;
-    bool opens = false, closes = false;
+    int count = 0, keys_end = 0, full_keys = 0;
+    bool opens = false, closes = false, begun = false;
     BranchUnit y = {};
     bool more = w.start(a, blockIdx.x, st);
-    for (bool begun = false; more; begun = true) {
-      if (count == 0) {
+    const int rows = a.cu[a.B] * a.g;
+    for (int n = 0;; ++n) {
+      if (more && count == 0) {
         more = w.next(a, y, count, keys_end, opens, closes, begun ? 0 : 1);
-        if (!more) break;
-      } else {
+        begun = true;
+        // keys that every row of the item sees: those of its first token,
+        // where the item belongs to one branch
+        const int r0 = y.t * kTM;
+        full_keys = keys_end;
+        if (more && y.branch >= 0)
+          full_keys = y.lo * a.g <= r0 && (y.lo + y.n) * a.g >= min(r0 + kTM, rows)
+                          ? branch_limit(r0 / a.g - y.lo, y.n, y.len, a.block)
+                          : 0;
+      } else if (more) {
         opens = false;
         y.k0 += kTN;
       }
       --count;
       y.nk = max(0, min(kTN, keys_end - y.k0));
-      y.flags = (y.flags & 4) | (opens ? 1 : 0) | (closes && count == 0 ? 2 : 0);
-      if (tid == kThreads) sm.unit = y;
-      for (int i = 0; i < 4; ++i) __syncthreads();
+      y.flags = !more ? 8
+                      : (y.flags & 4) | (opens ? 1 : 0) | (closes && count == 0 ? 2 : 0) |
+                            (y.nk == kTN && y.k0 + kTN <= full_keys ? 16 : 0);
+      if (tid == kThreads) sm.unit[n & 1] = y;
+      if (n > 0)
+        for (int i = 0; i < 4; ++i) __syncthreads();
+      if (!more) {
+        if (n == 0) __syncthreads();
+        break;
+      }
     }
-    if (tid == kThreads) {
-      sm.unit.flags = 8;
-      if (!a.by_item) a.cuts[blockIdx.x] = w.cut(a);
-    }
-    __syncthreads();
+    if (tid == kThreads && !a.by_item) a.cuts[blockIdx.x] = w.cut(a);
     pdl_trigger();
     return;
   }
   const int rows = a.cu[a.B] * a.g;
   float m[4], l[4], o[4][OC];
   bool bad = false;
-  while (true) {
-    __syncthreads();  // the unit is described; the previous one's products are done with K, V, P and Q
-    const BranchUnit x = sm.unit;
-    if (x.flags & 8) break;
-    const int r0 = x.t * kTM;
+  // a unit's keys and values, straight into their stage; its biases
+  auto load = [&](int n) {
+    const BranchUnit& x = sm.unit[n & 1];
+    const int g = kStages == 2 ? n & 1 : 0;
+    for (int e = tid; e < kTN * RV; e += kThreads) {
+      const int r = e / RV, c = e % RV;
+      const float *kp = (const float*)a.q, *vp = kp;
+      uint32_t bytes = 0;
+      if (r < x.nk) {
+        size_t at = 0;
+        bool ok = true;
+        if (x.branch < 0) {
+          at = (size_t)x.h * a.C + x.k0 + r;
+        } else {
+          const int pos = x.k0 + r;
+          const int id = a.table[(size_t)x.branch * a.max_pages + (pos >> a.page_shift)];
+          ok = id >= 0 && id < a.n_pages;
+          at = (((size_t)id * a.H + x.h) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+        }
+        if (ok) {
+          kp = (const float*)(x.branch < 0 ? a.pK : a.K) + at * D + c * VN;
+          vp = (const float*)(x.branch < 0 ? a.pV : a.V) + at * D + c * VN;
+          bytes = 16;
+        } else {
+          bad = true;
+        }
+      }
+      tc::cp_async16(tc::smem_u32(&sm.K[g][r][c * VN]), kp, bytes);
+      tc::cp_async16(tc::smem_u32(&sm.V[g][r][c * VN]), vp, bytes);
+    }
+    tc::cp_async_commit();
+    if (tid < kTN) {
+      float b = 0.f;
+      if (x.branch < 0 && a.m && tid < x.nk) {
+        const int c = a.m[(size_t)x.h * a.C + x.k0 + tid];
+        b = c > 0 ? log2f((float)c) : -INFINITY;
+      }
+      sm.bias[g][tid] = b;
+    }
+  };
+  __syncthreads();
+  bool last = sm.unit[0].flags & 8;
+  for (int n = 0; !last; ++n) {
+    if (n > 0) __syncthreads();  // the next unit is described; the products of the one before are done
+    const BranchUnit x = sm.unit[n & 1];
+    last = sm.unit[(n + 1) & 1].flags & 8;
+    const int r0 = x.t * kTM, g = kStages == 2 ? n & 1 : 0;
+    if (kStages == 1 || n == 0) load(n);
+    if (kStages == 2 && !last) load(n + 1);
     if (x.flags & 1) {
       for (int e = tid; e < kTM * RV; e += kThreads) {
         const int r = e / RV, c = e % RV;
-        float v[VN];
-#pragma unroll
-        for (int i = 0; i < VN; ++i) v[i] = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r0 + r < rows) {
           const size_t at = (size_t)(x.h * a.g + (int)((r0 + r) % a.g)) * a.N + (size_t)((r0 + r) / a.g);
-          ld_vec<T, VN>((const T*)a.q + at * D + c * VN, v);
+          v = *reinterpret_cast<const float4*>((const float*)a.q + at * D + c * VN);
         }
-#pragma unroll
-        for (int i = 0; i < VN; ++i) sm.Q[r][c * VN + i] = v[i];
+        *reinterpret_cast<float4*>(&sm.Q[r][c * VN]) = v;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -114,48 +171,11 @@ __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArg
         for (int d = 0; d < OC; ++d) o[i][d] = 0.f;
       }
     }
-    for (int e = tid; e < kTN * RV; e += kThreads) {
-      const int r = e / RV, c = e % RV;
-      float k[VN], v[VN];
-#pragma unroll
-      for (int i = 0; i < VN; ++i) k[i] = v[i] = 0.f;
-      if (r < x.nk) {
-        const T *kp, *vp;
-        bool ok = true;
-        size_t at;
-        if (x.branch < 0) {
-          at = (size_t)x.h * a.C + x.k0 + r;
-          kp = (const T*)a.pK;
-          vp = (const T*)a.pV;
-        } else {
-          const int pos = x.k0 + r;
-          const int id = a.table[(size_t)x.branch * a.max_pages + (pos >> a.page_shift)];
-          ok = id >= 0 && id < a.n_pages;
-          at = (((size_t)id * a.H + x.h) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-          kp = (const T*)a.K;
-          vp = (const T*)a.V;
-        }
-        if (ok) {
-          ld_vec<T, VN>(kp + at * D + c * VN, k);
-          ld_vec<T, VN>(vp + at * D + c * VN, v);
-        } else {
-          bad = true;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < VN; ++i) {
-        sm.K[r][c * VN + i] = k[i];
-        sm.V[r][c * VN + i] = v[i];
-      }
-    }
-    if (tid < kTN) {
-      float b = 0.f;
-      if (x.branch < 0 && a.m && tid < x.nk) {
-        const int c = a.m[(size_t)x.h * a.C + x.k0 + tid];
-        b = c > 0 ? log2f((float)c) : -INFINITY;
-      }
-      sm.bias[tid] = b;
-    }
+    if (kStages == 2 && !last)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+      tc::cp_async_wait_all();
+    float(*P)[kTN + 4] = reinterpret_cast<float(*)[kTN + 4]>(&sm.K[g][0][0]);
     __syncthreads();
     float s[4][4];
 #pragma unroll
@@ -174,7 +194,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArg
 #pragma unroll
       for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sm.Q[ty * 4 + i][k]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.K[tx + 16 * j][k]);
+      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.K[g][tx + 16 * j][k]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -187,12 +207,12 @@ __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArg
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + ty * 4 + i;
-      const int seen = r < rows ? branch_row_keys(a, x, r) : 0;
+      const int seen = x.flags & 16 ? kTN : r < rows ? branch_row_keys(a, x, r) : 0;
       float top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = tx + 16 * j;
-        s[i][j] = c < seen ? fmaf(s[i][j] + s1[i][j], scale2, sm.bias[c]) : -INFINITY;
+        s[i][j] = c < seen ? fmaf(s[i][j] + s1[i][j], scale2, sm.bias[g][c]) : -INFINITY;
         top = fmaxf(top, s[i][j]);
       }
 #pragma unroll
@@ -224,7 +244,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArg
       for (int c = 0; c < OC / 4; ++c) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const float4 v = *reinterpret_cast<const float4*>(&sm.V[k + kk][tx * 4 + 64 * c]);
+          const float4 v = *reinterpret_cast<const float4*>(&sm.V[g][k + kk][tx * 4 + 64 * c]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
@@ -248,7 +268,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArg
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = o[i][4 * c + e] * inv;
-            st_vec<T, 4>((T*)a.out + at * D + tx * 4 + 64 * c, v);
+            st_vec<float, 4>((float*)a.out + at * D + tx * 4 + 64 * c, v);
           }
           if (a.lse && tx == 0) a.lse[at] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
         } else {
@@ -265,10 +285,10 @@ __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArg
   pdl_trigger();
 }
 
-template <typename T, int D>
+template <int D>
 int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
   constexpr int smem = (int)sizeof(SimtSmem<D>);
-  auto kernel = branch_simt_kernel<T, D>;
+  auto kernel = branch_simt_kernel<D>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
       launch_pdl(kernel, dim3(a.G), dim3(kThreads + 32), smem, s, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -281,7 +301,7 @@ int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
 }  // namespace
 
 int launch_branch_simt(const BranchArgs& a, int32_t* st, cudaStream_t s) {
-  return a.D == 128 ? launch_t<float, 128>(a, st, s) : launch_t<float, 64>(a, st, s);
+  return a.D == 128 ? launch_t<128>(a, st, s) : launch_t<64>(a, st, s);
 }
 
 }  // namespace fastar
