@@ -125,58 +125,54 @@ __global__ void __launch_bounds__(kJoinThreads) branch_combine_kernel(BranchArgs
     if (x.U < a.G && branch_cut(x.U, j, a.G) == branch_cut(x.U, j + 1, a.G)) return -1;
     return j == c ? x.slot : 2 * j;
   };
-  float m = -INFINITY;
-  for (int k0 = sub; k0 < n; k0 += 16) {
-    float2 ml[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int k = k0 + 4 * e, slot = live && k < n ? slot_of(k) : -1;
-      ml[e] = slot >= 0 ? a.pml[(size_t)slot * a.slot_rows + i] : make_float2(-INFINITY, 0.f);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (ml[e].y != 0.f) m = fmaxf(m, ml[e].x);  // a run in which the row saw nothing has sum 0
-  }
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o[16];
+  float m = -INFINITY, l = 0.f, o[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) o[e] = 0.f;
   for (int k0 = sub; k0 < n; k0 += 8) {
-    float wk[2];
+    // two partials at a time, their statistics and columns in one round trip
+    float2 ml[2];
     float4 p[2][4];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int k = k0 + 4 * q, slot = live && k < n ? slot_of(k) : -1;
-      wk[q] = 0.f;
+      ml[q] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) p[q][e] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (slot >= 0) {
-        const float2 ml = a.pml[(size_t)slot * a.slot_rows + i];
+        ml[q] = a.pml[(size_t)slot * a.slot_rows + i];
         const float4* po =
             reinterpret_cast<const float4*>(a.po + (size_t)slot * a.slot_rows * a.D) + (size_t)(col / 4) * a.slot_rows + i;
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[q][e] = po[(size_t)e * a.slot_rows];
-        if (ml.y != 0.f) {
-          wk[q] = exp2f(ml.x - base);
-          l += wk[q] * ml.y;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) p[q][e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
       }
     }
+    const float mn = fmaxf(m, fmaxf(ml[0].y != 0.f ? ml[0].x : -INFINITY, ml[1].y != 0.f ? ml[1].x : -INFINITY));
+    const float nb = mn == -INFINITY ? 0.f : mn, alpha = l == 0.f ? 0.f : exp2f(m - nb);
+    l *= alpha;
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int e = 0; e < 16; ++e) o[e] *= alpha;
+    m = mn;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (ml[q].y == 0.f) continue;  // the row saw nothing in that run
+      const float w = exp2f(ml[q].x - nb);
+      l += w * ml[q].y;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        o[4 * e] = fmaf(wk[q], p[q][e].x, o[4 * e]);
-        o[4 * e + 1] = fmaf(wk[q], p[q][e].y, o[4 * e + 1]);
-        o[4 * e + 2] = fmaf(wk[q], p[q][e].z, o[4 * e + 2]);
-        o[4 * e + 3] = fmaf(wk[q], p[q][e].w, o[4 * e + 3]);
+        o[4 * e] = fmaf(w, p[q][e].x, o[4 * e]);
+        o[4 * e + 1] = fmaf(w, p[q][e].y, o[4 * e + 1]);
+        o[4 * e + 2] = fmaf(w, p[q][e].z, o[4 * e + 2]);
+        o[4 * e + 3] = fmaf(w, p[q][e].w, o[4 * e + 3]);
       }
+    }
   }
+  // the four sub-groups on one maximum
+  float top = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+  const float base = top == -INFINITY ? 0.f : top, scale = l == 0.f ? 0.f : exp2f(m - base);
+  l *= scale;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) o[e] *= scale;
   l += __shfl_xor_sync(0xffffffffu, l, 8);
   l += __shfl_xor_sync(0xffffffffu, l, 16);
 #pragma unroll
