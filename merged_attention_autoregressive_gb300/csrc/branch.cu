@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kJoinThreads) branch_combine_kernel(BranchArgs
   // the slot of the item's k-th run, -1 where that run is empty
   auto slot_of = [&](int k) {
     const int j = c + k;
-    if (x.U < a.G && branch_cut(x.U, j, a.G) == branch_cut(x.U, j + 1, a.G)) return -1;
+    if (x.empty(a, j)) return -1;
     return j == c ? x.slot : 2 * j;
   };
   float m = -INFINITY, l = 0.f, o[16];

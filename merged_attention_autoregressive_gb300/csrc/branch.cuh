@@ -121,14 +121,17 @@ struct BranchPlace {
       return;
     }
     bool ok = true;
+    sum = 0;
     const int size0 = a.size && lane < a.H ? a.size[lane] : a.C;  // on its way with the lengths
     int used = 0, t0[kLaneTiles], t1[kLaneTiles];
 #pragma unroll
     for (int e = 0; e < kLaneTiles; ++e) {
       const int t = lane + 32 * e;
       pages[e] = 0;
-      t0[e] = t < a.ntiles ? tile_begin(a, t) : 0x7fffffff;
-      t1[e] = t < a.ntiles ? tile_end(a, t) : 0;
+      if (a.ntiles > kFewTiles) {
+        t0[e] = t < a.ntiles ? tile_begin(a, t) : 0x7fffffff;
+        t1[e] = t < a.ntiles ? tile_end(a, t) : 0;
+      }
     }
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + lane;
@@ -141,7 +144,9 @@ struct BranchPlace {
         if (!ok) hi = lo = 0;
       }
       used = max(used, hi);
-      if (a.ntiles <= kFewTiles) {
+      if (a.ntiles == 1) {
+        if (hi > lo) sum += (branch_limit(hi - 1 - lo, hi - lo, len, a.block) + a.TN - 1) / a.TN;
+      } else if (a.ntiles <= kFewTiles) {
         // a branch per lane, the tiles one after the other
         for (int t = 0; t < a.ntiles; ++t) {
           const int last = min(hi, tile_end(a, t)) - 1;
@@ -163,15 +168,21 @@ struct BranchPlace {
         }
       }
     }
-    nt = (__reduce_max_sync(0xffffffffu, used) * a.g + a.TM - 1) / a.TM;
-    sum = 0;
+    used = __reduce_max_sync(0xffffffffu, used);
+    // an item over nothing still has a unit, to be written
+    if (a.ntiles == 1) {
+      nt = used > 0 ? 1 : 0;
+      sum = max(1, __reduce_add_sync(0xffffffffu, sum));
+    } else {
+      nt = (used * a.g + a.TM - 1) / a.TM;
+      sum = 0;
 #pragma unroll
-    for (int e = 0; e < kLaneTiles; ++e) {
-      // an item over nothing still has a unit, to be written
-      pages[e] = lane + 32 * e < nt ? max(1, pages[e]) : 0;
-      sum += pages[e];
+      for (int e = 0; e < kLaneTiles; ++e) {
+        pages[e] = lane + 32 * e < nt ? max(1, pages[e]) : 0;
+        sum += pages[e];
+      }
+      sum = __reduce_add_sync(0xffffffffu, sum);
     }
-    sum = __reduce_add_sync(0xffffffffu, sum);
     U = 0;
     for (int h0 = 0; h0 < a.H; h0 += 32) {
       const int h = h0 + lane;
@@ -190,6 +201,7 @@ struct BranchPlace {
   // Page units of row tile t.
   __device__ __forceinline__ int pages_of(const BranchArgs& a, int t) const {
     if (a.planned) return (int)(a.tile[t + 1] - a.tile[t]);
+    if (a.ntiles == 1) return sum;
     int v = 0;
 #pragma unroll
     for (int e = 0; e < kLaneTiles; ++e) {
@@ -273,8 +285,19 @@ struct BranchCut {
   int h, t;        // h = -1: none
   int run, last;   // the runs that begin and finish it
   int slot;        // the partial of the first; the later runs have slot 2 j
+  int parts, len;  // the item's own equal parts of its len units; 0: cut with the rest
   long long U;
+
+  // Whether run j has no unit.
+  __device__ __forceinline__ bool empty(const BranchArgs& a, int j) const {
+    if (parts) return part(len, j % parts, parts) == part(len, j % parts + 1, parts);
+    return U < a.G && branch_cut(U, j, a.G) == branch_cut(U, j + 1, a.G);
+  }
+  // First unit of part p of n <= 304 of an item of len < 2^23 units.
+  static __device__ __forceinline__ int part(int len, int p, int n) { return (unsigned)len * (unsigned)p / (unsigned)n; }
 };
+
+constexpr int kTwoItems = 4;
 
 // Walks the units of run c, a whole warp in step, a stretch of units of one
 // branch (or of the prefix) at a time.
@@ -283,7 +306,8 @@ struct BranchWalk {
   int h, t, c, left;               // item; run; units left in the run
   int off, units, from;            // next unit of the item, its units, the first one in this run
   int P, size;                     // units and rows of the prefix
-  long long end;                   // end of the run
+  int parts;                       // parts of each item; 0: an even cut of all units
+  long long end;                   // even cut: end of the run
   int T0, T1;
   bool head_item;                  // the run's first item
   bool whole;
@@ -307,17 +331,15 @@ struct BranchWalk {
     total = __shfl_sync(0xffffffffu, incl, 31);
   }
   __device__ __forceinline__ void enter(const BranchArgs& a, int at) {
-    const int rows = a.cu[a.B] * a.g;
-    const int r0 = t * a.TM, r1 = min(r0 + a.TM, rows);
-    T0 = r0 / a.g;
-    T1 = (r1 + a.g - 1) / a.g;
+    const int tokens = a.cu[a.B];
+    T0 = a.ntiles > 1 ? tile_begin(a, t) : 0;
+    T1 = a.ntiles > 1 ? min(tokens, tile_end(a, t)) : tokens;
     size = prefix_size(a, h);
     P = prefix_units(size, a.TN);
     units = P + place.pages_of(a, t);
     off = from = at;
     whole = at == 0 && units <= left;
-    // the join's record of an item that this run begins
-    if (at == 0 && a.by_item && (threadIdx.x & 31) == 0) a.cuts[h * a.ntiles + t] = cut(a);
+
     // first branch with tokens at or behind T0 (empty ones contribute nothing)
     bbase = a.ntiles > 1 ? max(0, warp_count_le(a.cu, a.B, T0) - 1) : 0;
     before = 0;
@@ -336,6 +358,27 @@ struct BranchWalk {
         for (int i = threadIdx.x & 31; i < a.H * a.ntiles; i += 32) a.cuts[i].h = -1;
       return false;
     }
+    // Few items: each in the same number of equal parts, when that makes a run
+    // at most kTwoItems units longer than an even cut of all units would.  An
+    // even cut gives some runs the end of an item and the begin of the next,
+    // and the queries, first softmax and output of two items cost that much
+    // more (4 branches of one token, 12 heads, 28 units each: the last CTA ends
+    // after 14.0 us, 13.0 us in parts).
+    parts = 0;
+    if (a.by_item && !a.whole && a.ntiles == 1) {
+      const int items = a.H, n = a.G / items;
+      if (U < (1 << 23) && (unsigned)U / (unsigned)(items * n) <= (unsigned)U / (unsigned)a.G + kTwoItems) parts = n;
+    }
+    if (parts) {
+      h = c / parts;
+      t = 0;
+      if (h >= a.H) return false;
+      const int len = prefix_units(prefix_size(a, h), a.TN) + place.pages_of(a, t);
+      const int u0 = BranchCut::part(len, c % parts, parts);
+      left = BranchCut::part(len, c % parts + 1, parts) - u0;
+      if (left > 0) enter(a, u0);
+      return left > 0;
+    }
     long long u = branch_cut(U, c, a.G), first = u;
     end = branch_cut(U, c + 1, a.G);
     if (a.whole && end < U) {
@@ -348,17 +391,23 @@ struct BranchWalk {
     if (left > 0) enter(a, (int)(u - first));
     return left > 0;
   }
+  // Writes the join's record of the present item, which the run has begun
+  // (calls of few items; any time while the walk is there), or of the run.
+  __device__ __forceinline__ void record(const BranchArgs& a, bool run) const {
+    if (run == (a.by_item != 0) || (threadIdx.x & 31) || (!run && from != 0)) return;
+    a.cuts[run ? c : h * a.ntiles + t] = cut(a);
+  }
   // The join's record of the present item: a run that begins an item and does
   // not finish it names the run that does.
   __device__ __forceinline__ BranchCut cut(const BranchArgs& a) const {
-    BranchCut x = {-1, 0, 0, 0, 0, place.U};
+    BranchCut x = {-1, 0, 0, 0, 0, parts, units, place.U};
     if (from == 0 && units - off > left) {
       x.h = h;
       x.t = t;
       x.run = c;
       x.slot = 2 * c + (head_item ? 0 : 1);
       const long long last = end - left - off + units, U = place.U;  // one behind the item's last unit
-      x.last = U < (1 << 23) ? (int)(((unsigned)last * (unsigned)a.G - 1) / (unsigned)U) : (int)((last * a.G - 1) / U);
+      x.last = parts ? c / parts * parts + parts - 1 : U < (1 << 23) ? (int)(((unsigned)last * (unsigned)a.G - 1) / (unsigned)U) : (int)((last * a.G - 1) / U);
     }
     return x;
   }

@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArg
                       : (y.flags & 4) | (opens ? 1 : 0) | (closes && count == 0 ? 2 : 0) |
                             (y.nk == kTN && y.k0 + kTN <= full_keys ? 16 : 0);
       if (tid == kThreads) sm.unit[n & 1] = y;
+      if (more && opens) w.record(a, false);
       if (n > 0)
         for (int i = 0; i < 4; ++i) __syncthreads();
       if (!more) {
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArg
         break;
       }
     }
-    if (tid == kThreads && !a.by_item) a.cuts[blockIdx.x] = w.cut(a);
+    w.record(a, true);
     pdl_trigger();
     return;
   }

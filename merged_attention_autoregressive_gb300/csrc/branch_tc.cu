@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     tc::prefetch_tensormap(&mapPV);
   }
   pdl_wait();
-  const bool stopped = status_bad(st);  // on its way while the CTA is set up
+  const bool stopped = warp == kIssuer + 1 && status_bad(st);
   if (tid == 0 && (tc::smem_u32(sm.tiles) & 1023u)) status_set(st, FASTAR_ERR_CUDA);
   // the loader finds the run's place while the others set the CTA up
   BranchWalk w;
@@ -280,9 +280,10 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           }
         }
         x.k0 += kN;
+        if (opens && i == 0) w.record(a, false);
       }
     }
-    if (lane == 0 && !a.by_item) a.cuts[blockIdx.x] = w.cut(a);
+    w.record(a, true);
     // no unit: the end of the run
     if (ok) {
       const int ds = j % S::kRing;

@@ -13,9 +13,10 @@ from types import SimpleNamespace
 
 import torch
 
-from . import (Cache, OP_ANNCA, OP_ANNSA, OP_ANNSA_PARTS, OP_MERGE, fastar_annca_attention, fastar_annca_prune,
-               fastar_annsa_attention, fastar_annsa_attention_part, fastar_annsa_combine, fastar_bucket_csr,
-               fastar_hash, fastar_hash_many, fastar_tempcache_merge, fastar_workspace_size)
+from . import (Cache, OP_ANNCA, OP_ANNSA, OP_ANNSA_PARTS, OP_MERGE, PagedKV, Prefix, branch_workspace_size,
+               fastar_annca_attention, fastar_annca_prune, fastar_annsa_attention, fastar_annsa_attention_part,
+               fastar_annsa_combine, fastar_branch_attention, fastar_bucket_csr, fastar_hash, fastar_hash_many,
+               fastar_page_append, fastar_tempcache_merge, fastar_workspace_size)
 
 DENSE_FRAC = 0.3  # sparse attention is off for this share of a chunk's denoising steps
 
@@ -307,6 +308,14 @@ class ChunkPath:
         self._dn = dn
         return dn
 
+    # -- branches ------------------------------------------------------------
+    def branches(self, B, tokens, max_len, **kw):
+        """B rollouts that continue this layer's merged history (its cache is
+        read, not written): a BranchRollout over the live groups with their
+        + ln m.  Arguments as for BranchRollout."""
+        return BranchRollout(B, self.H, self.D, tokens, max_len, prefix=Prefix.of(self.cache),
+                             dtype=self.dtype, device=self.q_codes.device, **kw)
+
     # -- internals ----------------------------------------------------------
     @staticmethod
     def _main(stream):
@@ -403,3 +412,81 @@ class ChunkStack:
                         dev_in=None if dev_in is None else dev_in[i], join=False)
         for p in self.paths:
             p.join_outputs(stream)
+
+
+class BranchRollout:
+    """B rollouts ("branches") of one layer that continue one history.
+
+    The history is a prefix that every branch attends (a Prefix, e.g. a merged
+    cache; None: none); each branch's own keys and values lie in pages of a
+    pool.  `step` adds tokens to the branches and attends: it rotates the new
+    queries and keys, puts keys and values into the pages and runs the
+    attention of all branches over the prefix and their pages.  Page ids and
+    lengths are counted on the host and copied to the device by `extend`;
+    `step` itself can be captured in a graph between two `extend`s.
+
+    tokens: most tokens of one step, all branches together; max_len: most
+    positions of a branch; Hq: query heads (a multiple of H, default H); plan:
+    RopePlan (None: queries and keys are taken as they are); block: 0, every
+    new token sees all positions of its branch, or n, those of its own and
+    earlier blocks of n positions (a frame's tokens, 1 for text)."""
+
+    def __init__(self, B, H, D, tokens, max_len, prefix=None, Hq=None, page=64, n_pages=None, plan=None, block=0,
+                 scale=None, dtype=torch.bfloat16, device="cuda"):
+        dev = torch.device(device)
+        most = -(-max_len // page)
+        self.B, self.H, self.D, self.Hq, self.max_len, self.tokens = B, H, D, Hq or H, max_len, tokens
+        self.prefix, self.plan, self.block = prefix, plan, block
+        self.scale = D ** -0.5 if scale is None else scale
+        self.pages = PagedKV(H, D, page, n_pages or B * most, B, most, dtype, dev)
+        self.cu = torch.zeros(B + 1, dtype=torch.int32, device=dev)
+        self.q = torch.zeros(self.Hq, tokens, D, dtype=dtype, device=dev)  # rotated queries
+        self.out = torch.zeros(self.Hq, tokens, D, dtype=dtype, device=dev)
+        self.lse = torch.zeros(self.Hq, tokens, dtype=torch.float32, device=dev)
+        self.ws = torch.empty(branch_workspace_size(self.Hq, H, tokens, D), dtype=torch.uint8, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.lengths = [0] * B
+        self.held = [[] for _ in range(B)]           # page ids of each branch
+        self.free = list(range(self.pages.n_pages))[::-1]
+
+    def extend(self, new):
+        """Make room for new[b] more positions of each branch: the next step's
+        tokens, laid out branch after branch."""
+        if len(new) != self.B or any(n < 0 for n in new) or sum(new) > self.tokens:
+            raise ValueError("one count of new tokens per branch, at most `tokens` in all")
+        lengths = [a + n for a, n in zip(self.lengths, new)]
+        if max(lengths, default=0) > self.max_len:
+            raise ValueError("a branch is longer than max_len")
+        page = self.pages.page
+        need = [-(-a // page) - len(h) for a, h in zip(lengths, self.held)]
+        if sum(need) > len(self.free):
+            raise ValueError("no pages left")
+        for h, n in zip(self.held, need):
+            h.extend(self.free.pop() for _ in range(n))
+        self.lengths = lengths
+        most = self.pages.max_pages
+        offsets = [0]
+        for n in new:
+            offsets.append(offsets[-1] + n)
+        i32 = dict(dtype=torch.int32)
+        self.pages.table.copy_(torch.tensor([h + [0] * (most - len(h)) for h in self.held], **i32).view(self.B, most))
+        self.pages.len.copy_(torch.tensor(lengths, **i32))
+        self.cu.copy_(torch.tensor(offsets, **i32))
+
+    def release(self, b):
+        """Branch b starts again: its pages return to the pool."""
+        self.free.extend(self.held[b][::-1])
+        self.held[b], self.lengths[b] = [], 0
+
+    def step(self, q, k, v, pos=None, stream=None):
+        """The new tokens of the last `extend`: q [Hq][tokens][D], k, v
+        [H][tokens][D] (any head and token strides; the rows behind the last
+        branch's are ignored), pos [tokens][axes] int32 with a plan.  Returns
+        (out [Hq][tokens][D], lse [Hq][tokens]), buffers of this object."""
+        rotated = self.q if self.plan is not None else q
+        fastar_page_append(self.pages, k, v, self.cu, pos=pos, plan=self.plan,
+                           q=q if self.plan is not None else None, q_out=self.q if self.plan is not None else None,
+                           status=self.status, stream=stream)
+        fastar_branch_attention(rotated, self.cu, self.prefix, self.pages, self.scale, self.out, lse=self.lse,
+                                block=self.block, ws=self.ws, status=self.status, stream=stream)
+        return self.out, self.lse

@@ -494,3 +494,107 @@ def test_two_calls_at_once_with_a_workspace_each(m):
     torch.cuda.synchronize()
     for i, out in enumerate(got):
         assert torch.equal(out, want[i % 2][4])
+
+
+def test_groups_wider_than_a_row_tile(m):
+    """150 query heads share a key/value head: a token's heads lie in two tiles."""
+    q, cu, prefix, pages, cu_h, length, table = _attention_case(m, BF, 64, 1, 150, 16, [3, 2], [20, 33], 70, True, 1,
+                                                                seed=13)
+    _check_attention(m, BF, q, cu, prefix, pages, 0.125, 1, cu_h, length, table)
+
+
+@pytest.mark.parametrize("shape", [
+    # D, H, g, page, new, past, C, counts, block, pad: the ways a call is laid out
+    (128, 8, 1, 64, [520, 300], [100, 900], 20000, True, 260, 7),      # wide items, long runs
+    (64, 4, 2, 128, [700], [64], 16000, False, 0, 0),                  # wide items, D 64
+    (64, 1, 2, 64, [4500], [0], 0, False, 16, 0),                      # more than 64 row tiles: planned
+    (128, 2, 1, 16, [1100] + [0] * 40 + [700], [0] * 42, 0, False, 1, 3),  # many row tiles, short items
+    (64, 1, 1, 16, [9] * 700, [5] * 700, 33, True, 3, 0),              # many tiles and branches: planned
+    (128, 40, 5, 32, [1] * 30, list(range(0, 300, 10)), 260, True, 0, 0),  # two row tiles, more items than CTAs / 2
+])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_branch_attention_layouts(m, shape, dtype):
+    D, H, g, page, new, past, C, counts, block, pad = shape
+    q, cu, prefix, pages, cu_h, length, table = _attention_case(m, dtype, D, H, g, page, new, past, C, counts, block,
+                                                                pad, seed=21)
+    _check_attention(m, dtype, q, cu, prefix, pages, D ** -0.5, block, cu_h, length, table)
+
+
+def test_workspace_and_streams_may_be_left_to_the_call(m):
+    q, cu, prefix, pages, cu_h, length, table = _attention_case(m, BF, 128, 2, 1, 64, [3, 1], [40, 9], 200, False, 0,
+                                                                seed=14)
+    px = m.Prefix(prefix[0], prefix[1])
+    want = torch.zeros_like(q)
+    m.fastar_branch_attention(q, cu, px, pages, 0.1, want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = torch.zeros_like(q)
+    m.fastar_branch_attention(q, cu, px, pages, 0.1, got, stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    got.zero_()
+    torch.cuda.synchronize()
+    m.fastar_branch_attention(q, cu, px, pages, 0.1, got, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_branches_of_a_merged_cache(m):
+    """A chunk is merged into the cache; two branches continue it and attend
+    its live groups; a branch that is released starts again on freed pages."""
+    from merged_attention_autoregressive_gb300.path import ChunkPath
+    gen, rng = torch.Generator().manual_seed(30), np.random.default_rng(30)
+    H, D, n_f = 3, 128, 96
+    p = ChunkPath(H, D, n_f, 2, 16, 2, 6, 512, 0.95)
+    p.planes.copy_(_randn(gen, *p.planes.shape))
+    base = torch.randn(H, 1, n_f, D, generator=gen)
+    k = (base + 0.05 * torch.randn(H, 2, n_f, D, generator=gen)).reshape(H, 2 * n_f, D).to(BF).cuda()
+    p.merge(k, _randn(gen, H, 2 * n_f, D), 0)
+    snap = p.cache.snapshot()
+    assert int(p.cache.m.max()) > 1
+    dims = (44, 42, 42)
+    plan, freqs = m.RopePlan(D, dims), O.ladder(dims)
+    roll = p.branches(2, 64, 100, page=16, n_pages=12, plan=plan, block=32, Hq=6)
+    host = [np.zeros((2, H, 100, D)), np.zeros((2, H, 100, D))]
+    lengths = [0, 0]
+    for new in ([32, 32], [1, 0], [32, 20], [1, 1]):
+        if new == [32, 20]:
+            roll.release(1)
+            lengths[1] = 0
+        roll.extend(new)
+        x = _randn(gen, 64, 4 * H, D).transpose(0, 1)
+        pos = torch.randint(0, 9000, (64, 3), generator=gen, dtype=torch.int32).cuda()
+        out, lse = roll.step(x[:2 * H], x[2 * H:3 * H], x[3 * H:], pos)
+        assert int(roll.status) == 0
+        off, ph = np.concatenate(([0], np.cumsum(new))), pos.cpu().numpy()
+        K = np.zeros((2, H, 100, D))
+        for b in range(2):
+            lengths[b] += new[b]
+            for i in range(lengths[b]):
+                at = int(roll.pages.table[b, i // 16])
+                K[b, :, i] = _f64(roll.pages.K[at, :, i % 16])
+                host[1][b, :, i] = _f64(roll.pages.V[at, :, i % 16])
+        turned = O.rope(_f64(x[2 * H:3 * H]), ph, dims, freqs, False)
+        for b in range(2):
+            own = turned[:, off[b]:off[b + 1]]
+            stored = K[b, :, lengths[b] - new[b]:lengths[b]]
+            assert (np.abs(stored - own) <= 2.0 ** -8 * np.abs(own) + 2.0 ** -17).all()
+            # what was there before is still there
+            assert (K[b, :, :lengths[b] - new[b]] == host[0][b, :, :lengths[b] - new[b]]).all()
+        host[0] = K
+        table, pages = np.arange(2)[:, None], (K, host[1])
+        ref, rl, A, X, keys = O.branch_attention(
+            _f64(roll.q), off, (_f64(p.cache.K), _f64(p.cache.V), p.cache.m.cpu().numpy(), p.cache.size.cpu().numpy()),
+            pages[0], pages[1], table, np.array(lengths), roll.scale, 32, bounds=True)
+        n = off[-1]
+        d = (D + 4) * 2.0 ** -23 * X + 2.0 ** -20
+        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 3 * d + keys * 2.0 ** -22)[..., None] * A
+        assert (np.abs(_f64(out) - ref)[:, :n] <= tol[:, :n]).all()
+        assert (np.abs(_f64(lse) - rl)[:, :n] <= (d + keys * 2.0 ** -23 + 2.0 ** -22 * np.abs(rl))[:, :n]).all()
+    for name, t in snap.items():  # the history is read only
+        assert torch.equal(t.view(torch.uint8), getattr(p.cache, name).view(torch.uint8))
+    with pytest.raises(ValueError):
+        roll.extend([64, 0])      # longer than max_len
+    with pytest.raises(ValueError):
+        roll.extend([33, 32])     # more than `tokens`
