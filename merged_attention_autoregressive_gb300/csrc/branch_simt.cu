@@ -1,7 +1,7 @@
 // fastar_branch_attention on the FP32 pipes.
 //
-// One CTA of 256 threads (and a warp that walks) takes its run of units (branch.cuh), 64 query rows
-// by 64 keys at a time: the scores of a unit (4 x 4 per thread), one pass of
+// One CTA of 256 threads takes its run of units (branch.cuh), 64 query rows by
+// 64 keys at a time: the scores of a unit (4 x 4 per thread), one pass of
 // the running softmax, and the product with the values (4 rows x D/16
 // columns per thread, O in registers).  Scores, statistics, probabilities and
 // O are fp32; the row statistics of a thread's 4 rows are joined over the 16
@@ -44,11 +44,14 @@ struct SimtSmem {
   float K[kStages][kTN][D + 4];  // a stage's keys, then its unit's probabilities [kTM][kTN + 4]
   float V[kStages][kTN][D];
   float bias[kStages][kTN];
+  BranchWalk walk[32];  // of warp 0, a lane each: it lives here between units, out of everybody's registers
+  int count, keys_end, full_keys, opens, closes, more;
+  BranchUnit next;
   BranchUnit unit[2];  // flag 8: none, the run is over; flag 16: every row sees every one of the 64 keys
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArgs a, int32_t* st) {
+__global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, int32_t* st) {
   branch_touch(a, st);
   pdl_wait();
   extern __shared__ uint4 raw[];
@@ -59,48 +62,55 @@ __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArg
   constexpr int kStages = SimtSmem<D>::kStages;
   constexpr int OC = D / 16;                            // O columns per thread
   const float scale2 = a.scale * kLog2e;
-  if (tid >= kThreads) {
-    // the last warp walks the run and describes each unit one ahead of its
-    // use; it meets the others at their four barriers a unit
-    BranchWalk w;
-    int count = 0, keys_end = 0, full_keys = 0;
-    bool opens = false, closes = false, begun = false;
-    BranchUnit y = {};
-    bool more = w.start(a, blockIdx.x, st);
-    const int rows = a.cu[a.B] * a.g;
-    for (int n = 0;; ++n) {
-      if (more && count == 0) {
-        more = w.next(a, y, count, keys_end, opens, closes, begun ? 0 : 1);
-        begun = true;
-        // keys that every row of the item sees: those of its first token,
-        // where the item belongs to one branch
-        const int r0 = y.t * kTM;
-        full_keys = keys_end;
-        if (more && y.branch >= 0)
-          full_keys = y.lo * a.g <= r0 && (y.lo + y.n) * a.g >= min(r0 + kTM, rows)
-                          ? branch_limit(r0 / a.g - y.lo, y.n, y.len, a.block)
-                          : 0;
-      } else if (more) {
-        opens = false;
-        y.k0 += kTN;
-      }
-      --count;
-      y.nk = max(0, min(kTN, keys_end - y.k0));
-      y.flags = !more ? 8
-                      : (y.flags & 4) | (opens ? 1 : 0) | (closes && count == 0 ? 2 : 0) |
-                            (y.nk == kTN && y.k0 + kTN <= full_keys ? 16 : 0);
-      if (tid == kThreads) sm.unit[n & 1] = y;
-      if (more && opens) w.record(a, false);
-      if (n > 0)
-        for (int i = 0; i < 4; ++i) __syncthreads();
-      if (!more) {
-        if (n == 0) __syncthreads();
-        break;
-      }
+  // Warp 0 walks the run and describes unit n, one ahead of its use.
+  auto describe = [&](int n) {
+    BranchWalk w = sm.walk[tid];
+    int count = sm.count, keys_end = sm.keys_end, full_keys = sm.full_keys;
+    bool opens = sm.opens, closes = sm.closes, more = sm.more;
+    BranchUnit y = sm.next;
+    __syncwarp();
+    if (more && count == 0) {
+      more = w.next(a, y, count, keys_end, opens, closes, n == 0 ? 1 : 0);
+      // keys that every row of the item sees: those of its first token, where
+      // the item belongs to one branch
+      const int r0 = y.t * kTM;
+      full_keys = keys_end;
+      if (more && y.branch >= 0)
+        full_keys = y.lo * a.g <= r0 && (y.lo + y.n) * a.g >= min(r0 + kTM, a.cu[a.B] * a.g)
+                        ? branch_limit(r0 / a.g - y.lo, y.n, y.len, a.block)
+                        : 0;
+    } else if (more) {
+      opens = false;
+      y.k0 += kTN;
     }
-    w.record(a, true);
-    pdl_trigger();
-    return;
+    --count;
+    y.nk = max(0, min(kTN, keys_end - y.k0));
+    y.flags = !more ? 8
+                    : (y.flags & 4) | (opens ? 1 : 0) | (closes && count == 0 ? 2 : 0) |
+                          (y.nk == kTN && y.k0 + kTN <= full_keys ? 16 : 0);
+    if (more && opens) w.record(a, false);
+    if (!more) w.record(a, true);
+    sm.walk[tid] = w;
+    if (tid == 0) {
+      sm.unit[n & 1] = sm.next = y;
+      sm.count = count;
+      sm.keys_end = keys_end;
+      sm.full_keys = full_keys;
+      sm.opens = opens;
+      sm.closes = closes;
+      sm.more = more;
+    }
+    __syncwarp();
+  };
+  if (tid < 32) {
+    const bool more = sm.walk[tid].start(a, blockIdx.x, st);
+    if (tid == 0) {
+      sm.count = 0;
+      sm.more = more;
+    }
+    __syncwarp();
+    describe(0);
+    if (more) describe(1);
   }
   const int rows = a.cu[a.B] * a.g;
   float m[4], l[4], o[4][OC];
@@ -176,6 +186,10 @@ __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArg
       asm volatile("cp.async.wait_group 1;" ::: "memory");
     else
       tc::cp_async_wait_all();
+    // a warp computes when one of its 8 rows has keys in the unit
+    const int w0 = r0 + (ty & ~1) * 4, lo = x.branch < 0 ? 0 : x.lo * a.g;
+    const int hi = x.branch < 0 ? rows : min(rows, (x.lo + x.n) * a.g);
+    const bool busy = x.nk > 0 && w0 < hi && w0 + 8 > lo;
     float(*P)[kTN + 4] = reinterpret_cast<float(*)[kTN + 4]>(&sm.K[g][0][0]);
     __syncthreads();
     float s[4][4];
@@ -189,68 +203,75 @@ __global__ void __launch_bounds__(kThreads + 32, 2) branch_simt_kernel(BranchArg
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s1[i][j] = 0.f;
+    if (busy) {
 #pragma unroll 4
-    for (int k = 0; k < D; k += 4) {
-      float4 qv[4], kv[4];
+      for (int k = 0; k < D; k += 4) {
+        float4 qv[4], kv[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sm.Q[ty * 4 + i][k]);
+        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sm.Q[ty * 4 + i][k]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.K[g][tx + 16 * j][k]);
+        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.K[g][tx + 16 * j][k]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          fma_pair(s[i][j], s1[i][j], qv[i].x, qv[i].y, kv[j].x, kv[j].y);
-          fma_pair(s[i][j], s1[i][j], qv[i].z, qv[i].w, kv[j].z, kv[j].w);
-        }
+          for (int j = 0; j < 4; ++j) {
+            fma_pair(s[i][j], s1[i][j], qv[i].x, qv[i].y, kv[j].x, kv[j].y);
+            fma_pair(s[i][j], s1[i][j], qv[i].z, qv[i].w, kv[j].z, kv[j].w);
+          }
+      }
     }
     __syncthreads();  // K has been read: its buffer takes the probabilities
+    if (busy) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + ty * 4 + i;
-      const int seen = x.flags & 16 ? kTN : r < rows ? branch_row_keys(a, x, r) : 0;
-      float top = -INFINITY;
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + ty * 4 + i;
+        const int seen = x.flags & 16 ? kTN : r < rows ? branch_row_keys(a, x, r) : 0;
+        float top = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = tx + 16 * j;
-        s[i][j] = c < seen ? fmaf(s[i][j] + s1[i][j], scale2, sm.bias[g][c]) : -INFINITY;
-        top = fmaxf(top, s[i][j]);
+        for (int j = 0; j < 4; ++j) {
+          const int c = tx + 16 * j;
+          s[i][j] = c < seen ? fmaf(s[i][j] + s1[i][j], scale2, sm.bias[g][c]) : -INFINITY;
+          top = fmaxf(top, s[i][j]);
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float mn = fmaxf(m[i], top);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float alpha = ex2(m[i] - base);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = ex2(s[i][j] - base);
+          sum += p;
+          P[ty * 4 + i][tx + 16 * j] = p;
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        m[i] = mn;
+        l[i] = l[i] * alpha + sum;
+#pragma unroll
+        for (int d = 0; d < OC; ++d) o[i][d] *= alpha;
       }
-#pragma unroll
-      for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      const float mn = fmaxf(m[i], top);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float alpha = ex2(m[i] - base);
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = ex2(s[i][j] - base);
-        sum += p;
-        P[ty * 4 + i][tx + 16 * j] = p;
-      }
-#pragma unroll
-      for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      m[i] = mn;
-      l[i] = l[i] * alpha + sum;
-#pragma unroll
-      for (int d = 0; d < OC; ++d) o[i][d] *= alpha;
     }
     __syncthreads();
+    if (tid < 32 && !last) describe(n + 2);  // in the place of this unit, of which everybody has a copy
+    if (busy) {
 #pragma unroll 2
-    for (int k = 0; k < kTN; k += 4) {
-      float4 pv[4];
+      for (int k = 0; k < kTN; k += 4) {
+        float4 pv[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(&P[ty * 4 + i][k]);
+        for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(&P[ty * 4 + i][k]);
 #pragma unroll
-      for (int c = 0; c < OC / 4; ++c) {
+        for (int c = 0; c < OC / 4; ++c) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const float4 v = *reinterpret_cast<const float4*>(&sm.V[g][k + kk][tx * 4 + 64 * c]);
+          for (int kk = 0; kk < 4; ++kk) {
+            const float4 v = *reinterpret_cast<const float4*>(&sm.V[g][k + kk][tx * 4 + 64 * c]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
-            fma_pair(o[i][4 * c], o[i][4 * c + 1], p, p, v.x, v.y);
-            fma_pair(o[i][4 * c + 2], o[i][4 * c + 3], p, p, v.z, v.w);
+            for (int i = 0; i < 4; ++i) {
+              const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
+              fma_pair(o[i][4 * c], o[i][4 * c + 1], p, p, v.x, v.y);
+              fma_pair(o[i][4 * c + 2], o[i][4 * c + 3], p, p, v.z, v.w);
+            }
           }
         }
       }
@@ -291,7 +312,7 @@ int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
   constexpr int smem = (int)sizeof(SimtSmem<D>);
   auto kernel = branch_simt_kernel<D>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-      launch_pdl(kernel, dim3(a.G), dim3(kThreads + 32), smem, s, a, st) != cudaSuccess) {
+      launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
   }
