@@ -620,7 +620,7 @@ int fastar_page_append(const fastar_pages* pages, const void* k, int64_t k_head,
 /*
  * The rows that every branch attends: K, V [H][C][D] dt; size [H] int32 live
  * rows of each head (NULL: C); m [H][C] int32 counts, added as + ln m (NULL:
- * 1 everywhere; m <= 0 hides the row).  A fastar_cache is one: its K, V, m
+ * 1 everywhere; m <= 0 hides the row, which may then hold anything).  A fastar_cache is one: its K, V, m
  * and size.  H * C < 2^31.
  */
 typedef struct {
@@ -648,7 +648,8 @@ typedef struct {
  * once for the tokens of all branches.
  *
  * q [Hq][N][D] dt, out [Hq][N][D] dt, optional lse [Hq][N] float; rows of
- * padding tokens are not written.  prefix NULL: none.  What lies behind
+ * padding tokens are not written.  out must not overlap an input.  prefix
+ * NULL: none.  What lies behind
  * size[h] and behind the positions that a branch sees may hold anything.
  * Values that some token sees must be finite (a hidden value times 0 is
  * added where another token of the call sees it).
@@ -657,7 +658,8 @@ typedef struct {
  * bf16 for the product with the values; scores, statistics and sums are fp32.
  * D in {64, 128}; Hq a multiple of H; N * (Hq / H) < 2^31 - 256.
  * FASTAR_ERR_DEVICE_ARG: cu not ascending within 0..N, a length outside
- * 0..max_pages * page, a size outside 0..C, a page id outside the pool.
+ * 0..max_pages * page, a size outside 0..C, a page id outside the pool,
+ * branches with 2^36 keys and more for one key/value head.
  */
 #define FASTAR_OP_BRANCH 7
 int fastar_branch_attention(fastar_dtype dt, const void* q, int Hq, int N,

@@ -89,8 +89,12 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
     if (h < a.H) a.head[h] = carry + x;
     carry += total;
   }
+  // (bad is false here) more than the walk's integers hold?
+  for (int t = tid; t < nt; t += kPlanThreads) bad = bad || a.tile[t + 1] - a.tile[t] > kMaxUnits;
+  bad = __syncthreads_or(bad || carry > (long long)kMaxUnits * a.G) != 0;
   if (tid == 0) {
-    a.head[a.H] = nt > 0 ? carry : 0;
+    if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
+    a.head[a.H] = nt > 0 && !bad ? carry : 0;
     a.head[a.H + 1] = nt;
   }
   pdl_trigger();
@@ -302,7 +306,8 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   a.G = x.G;
   a.ntiles = x.ntiles;
   a.slot_rows = x.slot_rows;
-  a.planned = a.ntiles > kMaxTiles || (a.ntiles > kFewTiles && a.B > kMaxBranches);
+  const long long units = (a.C + a.TN - 1) / a.TN + a.B * (((long long)a.max_pages << a.page_shift) / a.TN + 1);
+  a.planned = a.ntiles > kMaxTiles || (a.ntiles > kFewTiles && a.B > kMaxBranches) || units > kFewUnits / a.ntiles;
   // Short items (a few microseconds each) are not cut where there are enough
   // of them: the join costs as much as the imbalance (9 ragged prompts of up
   // to 858 keys, 256 items: 24 us, 32 us when cut).

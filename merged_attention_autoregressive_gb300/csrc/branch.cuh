@@ -100,6 +100,8 @@ constexpr int kLaneTiles = 2;               // row tiles per lane of an unplanne
 constexpr int kMaxTiles = 32 * kLaneTiles;  // row tiles, and above kFewTiles of them
 constexpr int kMaxBranches = 32;            // branches, of a call that goes without a plan
 constexpr int kFewTiles = 8;
+constexpr long long kFewUnits = 1 << 26;   // units of 32 heads fit an int: of a head without a plan
+constexpr int kMaxUnits = 1 << 30;         // units of an item, and of a run
 
 // First token of row tile t, and one behind its last.
 __device__ __forceinline__ int tile_begin(const BranchArgs& a, int t) { return t * a.TM / a.g; }
@@ -236,7 +238,7 @@ struct BranchPlace {
     for (int h0 = 0; h0 < a.H; h0 += 32) {
       const int x = h0 + lane;
       const int pu = x < a.H ? prefix_units(prefix_size(a, x), a.TN) : 0;
-      const int v = x < a.H ? pu * nt + sum : 0;  // an unplanned head has far fewer than 2^31 / 32 units
+      const int v = x < a.H ? pu * nt + sum : 0;  // at most kFewUnits
       const int inc = warp_incl_scan(v);
       const unsigned m = __ballot_sync(0xffffffffu, x < a.H && first + inc > u);
       if (m) {

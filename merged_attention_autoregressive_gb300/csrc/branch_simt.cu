@@ -221,6 +221,10 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
       }
     }
     __syncthreads();  // K has been read: its buffer takes the probabilities
+    // a hidden key may hold anything: its values take part with weight 0
+    if (x.branch < 0 && a.m && sm.bias[g][tid >> 2] == -INFINITY)
+      for (int c = tid & 3; c < RV; c += 4)
+        *reinterpret_cast<float4*>(&sm.V[g][tid >> 2][c * VN]) = make_float4(0.f, 0.f, 0.f, 0.f);
     if (busy) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -230,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = tx + 16 * j;
-          s[i][j] = c < seen ? fmaf(s[i][j] + s1[i][j], scale2, sm.bias[g][c]) : -INFINITY;
+          const float bias = sm.bias[g][c];
+          s[i][j] = c < seen && bias != -INFINITY ? fmaf(s[i][j] + s1[i][j], scale2, bias) : -INFINITY;
           top = fmaxf(top, s[i][j]);
         }
 #pragma unroll

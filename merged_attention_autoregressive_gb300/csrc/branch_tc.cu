@@ -1,28 +1,40 @@
 // fastar_branch_attention on the tensor cores (tcgen05 + TMEM, bf16).
 //
 // One persistent CTA per SM walks its run of units (branch.cuh; 128 keys per
-// unit) with three warpgroups:
-//   warps 0-3, 4-7  two softmax streams, one thread per query row;
-//   warp 8          loader: finds the units, describes each in a ring of
-//                   descriptors and fetches its key and value tiles by TMA
-//                   (prefix: two 128-row boxes a tile; pages: a box per page
-//                   and column half, one lane per page) into a ring of tiles;
-//   warps 9, 10     MMA issuers: S_s = Q_s K^T (M 128, N 128, K D) and O_s +=
-//                   P_s V (M 128, N D, K 128; P_s read from TMEM, where the
-//                   softmax wrote it over S_s);
-//   warp 11         only gives its registers away.
-// More than 128 rows of queries per key/value head: an item is 256 rows and
-// stream s owns rows 128 s .. 128 s + 127, so each tile that is fetched feeds
-// four products, and one stream's softmax runs under the other's products.
-// Up to 128 rows: both streams own the same rows and take the units in turn
-// (each with its own O, maximum and sum; joined in TMEM at the item's end),
-// which hides the softmax behind the loads of a memory-bound pass, and the
-// room of the second query tile holds one more key or value tile in flight.
-// A running maximum is only raised (and O in TMEM rescaled) when a unit's
-// exceeds it by more than 2^8, so P stays <= 256 and rescaling is rare.
+// unit):
+//   warps 0-7, 8-15  two softmax streams, two threads per query row: one for
+//                    each half of a unit's keys, in the same TMEM lane;
+//   warp 16          loader: finds the units, describes each in a ring of
+//                    descriptors and fetches its key and value tiles by TMA
+//                    (prefix: a 128-row box per column half; pages: a box per
+//                    page and column half, one lane per page) into a ring;
+//   warps 17, 18     MMA issuers: S_s = Q_s K^T (M 128, N 128, K D) and O_s +=
+//                    P_s V (M 128, N D, K 128; P_s read from TMEM, where the
+//                    softmax wrote it over S_s).
+// Wide items (256 rows of a key/value head's queries): stream s owns rows
+// 128 s .. 128 s + 127, so each tile that is fetched feeds four products, and
+// one stream's softmax runs under the other's products (one issuer).  Narrow
+// items (128 rows): both streams own the same rows and take the units in turn,
+// each with its own O, maximum, sum and issuer (joined in TMEM at the item's
+// end), which hides the softmax behind the loads of a memory-bound pass, and
+// the room of the second query tile holds one more tile in flight.
+//
+// Both halves of a row keep one maximum, raised (and O in TMEM rescaled) only
+// when a unit's exceeds it by more than 2^8, so P stays <= 256, rescaling is
+// rare, and otherwise the two warps of a row only meet at a barrier.
 // S, maxima, sums and O are fp32; P is rounded to bf16 for the second product
 // (2^-8 of each weight at most, as the inputs themselves; the sums take the
 // unrounded weights).
+//
+// What bounds it.  Single tokens: HBM (16 tokens of 40 heads over 13,460 keys:
+// 750 MB in 129 us, 5.8 TB/s with the join).  Wide items: the chain of one
+// stream - scores out of TMEM, biases, exponentials (2000 cycles), two
+// products of 512 cycles each and the handovers - against 2048 cycles of
+// products for both streams; 9360 queries of 12 heads over 41,000 keys take
+// 1.81 ms, 1250 TFLOP/s.  Beside the products, which read their operands from
+// shared memory at its full rate, a 16-byte read of a bias waits 33 cycles.
+// Units of 64 keys with the queries in TMEM (half of that traffic) were
+// slower: the handovers then come twice as often (2.29 ms).
 //
 // Waits are bounded: one that runs out sets the status word, and every warp
 // leaves its loop by its own bounded waits.
@@ -50,6 +62,7 @@ constexpr int kFull = 4;       // every row of the item sees every one of the 12
 constexpr int kBiased = 8;     // the keys have biases
 constexpr int kFirst = 16, kLast = 32;  // of the item, in this run
 constexpr int kEnd = 64;       // no unit: the run is over
+constexpr int kHidden = 128;   // some of the keys' counts are 0
 
 template <int D>
 struct Shape {
@@ -97,6 +110,34 @@ __device__ __forceinline__ bool bar_or(int id, bool p) {
   return r != 0;
 }
 __device__ __forceinline__ void bar_two(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// Rows of a tile whose weight is 0 must not hold an infinity or NaN where they
+// take part in a product: clears those from nk to the end of the last step of
+// 16, and those of hidden keys (a bit each).  Whole warp.
+template <int D>
+__device__ __forceinline__ void clear_rows(uint8_t* v, int nk, const uint32_t (&hidden)[4]) {
+  const int lane = threadIdx.x & 31;
+  auto clear = [&](int r, int c) {
+    *reinterpret_cast<uint4*>(v + (c >> 3) * kN * 128 + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+  };
+  for (int e = lane; e < (-nk & 15) * (D / 8); e += 32) clear(nk + e / (D / 8), e % (D / 8));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    for (uint32_t w = hidden[i]; w; w &= w - 1)
+      if (lane < D / 8) clear(32 * i + __ffs(w) - 1, lane);
+  tc::fence_proxy_async_smem();
+  __syncwarp();
+}
+// The hidden keys of a unit, a bit each (whole warp).
+__device__ __forceinline__ void hidden_keys(const float* bias, int bits, int nk, uint32_t (&hidden)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) hidden[i] = 0u;
+  if (!(bits & kHidden)) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    hidden[i] = __ballot_sync(0xffffffffu, lane + 32 * i < nk && bias[lane + 32 * i] == -INFINITY);
+}
 
 template <int D, bool split>
 __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_constant__ CUtensorMap mapPK,
@@ -225,14 +266,19 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         const int ds = j % S::kRing;
         if (j >= S::kRing) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dempty[ds], (j / S::kRing - 1) & 1u));
         if (!ok) break;
+        bool hidden = false;
         if (!own && counts) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sm.bias[ds][lane + 32 * e] = cnt[e] > 0 ? __log2f((float)cnt[e]) : -INFINITY;
+          for (int e = 0; e < 4; ++e) {
+            sm.bias[ds][lane + 32 * e] = cnt[e] > 0 ? __log2f((float)cnt[e]) : -INFINITY;
+            hidden = hidden || (cnt[e] <= 0 && lane + 32 * e < x.nk);
+          }
+          hidden = __any_sync(0xffffffffu, hidden);
         }
         if (lane == 0) {
           Desc& d = sm.desc[ds];
           d.x = x;
-          d.bits = act | (x.nk == kN && x.k0 + kN <= full_keys ? kFull : 0) | (!own && counts ? kBiased : 0) |
+          d.bits = act | (x.nk == kN && x.k0 + kN <= full_keys ? kFull : 0) | (!own && counts ? kBiased : 0) | (hidden ? kHidden : 0) |
                    (opens && i == 0 ? kFirst : 0) | (closes && i == count - 1 ? kLast : 0);
         }
         __syncwarp();
@@ -320,6 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     bool pend = false;               // S is out, its P V not yet
     uint32_t pslot = 0, pphase = 0;  // its value tile
     int pk = 0;                      // its keys
+    bool pclear = false;             // some value rows have to be cleared
+    uint32_t phidden[4];             // its hidden keys
     uint32_t acc = 0u;               // 0: O starts anew
     bool issued = false;
     auto pv = [&]() {
@@ -327,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       if (!ok) return;
       tc::tc_fence_after();
       const uint32_t vd = tc::desc_low(ring_addr + pslot * S::kTile, kN * 128);
+      if (pclear) clear_rows<D>(ring + (size_t)(base + pslot) * S::kTile, pk, phidden);
       if (pk == kN) {
         if (tc::elect_one()) {
 #pragma unroll
@@ -336,17 +385,6 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         }
       } else {
         const int steps = (pk + 15) / 16;
-        if (pk & 15) {
-          // value rows behind the unit's keys take part in the last step with
-          // weight 0: they must not hold an infinity or NaN
-          uint8_t* v = ring + (size_t)(base + pslot) * S::kTile;
-          for (int e = lane; e < (steps * 16 - pk) * (D / 8); e += 32) {
-            const int r = pk + e / (D / 8), c = e % (D / 8);
-            *reinterpret_cast<uint4*>(v + (c >> 3) * kN * 128 + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-        }
         if (tc::elect_one()) {
           for (int k = 0; k < steps; ++k)
             tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv, k > 0 ? 1u : acc);
@@ -363,6 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.dfull[ds], (j / S::kRing) & 1u));
       if (!ok) break;
       const int bits = sm.desc[ds].bits, nk = sm.desc[ds].x.nk;
+      uint32_t hidden[4];
+      hidden_keys(sm.bias[ds], bits, nk, hidden);
       __syncwarp();
       if (bits & kEnd) break;
       if (lane == 0) tc::mbar_arrive(&sm.dempty[ds]);
@@ -385,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         if (!ok) break;
         tc::tc_fence_after();
         const uint32_t kd = tc::desc_low(ring_addr + slot * S::kTile, 16);
+        if (bits & kHidden) clear_rows<D>(ring + (size_t)(base + slot) * S::kTile, 0, hidden);
         if (tc::elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -400,6 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         pslot = vslot;
         pphase = vphase;
         pk = nk;
+        pclear = (nk & 15) || (bits & kHidden);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) phidden[i] = hidden[i];
       }
       if (act) ++turn;
       if (mine) {
@@ -436,20 +480,12 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     // (one for both), its keys, and whether O starts anew
     int pend = 0, pk = 0;
     uint32_t pslot = 0, pphase = 0, np = 0u, acc = 0u;  // np, acc: a bit per stream
+    bool pclear = false;                                // some value rows have to be cleared
+    uint32_t phidden[4], hidden[4];                     // hidden keys, of the tile and of the unit read
     bool issued = false;
     auto values = [&]() {
       ok = ok && tc::mbar_wait(&sm.full[pslot], pphase);
-      if (pk & 15) {
-        // value rows behind the unit's keys take part in the last step with
-        // weight 0: they must not hold an infinity or NaN
-        uint8_t* v = ring + (size_t)pslot * S::kTile;
-        for (int e = lane; e < (16 - (pk & 15)) * (D / 8); e += 32) {
-          const int r = pk + e / (D / 8), c = e % (D / 8);
-          *reinterpret_cast<uint4*>(v + (c >> 3) * kN * 128 + r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-      }
+      if (pclear) clear_rows<D>(ring + (size_t)pslot * S::kTile, pk, phidden);
     };
     auto products = [&](const int s, const bool next, const bool next_last) {
       const bool old = pend >> s & 1;
@@ -503,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         return;
       bits = sm.desc[ds].bits;
       nk = sm.desc[ds].x.nk;
+      hidden_keys(sm.bias[ds], bits, nk, hidden);
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.dempty[ds]);
       read = true;
@@ -514,6 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       read = false;
       if (!ok || (bits & kEnd)) break;
       const int uact = bits & kAct, ubits = bits, unk = nk;
+      uint32_t uhidden[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) uhidden[i] = hidden[i];
       if (ubits & kFirst) {
         ok = ok && tc::mbar_wait(&sm.qfull, items & 1u);
         acc = 0u;
@@ -521,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       if (uact) {
         if (pend) values();
         ok = ok && tc::mbar_wait(&sm.full[slot], phase);
+        if (ubits & kHidden) clear_rows<D>(ring + (size_t)slot * S::kTile, 0, uhidden);
 #pragma unroll 1
         for (int s = 0; s < 2; ++s) {
           products(s, uact >> s & 1, (uact >> (s + 1)) == 0);
@@ -529,6 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         issued = true;
         pend = uact;
         pk = unk;
+        pclear = (unk & 15) || (ubits & kHidden);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) phidden[i] = uhidden[i];
         pslot = slot + 1 == slots ? 0 : slot + 1;
         pphase = slot + 1 == slots ? phase ^ 1u : phase;
         slot = pslot + 1 == slots ? 0 : pslot + 1;

@@ -307,6 +307,37 @@ def test_attention_over_nothing_at_all(m, dtype):
     assert bool((out[:, :3] == 0).all()) and bool(torch.isneginf(lse[:, :3]).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,H,g,new,past,C,block", [
+    (128, 2, 3, [1, 1, 1], [5, 0, 200], 1000, 0),    # single tokens
+    (64, 2, 1, [40, 9], [0, 3], 300, 1),             # rows of several branches in a tile
+    (128, 8, 1, [600, 640], [0, 100], 9700, 640),    # 256 rows at a time
+])
+def test_hidden_groups_may_hold_anything(m, dtype, D, H, g, new, past, C, block):
+    q, cu, prefix, pages, cu_h, length, table = _attention_case(m, dtype, D, H, g, 64, new, past, C, True, block, seed=6)
+    pK, pV, cnt, size = prefix
+    cnt[:, C // 3:C // 3 + 150] = 0
+    out, lse = _check_attention(m, dtype, q, cu, prefix, pages, D ** -0.5, block, cu_h, length, table)
+    hidden = _cuda(cnt <= 0)[..., None]
+    pK.masked_fill_(hidden, math.nan)
+    pV.masked_fill_(hidden, math.inf)
+    again, lse2 = torch.full_like(out, 9.0), torch.full_like(lse, 9.0)
+    m.fastar_branch_attention(q, cu, m.Prefix(pK, pV, m=_cuda(cnt), size=_cuda(size)), pages, D ** -0.5, again,
+                              lse=lse2, block=block)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tables_far_longer_than_the_branches(m, dtype):
+    """Room for 2^31 positions a branch: the units are counted in 64 bits."""
+    q, cu, prefix, pages, cu_h, length, table = _attention_case(
+        m, dtype, 64, 2, 2, 256, [1] * 5, [0, 255, 256, 600, 31], 300, True, 0, seed=8)
+    big = torch.zeros(5, 2 ** 23 - 1, dtype=torch.int32, device="cuda")
+    big[:, :table.shape[1]] = pages.table
+    far = m.PagedKV.view(K=pages.K, V=pages.V, table=big, length=pages.len)
+    _check_attention(m, dtype, q, cu, prefix, far, 0.125, 0, cu_h, length, table)
+
+
 def test_a_visible_nan_is_not_swallowed(m):
     q, cu, prefix, pages, cu_h, length, table = _attention_case(
         m, BF, 128, 2, 1, 64, [2, 2], [100, 100], 300, False, 0, seed=5, spoil=False)
