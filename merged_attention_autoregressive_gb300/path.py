@@ -449,9 +449,10 @@ class BranchRollout:
         self.held = [[] for _ in range(B)]           # page ids of each branch
         self.free = list(range(self.pages.n_pages))[::-1]
 
-    def extend(self, new):
+    def extend(self, new, stream=None):
         """Make room for new[b] more positions of each branch: the next step's
-        tokens, laid out branch after branch."""
+        tokens, laid out branch after branch.  The copies to the device go to
+        `stream` (default: the current one), which is also the next step's."""
         if len(new) != self.B or any(n < 0 for n in new) or sum(new) > self.tokens:
             raise ValueError("one count of new tokens per branch, at most `tokens` in all")
         lengths = [a + n for a, n in zip(self.lengths, new)]
@@ -469,9 +470,12 @@ class BranchRollout:
         for n in new:
             offsets.append(offsets[-1] + n)
         i32 = dict(dtype=torch.int32)
-        self.pages.table.copy_(torch.tensor([h + [0] * (most - len(h)) for h in self.held], **i32).view(self.B, most))
-        self.pages.len.copy_(torch.tensor(lengths, **i32))
-        self.cu.copy_(torch.tensor(offsets, **i32))
+        with torch.cuda.stream(None if stream is None else ChunkPath._main(stream)):
+            if any(need):  # (a released branch's old entries are not read)
+                table = [h + [0] * (most - len(h)) for h in self.held]
+                self.pages.table.copy_(torch.tensor(table, **i32).view(self.B, most))
+            self.pages.len.copy_(torch.tensor(lengths, **i32))
+            self.cu.copy_(torch.tensor(offsets, **i32))
 
     def release(self, b):
         """Branch b starts again: its pages return to the pool."""
@@ -480,8 +484,8 @@ class BranchRollout:
 
     def step(self, q, k, v, pos=None, stream=None):
         """The new tokens of the last `extend`: q [Hq][tokens][D], k, v
-        [H][tokens][D] (any head and token strides; the rows behind the last
-        branch's are ignored), pos [tokens][axes] int32 with a plan.  Returns
+        [H][tokens][D] (any head and token strides, but a q that is not rotated
+        is contiguous; the rows behind the last branch's are ignored), pos [tokens][axes] int32 with a plan.  Returns
         (out [Hq][tokens][D], lse [Hq][tokens]), buffers of this object."""
         rotated = self.q if self.plan is not None else q
         fastar_page_append(self.pages, k, v, self.cu, pos=pos, plan=self.plan,

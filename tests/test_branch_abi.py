@@ -2,8 +2,10 @@
 launched, so these run without a GPU."""
 import ctypes
 import math
+import types
 
 import pytest
+import torch
 
 VP = ctypes.c_void_p
 FAKE, ODD = VP(0x1000), VP(0x1008)  # never dereferenced: the checks come first
@@ -172,3 +174,37 @@ def test_binding_refuses_host_tensors_and_other_shapes(m):
         m.PagedKV.view(z(4, 2, 16, 64), z(4, 2, 16, 64), z(2, 2, dt=torch.int32), z(2, dt=torch.int64))
     with pytest.raises(ValueError):
         m.Prefix(z(2, 3, 64), z(2, 4, 64))
+
+
+def test_rollout_hands_out_pages():
+    from merged_attention_autoregressive_gb300.path import BranchRollout
+    zeros = lambda *shape: torch.zeros(*shape, dtype=torch.int32)
+    r = BranchRollout.__new__(BranchRollout)  # the host's part of one
+    r.B, r.tokens, r.max_len, r.lengths, r.held, r.free = 3, 100, 96, [0] * 3, [[], [], []], [4, 3, 2, 1, 0]
+    r.pages = types.SimpleNamespace(page=32, max_pages=3, n_pages=5, table=zeros(3, 3), len=zeros(3))
+    r.cu = zeros(4)
+
+    def check():
+        used = [p for h in r.held for p in h]
+        assert sorted(used + r.free) == list(range(5))  # no page twice, none lost
+        assert r.pages.len.tolist() == r.lengths
+        for b, h in enumerate(r.held):
+            assert len(h) == -(-r.lengths[b] // 32)
+            assert r.pages.table[b, :len(h)].tolist() == h
+
+    r.extend([1, 0, 40])
+    assert r.cu.tolist() == [0, 1, 1, 41]
+    check()
+    r.extend([31, 1, 0])  # the first branch's page is full now
+    assert r.cu.tolist() == [0, 31, 32, 32]
+    check()
+    held = [list(h) for h in r.held]
+    for new, why in [([64, 0, 25], "no pages"), ([65, 0, 0], "longer"), ([0, 0, 101], "at most"), ([0, -1, 0], "count"),
+                     ([1, 1], "per branch")]:
+        with pytest.raises(ValueError, match=why):
+            r.extend(new)
+        assert r.held == held and r.lengths == [32, 1, 40]  # as it was
+    r.release(2)
+    assert len(r.free) == 3 and r.lengths == [32, 1, 0]
+    r.extend([64, 0, 1])
+    check()
