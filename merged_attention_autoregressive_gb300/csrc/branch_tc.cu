@@ -645,12 +645,15 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       if (act0) ++turn;
       if (active) {
         int seen = 64;  // keys of this half that the row sees
-        bool any = true, all = true;
+        bool any = r - lane < rows, all = true, none = false;  // (warps behind the last token have nothing to do)
         if (!(bits & kFull)) {
           // rows behind the last token count as full: nobody reads their results
           seen = (r < rows ? branch_row_keys(a, sm.desc[ds].x, r) : kN) - half * 64;
           any = __any_sync(0xffffffffu, r < rows && seen + half * 64 > 0);  // alike in both halves
-          all = __all_sync(0xffffffffu, seen >= 64);
+          // rows that see nothing of it beside rows that see it whole (a unit of
+          // one branch among others): computed unmasked, and dropped at the end
+          none = split && seen <= 0;
+          all = __all_sync(0xffffffffu, none || seen >= 64);
         }
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sfull[s], ns & 1u));
         if (!ok) break;
@@ -665,6 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           tc::tmem_ld64_async(tS + half * 64, raw);
           const bool biased = bits & kBiased;
           const bool plain = !biased && all;
+          none = none && all;
           const float mul = plain ? scale2 : 1.f;
           tc::tmem_wait64(raw);
           if (!plain) {
@@ -693,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           }
           float top =
               fmaxf(tc::max3(tm[0], tm[1], tm[2]), tc::max3(tm[3], tm[4], tc::max3(tm[5], tm[6], tm[7]))) * mul;
+          if (none) top = -INFINITY;
           // both halves of a row keep one maximum: while neither exceeds it by
           // more than 2^8 they only meet here
           tc::tc_fence_before();
@@ -740,7 +745,11 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
             const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
             pk[i >> 1] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+          if (!none) l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+          if (split && __any_sync(0xffffffffu, none)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) pk[i] = none ? 0u : pk[i];
+          }
         } else {
           // no row of the warp is concerned: weights 0
 #pragma unroll
