@@ -497,13 +497,13 @@ def _rows(t, dev, what):
 def _positions(pos, N, plan, dev):
     if pos is None:
         return None
-    if pos.dtype != torch.int32 or tuple(pos.shape) != (N, plan.axes):
+    if pos.dtype is not torch.int32 or pos.shape != (N, plan.axes):
         raise ValueError(f"positions must be int32 [{N}][{plan.axes}]")
     return _at(pos, dev)
 
 
 def _int32(t, n, dev, what):
-    if t.dtype != torch.int32 or t.numel() != n:
+    if t.dtype is not torch.int32 or t.numel() != n:
         raise ValueError(f"{what} must be int32 with {n} entries")
     return _at(t, dev)
 
@@ -522,7 +522,7 @@ def _on(dev, stream, call, *args):
         stream = torch._C._cuda_getCurrentRawStream(dev)
     else:
         stream = _stream(stream)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         return call(*args, stream)
     with torch.cuda.device(dev):
         return call(*args, stream)
@@ -536,10 +536,12 @@ def fastar_rope(x, pos, plan: RopePlan, out, inverse=False, status=None, stream=
     inverse: turn back, which is also the gradient of the forward rotation."""
     shape = H, N, D = x.shape
     dev = _gpu(x)
-    if out.shape != shape or out.dtype != x.dtype or D != plan.D:
+    dt = x.dtype
+    if out.shape != shape or out.dtype is not dt or D != plan.D:
         raise ValueError("x, out and the plan must agree in shape and dtype")
-    rc = _on(dev, stream, lib().fastar_rope, _dt(x), *_rows(x, dev, "x"), H, N, D, _positions(pos, N, plan, dev),
-             plan.addr, 1 if inverse else 0, *_rows(out, dev, "out"), _at(status, dev))
+    rc = _on(dev, stream, (_lib or lib()).fastar_rope, BF16 if dt is torch.bfloat16 else _dt(x), *_rows(x, dev, "x"),
+             H, N, D, _positions(pos, N, plan, dev), plan.addr, 1 if inverse else 0, *_rows(out, dev, "out"),
+             _at(status, dev))
     if rc:
         raise FastarError(rc, "fastar_rope")
 
@@ -611,7 +613,8 @@ def fastar_page_append(pages: PagedKV, k, v, cu, pos=None, plan: RopePlan | None
     stored as they are); optional queries q [Hq][N][D] are rotated into q_out
     [Hq][N][D] in the same pass."""
     H, N, D = k.shape
-    if v.shape != k.shape or (H, D) != (pages.H, pages.D) or not k.dtype == v.dtype == pages.dtype:
+    dt = pages.dtype
+    if v.shape != k.shape or H != pages.H or D != pages.D or k.dtype is not dt or v.dtype is not dt:
         raise ValueError("k and v do not fit the pages")
     if (plan is None) != (pos is None):
         raise ValueError("positions and their plan come together")
@@ -622,10 +625,11 @@ def fastar_page_append(pages: PagedKV, k, v, cu, pos=None, plan: RopePlan | None
     dev = pages.device
     qa, Hq = (None, 0, 0), 0
     if q is not None:
-        if q.shape != q_out.shape or q.shape[1:] != k.shape[1:] or not q.dtype == q_out.dtype == k.dtype:
+        Hq, n, d = q.shape
+        if q_out.shape != (Hq, n, d) or n != N or d != D or q.dtype is not dt or q_out.dtype is not dt:
             raise ValueError("q and q_out do not fit k")
-        qa, Hq = _rows(q, dev, "q"), q.shape[0]
-    rc = _on(dev, stream, lib().fastar_page_append, pages.addr, *_rows(k, dev, "k"), *_rows(v, dev, "v"), N,
+        qa = _rows(q, dev, "q")
+    rc = _on(dev, stream, (_lib or lib()).fastar_page_append, pages.addr, *_rows(k, dev, "k"), *_rows(v, dev, "v"), N,
              _int32(cu, pages.B + 1, dev, "cu"), _positions(pos, N, plan, dev), None if plan is None else plan.addr,
              *qa, Hq, _at(q_out, dev), _at(status, dev))
     if rc:
@@ -661,7 +665,7 @@ def fastar_branch_attention(q, cu, prefix: Prefix | None, pages: PagedKV, scale,
         if stream is not None:  # the allocator must not hand it out again before that stream is done with it
             ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
                              torch.cuda.ExternalStream(int(_stream(stream)), device=q.device))
-    rc = _on(dev, stream, lib().fastar_branch_attention, pages.struct.dt, _at(q, dev), Hq, N,
+    rc = _on(dev, stream, (_lib or lib()).fastar_branch_attention, pages.struct.dt, _at(q, dev), Hq, N,
              _int32(cu, pages.B + 1, dev, "cu"), None if prefix is None else prefix.addr, pages.addr, scale, block,
              _at(out, dev), _at(lse, dev), _at(ws, dev), ws.numel() * ws.element_size(), _at(status, dev))
     if rc:
