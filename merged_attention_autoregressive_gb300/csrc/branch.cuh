@@ -43,6 +43,7 @@ struct BranchArgs {
   int slot_rows;          // rows of a partial
   int planned;            // branch_plan has written head and tile
   int whole;              // items are not cut: a run ends where an item begins
+  int item_units;         // whole: an item counts as so many units more
   int by_item;            // cuts has an entry per item (there are at most G), else per run
   BranchCut* cuts;        // [G] the items that are cut
   long long* head;        // planned: [H + 1] first unit of each head, then the tiles in use
@@ -192,7 +193,7 @@ struct BranchPlace {
       if (h < a.H) {
         const int size = h0 == 0 ? size0 : a.size ? a.size[h] : a.C;
         ok = ok && size >= 0 && size <= a.C;
-        v = prefix_units(min(max(size, 0), a.C), a.TN);
+        v = prefix_units(min(max(size, 0), a.C), a.TN) + a.item_units;
       }
       U += (long long)__reduce_add_sync(0xffffffffu, v) * nt + (long long)min(32, a.H - h0) * sum;
     }
@@ -218,7 +219,7 @@ struct BranchPlace {
     if (a.planned) {
       h = warp_count_le(a.head, a.H, u) - 1;
       const long long off = u - a.head[h];
-      const int p = prefix_units(prefix_size(a, h), a.TN);
+      const int p = prefix_units(prefix_size(a, h), a.TN) + a.item_units;
       int l = 0, r = nt;  // the row tile t with t p + tile[t] <= off < (t + 1) p + tile[t + 1]
       while (r - l > 1) {
         const int step = (r - l + 31) / 32;
@@ -237,7 +238,7 @@ struct BranchPlace {
     int p = 0;
     for (int h0 = 0; h0 < a.H; h0 += 32) {
       const int x = h0 + lane;
-      const int pu = x < a.H ? prefix_units(prefix_size(a, x), a.TN) : 0;
+      const int pu = x < a.H ? prefix_units(prefix_size(a, x), a.TN) + a.item_units : 0;
       const int v = x < a.H ? pu * nt + sum : 0;  // at most kFewUnits
       const int inc = warp_incl_scan(v);
       const unsigned m = __ballot_sync(0xffffffffu, x < a.H && first + inc > u);
@@ -340,6 +341,7 @@ struct BranchWalk {
     P = prefix_units(size, a.TN);
     units = P + place.pages_of(a, t);
     off = from = at;
+    left -= a.item_units;
     whole = at == 0 && units <= left;
 
     // first branch with tokens at or behind T0 (empty ones contribute nothing)
