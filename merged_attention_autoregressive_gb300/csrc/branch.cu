@@ -36,8 +36,12 @@ __device__ __forceinline__ long long block_scan_ll(long long v, long long* sh, l
   return res;
 }
 
-// Checks the lengths and writes the prefix sums of the units: one CTA, a warp
-// per branch and a lane per row tile that the branch touches.
+// Checks the lengths and writes the prefix sums of the units: one CTA, a lane
+// per branch; the row tiles of a branch behind its first kOwnTiles are counted
+// by its whole warp.  Bound by the latency of a few rounds of loads and
+// atomics (512 branches: about 15 us).
+constexpr int kOwnTiles = 4;
+
 __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a, int32_t* st) {
   pdl_wait();
   __shared__ long long sh[33];
@@ -46,18 +50,31 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
   for (int t = tid; t <= a.ntiles; t += kPlanThreads) a.tile[t] = 0;
   __syncthreads();
   bool bad = false;
-  for (int b = warp; b < a.B; b += kPlanThreads / 32) {
-    const int lo = a.cu[b], hi = a.cu[b + 1], len = a.len[b];
-    if (!branch_ok(a, b, lo, hi, len)) {
-      bad = true;
-      continue;
+  auto add = [&](int t, int lo, int hi, int len) {
+    const int T1 = (int)((((long long)t + 1) * a.TM + a.g - 1) / a.g);
+    const int keys = branch_limit(min(hi, T1) - 1 - lo, hi - lo, len, a.block);
+    atomicAdd((unsigned long long*)&a.tile[t], (unsigned long long)((keys + a.TN - 1) / a.TN));
+  };
+  for (int b0 = warp * 32; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + lane;
+    int lo = 0, hi = 0, len = 0;
+    if (b < a.B) {
+      lo = a.cu[b];
+      hi = a.cu[b + 1];
+      len = a.len[b];
+      if (!branch_ok(a, b, lo, hi, len)) {
+        bad = true;
+        hi = lo = 0;
+      }
     }
-    if (hi == lo) continue;
-    const int t0 = lo * a.g / a.TM, t1 = (hi * a.g - 1) / a.TM;
-    for (int t = t0 + lane; t <= t1; t += 32) {
-      const int T1 = (int)((((long long)t + 1) * a.TM + a.g - 1) / a.g);
-      const int keys = branch_limit(min(hi, T1) - 1 - lo, hi - lo, len, a.block);
-      atomicAdd((unsigned long long*)&a.tile[t], (unsigned long long)((keys + a.TN - 1) / a.TN));
+    const int t0 = lo * a.g / a.TM, t1 = hi > lo ? (hi * a.g - 1) / a.TM : t0 - 1;
+    for (int t = t0; t <= min(t1, t0 + kOwnTiles - 1); ++t) add(t, lo, hi, len);
+    for (unsigned more = __ballot_sync(0xffffffffu, t1 >= t0 + kOwnTiles); more; more &= more - 1) {
+      const int src = __ffs(more) - 1;
+      const int l = __shfl_sync(0xffffffffu, lo, src), r = __shfl_sync(0xffffffffu, hi, src);
+      const int n = __shfl_sync(0xffffffffu, len, src);
+      const int last = __shfl_sync(0xffffffffu, t1, src);
+      for (int t = __shfl_sync(0xffffffffu, t0, src) + kOwnTiles + lane; t <= last; t += 32) add(t, l, r, n);
     }
   }
   for (int h = tid; h < a.H; h += kPlanThreads)
@@ -294,16 +311,22 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   a.scale = scale;
   a.out = out;
   a.lse = lse;
-  // 256 rows per item pay where a branch fills them and the runs are long:
-  // every tile that is loaded then feeds four products (two branches of 4680
-  // tokens, 12 heads, 42,000 keys: 1.87 ms, against 2.26 ms at 128 rows).  A
-  // branch of few rows leaves most of a wide item idle while its pages pass
-  // (64 single tokens of 5 heads a group over 32,768 + 1,000 keys: 142 us
-  // against 119 us), and short runs are latency alone (9 ragged prompts of up
-  // to 858 keys: 53 us against 47 us).
+  // 256 rows per item pay where most of the keys concern most of them and the
+  // runs are long: every tile that is loaded then feeds four products.  So
+  // where a branch fills them (two branches of 4680 tokens, 12 heads, 42,000
+  // keys: 1.84 ms, 2.24 ms at 128 rows), or where the prefix is longer than
+  // the pages of all branches of an item together and few rows are padding
+  // (512 single tokens of 5 heads a group over 32,768 + up to 256 keys: 377 us,
+  // 433 us).  Otherwise most of a wide item idles while its pages pass (64 of
+  // those tokens, up to 2048 keys of their own: 129 us, 111 us at 128 rows),
+  // and short runs are latency alone (9 ragged prompts of up to 858 keys: 36
+  // us, 30 us).
   const long long rows = (long long)N * a.g;
-  const long long keys = (long long)a.C + ((long long)a.max_pages << a.page_shift);
-  const bool wide = rows / a.B >= 256 && a.H * ((rows + 255) / 256) * ((keys + 127) / 128) >= 16 * kSms;
+  const long long own = (long long)a.max_pages << a.page_shift, keys = a.C + own;
+  const long long wide_tiles = (rows + 255) / 256, narrow_tiles = (rows + 127) / 128;
+  const bool shared =
+      8 * wide_tiles <= 5 * narrow_tiles && (a.C + 127) / 128 * rows >= 256ll * a.B * ((own + 127) / 128);
+  const bool wide = (rows / a.B >= 256 || shared) && a.H * wide_tiles * ((keys + 127) / 128) >= 16 * kSms;
   const Geometry x = geometry(dt, wide, a.H, rows, a.D);
   a.TM = x.TM;
   a.TN = x.TN;
@@ -313,8 +336,8 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   const long long units = (a.C + a.TN - 1) / a.TN + a.B * (((long long)a.max_pages << a.page_shift) / a.TN + 1);
   a.planned = a.ntiles > kMaxTiles || (a.ntiles > kFewTiles && a.B > kMaxBranches) || units > kFewUnits / a.ntiles;
   // Short items (a few microseconds each) are not cut where there are enough
-  // of them: the join costs as much as the imbalance (9 ragged prompts of up
-  // to 858 keys, 256 items: 24 us, 32 us when cut).
+  // of them: the join costs more than the imbalance (9 ragged prompts of up to
+  // 858 keys, 256 items: 30 us, 38 us when cut).
   const long long items = (long long)a.H * a.ntiles;
   a.whole = items >= a.G && (keys + a.TN - 1) / a.TN <= 8;
   a.item_units = a.whole ? kItemUnits : 0;

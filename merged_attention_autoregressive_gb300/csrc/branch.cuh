@@ -366,8 +366,8 @@ struct BranchWalk {
     // at most kTwoItems units longer than an even cut of all units would.  An
     // even cut gives some runs the end of an item and the begin of the next,
     // and the queries, first softmax and output of two items cost that much
-    // more (4 branches of one token, 12 heads, 28 units each: the last CTA ends
-    // after 14.0 us, 13.0 us in parts).
+    // more (4 branches of one token, 12 heads, 28 units each: 19.6 us, 18.2 us
+    // in parts).
     parts = 0;
     if (a.by_item && !a.whole && a.ntiles == 1) {
       const int items = a.H, n = a.G / items;

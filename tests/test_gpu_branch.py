@@ -542,6 +542,7 @@ def test_groups_wider_than_a_row_tile(m):
     (128, 2, 1, 16, [1100] + [0] * 40 + [700], [0] * 42, 0, False, 1, 3),  # many row tiles, short items
     (64, 1, 1, 16, [9] * 700, [5] * 700, 33, True, 3, 0),              # many tiles and branches: planned
     (128, 40, 5, 32, [1] * 30, list(range(0, 300, 10)), 260, True, 0, 0),  # two row tiles, more items than CTAs / 2
+    (64, 16, 5, 32, [1] * 128, list(range(0, 64)) * 2, 8000, True, 0, 3),  # many single tokens over a long prefix: wide
 ])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_branch_attention_layouts(m, shape, dtype):
