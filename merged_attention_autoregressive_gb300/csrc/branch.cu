@@ -134,6 +134,11 @@ __global__ void __launch_bounds__(kJoinThreads) branch_combine_kernel(BranchArgs
   const int rows = a.cu[a.B] * a.g;
   // an item of padding alone has no record
   if (stop || (a.by_item && (int)(blockIdx.x % a.ntiles) * a.TM >= rows) || x.h < 0) return;
+  // nor has one whose run gave up a wait, which a call without a status word
+  // does not see: nothing out of range is followed
+  if (x.h >= a.H || x.t < 0 || x.t >= a.ntiles || x.run < 0 || x.last < x.run || x.last >= a.G || x.slot >> 1 != x.run ||
+      x.parts < 0 || x.parts > a.G)
+    return;
   const int lane = threadIdx.x & 31, c = x.run;
   const int w = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), groups = a.D / 16;
   const int i = w / groups * 8 + (lane & 7), col = w % groups * 16, sub = lane >> 3;

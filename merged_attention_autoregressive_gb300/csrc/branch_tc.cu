@@ -818,9 +818,10 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           w1 *= inv;
           const size_t at = live ? (size_t)(x.h * a.g + r % a.g) * a.N + r / a.g : 0;
           const int slot_row = (split ? 0 : s * kM) + wr;
-          // a finished row goes through the query tile (free by now; 16-byte
-          // piece c of row r at place c ^ r % 8) and leaves in whole lines; a
-          // partial is laid out so that the rows of a warp are neighbours
+          // a finished row goes through the place of its own queries (free by
+          // now; other warps may gather the next item's already) and leaves in
+          // whole lines; a partial is laid out so that the rows of a warp are
+          // neighbours
           uint8_t* const stage = sm.tiles + (split ? 0 : s) * S::kTile;
           if (split && whole) bar_stream(2);  // the maxima and sums in it have been read
 #pragma unroll 1
@@ -844,8 +845,8 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
             if (whole) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                st_vec<__nv_bfloat16, 8>(
-                    reinterpret_cast<__nv_bfloat16*>(stage + wr * (D * 2) + (((col / 8 + i) ^ (wr & 7)) << 4)), o + i * 8);
+                st_vec<__nv_bfloat16, 8>(reinterpret_cast<__nv_bfloat16*>(stage + tc::sw128_offset(wr, col / 8 + i, kM)),
+                                         o + i * 8);
             } else if (live) {
               float* po = a.po + (size_t)x.slot * a.slot_rows * D + ((size_t)(col / 4) * a.slot_rows + slot_row) * 4;
 #pragma unroll
@@ -868,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
               const int y = half * 16 + k + lane / per;  // row of the warp's 32
               const size_t to = __shfl_sync(0xffffffffu, at, y);
               const int yr = (warp & 3) * 32 + y;
-              const uint4 v = *reinterpret_cast<const uint4*>(stage + yr * (D * 2) + ((c ^ (yr & 7)) << 4));
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + tc::sw128_offset(yr, c, kM));
               if (r - lane + y < rows) *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + to * D + c * 8) = v;
             }
           }

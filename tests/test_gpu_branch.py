@@ -389,6 +389,24 @@ def test_results_do_not_change_from_run_to_run(m, dtype):
     assert all(torch.equal(a, outs[0][0]) and torch.equal(b, outs[0][1]) for a, b in outs)
 
 
+@pytest.mark.parametrize("D,H,new,C,block", [
+    (128, 40, [1300, 748], 700, 0),    # 256 rows at a time, items that are finished one after the other in a run
+    (64, 40, [1300, 748], 700, 1),
+    (128, 12, [40] * 50, 300, 8),      # 128 rows at a time
+])
+def test_many_items_of_a_run_do_not_disturb_each_other(m, D, H, new, C, block):
+    q, cu, prefix, pages, *_ = _attention_case(m, BF, D, H, 1, 64, new, [300] * len(new), C, True, block, seed=9,
+                                               spoil=False)
+    px = m.Prefix(prefix[0], prefix[1], m=_cuda(prefix[2]))
+    want = None
+    for _ in range(60):
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+        m.fastar_branch_attention(q, cu, px, pages, 0.09, out, lse=lse, block=block)
+        if want is None:
+            want = out, lse
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 def test_sticky_status_and_device_refusals(m):
     """Bad lengths, offsets and page ids set the status word; a set word
     stops every call; nothing faults."""
