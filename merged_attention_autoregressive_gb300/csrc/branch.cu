@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
 // by the latency of its launch and three round trips: 3.5 us of a short call.
 constexpr int kJoinThreads = 256;
 
-template <typename T>
+// kAhead: partials of a lane in one round trip.
+template <typename T, int kAhead>
 __global__ void __launch_bounds__(kJoinThreads) branch_combine_kernel(BranchArgs a, int32_t* st) {
   branch_touch(a, st);
   pdl_wait();
@@ -155,12 +156,12 @@ __global__ void __launch_bounds__(kJoinThreads) branch_combine_kernel(BranchArgs
   float m = -INFINITY, l = 0.f, o[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) o[e] = 0.f;
-  for (int k0 = sub; k0 < n; k0 += 8) {
-    // two partials at a time, their statistics and columns in one round trip
-    float2 ml[2];
-    float4 p[2][4];
+  for (int k0 = sub; k0 < n; k0 += 4 * kAhead) {
+    // kAhead partials at a time, their statistics and columns in one round trip
+    float2 ml[kAhead];
+    float4 p[kAhead][4];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < kAhead; ++q) {
       const int k = k0 + 4 * q, slot = live && k < n ? slot_of(k) : -1;
       ml[q] = make_float2(-INFINITY, 0.f);
 #pragma unroll
@@ -173,14 +174,16 @@ __global__ void __launch_bounds__(kJoinThreads) branch_combine_kernel(BranchArgs
         for (int e = 0; e < 4; ++e) p[q][e] = po[(size_t)e * a.slot_rows];
       }
     }
-    const float mn = fmaxf(m, fmaxf(ml[0].y != 0.f ? ml[0].x : -INFINITY, ml[1].y != 0.f ? ml[1].x : -INFINITY));
+    float mn = m;
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) mn = fmaxf(mn, ml[q].y != 0.f ? ml[q].x : -INFINITY);
     const float nb = mn == -INFINITY ? 0.f : mn, alpha = l == 0.f ? 0.f : exp2f(m - nb);
     l *= alpha;
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[e] *= alpha;
     m = mn;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < kAhead; ++q) {
       if (ml[q].y == 0.f) continue;  // the row saw nothing in that run
       const float w = exp2f(ml[q].x - nb);
       l += w * ml[q].y;
@@ -237,8 +240,13 @@ int launch_branch_combine(const BranchArgs& a, fastar_dtype dt, int32_t* st, cud
   const int rows = (int)min((long long)a.TM, (long long)a.N * a.g);
   const int warps = kJoinThreads / 32;
   const dim3 grid(a.by_item ? a.H * a.ntiles : a.G, ((rows + 7) / 8 * (a.D / 16) + warps - 1) / warps);
-  cudaError_t rc = dt == FASTAR_BF16 ? launch_pdl(branch_combine_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0, s, a, st)
-                                     : launch_pdl(branch_combine_kernel<float>, grid, dim3(kJoinThreads), 0, s, a, st);
+  // four where items have more than eight parts (4 tokens of 12 heads, 12 parts:
+  // 17.8 us, 18.1 us by two), else two (64 tokens of 5 heads a group, about 7
+  // parts: 111 us, 113 us by four, which leaves room for fewer CTAs)
+  const bool many = a.by_item && a.G > 8 * a.H * a.ntiles;
+  auto kernel = dt == FASTAR_BF16 ? (many ? branch_combine_kernel<__nv_bfloat16, 4> : branch_combine_kernel<__nv_bfloat16, 2>)
+                                  : (many ? branch_combine_kernel<float, 4> : branch_combine_kernel<float, 2>);
+  const cudaError_t rc = launch_pdl(kernel, grid, dim3(kJoinThreads), 0, s, a, st);
   if (rc != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;

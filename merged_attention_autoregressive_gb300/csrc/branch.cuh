@@ -372,11 +372,10 @@ struct BranchWalk {
     if (a.by_item && !a.whole && a.ntiles == 1) {
       const int items = a.H, n = a.G / items;
       if (U < (1 << 23) && (unsigned)U / (unsigned)(items * n) <= (unsigned)U / (unsigned)a.G + kTwoItems) {
-        // A part more saves a share of the units' time and costs the join an
-        // eighth of a round trip (0.8 us): len / p units of 0.75 us (5 us on
-        // the FP32 pipes) and p / 8 round trips are least at p = sqrt(8 len)
-        // (sqrt(48 len)).  One token of 2 heads, 22 units: 24 us in 76 parts,
-        // 16 us in 13.
+        // A part more saves a share of the units' time and costs the join
+        // about 0.1 us: len / p units of 0.75 us (5 us on the FP32 pipes) and p
+        // of those are least near p = sqrt(8 len) (sqrt(48 len)).  One token of
+        // 2 heads, 22 units: 15.5 us in 13 parts, 16.5 us in 16, 24 us in 76.
         const float len = (float)((unsigned)U / (unsigned)items);
         parts = max(1, min(n, (int)ceilf(sqrtf((a.TM == 64 ? 48.f : 8.f) * len))));
       }
