@@ -47,6 +47,7 @@ struct SimtSmem {
   float K[kStages][kTN][D + 4];  // a stage's keys, then its unit's probabilities [kTM][kTN + 4]
   float V[kStages][kTN][D];
   float bias[kStages][kTN];
+  uint64_t full[kStages];
   BranchWalk walk[32];  // of warp 0, a lane each: it lives here between units, out of everybody's registers
   int count, keys_end, full_keys, opens, closes, more;
   BranchUnit next;
@@ -110,6 +111,8 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
     if (tid == 0) {
       sm.count = 0;
       sm.more = more;
+      for (int i = 0; i < kStages; ++i) tc::mbar_init(&sm.full[i], 2 * kTN);
+      tc::fence_mbar_init();
     }
     __syncwarp();
     describe(0);
@@ -118,50 +121,53 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
   const int rows = a.cu[a.B] * a.g;
   float m[4], l[4], o[4][OC];
   bool bad = false;
-  // a unit's keys and values, straight into their stage; its biases
+  // a unit's keys and values, straight into their stage, a row per thread
+  // (16-byte copies of all threads took 3800 cycles of a unit to issue: 42 tokens
+  // of 12 heads over 4096 + 1205 keys 459 us, 428 us by rows); its biases
   auto load = [&](int n) {
     const BranchUnit& x = sm.unit[n & 1];
     const int g = kStages == 2 ? n & 1 : 0;
-    for (int e = tid; e < kTN * RV; e += kThreads) {
-      const int r = e / RV, c = e % RV;
-      const float *kp = (const float*)a.q, *vp = kp;
-      uint32_t bytes = 0;
-      if (r < x.nk) {
-        size_t at = 0;
-        bool ok = true;
-        if (x.branch < 0) {
-          at = (size_t)x.h * a.C + x.k0 + r;
-        } else {
-          const int pos = x.k0 + r;
-          const int id = a.table[(size_t)x.branch * a.max_pages + (pos >> a.page_shift)];
-          ok = id >= 0 && id < a.n_pages;
-          at = (((size_t)id * a.H + x.h) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-        }
-        if (ok) {
-          kp = (const float*)(x.branch < 0 ? a.pK : a.K) + at * D + c * VN;
-          vp = (const float*)(x.branch < 0 ? a.pV : a.V) + at * D + c * VN;
-          bytes = 16;
-        } else {
-          bad = true;
-        }
+    if (tid < 2 * kTN) {
+      const int r = tid % kTN;
+      const bool keys = tid < kTN;
+      float* const dst = keys ? sm.K[g][r] : sm.V[g][r];
+      size_t at = 0;
+      bool ok = r < x.nk;
+      if (ok && x.branch < 0) {
+        at = (size_t)x.h * a.C + x.k0 + r;
+      } else if (ok) {
+        const int pos = x.k0 + r;
+        const int id = a.table[(size_t)x.branch * a.max_pages + (pos >> a.page_shift)];
+        ok = id >= 0 && id < a.n_pages;
+        at = (((size_t)id * a.H + x.h) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+        bad = bad || !ok;
       }
-      tc::cp_async16(tc::smem_u32(&sm.K[g][r][c * VN]), kp, bytes);
-      tc::cp_async16(tc::smem_u32(&sm.V[g][r][c * VN]), vp, bytes);
-    }
-    tc::cp_async_commit();
-    if (tid < kTN) {
+      if (ok) {
+        const float* src = (const float*)(x.branch < 0 ? (keys ? a.pK : a.pV) : (keys ? a.K : a.V)) + at * D;
+        tc::mbar_arrive_expect_tx(&sm.full[g], D * 4);
+        tc::bulk_load(dst, src, D * 4, &sm.full[g]);
+      } else {
+        // takes part with weight 0
+        for (int c = 0; !keys && c < RV; ++c) *reinterpret_cast<float4*>(dst + c * VN) = make_float4(0.f, 0.f, 0.f, 0.f);
+        tc::mbar_arrive(&sm.full[g]);
+      }
+    } else if (tid < 3 * kTN) {
+      const int r = tid - 2 * kTN;
       float b = 0.f;
-      if (x.branch < 0 && a.m && tid < x.nk) {
-        const int c = a.m[(size_t)x.h * a.C + x.k0 + tid];
+      if (x.branch < 0 && a.m && r < x.nk) {
+        const int c = a.m[(size_t)x.h * a.C + x.k0 + r];
         b = c > 0 ? log2f((float)c) : -INFINITY;
       }
-      sm.bias[g][tid] = b;
+      sm.bias[g][r] = b;
     }
   };
   __syncthreads();
   bool last = sm.unit[0].flags & 8;
   for (int n = 0; !last; ++n) {
-    if (n > 0) __syncthreads();  // the next unit is described; the products of the one before are done
+    if (n > 0) {
+      tc::fence_proxy_async_smem();
+      __syncthreads();  // the next unit is described; the products of the one before are done
+    }
     const BranchUnit x = sm.unit[n & 1];
     last = sm.unit[(n + 1) & 1].flags & 8;
     const int r0 = x.t * kTM, g = kStages == 2 ? n & 1 : 0;
@@ -185,16 +191,19 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
         for (int d = 0; d < OC; ++d) o[i][d] = 0.f;
       }
     }
-    if (kStages == 2 && !last)
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else
-      tc::cp_async_wait_all();
+    const bool landed = tc::mbar_wait(&sm.full[g], (kStages == 2 ? n >> 1 : n) & 1);
     // a warp computes when one of its 8 rows has keys in the unit
     const int w0 = r0 + (ty & ~1) * 4, lo = x.branch < 0 ? 0 : x.lo * a.g;
     const int hi = x.branch < 0 ? rows : min(rows, (x.lo + x.n) * a.g);
     const bool busy = x.nk > 0 && w0 < hi && w0 + 8 > lo;
     float(*P)[kTN + 4] = reinterpret_cast<float(*)[kTN + 4]>(&sm.K[g][0][0]);
-    __syncthreads();
+    if (__syncthreads_or(!landed)) {
+      if (tid == 0) status_set(st, FASTAR_ERR_TIMEOUT);
+      // the copies have landed before the CTA exits
+      (void)tc::mbar_wait(&sm.full[g], (kStages == 2 ? n >> 1 : n) & 1);
+      if (kStages == 2 && !last) (void)tc::mbar_wait(&sm.full[g ^ 1], ((n + 1) >> 1) & 1);
+      break;
+    }
     float s[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
