@@ -516,13 +516,14 @@ def _gpu(t):
     return dev
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_gpu = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _on(dev, stream, call, *args):
     """call(*args, stream) on GPU `dev`: on its current stream by default."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        stream = _stream(stream)
-    if dev == torch._C._cuda_getDevice():
+    stream = _raw_stream(dev) if stream is None else _stream(stream)
+    if dev == _current_gpu():
         return call(*args, stream)
     with torch.cuda.device(dev):
         return call(*args, stream)
@@ -535,13 +536,18 @@ def fastar_rope(x, pos, plan: RopePlan, out, inverse=False, status=None, stream=
     projection's [N][H][D] output, for one); out may be x itself.
     inverse: turn back, which is also the gradient of the forward rotation."""
     shape = H, N, D = x.shape
-    dev = _gpu(x)
-    dt = x.dtype
+    dt, dev = x.dtype, x.get_device()
     if out.shape != shape or out.dtype is not dt or D != plan.D:
         raise ValueError("x, out and the plan must agree in shape and dtype")
-    rc = _on(dev, stream, (_lib or lib()).fastar_rope, BF16 if dt is torch.bfloat16 else _dt(x), *_rows(x, dev, "x"),
-             H, N, D, _positions(pos, N, plan, dev), plan.addr, 1 if inverse else 0, *_rows(out, dev, "out"),
-             _at(status, dev))
+    xs, os = x.stride(), out.stride()
+    if dev < 0 or out.get_device() != dev or xs[2] != 1 or os[2] != 1:
+        _gpu(x), _rows(x, dev, "x"), _rows(out, dev, "out")  # says which
+    args = (BF16 if dt is torch.bfloat16 else _dt(x), x.data_ptr(), xs[0], xs[1], H, N, D, _positions(pos, N, plan, dev),
+            plan.addr, 1 if inverse else 0, out.data_ptr(), os[0], os[1], _at(status, dev))
+    if stream is None and dev == _current_gpu():
+        rc = (_lib or lib()).fastar_rope(*args, _raw_stream(dev))
+    else:
+        rc = _on(dev, stream, lib().fastar_rope, *args)
     if rc:
         raise FastarError(rc, "fastar_rope")
 
@@ -612,9 +618,9 @@ def fastar_page_append(pages: PagedKV, k, v, cu, pos=None, plan: RopePlan | None
     position len[b] - n_b + i.  The keys are rotated by pos and plan (none:
     stored as they are); optional queries q [Hq][N][D] are rotated into q_out
     [Hq][N][D] in the same pass."""
-    H, N, D = k.shape
-    dt = pages.dtype
-    if v.shape != k.shape or H != pages.H or D != pages.D or k.dtype is not dt or v.dtype is not dt:
+    shape = H, N, D = k.shape
+    dt, dev = pages.dtype, pages.device
+    if v.shape != shape or H != pages.H or D != pages.D or k.dtype is not dt or v.dtype is not dt:
         raise ValueError("k and v do not fit the pages")
     if (plan is None) != (pos is None):
         raise ValueError("positions and their plan come together")
@@ -622,16 +628,22 @@ def fastar_page_append(pages: PagedKV, k, v, cu, pos=None, plan: RopePlan | None
         raise ValueError("q and q_out come together")
     if plan is not None and plan.D != D:
         raise ValueError("the plan has another head dimension")
-    dev = pages.device
-    qa, Hq = (None, 0, 0), 0
+    ks, vs = k.stride(), v.stride()
+    if k.get_device() != dev or v.get_device() != dev or ks[2] != 1 or vs[2] != 1:
+        _rows(k, dev, "k"), _rows(v, dev, "v")  # says which
+    qa, Hq, qs = None, 0, (0, 0)
     if q is not None:
         Hq, n, d = q.shape
         if q_out.shape != (Hq, n, d) or n != N or d != D or q.dtype is not dt or q_out.dtype is not dt:
             raise ValueError("q and q_out do not fit k")
-        qa = _rows(q, dev, "q")
-    rc = _on(dev, stream, (_lib or lib()).fastar_page_append, pages.addr, *_rows(k, dev, "k"), *_rows(v, dev, "v"), N,
-             _int32(cu, pages.B + 1, dev, "cu"), _positions(pos, N, plan, dev), None if plan is None else plan.addr,
-             *qa, Hq, _at(q_out, dev), _at(status, dev))
+        qa, *qs = _rows(q, dev, "q")
+    args = (pages.addr, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], N,
+            _int32(cu, pages.B + 1, dev, "cu"), _positions(pos, N, plan, dev), None if plan is None else plan.addr,
+            qa, qs[0], qs[1], Hq, _at(q_out, dev), _at(status, dev))
+    if stream is None and dev == _current_gpu():
+        rc = (_lib or lib()).fastar_page_append(*args, _raw_stream(dev))
+    else:
+        rc = _on(dev, stream, lib().fastar_page_append, *args)
     if rc:
         raise FastarError(rc, "fastar_page_append")
 
