@@ -552,11 +552,34 @@ def fastar_rope(x, pos, plan: RopePlan, out, inverse=False, status=None, stream=
         raise FastarError(rc, "fastar_rope")
 
 
-class PagedKV:
+class _Bound:
+    """Holds the tensors that a call's struct points at.  Assigning one of them
+    drops the struct and what follows from the shapes; the next use takes them
+    from the tensors that are there then."""
+    _tensors = _derived = ()
+
+    def __setattr__(self, name, value):
+        if name in self._tensors:
+            for d in self._derived:
+                self.__dict__.pop(d, None)
+        object.__setattr__(self, name, value)
+
+    def __getattr__(self, name):
+        if name not in self._derived:
+            raise AttributeError(f"{type(self).__name__!r} object has no attribute {name!r}")
+        self._bind()
+        return self.__dict__[name]
+
+
+class PagedKV(_Bound):
     """Keys and values of a layer's branches in pages (torch-owned):
     K, V [n_pages][H][page][D], table [B][max_pages] int32 page ids, len [B]
     int32 positions of each branch, the new tokens of a call included.  The
-    caller hands out the pages (table) and counts the positions (len)."""
+    caller hands out the pages (table) and counts the positions (len): in
+    place, or by assigning another tensor (a tensor whose own storage is
+    replaced, as by resize_, has to be assigned again)."""
+    _tensors = ("K", "V", "table", "len")
+    _derived = ("n_pages", "H", "page", "D", "B", "max_pages", "dtype", "device", "struct", "addr")
 
     def __init__(self, H, D, page, n_pages, B, max_pages, dtype=torch.bfloat16, device="cuda"):
         dev = torch.device(device)
@@ -573,37 +596,46 @@ class PagedKV:
         return p
 
     def _set(self, K, V, table, length):
+        self.K, self.V, self.table, self.len = K, V, table, length
+        self._bind()
+
+    def _bind(self):
+        K, V, table, length = self.K, self.V, self.table, self.len
         if K.shape != V.shape or K.dtype != V.dtype or K.dim() != 4 or table.dim() != 2:
             raise ValueError("K and V are [n_pages][H][page][D], the table [B][max_pages]")
-        self.K, self.V, self.table, self.len = K, V, table, length
-        self.n_pages, self.H, self.page, self.D = K.shape
-        self.B, self.max_pages = table.shape
-        self.dtype = K.dtype
-        self.device = _gpu(K)
-        self.struct = PagesStruct(self.H, self.D, self.page, self.n_pages, self.B, self.max_pages, _dt(K),
-                                  _at(K, self.device), _at(V, self.device),
-                                  _int32(table, table.numel(), self.device, "the table"),
-                                  _int32(length, self.B, self.device, "the lengths"))
-        self.addr = ctypes.addressof(self.struct)
+        n_pages, H, page, D = K.shape
+        B, max_pages = table.shape
+        dev = _gpu(K)
+        struct = PagesStruct(H, D, page, n_pages, B, max_pages, _dt(K), _at(K, dev), _at(V, dev),
+                             _int32(table, table.numel(), dev, "the table"), _int32(length, B, dev, "the lengths"))
+        self.n_pages, self.H, self.page, self.D, self.B, self.max_pages = n_pages, H, page, D, B, max_pages
+        self.dtype, self.device, self.struct, self.addr = K.dtype, dev, struct, ctypes.addressof(struct)
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.K, self.V, self.table, self.len))
 
 
-class Prefix:
+class Prefix(_Bound):
     """The rows that every branch attends: K, V [H][C][D], optional counts m
-    [H][C] int32 (+ ln m) and live rows size [H] int32."""
+    [H][C] int32 (+ ln m) and live rows size [H] int32.  They change in place
+    or by assigning other tensors."""
+    _tensors = ("K", "V", "m", "size")
+    _derived = ("device", "struct", "addr")
 
     def __init__(self, K, V, m=None, size=None):
+        self.K, self.V, self.m, self.size = K, V, m, size
+        self._bind()
+
+    def _bind(self):
+        K, V, m, size = self.K, self.V, self.m, self.size
         if K.shape != V.shape or K.dtype != V.dtype or K.dim() != 3:
             raise ValueError("K and V are [H][C][D]")
-        self.K, self.V, self.m, self.size = K, V, m, size
         H, C, D = K.shape
-        self.device = dev = _gpu(K)
-        self.struct = PrefixStruct(H, C, D, _dt(K), _at(K, dev), _at(V, dev),
-                                   None if m is None else _int32(m, H * C, dev, "m"),
-                                   None if size is None else _int32(size, H, dev, "size"))
-        self.addr = ctypes.addressof(self.struct)
+        dev = _gpu(K)
+        struct = PrefixStruct(H, C, D, _dt(K), _at(K, dev), _at(V, dev),
+                              None if m is None else _int32(m, H * C, dev, "m"),
+                              None if size is None else _int32(size, H, dev, "size"))
+        self.device, self.struct, self.addr = dev, struct, ctypes.addressof(struct)
 
     @classmethod
     def of(cls, cache: Cache):
