@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
   auto add = [&](int t, int lo, int hi, int len) {
     const int T1 = (int)((((long long)t + 1) * a.TM + a.g - 1) / a.g);
     const int keys = branch_limit(min(hi, T1) - 1 - lo, hi - lo, len, a.block);
-    atomicAdd((unsigned long long*)&a.tile[t], (unsigned long long)((keys + a.TN - 1) / a.TN));
+    atomicAdd((unsigned long long*)&a.tile[t], (unsigned long long)key_units(keys, a.TN));
   };
   for (int b0 = warp * 32; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + lane;
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
   carry = 0;
   for (int h0 = 0; h0 < a.H; h0 += kPlanThreads) {
     const int h = h0 + tid;
-    const long long v = h < a.H ? (long long)nt * (prefix_units(prefix_size(a, h), a.TN) + a.item_units) + pages : 0;
+    const long long v = h < a.H ? (long long)nt * (key_units(prefix_size(a, h), a.TN) + a.item_units) + pages : 0;
     const long long x = block_scan_ll(v, sh, &total);
     if (h < a.H) a.head[h] = carry + x;
     carry += total;
@@ -339,7 +339,7 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   const long long own = (long long)a.max_pages << a.page_shift, keys = a.C + own;
   const long long wide_tiles = (rows + 255) / 256, narrow_tiles = (rows + 127) / 128;
   const bool shared =
-      8 * wide_tiles <= 5 * narrow_tiles && (a.C + 127) / 128 * rows >= 256ll * a.B * ((own + 127) / 128);
+      8 * wide_tiles <= 5 * narrow_tiles && key_units(a.C, 128) * rows >= 256ll * a.B * ((own + 127) / 128);
   const bool wide = (rows / a.B >= 256 || shared) && a.H * wide_tiles * ((keys + 127) / 128) >= 16 * kSms;
   const Geometry x = geometry(dt, wide, a.H, rows, a.D);
   a.TM = x.TM;
@@ -347,7 +347,7 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   a.G = x.G;
   a.ntiles = x.ntiles;
   a.slot_rows = x.slot_rows;
-  const long long units = (a.C + a.TN - 1) / a.TN + a.B * (((long long)a.max_pages << a.page_shift) / a.TN + 1);
+  const long long units = key_units(a.C, a.TN) + a.B * (((long long)a.max_pages << a.page_shift) / a.TN + 1);
   a.planned = a.ntiles > kMaxTiles || (a.ntiles > kFewTiles && a.B > kMaxBranches) || units > kFewUnits / a.ntiles;
   // Short items (a few microseconds each) are not cut where there are enough
   // of them: the join costs more than the imbalance (9 ragged prompts of up to

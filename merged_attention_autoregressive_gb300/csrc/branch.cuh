@@ -67,10 +67,14 @@ __device__ __forceinline__ int branch_limit(int i, int n, int len, int block) {
   const int blocks = t / block + 1;
   return blocks > len / block ? len : blocks * block;
 }
+// Units of TN keys that hold `keys` of them (up to 2^31 - 1, whose sum with TN
+// is past an int).
+__host__ __device__ __forceinline__ int key_units(int keys, int TN) {
+  return (int)(((unsigned)keys + (unsigned)TN - 1) / (unsigned)TN);
+}
 __device__ __forceinline__ int prefix_size(const BranchArgs& a, int h) {
   return a.size ? min(max(a.size[h], 0), a.C) : a.C;
 }
-__device__ __forceinline__ int prefix_units(int size, int TN) { return (size + TN - 1) / TN; }
 
 // Entries of the ascending list x[0..n) that are <= v (whole warp).
 template <typename T>
@@ -148,13 +152,13 @@ struct BranchPlace {
       }
       used = max(used, hi);
       if (a.ntiles == 1) {
-        if (hi > lo) sum += (branch_limit(hi - 1 - lo, hi - lo, len, a.block) + a.TN - 1) / a.TN;
+        if (hi > lo) sum += key_units(branch_limit(hi - 1 - lo, hi - lo, len, a.block), a.TN);
       } else if (a.ntiles <= kFewTiles) {
         // a branch per lane, the tiles one after the other
         for (int t = 0; t < a.ntiles; ++t) {
           const int last = min(hi, tile_end(a, t)) - 1;
           int v = 0;
-          if (last >= max(lo, tile_begin(a, t))) v = (branch_limit(last - lo, hi - lo, len, a.block) + a.TN - 1) / a.TN;
+          if (last >= max(lo, tile_begin(a, t))) v = key_units(branch_limit(last - lo, hi - lo, len, a.block), a.TN);
           v = __reduce_add_sync(0xffffffffu, v);
           if (lane == t) pages[0] += v;
         }
@@ -166,7 +170,7 @@ struct BranchPlace {
 #pragma unroll
           for (int e = 0; e < kLaneTiles; ++e) {
             const int last = min(r, t1[e]) - 1;
-            if (last >= max(l, t0[e])) pages[e] += (branch_limit(last - l, r - l, n, a.block) + a.TN - 1) / a.TN;
+            if (last >= max(l, t0[e])) pages[e] += key_units(branch_limit(last - l, r - l, n, a.block), a.TN);
           }
         }
       }
@@ -193,7 +197,7 @@ struct BranchPlace {
       if (h < a.H) {
         const int size = h0 == 0 ? size0 : a.size ? a.size[h] : a.C;
         ok = ok && size >= 0 && size <= a.C;
-        v = prefix_units(min(max(size, 0), a.C), a.TN) + a.item_units;
+        v = key_units(min(max(size, 0), a.C), a.TN) + a.item_units;
       }
       U += (long long)__reduce_add_sync(0xffffffffu, v) * nt + (long long)min(32, a.H - h0) * sum;
     }
@@ -219,7 +223,7 @@ struct BranchPlace {
     if (a.planned) {
       h = warp_count_le(a.head, a.H, u) - 1;
       const long long off = u - a.head[h];
-      const int p = prefix_units(prefix_size(a, h), a.TN) + a.item_units;
+      const int p = key_units(prefix_size(a, h), a.TN) + a.item_units;
       int l = 0, r = nt;  // the row tile t with t p + tile[t] <= off < (t + 1) p + tile[t + 1]
       while (r - l > 1) {
         const int step = (r - l + 31) / 32;
@@ -238,7 +242,7 @@ struct BranchPlace {
     int p = 0;
     for (int h0 = 0; h0 < a.H; h0 += 32) {
       const int x = h0 + lane;
-      const int pu = x < a.H ? prefix_units(prefix_size(a, x), a.TN) + a.item_units : 0;
+      const int pu = x < a.H ? key_units(prefix_size(a, x), a.TN) + a.item_units : 0;
       const int v = x < a.H ? pu * nt + sum : 0;  // at most kFewUnits
       const int inc = warp_incl_scan(v);
       const unsigned m = __ballot_sync(0xffffffffu, x < a.H && first + inc > u);
@@ -328,7 +332,7 @@ struct BranchWalk {
       len = a.len[b];
       const int last = min(hi, T1) - 1;
       if (last >= max(lo, T0)) keys = branch_limit(last - lo, n, len, a.block);
-      nu = (keys + a.TN - 1) / a.TN;
+      nu = key_units(keys, a.TN);
     }
     incl = warp_incl_scan(nu);
     total = __shfl_sync(0xffffffffu, incl, 31);
@@ -338,7 +342,7 @@ struct BranchWalk {
     T0 = a.ntiles > 1 ? tile_begin(a, t) : 0;
     T1 = a.ntiles > 1 ? min(tokens, tile_end(a, t)) : tokens;
     size = prefix_size(a, h);
-    P = prefix_units(size, a.TN);
+    P = key_units(size, a.TN);
     units = P + place.pages_of(a, t);
     off = from = at;
     left -= a.item_units;
@@ -384,7 +388,7 @@ struct BranchWalk {
       h = c / parts;
       t = 0;
       if (h >= a.H) return false;
-      const int len = prefix_units(prefix_size(a, h), a.TN) + place.pages_of(a, t);
+      const int len = key_units(prefix_size(a, h), a.TN) + place.pages_of(a, t);
       const int u0 = BranchCut::part(len, c % parts, parts);
       left = BranchCut::part(len, c % parts + 1, parts) - u0;
       if (left > 0) enter(a, u0);

@@ -248,8 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       int id, cnt[4];
       auto fetch = [&](int k, int* v) {
         if (own) {
-          const int p = k + lane * box;
-          v[0] = p < keys_end && lane * box < kN ? table[p >> a.page_shift] : -1;
+          v[0] = lane * box < kN && k + lane * box < keys_end ? table[(k + lane * box) >> a.page_shift] : -1;
         } else if (counts) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {

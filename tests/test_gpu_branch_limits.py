@@ -1,0 +1,65 @@
+"""The branched-rollout calls at the ends of what they accept: lengths near
+2^31, a status word that is set already, bad page ids beside good ones."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+@pytest.fixture(scope="module")
+def m():
+    import merged_attention_autoregressive_gb300 as m
+    return m
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("branches,new", [(1, 1), (5, 1), (1, 130)])  # without a plan, with one, several row tiles
+def test_a_branch_of_almost_2_31_positions(m, dtype, branches, new):
+    """max_pages * page = 2^31 - 64 positions: one page stands in all places of
+    the table but the first, so softmax and log-sum-exp have a closed form.
+
+    Bounds.  A run has n units of TN keys.  Its sums take n terms, each
+    rounded by at most 2^-24 of the sum, and its products with the values 8
+    steps a unit on the tensor cores (each off by at most 2^-23 of the sum) or
+    64 multiply-adds a unit (2^-24 each); scores and weights as in the tests
+    of ordinary lengths.  All values are positive, so that the sum of p |v| is
+    the result itself."""
+    D, page, last = 64, 64, 2 ** 25 - 1
+    gen = torch.Generator().manual_seed(branches + new)
+    K = torch.randn(2, 1, page, D, generator=gen).to(dtype).cuda()
+    V = (1 + torch.rand(2, 1, page, D, generator=gen)).to(dtype).cuda()
+    V[0] *= 50
+    table = torch.zeros(branches, last, dtype=I32, device="cuda")
+    table[0, 1:] = 1
+    length = torch.full((branches,), 64, dtype=I32, device="cuda")
+    length[0] = last * page
+    N = new + branches - 1
+    cu = torch.tensor([0] + list(range(new, N + 1)), dtype=I32, device="cuda")
+    q = torch.randn(1, N, D, generator=gen).to(dtype).cuda()
+    out, lse = torch.zeros_like(q), torch.zeros(1, N, device="cuda")
+    st = torch.zeros(1, dtype=I32, device="cuda")
+    m.fastar_branch_attention(q, cu, None, m.PagedKV.view(K, V, table, length), D ** -0.5, out, lse=lse, status=st)
+    assert int(st) == 0
+    scale = D ** -0.5
+    x = scale * (q[0].double() @ K[:, 0].double().flatten(0, 1).T)        # [N][128]: first page, repeated page
+    copies = torch.ones(N, 2 * page, dtype=torch.float64, device="cuda")
+    copies[:new, page:] = last - 1
+    copies[new:, page:] = 0                                               # the other branches: the first page alone
+    top = x.amax(1, keepdim=True)
+    w = copies * (x - top).exp()
+    total = w.sum(1, keepdim=True)
+    ref, rl = (w @ V[:, 0].double().flatten(0, 1)) / total, (top + total.log())[:, 0]
+    X = float((scale * (q[0].double().abs() @ K[:, 0].double().abs().flatten(0, 1).T)).max())
+    d = (D + 4) * 2.0 ** -23 * X + 2.0 ** -20
+    tiles = -(-N // (128 if dtype == BF else 64))
+    runs, TN = (152, 128) if dtype == BF else (304, 64)
+    n = tiles * (last * page // TN + branches) / runs + 1
+    sums = (n + runs) * 2.0 ** -24
+    products = n * 8 * 2.0 ** -23 if dtype == BF else n * 64 * 2.0 ** -24
+    rounding = 2.0 ** -8 + 2.0 ** -8 if dtype == BF else 0.0              # the weights, the result
+    assert bool(((lse[0].double() - rl).abs() <= d + sums * 1.01 + 2.0 ** -22 * rl.abs()).all())
+    assert bool(((out[0].double() - ref).abs() <= (rounding + 3 * d + (sums + products) * 1.2) * ref).all())
+    assert float(rl[:new].min()) > math.log(last) - X                     # a bound that a lost branch cannot meet
