@@ -46,7 +46,16 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
   pdl_wait();
   __shared__ long long sh[33];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (block_status_bad(st)) return;
+  // nothing to do for the kernels behind: their loaders read the lists before
+  // they know of the status, so these are written in any case, and also where
+  // the call has no status word
+  auto no_units = [&]() {
+    for (int h = tid; h <= a.H + 1; h += kPlanThreads) a.head[h] = 0;
+  };
+  if (block_status_bad(st)) {
+    no_units();
+    return;
+  }
   for (int t = tid; t <= a.ntiles; t += kPlanThreads) a.tile[t] = 0;
   __syncthreads();
   bool bad = false;
@@ -81,8 +90,7 @@ __global__ void __launch_bounds__(kPlanThreads) branch_plan_kernel(BranchArgs a,
     if (a.size && (a.size[h] < 0 || a.size[h] > a.C)) bad = true;
   if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
   if (__syncthreads_or(bad)) {
-    // nothing to do for the kernels behind, also without a status word
-    for (int h = tid; h <= a.H + 1; h += kPlanThreads) a.head[h] = 0;
+    no_units();
     return;
   }
   const long long rows = (long long)a.cu[a.B] * a.g;

@@ -63,3 +63,24 @@ def test_a_branch_of_almost_2_31_positions(m, dtype, branches, new):
     assert bool(((lse[0].double() - rl).abs() <= d + sums * 1.01 + 2.0 ** -22 * rl.abs()).all())
     assert bool(((out[0].double() - ref).abs() <= (rounding + 3 * d + (sums + products) * 1.2) * ref).all())
     assert float(rl[:new].min()) > math.log(last) - X                     # a bound that a lost branch cannot meet
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_set_status_stops_a_planned_call_on_a_workspace_of_any_content(m, dtype):
+    """The status word is set before the call, which has more row tiles than go
+    without a plan: no list of the workspace is read that was not written."""
+    H, N, D, page = 2, 9000, 64, 64
+    pages = m.PagedKV(H, D, page, 150, 1, 150, dtype)
+    pages.table.copy_(torch.arange(150, dtype=I32)[None])
+    pages.len.fill_(N)
+    q = torch.randn(H, N, D, device="cuda").to(dtype)
+    cu = torch.tensor([0, N], dtype=I32, device="cuda")
+    ws = torch.full((m.branch_workspace_size(H, H, N, D),), 0x7f, dtype=torch.uint8, device="cuda")
+    out, lse = torch.full_like(q, 5.0), torch.full((H, N), 5.0, device="cuda")
+    st = torch.full((1,), 18, dtype=I32, device="cuda")
+    m.fastar_branch_attention(q, cu, None, pages, 0.1, out, lse=lse, block=1, ws=ws, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 18 and bool((out == 5.0).all()) and bool((lse == 5.0).all())
+    st.zero_()  # the same call on the same workspace with a clear word
+    m.fastar_branch_attention(q, cu, None, pages, 0.1, out, lse=lse, block=1, ws=ws, status=st)
+    assert int(st) == 0 and bool((out[:, :, 0] != 5.0).any()) and bool(torch.isfinite(lse).all())
