@@ -608,7 +608,9 @@ typedef struct {
  * heads; NULL and 0: none): rotated into q_out [Hq][N][D].  Rows of the pages
  * and of q_out that no token owns stay as they were.  A position outside the
  * table, or a page id outside 0..n_pages-1, sets FASTAR_ERR_DEVICE_ARG and
- * that token is skipped.  Two tokens of one call must not share a row.
+ * that token is skipped; the other tokens of the call are written (also, in
+ * such a call, where the word held FASTAR_ERR_DEVICE_ARG before).  Two tokens
+ * of one call must not share a row.
  */
 int fastar_page_append(const fastar_pages* pages, const void* k, int64_t k_head,
                        int64_t k_token, const void* v, int64_t v_head,

@@ -81,6 +81,29 @@ __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
   y = a * s + b * c;
 }
 
+// Row of position len - back of branch b in the pages of head 0; -1: the position
+// is outside the table or its page outside the pool.
+__device__ __forceinline__ int page_row_of(const AppendArgs& ap, int b, int len, int back) {
+  const int slot = len - back, pi = slot >> ap.page_shift;
+  if (slot < 0 || pi >= ap.max_pages) return -1;
+  const int id = ap.table[(size_t)b * ap.max_pages + pi];
+  if (id < 0 || id >= ap.n_pages) return -1;
+  return ((id * ap.H) << ap.page_shift) + (slot & ((1 << ap.page_shift) - 1));
+}
+
+// Whether some token of the call has no place (whole warp, offsets checked): a
+// branch at a time, a lane per page.
+__device__ __noinline__ bool some_token_lacks_a_place(const AppendArgs ap) {
+  bool bad = false;
+  for (int b = 0; b < ap.B; ++b) {
+    const int len = ap.len[b], n = ap.cu[b + 1] - ap.cu[b];
+    for (int back = n - ((threadIdx.x & 31) << ap.page_shift); back > 0 && !bad; back -= 32 << ap.page_shift)
+      bad = page_row_of(ap, b, len, back) < 0;
+    if (n > 0) bad = bad || page_row_of(ap, b, len, 1) < 0;
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
 template <typename T, bool kHalves, bool kAppend>
 __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant__ fastar_rope_plan plan, int D,
                                                         const RopeArgs a, const AppendArgs ap, int32_t* st) {
@@ -91,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
   const int tid = threadIdx.x;
   const int lt = tid / items, i = tid % items;
   const int n0 = blockIdx.x * toks, n = n0 + lt;
-  bool bad = status_bad(st);
+  const int32_t word = st ? *(volatile const int32_t*)st : 0;
   int page_row = -1;  // row of the token in its page, over all pages of head 0
   bool live = n < a.N;
   if constexpr (kAppend) {
@@ -113,25 +136,27 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
       }
     }
     if (bad_cu) status_set(st, FASTAR_ERR_DEVICE_ARG);
-    bad = __syncthreads_or(bad || bad_cu) != 0;
+    bad_cu = __syncthreads_or(bad_cu) != 0;
     const int b = s_branch[lt];
     live = live && b >= 0;
     if (live) {
-      const int slot = ap.len[b] - s_count[lt] + (n - s_first[lt]);
-      const int pi = slot >> ap.page_shift;
-      bool ok = slot >= 0 && pi < ap.max_pages;
-      if (ok) {
-        const int id = ap.table[(size_t)b * ap.max_pages + pi];
-        ok = id >= 0 && id < ap.n_pages;
-        if (ok) page_row = ((id * ap.H) << ap.page_shift) + (slot & ((1 << ap.page_shift) - 1));
-      }
-      if (!ok) {
+      page_row = page_row_of(ap, b, ap.len[b], s_count[lt] - (n - s_first[lt]));
+      if (page_row < 0) {
         status_set(st, FASTAR_ERR_DEVICE_ARG);
         live = false;
       }
     }
+    if (bad_cu) return;
+    // A warp that started before may have set the word, for a token of this very
+    // call that has no place: that token alone is skipped.  (The places are
+    // looked through only where the word is set; without a barrier, since one in
+    // this branch made the whole kernel slower: a chunk 62 us instead of 59.)
+    const bool set = __any_sync(0xffffffffu, word != 0);
+    if (set && (__any_sync(0xffffffffu, word != 0 && word != FASTAR_ERR_DEVICE_ARG) || !some_token_lacks_a_place(ap))) return;
+  } else if (word != 0) {
+    return;
   }
-  if (bad || !live) return;
+  if (!live) return;
 
   // the item's channels and the sines and cosines of its pairs
   int ca, cb;

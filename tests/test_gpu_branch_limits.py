@@ -84,3 +84,62 @@ def test_a_set_status_stops_a_planned_call_on_a_workspace_of_any_content(m, dtyp
     st.zero_()  # the same call on the same workspace with a clear word
     m.fastar_branch_attention(q, cu, None, pages, 0.1, out, lse=lse, block=1, ws=ws, status=st)
     assert int(st) == 0 and bool((out[:, :, 0] != 5.0).any()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (F32, 64)])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("bad", [-1, 2 ** 31 - 1])
+def test_append_skips_the_tokens_of_a_bad_page_and_no_others(m, dtype, D, where, bad):
+    """Several waves of CTAs: the ones that start after the status word was set
+    by a token of the same call go on."""
+    H, Hq, page, per, B = 12, 3, 64, 5000, 8
+    most = -(-per // page)
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    rows = torch.randn(B * per, Hq + 2 * H, D, generator=gen, device="cuda").to(dtype).transpose(0, 1)
+    q, k, v = rows[:Hq], rows[Hq:Hq + H], rows[Hq + H:]
+    cu = torch.arange(0, B * per + 1, per, dtype=I32, device="cuda")
+    table = torch.arange(B * most, dtype=I32, device="cuda").view(B, most)
+    at = {"first": (0, 0), "middle": (3, most // 2), "last": (B - 1, most - 1)}[where]
+    pos = torch.arange(B * per, dtype=I32, device="cuda")[:, None]
+    plan = m.RopePlan(D, (D,))
+
+    def append(t):
+        pages = m.PagedKV(H, D, page, B * most, B, most, dtype)
+        pages.K.fill_(7.0), pages.V.fill_(7.0)
+        pages.table.copy_(t)
+        pages.len.fill_(per)
+        q_out, st = torch.full((Hq, B * per, D), 7.0, dtype=dtype, device="cuda"), torch.zeros(1, dtype=I32, device="cuda")
+        m.fastar_page_append(pages, k, v, cu, pos=pos, plan=plan, q=q, q_out=q_out, status=st)
+        return pages.K, pages.V, q_out, int(st)
+
+    K, V, q_out, st = append(table)
+    assert st == 0
+    mine = int(table[at])                            # nobody else has that page
+    first = at[0] * per + at[1] * page
+    K[mine] = V[mine] = 7.0
+    q_out[:, first:min(first + page, (at[0] + 1) * per)] = 7.0
+    spoiled = table.clone()
+    spoiled[at] = bad
+    for _ in range(5):
+        got = append(spoiled)
+        assert got[3] == 18
+        assert torch.equal(got[0], K) and torch.equal(got[1], V) and torch.equal(got[2], q_out)
+
+
+def test_append_writes_nothing_where_the_status_was_set_before(m):
+    pages = m.PagedKV(2, 64, 16, 8, 2, 4)
+    pages.table.copy_(torch.arange(8, dtype=I32).view(2, 4))
+    pages.len.fill_(20)
+    k, cu = torch.ones(2, 40, 64, dtype=BF, device="cuda"), torch.tensor([0, 20, 40], dtype=I32, device="cuda")
+    for word in (16, 17, 18):
+        st = torch.full((1,), word, dtype=I32, device="cuda")
+        m.fastar_page_append(pages, k, k, cu, status=st)
+        assert int(st) == word and not bool(pages.K.any()) and not bool(pages.V.any())
+    for word in (16, 17):  # with a bad page of its own, too
+        pages.table[1, 0] = -1
+        st = torch.full((1,), word, dtype=I32, device="cuda")
+        m.fastar_page_append(pages, k, k, cu, status=st)
+        assert int(st) == word and not bool(pages.K.any())
+    pages.table[1, 0] = 4
+    m.fastar_page_append(pages, k, k, cu)
+    assert bool((pages.K[:, :, 0] == 1).any())
