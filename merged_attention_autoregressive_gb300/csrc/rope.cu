@@ -82,10 +82,11 @@ __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
 }
 
 // Row of position len - back of branch b in the pages of head 0; -1: the position
-// is outside the table or its page outside the pool.
+// is outside the table (as all are of a negative length, whose difference may
+// come round to a positive one) or its page outside the pool.
 __device__ __forceinline__ int page_row_of(const AppendArgs& ap, int b, int len, int back) {
   const int slot = len - back, pi = slot >> ap.page_shift;
-  if (slot < 0 || pi >= ap.max_pages) return -1;
+  if (len < 0 || slot < 0 || pi >= ap.max_pages) return -1;
   const int id = ap.table[(size_t)b * ap.max_pages + pi];
   if (id < 0 || id >= ap.n_pages) return -1;
   return ((id * ap.H) << ap.page_shift) + (slot & ((1 << ap.page_shift) - 1));

@@ -143,3 +143,19 @@ def test_append_writes_nothing_where_the_status_was_set_before(m):
     pages.table[1, 0] = 4
     m.fastar_page_append(pages, k, k, cu)
     assert bool((pages.K[:, :, 0] == 1).any())
+
+
+def test_append_refuses_every_position_of_a_negative_length(m):
+    """A table of 2^31 - 64 positions: len - n must not come round to its end."""
+    page, most, n = 64, 2 ** 25 - 1, 100
+    pages = m.PagedKV(1, 64, page, 2, 2, 1)
+    pages.table = torch.zeros(2, most, dtype=I32, device="cuda")
+    pages.table[1, 0] = 1
+    k, cu = torch.ones(1, n + 1, 64, dtype=BF, device="cuda"), torch.tensor([0, n, n + 1], dtype=I32, device="cuda")
+    for length in (-2 ** 31, -2 ** 31 + 60, -1):
+        pages.len.copy_(torch.tensor([length, 1], dtype=I32))
+        pages.K.zero_()
+        st = torch.zeros(1, dtype=I32, device="cuda")
+        m.fastar_page_append(pages, k, k, cu, status=st)
+        assert int(st) == 18 and not bool(pages.K[0].any())
+        assert bool((pages.K[1, 0, 0] == 1).all())   # the other branch's token
