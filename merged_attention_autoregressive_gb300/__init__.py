@@ -705,10 +705,12 @@ def fastar_branch_attention(q, cu, prefix: Prefix | None, pages: PagedKV, scale,
     if prefix is not None and prefix.device != dev:
         raise ValueError("tensors must be on one GPU")
     if ws is None:
-        ws = torch.empty(max(1, branch_workspace_size(Hq, pages.H, N, D)), dtype=torch.uint8, device=q.device)
-        if stream is not None:  # the allocator must not hand it out again before that stream is done with it
-            ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                             torch.cuda.ExternalStream(int(_stream(stream)), device=q.device))
+        # from the pool of the call's stream: a free block of another stream's may
+        # still be in use there
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(_stream(stream)), device=q.device)
+        with torch.cuda.stream(stream):
+            ws = torch.empty(max(1, branch_workspace_size(Hq, pages.H, N, D)), dtype=torch.uint8, device=q.device)
     rc = _on(dev, stream, (_lib or lib()).fastar_branch_attention, pages.struct.dt, _at(q, dev), Hq, N,
              _int32(cu, pages.B + 1, dev, "cu"), None if prefix is None else prefix.addr, pages.addr, scale, block,
              _at(out, dev), _at(lse, dev), _at(ws, dev), ws.numel() * ws.element_size(), _at(status, dev))

@@ -159,3 +159,27 @@ def test_append_refuses_every_position_of_a_negative_length(m):
         m.fastar_page_append(pages, k, k, cu, status=st)
         assert int(st) == 18 and not bool(pages.K[0].any())
         assert bool((pages.K[1, 0, 0] == 1).all())   # the other branch's token
+
+
+@pytest.mark.parametrize("kind", ["none", "stream", "handle"])
+def test_a_workspace_of_the_call_belongs_to_its_stream(m, monkeypatch, kind):
+    """A block of the current stream's pool may still be in use there by a
+    tensor that has been freed, so the allocation is made on the call's stream."""
+    side = torch.cuda.Stream()
+    pages = m.PagedKV(1, 64, 16, 2, 1, 2)
+    pages.len.fill_(20)
+    q, cu = torch.ones(1, 20, 64, dtype=BF, device="cuda"), torch.tensor([0, 20], dtype=I32, device="cuda")
+    out = torch.zeros_like(q)
+    torch.cuda.synchronize()
+    made, empty = [], torch.empty
+
+    def spy(*a, **kw):
+        made.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", spy)
+    stream = {"none": None, "stream": side, "handle": side.cuda_stream}[kind]
+    before = torch.cuda.current_stream()
+    m.fastar_branch_attention(q, cu, None, pages, 0.1, out, stream=stream)
+    assert made == [before.cuda_stream if stream is None else side.cuda_stream]
+    assert torch.cuda.current_stream() == before
