@@ -448,6 +448,8 @@ class BranchRollout:
         self.lengths = [0] * B
         self.held = [[] for _ in range(B)]           # page ids of each branch
         self.free = list(range(self.pages.n_pages))[::-1]
+        # the fills above are over before another stream's `extend` or `step`
+        torch.cuda.current_stream(dev).synchronize()
 
     def extend(self, new, stream=None):
         """Make room for new[b] more positions of each branch: the next step's

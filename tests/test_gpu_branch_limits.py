@@ -183,3 +183,23 @@ def test_a_workspace_of_the_call_belongs_to_its_stream(m, monkeypatch, kind):
     m.fastar_branch_attention(q, cu, None, pages, 0.1, out, stream=stream)
     assert made == [before.cuda_stream if stream is None else side.cuda_stream]
     assert torch.cuda.current_stream() == before
+
+
+def test_a_rollout_may_be_used_on_another_stream_at_once(m):
+    """The buffers of a rollout are filled on the stream that is current when it
+    is made; a step on another stream does not run ahead of that."""
+    from merged_attention_autoregressive_gb300.path import BranchRollout
+    gen = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn(2, 20, 64, generator=gen).to(BF).cuda() for _ in range(3))
+    side = torch.cuda.Stream()
+    got = []
+    for stream in (None, side):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(400_000_000)  # the current stream is busy for a fraction of a second
+        r = BranchRollout(2, 2, 64, 20, 32, page=16, block=1)
+        r.extend([13, 7], stream=stream)
+        out, lse = r.step(q, k, v, stream=stream)
+        torch.cuda.synchronize()
+        assert r.cu.tolist() == [0, 13, 20] and r.pages.len.tolist() == [13, 7] and int(r.status) == 0
+        got.append((out.clone(), lse.clone(), r.pages.K.clone()))
+    assert bool(got[0][0].any()) and all(torch.equal(a, b) for a, b in zip(*got))
