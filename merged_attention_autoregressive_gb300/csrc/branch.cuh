@@ -17,6 +17,8 @@
 // the units first and each CTA finds its place in them by searching.
 #pragma once
 
+#include <math.h>
+
 #include "common.cuh"
 
 namespace fastar {
@@ -205,6 +207,13 @@ struct BranchPlace {
     if (!ok && lane == 0) status_set(st, FASTAR_ERR_DEVICE_ARG);
     if (!ok || nt == 0) U = 0;
   }
+  // Units of the longest item of a call of one row tile (the sizes are in L1).
+  __device__ __forceinline__ int longest_item(const BranchArgs& a) const {
+    int v = 0;
+#pragma unroll 1
+    for (int h = threadIdx.x & 31; h < a.H; h += 32) v = max(v, prefix_size(a, h));
+    return key_units(__reduce_max_sync(0xffffffffu, v), a.TN) + pages_of(a, 0);
+  }
   // Page units of row tile t.
   __device__ __forceinline__ int pages_of(const BranchArgs& a, int t) const {
     if (a.planned) return (int)(a.tile[t + 1] - a.tile[t]);
@@ -304,7 +313,28 @@ struct BranchCut {
   static __device__ __forceinline__ int part(int len, int p, int n) { return (unsigned)len * (unsigned)p / (unsigned)n; }
 };
 
+// Parts of each of `items` items of U units together, the longest of `longest`,
+// on G runs; 0: an even cut of all units instead.
+//
+// Few items: each in the same number of equal parts, when that makes a run at
+// most kTwoItems units longer than an even cut of all units would.  An even cut
+// gives some runs the end of an item and the begin of the next, and the queries,
+// first softmax and output of two items cost that much more (4 branches of one
+// token, 12 heads, 28 units each: 19.6 us, 18.2 us in parts).  The longest item
+// decides: heads of a merged cache differ in their live rows.
+//
+// A part more saves a share of the units' time and costs the join about 0.1 us:
+// len / p units of 0.75 us (5 us on the FP32 pipes) and p of those are least near
+// p = sqrt(8 len) (sqrt(48 len)).  One token of 2 heads, 22 units: 15.5 us in 13
+// parts, 16.5 us in 16, 24 us in 76.
 constexpr int kTwoItems = 4;
+__host__ __device__ inline int branch_parts(long long U, int longest, int items, int G, bool fp32) {
+  if (U >= (1 << 23)) return 0;
+  const unsigned n = (unsigned)(G / items), u = (unsigned)U, g = (unsigned)G;
+  if (((unsigned)longest + n - 1) / n > (u + g - 1) / g + kTwoItems) return 0;
+  const int best = (int)ceilf(sqrtf((fp32 ? 48.f : 8.f) * (float)longest));
+  return best < 1 ? 1 : best < (int)n ? best : (int)n;
+}
 
 // Walks the units of run c, a whole warp in step, a stretch of units of one
 // branch (or of the prefix) at a time.
@@ -366,24 +396,8 @@ struct BranchWalk {
         for (int i = threadIdx.x & 31; i < a.H * a.ntiles; i += 32) a.cuts[i].h = -1;
       return false;
     }
-    // Few items: each in the same number of equal parts, when that makes a run
-    // at most kTwoItems units longer than an even cut of all units would.  An
-    // even cut gives some runs the end of an item and the begin of the next,
-    // and the queries, first softmax and output of two items cost that much
-    // more (4 branches of one token, 12 heads, 28 units each: 19.6 us, 18.2 us
-    // in parts).
     parts = 0;
-    if (a.by_item && !a.whole && a.ntiles == 1) {
-      const int items = a.H, n = a.G / items;
-      if (U < (1 << 23) && (unsigned)U / (unsigned)(items * n) <= (unsigned)U / (unsigned)a.G + kTwoItems) {
-        // A part more saves a share of the units' time and costs the join
-        // about 0.1 us: len / p units of 0.75 us (5 us on the FP32 pipes) and p
-        // of those are least near p = sqrt(8 len) (sqrt(48 len)).  One token of
-        // 2 heads, 22 units: 15.5 us in 13 parts, 16.5 us in 16, 24 us in 76.
-        const float len = (float)((unsigned)U / (unsigned)items);
-        parts = max(1, min(n, (int)ceilf(sqrtf((a.TM == 64 ? 48.f : 8.f) * len))));
-      }
-    }
+    if (a.by_item && !a.whole && a.ntiles == 1) parts = branch_parts(U, place.longest_item(a), a.H, a.G, a.TM == 64);
     if (parts) {
       h = c / parts;
       t = 0;

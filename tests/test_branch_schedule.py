@@ -1,6 +1,8 @@
 """The schedule rules of fastar_branch_attention, evaluated on the host: the
 same functions that the kernels call, compiled into a small program."""
+import math
 import os
+import random
 import subprocess
 
 import pytest
@@ -17,6 +19,11 @@ int main() {
       int keys, TN;
       if (scanf("%d %d", &keys, &TN) != 2) return 1;
       printf("%d\n", key_units(keys, TN));
+    } else if (!strcmp(what, "parts")) {
+      long long U;
+      int longest, items, G, fp32;
+      if (scanf("%lld %d %d %d %d", &U, &longest, &items, &G, &fp32) != 5) return 1;
+      printf("%d\n", branch_parts(U, longest, items, G, fp32 != 0));
     } else {
       return 1;
     }
@@ -50,3 +57,48 @@ def test_units_of_any_number_of_keys(ask):
                                                   2 ** 31 - 128, 2 ** 31 - 127, 2 ** 31 - 64, 2 ** 31 - 1)]
     got = ask(*[("key_units", n, TN) for n, TN in cases])
     assert [g[0] for g in got] == [-(-n // TN) for n, TN in cases]
+
+
+UNEVEN = [
+    [257] + [10] * 39,               # one head full, the others near empty
+    [257] + [20] * 11,
+    [1000, 1],
+    [28] * 12,
+    [301] * 40,
+    [22, 22],
+    [1] * 152,
+    [2 ** 22, 2 ** 21],
+    [0 + 1, 2 ** 22],
+]
+
+
+def test_equal_parts_are_bounded_by_the_longest_item(ask):
+    """In parts, the longest run is at most 4 units longer than the even cut's,
+    or the parts are as few as the join's cost asks for."""
+    rng = random.Random(3)
+    cases = [(units, fp32) for units in UNEVEN for fp32 in (0, 1)]
+    for _ in range(500):
+        items = rng.choice((1, 2, 3, 5, 8, 12, 24, 40, 76, 100, 152))
+        top = 2 ** rng.randint(0, 12)
+        cases.append(([1 + (rng.randrange(top) if rng.random() < 0.5 else top // 7) for _ in range(items)], rng.randint(0, 1)))
+    got = ask(*[("parts", sum(u), max(u), len(u), 304 if fp32 else 152, fp32) for u, fp32 in cases])
+    cut = 0
+    for (units, fp32), (parts,) in zip(cases, got):
+        G = 304 if fp32 else 152
+        n, even = G // len(units), -(-sum(units) // G)
+        assert 0 <= parts <= n
+        if parts == 0:
+            cut += 1
+            continue
+        wanted = math.ceil(math.sqrt((48 if fp32 else 8) * max(units)))
+        assert parts == min(n, wanted) or abs(parts - wanted) <= 1
+        assert -(-max(units) // n) <= even + 4
+        if parts == n:
+            assert -(-max(units) // parts) <= even + 4
+    assert 0 < cut < len(cases)
+
+
+def test_parts_of_the_measured_calls(ask):
+    # 12 heads of 28 units; 2 heads of 22; one head full beside near empty ones; 40 heads of 301
+    assert ask(("parts", 336, 28, 12, 152, 0), ("parts", 44, 22, 2, 152, 0), ("parts", 647, 257, 40, 152, 0),
+               ("parts", 477, 257, 12, 152, 0), ("parts", 12040, 301, 40, 152, 0)) == [[12], [14], [0], [0], [0]]
