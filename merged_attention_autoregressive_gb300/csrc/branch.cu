@@ -357,11 +357,8 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   a.slot_rows = x.slot_rows;
   const long long units = key_units(a.C, a.TN) + a.B * (((long long)a.max_pages << a.page_shift) / a.TN + 1);
   a.planned = a.ntiles > kMaxTiles || (a.ntiles > kFewTiles && a.B > kMaxBranches) || units > kFewUnits / a.ntiles;
-  // Short items (a few microseconds each) are not cut where there are enough
-  // of them: the join costs more than the imbalance (9 ragged prompts of up to
-  // 858 keys, 256 items: 30 us, 38 us when cut).
   const long long items = (long long)a.H * a.ntiles;
-  a.whole = items >= a.G && (keys + a.TN - 1) / a.TN <= 8;
+  a.whole = branch_whole(items, a.G, a.TM, a.TN, rows, a.B, a.C, own);
   a.item_units = a.whole ? kItemUnits : 0;
   a.by_item = items <= a.G;
   char* w = (char*)ws;

@@ -313,6 +313,32 @@ struct BranchCut {
   static __device__ __forceinline__ int part(int len, int p, int n) { return (unsigned)len * (unsigned)p / (unsigned)n; }
 };
 
+// Whether the items of a call are left whole: short items (a few microseconds
+// each) are not cut where there are enough of them, since partials and join cost
+// more than the imbalance (9 ragged prompts of up to 858 keys, 4 heads, 256
+// items: 29.5 us, 36.6 us when cut; 40 prompts of 200 tokens over 300, 12 heads:
+// 90 and 104 us; 300 of 20 over 300: 154 and 168 us).  rows: of all tokens of a
+// head; B: branches; own: positions that a branch has room for.
+//
+// An item holds the keys of every branch with tokens in its row tile, `units` of
+// them where the branches share the rows evenly.  Whole, some run takes one item
+// more than others: that is weighed against the cut's cost (2,560 single tokens
+// of 8 heads over 1,024 keys each, 160 items: 2.63 ms whole, 1.52 ms cut; fp32,
+// whose units take 5 us: 16 prompts of 250 tokens, 8 heads 150 and 131 us).
+// Branches of about one tile of rows on average are likely to be long ones beside
+// short ones, and then a few tiles hold most of the keys (7 single tokens and a
+// prompt of 1,024 tokens, 40 heads, causal: 125 us whole, 87 us cut).
+constexpr int kWholeKeys = 8, kWholeUnits = 24;  // units of one branch, of an item
+__host__ __device__ inline bool branch_whole(long long items, int G, int TM, int TN, long long rows, int B, int C,
+                                             long long own) {
+  if (items < G || (C + own + TN - 1) / TN > kWholeKeys) return false;
+  const long long others = B * (long long)TM / rows;  // branches of a tile beside the first
+  const long long units = key_units(C, TN) + (others + 1) * ((own + TN - 1) / TN);
+  if (units > kWholeUnits || (others == 0 && 2 * rows < 3ll * TM * B)) return false;
+  const long long cut = TN == 64 ? 2 : 12;  // partials and join, in units
+  return (items + G - 1) / G * units * G <= items * units + cut * G;
+}
+
 // Parts of each of `items` items of U units together, the longest of `longest`,
 // on G runs; 0: an even cut of all units instead.
 //

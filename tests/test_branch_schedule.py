@@ -24,6 +24,11 @@ int main() {
       int longest, items, G, fp32;
       if (scanf("%lld %d %d %d %d", &U, &longest, &items, &G, &fp32) != 5) return 1;
       printf("%d\n", branch_parts(U, longest, items, G, fp32 != 0));
+    } else if (!strcmp(what, "whole")) {
+      long long items, rows, own;
+      int G, TM, TN, B, C;
+      if (scanf("%lld %d %d %d %lld %d %d %lld", &items, &G, &TM, &TN, &rows, &B, &C, &own) != 8) return 1;
+      printf("%d\n", branch_whole(items, G, TM, TN, rows, B, C, own) ? 1 : 0);
     } else {
       return 1;
     }
@@ -102,3 +107,31 @@ def test_parts_of_the_measured_calls(ask):
     # 12 heads of 28 units; 2 heads of 22; one head full beside near empty ones; 40 heads of 301
     assert ask(("parts", 336, 28, 12, 152, 0), ("parts", 44, 22, 2, 152, 0), ("parts", 647, 257, 40, 152, 0),
                ("parts", 477, 257, 12, 152, 0), ("parts", 12040, 301, 40, 152, 0)) == [[12], [14], [0], [0], [0]]
+
+
+def _whole(H, g, new, own, C=0, fp32=False):
+    """The rule's arguments for branches of `new` tokens with room for `own`."""
+    TM, TN, G = (64, 64, 304) if fp32 else (128, 128, 152)
+    rows = sum(new) * g
+    return ("whole", H * -(-rows // TM), G, TM, TN, rows, len(new), C, own)
+
+
+def test_items_are_left_whole_where_they_are_short(ask):
+    ragged = [int(601 * ((b * 7919 + 104729) % 9973) / 9973) for b in range(9)]
+    cases = [
+        (_whole(4, 3, ragged, 864), 1),                              # as measured beside the rule
+        (_whole(12, 1, [200] * 40, 512), 1),
+        (_whole(12, 1, [20] * 300, 320), 1),
+        (_whole(8, 1, [1] * 2560, 1024), 0),                         # 128 branches to a tile
+        (_whole(40, 1, [1] * 640, 512), 0),
+        (_whole(40, 1, [1] * 7 + [1024], 1024), 0),                  # long beside short
+        (_whole(40, 1, [1] * 8 + [1000], 1024), 0),
+        (_whole(8, 1, [250] * 16, 400, fp32=True), 0),
+        (_whole(8, 1, [1] * 2560, 500, fp32=True), 0),
+        (_whole(4, 3, ragged, 2048), 0),                             # long keys
+        (_whole(4, 3, ragged, 200, C=900), 0),
+        (_whole(1, 1, ragged, 864), 0),                              # few items
+        (("whole", 2 ** 44, 152, 128, 128, 2 ** 31 - 300, 2 ** 31 - 300, 2 ** 31 - 1, 2 ** 31 - 256), 0),  # no overflow
+    ]
+    got = ask(*[c for c, _ in cases])
+    assert [g[0] for g in got] == [want for _, want in cases]

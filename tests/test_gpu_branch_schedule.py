@@ -33,3 +33,15 @@ def test_heads_of_different_lengths(m, dtype, D, H, g, new, past, C, rest):
         k.masked_fill_(dead, float("nan"))
         v.masked_fill_(dead, float("inf"))
         T._check_attention(m, dtype, q, cu, (k, v, cnt, size), pages, D ** -0.5, 0, cu_h, length, table)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,H,g,new,past,C,block", [
+    (64, 8, 1, [1] * 2560, [90, 0, 31, 400] * 640, 0, 0),        # 128 branches to a tile, more items than CTAs
+    (128, 5, 2, [1] * 1300, list(range(130)) * 10, 130, 1),
+    (64, 40, 1, [1] * 7 + [600], [500] * 7 + [20], 0, 1),        # single tokens beside a prompt
+    (64, 12, 1, [20] * 120, list(range(0, 240, 2)), 0, 1),       # several short prompts to a tile
+])
+def test_many_branches_to_a_tile(m, dtype, D, H, g, new, past, C, block):
+    q, cu, prefix, pages, cu_h, length, table = T._attention_case(m, dtype, D, H, g, 64, new, past, C, True, block, 3, seed=32)
+    T._check_attention(m, dtype, q, cu, prefix, pages, D ** -0.5, block, cu_h, length, table)
