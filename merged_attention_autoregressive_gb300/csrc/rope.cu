@@ -81,6 +81,24 @@ __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
   y = a * s + b * c;
 }
 
+// Sine and cosine of t / 2^32 of a turn.  32-bit rows: the nearest quarter turn
+// is taken off in integers, so that the rest, at most 1/4 half turn, is rounded
+// by 2^-27 and not by 2^-25 half turns (the error of an angle is pi times that,
+// 2.3e-8); bf16 rows round far above either.
+template <typename T>
+__device__ __forceinline__ void sincos_turn(uint32_t t, float& s, float& c) {
+  constexpr float kStep = 4.656612873077393e-10f;  // 2^-31: half turns
+  if constexpr (sizeof(T) == 4) {
+    const uint32_t k = (t + 0x20000000u) >> 30;
+    float a, b;
+    sincospif((float)(int32_t)(t - (k << 30)) * kStep, &a, &b);
+    s = __uint_as_float(__float_as_uint(k & 1 ? b : a) ^ (k << 30 & 0x80000000u));
+    c = __uint_as_float(__float_as_uint(k & 1 ? a : b) ^ ((k + 1) << 30 & 0x80000000u));
+  } else {
+    sincospif((float)(int32_t)t * kStep, &s, &c);
+  }
+}
+
 // Row of position len - back of branch b in the pages of head 0; -1: the position
 // is outside the table (as all are of a negative length, whose difference may
 // come round to a positive one) or its page outside the pool.
@@ -175,8 +193,7 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
       if (p < plan.pairs) {
         const int64_t x = a.pos[(size_t)n * plan.axes + plan.axis[p]];
         const uint64_t frac = plan.turn[p] * (uint64_t)x;  // of a turn, modulo 1
-        const float half_turns = (float)(int32_t)(frac >> 32) * 4.656612873077393e-10f;  // 2^-31
-        sincospif(half_turns, &sn[e], &cs[e]);
+        sincos_turn<T>((uint32_t)(frac >> 32), sn[e], cs[e]);
         sn[e] = __uint_as_float(__float_as_uint(sn[e]) ^ a.flip);
       }
     }

@@ -203,3 +203,60 @@ def test_a_rollout_may_be_used_on_another_stream_at_once(m):
         assert r.cu.tolist() == [0, 13, 20] and r.pages.len.tolist() == [13, 7] and int(r.status) == 0
         got.append((out.clone(), lse.clone(), r.pages.K.clone()))
     assert bool(got[0][0].any()) and all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rotation_in_32_bits_keeps_the_bits_of_the_angle(m, inverse):
+    """Rows (1, 0) turn into cosines and sines.  From the nearest quarter turn the
+    rest of the angle is at most 1/4 half turn, 2^-27 of a half turn off as a
+    32-bit number (pi 2^-27 in the angle) and 2^-31 by the fixed-point product's
+    lower half, which is dropped; sine and cosine of it are within one unit in the
+    last place."""
+    import numpy as np
+    D, N = 64, 30000
+    plan = m.RopePlan(D, (D,), base=500.0)
+    gen = torch.Generator().manual_seed(3)
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (N, 1), generator=gen, dtype=torch.int64)
+    pos[:200, 0] = torch.arange(-100, 100)
+    x = torch.zeros(1, N, D, device="cuda")
+    x[..., 0::2] = 1.0
+    y = torch.empty_like(x)
+    m.fastar_rope(x, pos.to(torch.int32).cuda(), plan, y, inverse=inverse)
+    turn = np.array(list(plan.struct.turn)[:D // 2], dtype=np.uint64)
+    with np.errstate(over="ignore"):
+        frac = pos.numpy().astype(np.int64).view(np.uint64) * turn[None]             # of a turn, modulo 1
+    quarter = (frac + np.uint64(1 << 61)) >> np.uint64(62)
+    rest = (frac - (quarter << np.uint64(62))).view(np.int64) * (2.0 * np.pi / 2.0 ** 64)
+    s, c = np.sin(rest), np.cos(rest)
+    k = quarter.astype(np.int64)
+    sin = np.choose(k, (s, c, -s, -c)) * (-1.0 if inverse else 1.0)
+    cos = np.choose(k, (c, -s, -c, s))
+    got = y[0].double().cpu().numpy()
+    for ref, g in ((cos, got[:, 0::2]), (sin, got[:, 1::2])):
+        tol = np.spacing(np.abs(ref).astype(np.float32)).astype(np.float64) + np.pi * 2.0 ** -27 + np.pi * 2.0 ** -31
+        err = np.abs(g - ref)
+        assert (err <= tol).all(), f"worst {(err / tol).max():.3g} of the bound"
+
+
+@pytest.mark.parametrize("dtype,D,dims,pairing", [(BF, 128, (44, 42, 42), "adjacent"), (F32, 64, (32, 16), "halves")])
+def test_rotation_there_and_back(m, dtype, D, dims, pairing):
+    """The inverse undoes the rotation: each way products and sum round in 32
+    bits (2^-20 of |x0| + |x1| with the angle's error) and once to the type."""
+    gen = torch.Generator().manual_seed(7)
+    x = torch.randn(5, 300, D, generator=gen).to(dtype).cuda()
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (300, len(dims)), generator=gen, dtype=torch.int64).to(torch.int32).cuda()
+    plan, y = m.RopePlan(D, dims, pairing=pairing), x.clone()
+    m.fastar_rope(y, pos, plan, y)
+    assert not torch.equal(y, x)
+    m.fastar_rope(y, pos, plan, y, inverse=True)
+    turned = sum(dims)
+    z, back = x[..., :turned].double(), y[..., :turned].double()
+    if pairing == "halves":
+        size = z.abs().unflatten(-1, (2, -1)).sum(-2).repeat(1, 1, 2)
+    else:
+        size = z.abs().unflatten(-1, (-1, 2)).sum(-1, keepdim=True).expand(-1, -1, -1, 2).flatten(-2)
+    half = torch.finfo(dtype).eps / 2
+    # a pair's turned values are at most |x0| + |x1| each, and come back through a sine and a cosine
+    tol = 2 * 1.01 * (2.0 ** -20 + half) * size + half * z.abs() * 1.01
+    assert bool(((back - z).abs() <= tol).all())
+    assert torch.equal(y[..., turned:], x[..., turned:])
