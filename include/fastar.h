@@ -651,10 +651,11 @@ typedef struct {
  *
  * q [Hq][N][D] dt, out [Hq][N][D] dt, optional lse [Hq][N] float; rows of
  * padding tokens are not written.  out must not overlap an input.  prefix
- * NULL: none.  What lies behind
- * size[h] and behind the positions that a branch sees may hold anything.
- * Values that some token sees must be finite (a hidden value times 0 is
- * added where another token of the call sees it).
+ * NULL: none.  scale is positive and finite.  What lies behind size[h] and
+ * behind the positions that a branch sees may hold anything.  Values that some
+ * token sees must be finite (a hidden value times 0 is added where another
+ * token of the call sees it); fp32: where another token of the same branch
+ * sees it, so that a branch never changes another one's results.
  * ws: fastar_workspace_size(FASTAR_OP_BRANCH, Hq, N, D, H, 0, 0) bytes; two
  * calls that may overlap need one each.  bf16: probabilities are rounded to
  * bf16 for the product with the values; scores, statistics and sums are fp32.

@@ -237,11 +237,13 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
     if (x.branch < 0 && a.m && sm.bias[g][tid >> 2] == -INFINITY)
       for (int c = tid & 3; c < RV; c += 4)
         *reinterpret_cast<float4*>(&sm.V[g][tid >> 2][c * VN]) = make_float4(0.f, 0.f, 0.f, 0.f);
+    int sees = 0;  // rows that see a key of the unit, or are nobody's
     if (busy) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = r0 + ty * 4 + i;
         const int seen = x.flags & 16 ? kTN : r < rows ? branch_row_keys(a, x, r) : 0;
+        sees |= (seen > 0 || r >= rows ? 1 : 0) << i;
         float top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
     }
     __syncthreads();
     if (tid < 32 && !last) describe(n + 2);  // in the place of this unit, of which everybody has a copy
-    if (busy) {
+    if (sees == 15) {
 #pragma unroll 2
       for (int k = 0; k < kTN; k += 4) {
         float4 pv[4];
@@ -292,6 +294,27 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
           }
         }
       }
+    } else if (sees) {
+      // a unit of another branch leaves a row as it is, also where its values
+      // are no numbers (a weight of 0 would not)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (sees >> i & 1) {
+#pragma unroll 2
+          for (int k = 0; k < kTN; k += 4) {
+            const float4 pv = *reinterpret_cast<const float4*>(&P[ty * 4 + i][k]);
+#pragma unroll
+            for (int c = 0; c < OC / 4; ++c) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const float4 v = *reinterpret_cast<const float4*>(&sm.V[g][k + kk][tx * 4 + 64 * c]);
+                const float p = kk == 0 ? pv.x : kk == 1 ? pv.y : kk == 2 ? pv.z : pv.w;
+                fma_pair(o[i][4 * c], o[i][4 * c + 1], p, p, v.x, v.y);
+                fma_pair(o[i][4 * c + 2], o[i][4 * c + 3], p, p, v.z, v.w);
+              }
+            }
+          }
+        }
     }
     if (x.flags & 2) {
 #pragma unroll
