@@ -652,10 +652,10 @@ typedef struct {
  * q [Hq][N][D] dt, out [Hq][N][D] dt, optional lse [Hq][N] float; rows of
  * padding tokens are not written.  out must not overlap an input.  prefix
  * NULL: none.  scale is positive and finite.  What lies behind size[h] and
- * behind the positions that a branch sees may hold anything.  Values that some
- * token sees must be finite (a hidden value times 0 is added where another
- * token of the call sees it); fp32: where another token of the same branch
- * sees it, so that a branch never changes another one's results.
+ * behind the positions that a branch sees may hold anything.  A branch's keys
+ * and values, finite or not, change no other branch's results.  Within one
+ * branch, values that some token of the call sees must be finite (a value that
+ * is hidden from a token takes part with weight 0 where another one sees it).
  * ws: fastar_workspace_size(FASTAR_OP_BRANCH, Hq, N, D, H, 0, 0) bytes; two
  * calls that may overlap need one each.  bf16: probabilities are rounded to
  * bf16 for the product with the values; scores, statistics and sums are fp32.

@@ -22,6 +22,12 @@
 // Both halves of a row keep one maximum, raised (and O in TMEM rescaled) only
 // when a unit's exceeds it by more than 2^8, so P stays <= 256, rescaling is
 // rare, and otherwise the two warps of a row only meet at a barrier.
+// A unit of a branch's pages leaves the lanes of O of other branches' rows out
+// of its second product: with a weight of 0 an infinity or NaN among its values
+// would reach them.  The masks cost 0 to 4 % of a call of many branches (16
+// tokens of 40 heads 134 -> 136 us, 64 of 5 heads a group 110.0 -> 111.4 us, 42 of
+// 12 heads over 4,096 + 1,205 keys 68.4 -> 71.1 us).
+//
 // S, maxima, sums and O are fp32; P is rounded to bf16 for the second product
 // (2^-8 of each weight at most, as the inputs themselves; the sums take the
 // unrounded weights).
@@ -67,6 +73,10 @@ constexpr int kBiased = 8;     // the keys have biases
 constexpr int kFirst = 16, kLast = 32;  // of the item, in this run
 constexpr int kEnd = 64;       // no unit: the run is over
 constexpr int kHidden = 128;   // some of the keys' counts are 0
+constexpr int kPart = 256;     // it concerns some rows of the item only: these, 9 bits each
+__device__ __forceinline__ int part_of(int lo, int hi) { return kPart | lo << 9 | hi << 18; }
+__device__ __forceinline__ int part_lo(int bits) { return bits >> 9 & 511; }
+__device__ __forceinline__ int part_hi(int bits) { return bits >> 18 & 511; }
 
 template <int D>
 struct Shape {
@@ -141,6 +151,13 @@ __device__ __forceinline__ void hidden_keys(const float* bias, int bits, int nk,
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     hidden[i] = __ballot_sync(0xffffffffu, lane + 32 * i < nk && bias[lane + 32 * i] == -INFINITY);
+}
+
+// The lanes of a 128-row tile outside rows lo .. hi - 1, a bit each.
+__device__ __forceinline__ void lanes_outside(int lo, int hi, uint32_t (&off)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) off[i] = __ballot_sync(0xffffffffu, lane + 32 * i < lo || lane + 32 * i >= hi);
 }
 
 template <int D, bool split>
@@ -240,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         full_keys = x.lo * a.g <= r0 && (x.lo + x.n) * a.g >= min(r0 + a.TM, rows)
                         ? branch_limit(r0 / a.g - x.lo, x.n, x.len, a.block)
                         : 0;
+      const int part = lo < hi && (lo > r0 || hi < min(r0 + a.TM, rows)) ? part_of(lo - r0, hi - r0) : 0;
       const int acts = hi <= lo ? 0 : split ? 1 : ((lo < r0 + kM ? 1 : 0) | (hi > r0 + kM ? 2 : 0));
       // page id of box `lane` (or the counts of rows lane + 32 e) of the unit
       // at k, fetched one unit ahead
@@ -281,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         if (lane == 0) {
           Desc& d = sm.desc[ds];
           d.x = x;
-          d.bits = act | (x.nk == kN && x.k0 + kN <= full_keys ? kFull : 0) | (!own && counts ? kBiased : 0) | (hidden ? kHidden : 0) |
+          d.bits = act | part | (x.nk == kN && x.k0 + kN <= full_keys ? kFull : 0) | (!own && counts ? kBiased : 0) | (hidden ? kHidden : 0) |
                    (opens && i == 0 ? kFirst : 0) | (closes && i == count - 1 ? kLast : 0);
         }
         __syncwarp();
@@ -371,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     int pk = 0;                      // its keys
     bool pclear = false;             // some value rows have to be cleared
     uint32_t phidden[4];             // its hidden keys
+    int pbits = 0;                   // its descriptor's
     uint32_t acc = 0u;               // 0: O starts anew
     bool issued = false;
     auto pv = [&]() {
@@ -379,7 +398,18 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       tc::tc_fence_after();
       const uint32_t vd = tc::desc_low(ring_addr + pslot * S::kTile, kN * 128);
       if (pclear) clear_rows<D>(ring + (size_t)(base + pslot) * S::kTile, pk, phidden);
-      if (pk == kN) {
+      if (pbits & kPart) {
+        // O was cleared where this is the first (see the softmax)
+        const int steps = (pk + 15) / 16;
+        uint32_t off[4];
+        lanes_outside(part_lo(pbits), part_hi(pbits), off);
+        if (tc::elect_one()) {
+#pragma unroll 2
+          for (int k = 0; k < steps; ++k)
+            tc::mma_bf16_tmem_a_low_rows(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv, 1u, off);
+          tc::mma_commit(&empty[pslot]);
+        }
+      } else if (pk == kN) {
         if (tc::elect_one()) {
 #pragma unroll
           for (int k = 0; k < kN / 16; ++k)
@@ -445,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         pphase = vphase;
         pk = nk;
         pclear = (nk & 15) || (bits & kHidden);
+        pbits = bits;
 #pragma unroll
         for (int i = 0; i < 4; ++i) phidden[i] = hidden[i];
       }
@@ -484,6 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     int pend = 0, pk = 0;
     uint32_t pslot = 0, pphase = 0, np = 0u, acc = 0u;  // np, acc: a bit per stream
     bool pclear = false;                                // some value rows have to be cleared
+    int pbits = 0;                                      // its descriptor's
     uint32_t phidden[4], hidden[4];                     // hidden keys, of the tile and of the unit read
     bool issued = false;
     auto values = [&]() {
@@ -504,10 +536,17 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         acc |= 1u << s;
         pend &= ~(1 << s);
       }
+      uint32_t off[4];
+      if (pbits & kPart) lanes_outside(part_lo(pbits) - s * kM, part_hi(pbits) - s * kM, off);
       tc::tc_fence_after();
       if (leader && ok) {
         if (old) {
-          if (pk == kN) {
+          if (pbits & kPart) {
+            const int steps = (pk + 15) / 16;
+#pragma unroll 2
+            for (int k = 0; k < steps; ++k)
+              tc::mma_bf16_tmem_a_low_rows(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv, 1u, off);
+          } else if (pk == kN) {
 #pragma unroll
             for (int k = 0; k < kN / 16; ++k)
               tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv,
@@ -574,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         pend = uact;
         pk = unk;
         pclear = (unk & 15) || (ubits & kHidden);
+        pbits = ubits;
 #pragma unroll
         for (int i = 0; i < 4; ++i) phidden[i] = uhidden[i];
         pslot = slot + 1 == slots ? 0 : slot + 1;
@@ -657,6 +697,15 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
           // one branch among others): computed unmasked, and dropped at the end
           none = split && seen <= 0;
           all = __all_sync(0xffffffffu, none || seen >= 64);
+        }
+        if (!started && (bits & kPart)) {
+          // the product with the values leaves the other rows' O as it is, so
+          // that no value of one branch reaches another's: here O begins at 0
+          uint32_t zero[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) zero[i] = 0u;
+#pragma unroll 1
+          for (int q = 0; q < D / 64; ++q) tc::tmem_st32u(tO + q * 32, zero);
         }
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sfull[s], ns & 1u));
         if (!ok) break;

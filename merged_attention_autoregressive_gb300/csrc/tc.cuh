@@ -282,6 +282,20 @@ __device__ __forceinline__ void mma_bf16_tmem_a_low(uint32_t d_tmem, uint32_t a_
       : "memory");
 }
 
+// mma_bf16_tmem_a_low without the lanes of D whose bits are set in `off`: they
+// stay as they are.
+__device__ __forceinline__ void mma_bf16_tmem_a_low_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t blow, uint32_t idesc,
+                                                         uint32_t accumulate, const uint32_t (&off)[4]) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, {%6, %7, %8, %9}, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blow), "r"(idesc), "r"(accumulate), "r"(kDescHigh), "r"(off[0]), "r"(off[1]), "r"(off[2]),
+      "r"(off[3])
+      : "memory");
+}
+
 // 32 lanes x 32 columns (32-bit): thread i of the warp gets lane (base + i),
 // columns col .. col+31.  The load and its wait are one asm statement, so no
 // register is read before the data has arrived.

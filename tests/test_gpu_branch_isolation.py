@@ -31,7 +31,7 @@ def m():
 
 
 @pytest.mark.parametrize("case", range(len(CASES)))
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_a_spoiled_branch_leaves_the_others_as_they_are(m, case, dtype):
     D, H, g, page, new, past, C, counts, block, pad = CASES[case]
     q, cu, prefix, pages, cu_h, length, table = T._attention_case(m, dtype, D, H, g, page, new, past, C, counts, block,
