@@ -24,9 +24,10 @@
 // rare, and otherwise the two warps of a row only meet at a barrier.
 // A unit of a branch's pages leaves the lanes of O of other branches' rows out
 // of its second product: with a weight of 0 an infinity or NaN among its values
-// would reach them.  The masks cost 0 to 4 % of a call of many branches (16
-// tokens of 40 heads 134 -> 136 us, 64 of 5 heads a group 110.0 -> 111.4 us, 42 of
-// 12 heads over 4,096 + 1,205 keys 68.4 -> 71.1 us).
+// would reach them.  Those products are slower to issue, which costs a call of
+// many branches 0 to 5 % (16 tokens of 40 heads 133.6 -> 136 us, 64 of 5 heads a
+// group 110.0 -> 111.5 us, 512 of them over 32,768 + 256 keys 407 -> 413 us, 128 of
+// them 131 -> 138 us).
 //
 // S, maxima, sums and O are fp32; P is rounded to bf16 for the second product
 // (2^-8 of each weight at most, as the inputs themselves; the sums take the
@@ -153,11 +154,23 @@ __device__ __forceinline__ void hidden_keys(const float* bias, int bits, int nk,
     hidden[i] = __ballot_sync(0xffffffffu, lane + 32 * i < nk && bias[lane + 32 * i] == -INFINITY);
 }
 
-// The lanes of a 128-row tile outside rows lo .. hi - 1, a bit each.
+// The lanes of a 128-row tile outside rows lo .. hi - 1, a bit each (whole warp).
 __device__ __forceinline__ void lanes_outside(int lo, int hi, uint32_t (&off)[4]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < 4; ++i) off[i] = __ballot_sync(0xffffffffu, lane + 32 * i < lo || lane + 32 * i >= hi);
+}
+// The product with the values for rows lo .. hi - 1 alone (one thread): a function
+// of its own, so that the issue of the other products is as if it were not there
+// (two branches of 4,680 tokens 1.93 ms, 1.97 ms with it in line).
+__device__ __noinline__ void part_products(uint32_t dO, uint32_t dS, uint32_t vd, uint32_t idesc, int steps, int lo, int hi) {
+  auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+  uint32_t off[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) off[i] = ~below(hi - 32 * i) | below(lo - 32 * i);
+#pragma unroll 2
+  for (int k = 0; k < steps; ++k)
+    tc::mma_bf16_tmem_a_low_rows(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc, 1u, off);
 }
 
 template <int D, bool split>
@@ -516,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
     uint32_t pslot = 0, pphase = 0, np = 0u, acc = 0u;  // np, acc: a bit per stream
     bool pclear = false;                                // some value rows have to be cleared
     int pbits = 0;                                      // its descriptor's
+    bool pfast = false;                                 // all of its keys, for all rows
     uint32_t phidden[4], hidden[4];                     // hidden keys, of the tile and of the unit read
     bool issued = false;
     auto values = [&]() {
@@ -536,26 +550,23 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         acc |= 1u << s;
         pend &= ~(1 << s);
       }
-      uint32_t off[4];
-      if (pbits & kPart) lanes_outside(part_lo(pbits) - s * kM, part_hi(pbits) - s * kM, off);
       tc::tc_fence_after();
       if (leader && ok) {
         if (old) {
-          if (pbits & kPart) {
-            const int steps = (pk + 15) / 16;
-#pragma unroll 2
-            for (int k = 0; k < steps; ++k)
-              tc::mma_bf16_tmem_a_low_rows(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv, 1u, off);
-          } else if (pk == kN) {
+          if (pfast) {
 #pragma unroll
             for (int k = 0; k < kN / 16; ++k)
               tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv,
                                       k > 0 ? 1u : ac);
           } else {
             const int steps = (pk + 15) / 16;
-            for (int k = 0; k < steps; ++k)
-              tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv,
-                                      k > 0 ? 1u : ac);
+            if (pbits & kPart) {
+              part_products(dO, dS, vd, idesc_pv, steps, part_lo(pbits) - s * kM, part_hi(pbits) - s * kM);
+            } else {
+              for (int k = 0; k < steps; ++k)
+                tc::mma_bf16_tmem_a_low(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc_pv,
+                                        k > 0 ? 1u : ac);
+            }
           }
           if (pend == 0) tc::mma_commit(&sm.empty[pslot]);  // no stream wants the tile any more
         }
@@ -614,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         pk = unk;
         pclear = (unk & 15) || (ubits & kHidden);
         pbits = ubits;
+        pfast = unk == kN && !(ubits & kPart);
 #pragma unroll
         for (int i = 0; i < 4; ++i) phidden[i] = uhidden[i];
         pslot = slot + 1 == slots ? 0 : slot + 1;
