@@ -312,7 +312,8 @@ class ChunkPath:
     def branches(self, B, tokens, max_len, **kw):
         """B rollouts that continue this layer's merged history (its cache is
         read, not written): a BranchRollout over the live groups with their
-        + ln m.  Arguments as for BranchRollout."""
+        + ln m.  Arguments as for BranchRollout; the scale is this layer's."""
+        kw.setdefault("scale", self.scale)
         return BranchRollout(B, self.H, self.D, tokens, max_len, prefix=Prefix.of(self.cache),
                              dtype=self.dtype, device=self.q_codes.device, **kw)
 

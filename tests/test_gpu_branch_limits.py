@@ -260,3 +260,11 @@ def test_rotation_there_and_back(m, dtype, D, dims, pairing):
     tol = 2 * 1.01 * (2.0 ** -20 + half) * size + half * z.abs() * 1.01
     assert bool(((back - z).abs() <= tol).all())
     assert torch.equal(y[..., turned:], x[..., turned:])
+
+
+def test_branches_of_a_layer_attend_with_its_scale(m):
+    from merged_attention_autoregressive_gb300.path import ChunkPath
+    p = ChunkPath(2, 64, 32, 1, 8, 2, 4, 64, 0.9)
+    assert p.branches(1, 8, 32).scale == 0.125
+    p.scale = 0.3
+    assert p.branches(1, 8, 32).scale == 0.3 and p.branches(1, 8, 32, scale=0.2).scale == 0.2
