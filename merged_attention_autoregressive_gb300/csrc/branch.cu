@@ -249,8 +249,8 @@ int launch_branch_combine(const BranchArgs& a, fastar_dtype dt, int32_t* st, cud
   const int warps = kJoinThreads / 32;
   const dim3 grid(a.by_item ? a.H * a.ntiles : a.G, ((rows + 7) / 8 * (a.D / 16) + warps - 1) / warps);
   // four where items have more than eight parts (4 tokens of 12 heads, 12 parts:
-  // 17.8 us, 18.1 us by two), else two (64 tokens of 5 heads a group, about 7
-  // parts: 111 us, 113 us by four, which leaves room for fewer CTAs)
+  // 17.4 us, 17.8 us by two), else two (64 tokens of 5 heads a group, about 7
+  // parts: 111 us, 114 us by four, which leaves room for fewer CTAs)
   const bool many = a.by_item && a.G > 8 * a.H * a.ntiles;
   auto kernel = dt == FASTAR_BF16 ? (many ? branch_combine_kernel<__nv_bfloat16, 4> : branch_combine_kernel<__nv_bfloat16, 2>)
                                   : (many ? branch_combine_kernel<float, 4> : branch_combine_kernel<float, 2>);
@@ -266,7 +266,7 @@ int launch_branch_combine(const BranchArgs& a, fastar_dtype dt, int32_t* st, cud
 namespace {
 // Where items are not cut, a run's items count this many units each beside
 // their own: their queries, first softmax and output (9 ragged prompts, 256
-// items: 29.4 us; 31.3 us by units alone, 29.9 us at 6).
+// items: 29.5 us; 31.4 us by units alone, 29.6 us at 6).
 constexpr int kItemUnits = 3;
 // Units, runs and partials of a call.  bf16: one CTA per SM, 256 (wide) or
 // 128 rows and 128 keys; fp32: two CTAs per SM, 64 rows and 64 keys.
@@ -336,13 +336,14 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   // 256 rows per item pay where most of the keys concern most of them and the
   // runs are long: every tile that is loaded then feeds four products.  So
   // where a branch fills them (two branches of 4680 tokens, 12 heads, 42,000
-  // keys: 1.84 ms, 2.24 ms at 128 rows), or where the prefix is longer than
+  // keys: 1.92 ms, 2.33 ms at 128 rows), or where the prefix is longer than
   // the pages of all branches of an item together and few rows are padding
-  // (512 single tokens of 5 heads a group over 32,768 + up to 256 keys: 377 us,
-  // 433 us).  Otherwise most of a wide item idles while its pages pass (64 of
-  // those tokens, up to 2048 keys of their own: 129 us, 111 us at 128 rows),
-  // and short runs are latency alone (9 ragged prompts of up to 858 keys: 36
-  // us, 30 us).
+  // (512 single tokens of 5 heads a group over 32,768 + 256 keys: 413 us, 473
+  // us).  Otherwise most of a wide item idles while its pages pass (64 of those
+  // tokens, up to 2048 keys of their own: 137 us, 111 us at 128 rows), and short
+  // runs are latency alone (9 ragged prompts of up to 858 keys: 36.5 us, 29.6
+  // us).  Tables, prefix and N have room for as much; the lengths are not known
+  // here.
   const long long rows = (long long)N * a.g;
   const long long own = (long long)a.max_pages << a.page_shift, keys = a.C + own;
   const long long wide_tiles = (rows + 255) / 256, narrow_tiles = (rows + 127) / 128;

@@ -4,17 +4,24 @@
 // row r = token r / g, head h g + r % g: a row tile holds consecutive tokens,
 // so consecutive branches.  The keys of a row tile are the live prefix rows,
 // read once for every branch of the tile, followed by the page keys of each
-// branch that has tokens in the tile.  A unit is TN of those keys.  All units
-// of all (head, row tile) items are laid end to end, head after head, and cut
-// into G equal runs, one per CTA: the split along a long cache needs no
-// special case, no CTA waits for a longer one, and the cut depends on the
-// lengths alone, so results do not change from run to run.  An item inside
-// one run is finished there; one that is cut leaves a partial (O in fp32,
-// running max and sum) per run, and branch_combine joins them in order.
+// branch that has tokens in the tile.  A unit is TN of those keys.  The units of
+// all (head, row tile) items are laid end to end, head after head, and shared
+// out to G runs, one per CTA, in one of three ways:
+//   even   G equal runs, wherever they begin and end: the split along a long
+//          cache needs no special case, and no CTA waits for a longer one;
+//   parts  one row tile (single tokens): each head's item in the same number of
+//          equal parts, so that no run has two items (branch_parts);
+//   whole  many short items: a run ends where an item begins (branch_whole).
+// The cut depends on the lengths alone, so results do not change from run to
+// run.  An item inside one run is finished there; one that is cut leaves a
+// partial (O in fp32, running max and sum) per run, and branch_combine joins them
+// in order.
 //
-// The lengths live on the device.  With one row tile (single tokens) every
-// CTA sums the units itself; with more, branch_plan writes the prefix sums of
-// the units first and each CTA finds its place in them by searching.
+// The lengths live on the device.  Up to 8 row tiles, or 64 with at most 32
+// branches, every CTA sums the units itself; with more, or where tables and
+// prefix have room for more units than its integers hold (kFewUnits),
+// branch_plan writes the prefix sums of the units first and each CTA finds its
+// place in them by searching.
 #pragma once
 
 #include <math.h>
@@ -316,18 +323,18 @@ struct BranchCut {
 // Whether the items of a call are left whole: short items (a few microseconds
 // each) are not cut where there are enough of them, since partials and join cost
 // more than the imbalance (9 ragged prompts of up to 858 keys, 4 heads, 256
-// items: 29.5 us, 36.6 us when cut; 40 prompts of 200 tokens over 300, 12 heads:
-// 90 and 104 us; 300 of 20 over 300: 154 and 168 us).  rows: of all tokens of a
+// items: 29.6 us, 37.3 us when cut; 40 prompts of 200 tokens over 300, 12 heads:
+// 92 and 105 us; 300 of 20 over 300: 156 and 169 us).  rows: of all tokens of a
 // head; B: branches; own: positions that a branch has room for.
 //
 // An item holds the keys of every branch with tokens in its row tile, `units` of
 // them where the branches share the rows evenly.  Whole, some run takes one item
 // more than others: that is weighed against the cut's cost (2,560 single tokens
-// of 8 heads over 1,024 keys each, 160 items: 2.63 ms whole, 1.52 ms cut; fp32,
-// whose units take 5 us: 16 prompts of 250 tokens, 8 heads 150 and 131 us).
+// of 8 heads over 1,024 keys each, 160 items: 2.67 ms whole, 1.52 ms cut; fp32,
+// whose units take 5 us: 16 prompts of 250 tokens, 8 heads 149 and 130 us).
 // Branches of about one tile of rows on average are likely to be long ones beside
 // short ones, and then a few tiles hold most of the keys (7 single tokens and a
-// prompt of 1,024 tokens, 40 heads, causal: 125 us whole, 87 us cut).
+// prompt of 1,024 tokens, 40 heads, causal: 126 us whole, 89 us cut).
 constexpr int kWholeKeys = 8, kWholeUnits = 24;  // units of one branch, of an item
 __host__ __device__ inline bool branch_whole(long long items, int G, int TM, int TN, long long rows, int B, int C,
                                              long long own) {
@@ -346,13 +353,15 @@ __host__ __device__ inline bool branch_whole(long long items, int G, int TM, int
 // most kTwoItems units longer than an even cut of all units would.  An even cut
 // gives some runs the end of an item and the begin of the next, and the queries,
 // first softmax and output of two items cost that much more (4 branches of one
-// token, 12 heads, 28 units each: 19.6 us, 18.2 us in parts).  The longest item
-// decides: heads of a merged cache differ in their live rows.
+// token, 12 heads, 28 units each: 19.7 us, 17.4 us in parts).  The longest item
+// decides: heads of a merged cache differ in their live rows (40 heads, one of
+// 32,768 rows and the others of 1,200: 118 us in parts, 32 us by an even cut).
 //
 // A part more saves a share of the units' time and costs the join about 0.1 us:
 // len / p units of 0.75 us (5 us on the FP32 pipes) and p of those are least near
-// p = sqrt(8 len) (sqrt(48 len)).  One token of 2 heads, 22 units: 15.5 us in 13
-// parts, 16.5 us in 16, 24 us in 76.
+// p = sqrt(8 len) (sqrt(48 len)).  One token of 2 heads, 23 units: 14.9 us in 14
+// parts, 16.0 us in 17, 21.0 us in 76 (fp32, 45 units: 19.6 us in 47, 29.9 us in 17,
+// 31.7 us in 152).
 constexpr int kTwoItems = 4;
 __host__ __device__ inline int branch_parts(long long U, int longest, int items, int G, bool fp32) {
   if (U >= (1 << 23)) return 0;

@@ -9,7 +9,7 @@
 // two CTAs fit on an SM and one computes while the other waits or takes
 // exponentials.  Bound by the FP32 pipes and, where runs are short, by start
 // and join: three frames of 256 tokens, 4 heads of 64 channels over 1,536 keys
-// take 51 us, of which the multiply-adds are 16 us.
+// take 50 us, of which the multiply-adds are 16 us.
 #include <math.h>
 
 #include "branch.cuh"
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
   float m[4], l[4], o[4][OC];
   bool bad = false;
   // a unit's keys and values, straight into their stage, a row per thread
-  // (16-byte copies of all threads took 3800 cycles of a unit to issue: 42 tokens
-  // of 12 heads over 4096 + 1205 keys 459 us, 428 us by rows); its biases
+  // (16-byte copies of all threads took 3800 cycles of a unit to issue, 7 % of 42
+  // tokens of 12 heads over 4096 + 1205 keys); its biases
   auto load = [&](int n) {
     const BranchUnit& x = sm.unit[n & 1];
     const int g = kStages == 2 ? n & 1 : 0;
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
 #pragma unroll
       for (int j = 0; j < 4; ++j) s1[i][j] = 0.f;
     if (busy) {
-#pragma unroll 8  // (400 tokens of 8 / 4 heads, 128 channels: 188 us; 4: 194 us; 16: 189 us, and more code to fetch)
+#pragma unroll 4  // (42 single tokens of 12 heads over 4096 + 1205 keys: 414 us; 8: 423 us; 400 tokens of 8 / 4 heads: 196 us either way)
       for (int k = 0; k < D; k += 4) {
         float4 qv[4], kv[4];
 #pragma unroll

@@ -34,18 +34,18 @@
 // unrounded weights).
 //
 // What bounds it.  Single tokens: HBM where the loads are long (16 tokens of 40
-// heads over 13,460 keys: 750 MB in 133 us, 5.6 TB/s with start and join; the
+// heads over 13,460 keys: 750 MB in 136 us, 5.5 TB/s with start and join; the
 // copies of a run are issued by one warp at about HBM's rate, and more of them
-// in flight made some runs wait for others: 143 us), the chain of a stream
+// in flight made some runs wait for others: 7 % slower), the chain of a stream
 // where the prefix comes out of L2 (64 tokens of 5 heads a group: 1.2 us a
-// unit, 111 us), start and join where they are short (4 tokens: 18 us).  Wide
+// unit, 111 us), start and join where they are short (4 tokens: 17.4 us).  Wide
 // items: the chain of one stream - scores out of TMEM, biases, exponentials
 // (2000 cycles), two products of 512 cycles each and the handovers - against
 // 2048 cycles of products for both streams; 9360 queries of 12 heads over
-// 41,000 keys take 1.84 ms, 1230 TFLOP/s.  Beside the products, which read
+// 41,000 keys take 1.92 to 1.97 ms by the clock under that load, 1160 TFLOP/s.  Beside the products, which read
 // their operands from shared memory at its full rate, a 16-byte read of a bias
 // waits 33 cycles.  Units of 64 keys with the queries in TMEM (half of that
-// traffic) were slower: the handovers then come twice as often (2.29 ms).
+// traffic) were slower by a quarter: the handovers then come twice as often.
 //
 // Waits are bounded: one that runs out sets the status word, and every warp
 // leaves its loop by its own bounded waits.

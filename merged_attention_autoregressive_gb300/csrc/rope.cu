@@ -16,8 +16,8 @@
 // angle is taken once per token and head group, and every access of a warp is
 // 64 or 128 contiguous bytes per row on both sides whatever the strides.
 // Heads are split over grid y until the grid fills the GPU.  10800 tokens of 40
-// bf16 heads: 39.6 us, 5.6 TB/s; appended with their values and queries (18,720
-// tokens of 12 heads): 61 us, 5.7 TB/s; a few tokens: 4 to 5 us, a launch.
+// bf16 heads: 38.8 us, 5.7 TB/s; appended with their values and queries (18,720
+// tokens of 12 heads): 59.3 us, 5.8 TB/s; a few tokens: 4 to 5 us, a launch.
 #include <math.h>
 
 #include "common.cuh"
@@ -241,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
     if (h >= a.k.H) h -= a.k.H;
     return base + ((size_t)page_row + ((size_t)h << ap.page_shift)) * D;
   };
-  // streaming loads and stores: the rows pass through once (40 us for 10800
-  // tokens of 40 bf16 heads, 62 us with plain ones)
+  // streaming loads and stores: the rows pass through once (10800 tokens of 40
+  // bf16 heads 38.8 us, 61.3 us with plain ones; the append above 59.3 and 88.6 us)
   for (int h = h0; h < h1; h += kUnroll) {
     uint4 u[kUnroll], w[kUnroll];
 #pragma unroll
@@ -272,8 +272,9 @@ int launch_rope_t(const fastar_rope_plan& plan, int D, RopeArgs a, const AppendA
   const int total = a.q.H + a.k.H + a.v.H;
   // split the heads until about 32 CTAs per SM are there (the angles are taken
   // again by each part), in steps of the heads in flight: 10800 tokens of 40
-  // bf16 heads took 39.6 us so, 51 us at half the parts (the last of few waves
-  // runs alone) and 48 us at twice (the angles)
+  // bf16 heads take 38.8 us so and 45.9 us at twice the parts (the angles).  Half
+  // of them is as good: 38.3 us, 4680 tokens 19.4 against 22.9 us, but 20,000
+  // tokens 66.2 against 65.3 us and 64.3 against 62.8 us in fp32.
   int parts = (152 * 32 + gx - 1) / gx;
   int per = (total + parts - 1) / parts;
   per = (per + kUnroll - 1) / kUnroll * kUnroll;

@@ -426,11 +426,16 @@ class BranchRollout:
     lengths are counted on the host and copied to the device by `extend`;
     `step` itself can be captured in a graph between two `extend`s.
 
-    tokens: most tokens of one step, all branches together; max_len: most
-    positions of a branch; Hq: query heads (a multiple of H, default H); plan:
+    tokens: most tokens of one step, all branches together (every step's calls
+    are made for that many rows, so an object whose steps are much smaller than
+    its largest one pays for the difference); max_len: most positions of a
+    branch, whose table and pages are sized by it; Hq: query heads (a multiple of H, default H); plan:
     RopePlan (None: queries and keys are taken as they are); block: 0, every
     new token sees all positions of its branch, or n, those of its own and
-    earlier blocks of n positions (a frame's tokens, 1 for text)."""
+    earlier blocks of n positions (a frame's tokens, 1 for text).
+
+    Branches are independent: infinities and NaN among the keys and values of
+    one reach no other's outputs."""
 
     def __init__(self, B, H, D, tokens, max_len, prefix=None, Hq=None, page=64, n_pages=None, plan=None, block=0,
                  scale=None, dtype=torch.bfloat16, device="cuda"):
