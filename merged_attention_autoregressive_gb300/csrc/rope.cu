@@ -111,14 +111,23 @@ __device__ __forceinline__ int page_row_of(const AppendArgs& ap, int b, int len,
 }
 
 // Whether some token of the call has no place (whole warp, offsets checked): a
-// branch at a time, a lane per page.
+// branch per lane, and a page per lane for the pages between its first and last.
 __device__ __noinline__ bool some_token_lacks_a_place(const AppendArgs ap) {
+  const int lane = threadIdx.x & 31;
   bool bad = false;
-  for (int b = 0; b < ap.B; ++b) {
-    const int len = ap.len[b], n = ap.cu[b + 1] - ap.cu[b];
-    for (int back = n - ((threadIdx.x & 31) << ap.page_shift); back > 0 && !bad; back -= 32 << ap.page_shift)
-      bad = page_row_of(ap, b, len, back) < 0;
-    if (n > 0) bad = bad || page_row_of(ap, b, len, 1) < 0;
+  for (int b0 = 0; b0 < ap.B; b0 += 32) {
+    int len = 0, n = 0;
+    if (b0 + lane < ap.B) {
+      len = ap.len[b0 + lane];
+      n = ap.cu[b0 + lane + 1] - ap.cu[b0 + lane];
+    }
+    if (n > 0) bad = bad || page_row_of(ap, b0 + lane, len, n) < 0 || page_row_of(ap, b0 + lane, len, 1) < 0;
+    for (unsigned more = __ballot_sync(0xffffffffu, n > 1 << ap.page_shift); more; more &= more - 1) {
+      const int src = __ffs(more) - 1;
+      const int l = __shfl_sync(0xffffffffu, len, src);
+      for (int back = __shfl_sync(0xffffffffu, n, src) - (lane << ap.page_shift); back > 0; back -= 32 << ap.page_shift)
+        bad = bad || page_row_of(ap, b0 + src, l, back) < 0;
+    }
   }
   return __any_sync(0xffffffffu, bad);
 }

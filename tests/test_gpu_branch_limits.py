@@ -268,3 +268,33 @@ def test_branches_of_a_layer_attend_with_its_scale(m):
     assert p.branches(1, 8, 32).scale == 0.125
     p.scale = 0.3
     assert p.branches(1, 8, 32).scale == 0.3 and p.branches(1, 8, 32, scale=0.2).scale == 0.2
+
+
+@pytest.mark.parametrize("at", [0, 31, 32, 299, 777])
+def test_append_of_many_branches_skips_the_one_of_a_bad_page(m, at):
+    """A token each, and one branch with a prompt of several pages in front of them."""
+    B, H, D, page, prompt = 778, 24, 128, 16, 2000
+    new = [prompt] + [1] * (B - 1)
+    gen = torch.Generator(device="cuda").manual_seed(at)
+    N = sum(new)
+    rows = torch.randn(N, 2 * H, D, generator=gen, device="cuda").to(BF).transpose(0, 1)
+    cu = torch.tensor([0] + [prompt + i for i in range(B)], dtype=I32, device="cuda")
+    table = torch.zeros(B, prompt // page, dtype=I32, device="cuda")
+    table[0] = torch.arange(prompt // page)
+    table[1:, 0] = prompt // page + torch.arange(B - 1)
+    spoiled = table.clone()
+    spoiled[at, 70 if at == 0 else 0] = -5
+    got = []
+    for t in (table, spoiled, spoiled):
+        pages = m.PagedKV(H, D, page, prompt // page + B, B, prompt // page)
+        pages.table.copy_(t)
+        pages.len.copy_(torch.tensor(new, dtype=I32))
+        st = torch.zeros(1, dtype=I32, device="cuda")
+        m.fastar_page_append(pages, rows[:H], rows[H:], cu, status=st)
+        got.append((pages.K, pages.V, int(st)))
+    assert [g[2] for g in got] == [0, 18, 18]
+    mine = int(table[at, 70 if at == 0 else 0])
+    for i in (0, 1):
+        assert bool(got[0][i][mine].any())
+        got[0][i][mine] = 0.0
+        assert torch.equal(got[1][i], got[0][i]) and torch.equal(got[2][i], got[0][i])
