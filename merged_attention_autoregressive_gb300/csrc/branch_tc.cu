@@ -25,9 +25,9 @@
 // A unit of a branch's pages leaves the lanes of O of other branches' rows out
 // of its second product: with a weight of 0 an infinity or NaN among its values
 // would reach them.  Those products are slower to issue, which costs a call of
-// many branches 0 to 5 % (16 tokens of 40 heads 133.6 -> 136 us, 64 of 5 heads a
-// group 110.0 -> 111.5 us, 512 of them over 32,768 + 256 keys 407 -> 413 us, 128 of
-// them 131 -> 138 us).
+// many branches 0 to 5 % (16 tokens of 40 heads 133.6 -> 134.8 us, 64 of 5 heads a
+// group 110.1 -> 110.9 us, 512 of them over 32,768 + 256 keys 407 -> 414 us, 128 of
+// them 131 -> 139 us).
 //
 // S, maxima, sums and O are fp32; P is rounded to bf16 for the second product
 // (2^-8 of each weight at most, as the inputs themselves; the sums take the
@@ -159,6 +159,15 @@ __device__ __forceinline__ void lanes_outside(int lo, int hi, uint32_t (&off)[4]
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < 4; ++i) off[i] = __ballot_sync(0xffffffffu, lane + 32 * i < lo || lane + 32 * i >= hi);
+}
+// Zeros in 32 n columns of the thread's TMEM lane (whole warp); rare, and in
+// line its registers cost the softmax (16 tokens of 40 heads 136 us).
+__device__ __noinline__ void clear_lanes(uint32_t taddr, int n) {
+  uint32_t zero[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) zero[i] = 0u;
+#pragma unroll 1
+  for (int q = 0; q < n; ++q) tc::tmem_st32u(taddr + q * 32, zero);
 }
 // The product with the values for rows lo .. hi - 1 alone (one thread): a function
 // of its own, so that the issue of the other products is as if it were not there
@@ -713,11 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         if (!started && (bits & kPart)) {
           // the product with the values leaves the other rows' O as it is, so
           // that no value of one branch reaches another's: here O begins at 0
-          uint32_t zero[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) zero[i] = 0u;
-#pragma unroll 1
-          for (int q = 0; q < D / 64; ++q) tc::tmem_st32u(tO + q * 32, zero);
+          clear_lanes(tO, D / 64);
         }
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sfull[s], ns & 1u));
         if (!ok) break;
