@@ -338,7 +338,7 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   // where a branch fills them (two branches of 4680 tokens, 12 heads, 42,000
   // keys: 1.92 ms, 2.33 ms at 128 rows), or where the prefix is longer than
   // the pages of all branches of an item together and few rows are padding
-  // (512 single tokens of 5 heads a group over 32,768 + 256 keys: 413 us, 473
+  // (512 single tokens of 5 heads a group over 32,768 + 256 keys: 414 us, 473
   // us).  Otherwise most of a wide item idles while its pages pass (64 of those
   // tokens, up to 2048 keys of their own: 137 us, 111 us at 128 rows), and short
   // runs are latency alone (9 ragged prompts of up to 858 keys: 36.5 us, 29.6

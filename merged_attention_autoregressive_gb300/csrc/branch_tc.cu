@@ -34,7 +34,7 @@
 // unrounded weights).
 //
 // What bounds it.  Single tokens: HBM where the loads are long (16 tokens of 40
-// heads over 13,460 keys: 750 MB in 136 us, 5.5 TB/s with start and join; the
+// heads over 13,460 keys: 750 MB in 135 us, 5.6 TB/s with start and join; the
 // copies of a run are issued by one warp at about HBM's rate, and more of them
 // in flight made some runs wait for others: 7 % slower), the chain of a stream
 // where the prefix comes out of L2 (64 tokens of 5 heads a group: 1.2 us a
