@@ -671,6 +671,115 @@ int fastar_branch_attention(fastar_dtype dt, const void* q, int Hq, int N,
                             void* out, float* lse, void* ws, size_t ws_bytes,
                             int32_t* dev_status, cudaStream_t stream);
 
+/*
+ * fastar_tree_attention -- fastar_branch_attention of a tree of drafted tokens
+ * for each branch.
+ *
+ * Passage: as fastar_branch_attention; the paper decodes one token or chunk at a
+ * time and has no drafts.  The n_b new tokens of branch b hang on one another:
+ * parent [N] int32, counted within the branch, -1 <= parent[cu[b] + i] < i (-1:
+ * the token follows the last position before the drafts).  Token i stands at
+ * position len[b] - n_b + i of the pages and sees the prefix, every position
+ * before len[b] - n_b, itself and the drafts above it: parent(i),
+ * parent(parent(i)), ...  (Its rotary position is the caller's: siblings share
+ * one.)  Everything else, limits and workspace included, is as in
+ * fastar_branch_attention; a chain (parent i - 1) gives the results of block 1.
+ * A parent outside its range sets FASTAR_ERR_DEVICE_ARG.  Trees of tens to
+ * hundreds of drafts are meant: a token walks up its branch of the tree.
+ */
+int fastar_tree_attention(fastar_dtype dt, const void* q, int Hq, int N,
+                          const int32_t* cu, const int32_t* parent,
+                          const fastar_prefix* prefix, const fastar_pages* pages,
+                          float scale, void* out, float* lse, void* ws,
+                          size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * fastar_page_keep -- the new tokens that stay move to the front of the new
+ * positions, in order (the accepted path of a tree of drafts).
+ *
+ * Of branch b's n_b = cu[b+1] - cu[b] new tokens (the last positions of len[b]),
+ * those named by rows[cu_keep[b]] .. rows[cu_keep[b+1] - 1] stay: token ids in
+ * cu[b] .. cu[b+1] - 1, ascending.  The j-th of them moves to position len[b] -
+ * n_b + j, in all heads.  What lies behind the last one is unspecified; len itself
+ * is the caller's to count: len[b] - n_b + the number that stay.  rows [M] int32,
+ * cu_keep [B + 1] int32 ascending from 0, on the device.  Offsets, ids or
+ * positions out of range, or ids that do not ascend, set FASTAR_ERR_DEVICE_ARG;
+ * the pages of the branches then hold rows of either state.  Pages that new
+ * tokens lie in must not be shared.
+ */
+int fastar_page_keep(const fastar_pages* pages, const int32_t* cu,
+                     const int32_t* rows, int M, const int32_t* cu_keep,
+                     int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * What the rows of the pages have drawn: mass [n_pages][H][page] float, the
+ * attention weight of each row, summed over queries; born [n_pages][H][page]
+ * int32, the number of its token in the branch, and total [B] int32, the tokens
+ * that each branch has had so far, the new ones included.  born and total may both
+ * be NULL: the position of a row is then its age.  16-byte aligned.
+ */
+typedef struct {
+  float* mass;
+  int32_t* born;
+  const int32_t* total;
+} fastar_mass;
+
+/*
+ * fastar_page_mass -- add the attention weights of new tokens to the masses of
+ * the positions that they see.
+ *
+ *   w(i, p) = sum over the group's heads of exp(scale q_i . K_b[p] - lse_i)
+ *   mass(p) = (p < len[b] - n_b ? decay mass(p) : 0) + sum_i w(i, p)
+ *
+ * over the tokens i of branch b that see position p by the rule of
+ * fastar_branch_attention (block); lse is that call's, so that the weights are
+ * those with which the values were taken.  The new positions, the last n_b of
+ * len[b], start at 0 and get their token's number, born = total[b] - len[b] + p.
+ * A branch without new tokens stays as it is.
+ *
+ * q [Hq][N][D] and lse [Hq][N] float are rows of the attention call; token i of
+ * the M in cu is row rows[i] of them (NULL: row i, and M = N), e.g. the drafts
+ * that were accepted, after fastar_page_keep and with the new len.  A row whose
+ * lse is -inf adds nothing.  A key that is not finite spoils its own mass only, a
+ * query or lse that is not finite those of the positions that it sees.  Sums in
+ * fp32, in an order that does not change from call to call.  scale is positive
+ * and finite; decay is finite and not negative.  ws:
+ * fastar_workspace_size(FASTAR_OP_MASS, Hq, M, D, H, 0, 0) bytes; two calls that
+ * may overlap need one each.  Pages whose masses are written must not be shared.
+ * FASTAR_ERR_DEVICE_ARG: cu not ascending within 0..M, a length outside
+ * 0..max_pages * page, a row outside 0..N-1, a page id outside the pool.
+ */
+#define FASTAR_OP_MASS 8
+int fastar_page_mass(const fastar_pages* pages, const void* q, const float* lse,
+                     int Hq, int N, const int32_t* rows, int M, const int32_t* cu,
+                     float scale, int block, float decay, const fastar_mass* mass,
+                     void* ws, size_t ws_bytes, int32_t* dev_status,
+                     cudaStream_t stream);
+
+/*
+ * fastar_page_evict -- every branch and head keeps `budget` of its rows.
+ *
+ * A branch of len[b] > budget positions keeps, in each head, the rows of the
+ * first `first` and the last `recent` tokens (born < first, born >= total[b] -
+ * recent; without stamps positions p < first and p >= len[b] - recent), then those
+ * of the largest masses (a NaN is below every number; ties: lower position).
+ * Kept rows at positions below budget stay where they are; the others move, in
+ * order, into the places of the rows that go, also in order.  The heads of a
+ * branch keep different tokens; the rows' rotations go with them, so attention
+ * over the kept rows is as it was.  What lies at budget and behind is
+ * unspecified; len itself is the caller's to count: min(len[b], budget).
+ *
+ * Masses and stamps move with their rows; with `out` (other arrays, born given
+ * alike) the masses and stamps of the positions that are left are written there,
+ * and those of `mass` stay as they are.  0 <= first + recent <= budget;
+ * max_pages * page <= 2^19 (FASTAR_ERR_UNSUPPORTED).  A length or page id out of
+ * range sets FASTAR_ERR_DEVICE_ARG; the pages then hold rows of either state.
+ * Pages of branches that are over the budget must not be shared.
+ */
+int fastar_page_evict(const fastar_pages* pages, const fastar_mass* mass,
+                      int budget, int first, int recent, const fastar_mass* out,
+                      int32_t* dev_status, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,6 +24,7 @@ REPS = {"last": REP_LAST, "mean": REP_MEAN}
 SEARCH_PREV, SEARCH_LSH, SEARCH_QUANT = 0, 1, 2
 OP_QUANT = 6
 OP_BRANCH = 7
+OP_MASS = 8
 ROPE_MAX_AXES, ROPE_MAX_PAIRS = 4, 64
 PAIRINGS = {"adjacent": 0, "halves": 1}
 
@@ -48,7 +49,8 @@ EXPORTS = ["fastar_status_string", "fastar_version", "fastar_launch_count",
            "fastar_annsa_attention", "fastar_check_bounded_wait", "fastar_tempcache_merge_rep",
            "fastar_annsa_attention_part", "fastar_annsa_combine", "fastar_tempcache_merge_search",
            "fastar_annsa_quant_attention", "fastar_annca_quant_attention",
-           "fastar_rope_plan_init", "fastar_rope", "fastar_page_append", "fastar_branch_attention"]
+           "fastar_rope_plan_init", "fastar_rope", "fastar_page_append", "fastar_branch_attention",
+           "fastar_tree_attention", "fastar_page_keep", "fastar_page_mass", "fastar_page_evict"]
 
 
 class FastarError(RuntimeError):
@@ -84,6 +86,10 @@ class PrefixStruct(ctypes.Structure):
     _fields_ = [("H", ctypes.c_int), ("C", ctypes.c_int), ("D", ctypes.c_int), ("dt", ctypes.c_int),
                 ("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("m", ctypes.c_void_p),
                 ("size", ctypes.c_void_p)]
+
+
+class MassStruct(ctypes.Structure):
+    _fields_ = [("mass", ctypes.c_void_p), ("born", ctypes.c_void_p), ("total", ctypes.c_void_p)]
 
 
 _lib = None
@@ -146,6 +152,10 @@ def lib() -> ctypes.CDLL:
         L.fastar_page_append.argtypes = [_VP, _VP, _I64, _I64, _VP, _I64, _I64, _I, _VP, _VP, _VP, _VP, _I64, _I64,
                                          _I, _VP, _VP, _VP]
         L.fastar_branch_attention.argtypes = [_I, _VP, _I, _I, _VP, _VP, _VP, _F, _I, _VP, _VP, _VP, _SZ, _VP, _VP]
+        L.fastar_tree_attention.argtypes = [_I, _VP, _I, _I, _VP, _VP, _VP, _VP, _F, _VP, _VP, _VP, _SZ, _VP, _VP]
+        L.fastar_page_keep.argtypes = [_VP, _VP, _VP, _I, _VP, _VP, _VP]
+        L.fastar_page_mass.argtypes = [_VP, _VP, _VP, _I, _I, _VP, _I, _VP, _F, _I, _F, _VP, _VP, _SZ, _VP, _VP]
+        L.fastar_page_evict.argtypes = [_VP, _VP, _I, _I, _I, _VP, _VP, _VP]
         for name in EXPORTS[7:]:
             getattr(L, name).restype = _I
         _lib = L
@@ -696,6 +706,19 @@ def fastar_branch_attention(q, cu, prefix: Prefix | None, pages: PagedKV, scale,
     positions (1: causal).  ws: a uint8 device tensor of at least
     branch_workspace_size(Hq, H, N, D) bytes; one is allocated for the call
     when it is None."""
+    _attend("fastar_branch_attention", q, cu, None, prefix, pages, scale, out, lse, block, ws, status, stream)
+
+
+def _ws_on(stream, nbytes, device):
+    """A workspace from the pool of the call's stream: a free block of another
+    stream's may still be in use there."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(_stream(stream)), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(1, nbytes), dtype=torch.uint8, device=device)
+
+
+def _attend(name, q, cu, parent, prefix, pages, scale, out, lse, block, ws, status, stream):
     Hq, N, D = q.shape
     if out.shape != q.shape or not out.dtype == q.dtype == pages.dtype or D != pages.D:
         raise ValueError("q, out and the pages must agree in shape and dtype")
@@ -705,14 +728,131 @@ def fastar_branch_attention(q, cu, prefix: Prefix | None, pages: PagedKV, scale,
     if prefix is not None and prefix.device != dev:
         raise ValueError("tensors must be on one GPU")
     if ws is None:
-        # from the pool of the call's stream: a free block of another stream's may
-        # still be in use there
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(_stream(stream)), device=q.device)
-        with torch.cuda.stream(stream):
-            ws = torch.empty(max(1, branch_workspace_size(Hq, pages.H, N, D)), dtype=torch.uint8, device=q.device)
-    rc = _on(dev, stream, (_lib or lib()).fastar_branch_attention, pages.struct.dt, _at(q, dev), Hq, N,
-             _int32(cu, pages.B + 1, dev, "cu"), None if prefix is None else prefix.addr, pages.addr, scale, block,
-             _at(out, dev), _at(lse, dev), _at(ws, dev), ws.numel() * ws.element_size(), _at(status, dev))
+        ws = _ws_on(stream, branch_workspace_size(Hq, pages.H, N, D), q.device)
+    head = (pages.struct.dt, _at(q, dev), Hq, N, _int32(cu, pages.B + 1, dev, "cu"))
+    mid = (None if prefix is None else prefix.addr, pages.addr, scale)
+    last = (_at(out, dev), _at(lse, dev), _at(ws, dev), ws.numel() * ws.element_size(), _at(status, dev))
+    L = _lib or lib()
+    if parent is None:
+        rc = _on(dev, stream, L.fastar_branch_attention, *head, *mid, block, *last)
+    else:
+        rc = _on(dev, stream, L.fastar_tree_attention, *head, parent, *mid, *last)
     if rc:
-        raise FastarError(rc, "fastar_branch_attention")
+        raise FastarError(rc, name)
+
+
+def fastar_tree_attention(q, cu, parent, prefix: Prefix | None, pages: PagedKV, scale, out, lse=None, ws=None,
+                          status=None, stream=None):
+    """out [Hq][N][D] (and lse [Hq][N]): a tree of drafted tokens of every
+    branch over the shared prefix and the branch's own pages.
+
+    parent [N] int32: token cu[b] + i hangs on token parent[cu[b] + i] < i of its
+    branch, or (-1) on the last position before the drafts.  It sees the prefix,
+    every earlier position, itself and the tokens above it.  The rest is as in
+    fastar_branch_attention."""
+    N = q.shape[1]
+    _attend("fastar_tree_attention", q, cu, _int32(parent, N, pages.device, "parent"), prefix, pages, scale, out, lse, 1,
+            ws, status, stream)
+
+
+def fastar_page_keep(pages: PagedKV, cu, rows, cu_keep, status=None, stream=None):
+    """The new tokens rows[cu_keep[b]:cu_keep[b + 1]] of branch b (ids in cu[b] ..
+    cu[b + 1] - 1, ascending; int32 on the GPU) move to the front of its new
+    positions: the drafts that were accepted.  The caller then counts them in
+    pages.len."""
+    dev = pages.device
+    rc = _on(dev, stream, (_lib or lib()).fastar_page_keep, pages.addr, _int32(cu, pages.B + 1, dev, "cu"),
+             _int32(rows, rows.numel(), dev, "rows"), rows.numel(), _int32(cu_keep, pages.B + 1, dev, "cu_keep"),
+             _at(status, dev))
+    if rc:
+        raise FastarError(rc, "fastar_page_keep")
+
+
+class PageMass(_Bound):
+    """What the rows of a PagedKV have drawn: mass [n_pages][H][page] float32,
+    and, unless born is None, born [n_pages][H][page] int32, the number of each
+    row's token in its branch, with total [B] int32, the tokens that each branch
+    has had so far (the caller counts them, the new ones of a call included)."""
+    _tensors = ("mass", "born", "total")
+    _derived = ("device", "struct", "addr")
+
+    def __init__(self, pages: PagedKV, born=True):
+        dev = pages.K.device
+        shape = (pages.n_pages, pages.H, pages.page)
+        self._set(torch.zeros(shape, dtype=torch.float32, device=dev),
+                  torch.zeros(shape, dtype=torch.int32, device=dev) if born else None,
+                  torch.zeros(pages.B, dtype=torch.int32, device=dev) if born else None)
+
+    @classmethod
+    def view(cls, mass, born=None, total=None):
+        """Masses over existing tensors (nothing is allocated)."""
+        x = cls.__new__(cls)
+        x._set(mass, born, total)
+        return x
+
+    def _set(self, mass, born, total):
+        self.mass, self.born, self.total = mass, born, total
+        self._bind()
+
+    def _bind(self):
+        mass, born, total = self.mass, self.born, self.total
+        if mass.dtype is not torch.float32 or mass.dim() != 3:
+            raise ValueError("the masses are float32 [n_pages][H][page]")
+        if (born is None) != (total is None):
+            raise ValueError("born and total come together")
+        dev = _gpu(mass)
+        struct = MassStruct(_at(mass, dev), None if born is None else _int32(born, mass.numel(), dev, "born"),
+                            None if total is None else _int32(total, total.numel(), dev, "total"))
+        self.device, self.struct, self.addr = dev, struct, ctypes.addressof(struct)
+
+    def _fits(self, pages):
+        if self.mass.shape != (pages.n_pages, pages.H, pages.page) or self.device != pages.device:
+            raise ValueError("the masses do not fit the pages")
+        if self.total is not None and self.total.numel() != pages.B:
+            raise ValueError("total has an entry per branch")
+        return self.addr
+
+
+def mass_workspace_size(Hq: int, H: int, M: int, D: int) -> int:
+    """Bytes of workspace of fastar_page_mass for M tokens."""
+    return fastar_workspace_size(OP_MASS, Hq, M, D, H, 0, 0)
+
+
+def fastar_page_mass(pages: PagedKV, q, lse, cu, scale, mass: PageMass, block=0, rows=None, decay=1.0, ws=None,
+                     status=None, stream=None):
+    """Add to `mass` the attention weights exp(scale q.k - lse) of the tokens in cu
+    [B + 1] over the positions that they see (block as in
+    fastar_branch_attention); the new positions start at 0, the others' masses fade
+    by `decay` first.  q [Hq][N][D] and lse [Hq][N] are those of the attention
+    call; rows [M] int32 names the tokens' rows there (the drafts that were
+    accepted; by default all of them in order).  ws: a uint8 device tensor of at
+    least mass_workspace_size(Hq, H, M, D) bytes; one is allocated for the call
+    when it is None."""
+    Hq, N, D = q.shape
+    dev = pages.device
+    if q.dtype is not pages.dtype or D != pages.D:
+        raise ValueError("q does not fit the pages")
+    if lse.dtype is not torch.float32 or lse.shape != (Hq, N):
+        raise ValueError("lse must be float32 [Hq][N]")
+    M = N if rows is None else rows.numel()
+    if ws is None:
+        ws = _ws_on(stream, mass_workspace_size(Hq, pages.H, M, D), q.device)
+    rc = _on(dev, stream, (_lib or lib()).fastar_page_mass, pages.addr, _at(q, dev), _at(lse, dev), Hq, N,
+             None if rows is None else _int32(rows, M, dev, "rows"), M, _int32(cu, pages.B + 1, dev, "cu"), scale,
+             block, decay, mass._fits(pages), _at(ws, dev), ws.numel() * ws.element_size(), _at(status, dev))
+    if rc:
+        raise FastarError(rc, "fastar_page_mass")
+
+
+def fastar_page_evict(pages: PagedKV, mass: PageMass, budget, first=0, recent=0, out: PageMass | None = None,
+                      status=None, stream=None):
+    """Every branch of more than `budget` positions keeps, in each head, the rows of
+    its `first` first and `recent` last tokens and those of the largest masses,
+    `budget` in all; the kept rows behind the budget move into the places of those
+    that go.  The caller then counts min(len, budget) in pages.len.  The masses move
+    along in place, or into `out`."""
+    dev = pages.device
+    rc = _on(dev, stream, (_lib or lib()).fastar_page_evict, pages.addr, mass._fits(pages), budget, first, recent,
+             None if out is None else out._fits(pages), _at(status, dev))
+    if rc:
+        raise FastarError(rc, "fastar_page_evict")

@@ -303,8 +303,8 @@ size_t branch_ws_bytes(int Hq, int H, int N, int D) {
   return most;
 }
 
-int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* cu, const fastar_prefix* px,
-                  const fastar_pages* pg, float scale, int block, void* out, float* lse, void* ws, int32_t* st,
+int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* cu, const int32_t* parent,
+                  const fastar_prefix* px, const fastar_pages* pg, float scale, int block, void* out, float* lse, void* ws, int32_t* st,
                   cudaStream_t s) {
   BranchArgs a = {};
   a.q = q;
@@ -313,6 +313,7 @@ int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* 
   a.table = pg->table;
   a.K = pg->K;
   a.V = pg->V;
+  a.parent = parent;
   if (px) {
     a.pK = px->K;
     a.pV = px->V;

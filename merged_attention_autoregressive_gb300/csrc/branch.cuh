@@ -43,6 +43,7 @@ struct BranchArgs {
   const int32_t* size;    // [H] or null (C)
   const void* K;          // pages
   const void* V;
+  const int32_t* parent;  // [N] a tree of drafts (block is 1 then), or null
   int N, Hq, H, g, B, C, D, max_pages, page_shift, n_pages, block;
   float scale;
   void* out;
@@ -537,6 +538,34 @@ __device__ __forceinline__ int branch_row_keys(const BranchArgs& a, const Branch
   const int i = r / a.g - x.lo;
   if (i < 0 || i >= x.n) return 0;
   return max(0, min(x.nk, branch_limit(i, x.n, x.len, a.block) - x.k0));
+}
+
+// Drafts in a tree: token i of a branch sees the positions before the new tokens,
+// itself, and the tokens above it, i > parent(i) > parent(parent(i)) ... down to
+// -1.  All of them lie among the positions that it would see in a plain row of
+// tokens, so a tree has the schedule of block 1, and only units that hold new
+// tokens differ.  There a row walks up from its token, which is a read of L1 per
+// step (the rows of a warp share the list) and ends with the unit; no mask is
+// stored, and a branch may have any number of drafts.
+//
+// The keys from..from + 63 of unit x (from: 0 or 64) that row r of its item sees,
+// a bit each.  bad: a parent is not below its token; the walk ends there.
+__device__ __forceinline__ uint64_t tree_row_keys(const BranchArgs& a, const BranchUnit& x, int r, int from, bool& bad) {
+  auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
+  if (x.branch < 0) return below(x.nk - from);
+  const int i = r / a.g - x.lo;
+  if (i < 0 || i >= x.n) return 0ull;
+  const int past = x.len - x.n - x.k0 - from;  // keys before the drafts, counted from `from`
+  uint64_t seen = below(past);
+  if (past >= 64) return seen;
+  for (int j = i; past + j >= 0;) {
+    if (past + j < 64) seen |= 1ull << (past + j);
+    const int p = a.parent[x.lo + j];
+    if (p < -1 || p >= j) bad = true;
+    if (p < 0 || p >= j) break;
+    j = p;
+  }
+  return seen;
 }
 
 int launch_branch_plan(const BranchArgs& a, int32_t* st, cudaStream_t s);

@@ -54,7 +54,7 @@ struct SimtSmem {
   BranchUnit unit[2];  // flag 8: none, the run is over; flag 16: every row sees every one of the 64 keys
 };
 
-template <int D>
+template <int D, bool tree>
 __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, int32_t* st) {
   branch_touch(a, st);
   pdl_wait();
@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
         full_keys = y.lo * a.g <= r0 && (y.lo + y.n) * a.g >= min(r0 + kTM, a.cu[a.B] * a.g)
                         ? branch_limit(r0 / a.g - y.lo, y.n, y.len, a.block)
                         : 0;
+      if (tree && more && y.branch >= 0) full_keys = min(full_keys, y.len - y.n);
     } else if (more) {
       opens = false;
       y.k0 += kTN;
@@ -243,13 +244,15 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
       for (int i = 0; i < 4; ++i) {
         const int r = r0 + ty * 4 + i;
         const int seen = x.flags & 16 ? kTN : r < rows ? branch_row_keys(a, x, r) : 0;
-        sees |= (seen > 0 || r >= rows ? 1 : 0) << i;
+        uint64_t which = ~0ull;
+        if (tree && seen > 0 && !(x.flags & 16)) which = tree_row_keys(a, x, r, 0, bad);
+        sees |= ((seen > 0 && which) || r >= rows ? 1 : 0) << i;
         float top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = tx + 16 * j;
           const float bias = sm.bias[g][c];
-          s[i][j] = c < seen && bias != -INFINITY ? fmaf(s[i][j] + s1[i][j], scale2, bias) : -INFINITY;
+          s[i][j] = c < seen && (!tree || (which >> c & 1u)) && bias != -INFINITY ? fmaf(s[i][j] + s1[i][j], scale2, bias) : -INFINITY;
           top = fmaxf(top, s[i][j]);
         }
 #pragma unroll
@@ -347,23 +350,24 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
   pdl_trigger();
 }
 
-template <int D>
+template <int D, bool tree>
 int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
   constexpr int smem = (int)sizeof(SimtSmem<D>);
-  auto kernel = branch_simt_kernel<D>;
+  auto kernel = branch_simt_kernel<D, tree>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
       launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
   }
-  FASTAR_LAUNCHED(s, "branch_simt");
+  FASTAR_LAUNCHED(s, tree ? "branch_simt_tree" : "branch_simt");
   return FASTAR_OK;
 }
 
 }  // namespace
 
 int launch_branch_simt(const BranchArgs& a, int32_t* st, cudaStream_t s) {
-  return a.D == 128 ? launch_t<128>(a, st, s) : launch_t<64>(a, st, s);
+  if (a.parent) return a.D == 128 ? launch_t<128, true>(a, st, s) : launch_t<64, true>(a, st, s);
+  return a.D == 128 ? launch_t<128, false>(a, st, s) : launch_t<64, false>(a, st, s);
 }
 
 }  // namespace fastar

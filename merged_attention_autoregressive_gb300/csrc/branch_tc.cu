@@ -182,7 +182,7 @@ __device__ __noinline__ void part_products(uint32_t dO, uint32_t dS, uint32_t vd
     tc::mma_bf16_tmem_a_low_rows(dO, dS + (k >> 2) * 64 + (k & 3) * 8, vd + k * (16 * 128 / 16), idesc, 1u, off);
 }
 
-template <int D, bool split>
+template <int D, bool split, bool tree>
 __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_constant__ CUtensorMap mapPK,
                                                                const __grid_constant__ CUtensorMap mapPV,
                                                                const __grid_constant__ CUtensorMap mapK,
@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
         full_keys = x.lo * a.g <= r0 && (x.lo + x.n) * a.g >= min(r0 + a.TM, rows)
                         ? branch_limit(r0 / a.g - x.lo, x.n, x.len, a.block)
                         : 0;
+      if (tree && own) full_keys = min(full_keys, x.len - x.n);
       const int part = lo < hi && (lo > r0 || hi < min(r0 + a.TM, rows)) ? part_of(lo - r0, hi - r0) : 0;
       const int acts = hi <= lo ? 0 : split ? 1 : ((lo < r0 + kM ? 1 : 0) | (hi > r0 + kM ? 2 : 0));
       // page id of box `lane` (or the counts of rows lane + 32 e) of the unit
@@ -709,15 +710,17 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
       if (act0) ++turn;
       if (active) {
         int seen = 64;  // keys of this half that the row sees
+        uint64_t sees = ~0ull;  // tree: which of them
         bool any = r - lane < rows, all = true, none = false;  // (warps behind the last token have nothing to do)
         if (!(bits & kFull)) {
           // rows behind the last token count as full: nobody reads their results
           seen = (r < rows ? branch_row_keys(a, sm.desc[ds].x, r) : kN) - half * 64;
           any = __any_sync(0xffffffffu, r < rows && seen + half * 64 > 0);  // alike in both halves
+          if (tree) sees = r < rows ? tree_row_keys(a, sm.desc[ds].x, r, half * 64, bad) : ~0ull;
           // rows that see nothing of it beside rows that see it whole (a unit of
           // one branch among others): computed unmasked, and dropped at the end
-          none = split && seen <= 0;
-          all = __all_sync(0xffffffffu, none || seen >= 64);
+          none = split && (tree ? sees == 0ull : seen <= 0);
+          all = __all_sync(0xffffffffu, none || (tree ? sees == ~0ull : seen >= 64));
         }
         if (!started && (bits & kPart)) {
           // the product with the values leaves the other rows' O as it is, so
@@ -755,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
             }
             if (!all) {
 #pragma unroll
-              for (int i = 0; i < 64; ++i) v[i] = i < seen ? v[i] : -INFINITY;
+              for (int i = 0; i < 64; ++i) v[i] = (tree ? (uint32_t)(sees >> (i & 32)) >> (i & 31) & 1u : i < seen) ? v[i] : -INFINITY;
             }
           }
           float tm[8];
@@ -971,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
   pdl_trigger();
 }
 
-template <int D, bool split>
+template <int D, bool split, bool tree>
 int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
   CUtensorMap pk, pv, k, v;
   const uint32_t box = (1u << a.page_shift) < (uint32_t)kN ? (1u << a.page_shift) : (uint32_t)kN;
@@ -984,21 +987,25 @@ int launch_t(const BranchArgs& a, int32_t* st, cudaStream_t s) {
   if (rc != FASTAR_OK) return rc;
   constexpr int smem = (int)sizeof(Smem<D>);
   static_assert(smem <= 227 * 1024, "shared memory");
-  auto kernel = branch_tc_kernel<D, split>;
+  auto kernel = branch_tc_kernel<D, split, tree>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
       launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, pk, pv, k, v, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
   }
-  FASTAR_LAUNCHED(s, "branch_tc");
+  FASTAR_LAUNCHED(s, tree ? "branch_tc_tree" : "branch_tc");
   return FASTAR_OK;
 }
 
 }  // namespace
 
+template <bool tree>
+static int launch_d(const BranchArgs& a, int32_t* st, cudaStream_t s) {
+  if (a.TM == kM) return a.D == 128 ? launch_t<128, true, tree>(a, st, s) : launch_t<64, true, tree>(a, st, s);
+  return a.D == 128 ? launch_t<128, false, tree>(a, st, s) : launch_t<64, false, tree>(a, st, s);
+}
 int launch_branch_tc(const BranchArgs& a, int32_t* st, cudaStream_t s) {
-  if (a.TM == kM) return a.D == 128 ? launch_t<128, true>(a, st, s) : launch_t<64, true>(a, st, s);
-  return a.D == 128 ? launch_t<128, false>(a, st, s) : launch_t<64, false>(a, st, s);
+  return a.parent ? launch_d<true>(a, st, s) : launch_d<false>(a, st, s);
 }
 
 }  // namespace fastar

@@ -221,9 +221,17 @@ int launch_page_append(const fastar_pages* pg, const void* k, int64_t kh, int64_
                        int64_t vt, int N, const int32_t* cu, const int32_t* pos, const fastar_rope_plan* plan,
                        const void* q, int64_t qh, int64_t qt, int Hq, void* q_out, int32_t* st, cudaStream_t s);
 size_t branch_ws_bytes(int Hq, int H, int N, int D);
-int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* cu, const fastar_prefix* px,
-                  const fastar_pages* pg, float scale, int block, void* out, float* lse, void* ws, int32_t* st,
+int launch_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* cu, const int32_t* parent,
+                  const fastar_prefix* px, const fastar_pages* pg, float scale, int block, void* out, float* lse, void* ws, int32_t* st,
                   cudaStream_t s);
+int launch_page_keep(const fastar_pages* pg, const int32_t* cu, const int32_t* rows, int M,
+                     const int32_t* cu_keep, int32_t* st, cudaStream_t s);
+size_t mass_ws_bytes(int Hq, int H, int M, int D);
+int launch_page_mass(const fastar_pages* pg, const void* q, const float* lse, int Hq, int N, const int32_t* rows,
+                     int M, const int32_t* cu, float scale, int block, float decay, const fastar_mass* mass, void* ws,
+                     int32_t* st, cudaStream_t s);
+int launch_page_evict(const fastar_pages* pg, const fastar_mass* mass, int budget, int first, int recent,
+                      const fastar_mass* out, int32_t* st, cudaStream_t s);
 }  // namespace fastar
 
 namespace fastar {

@@ -152,6 +152,7 @@ size_t fastar_workspace_size(int op, int H, int N, int D, int T, int B, int C) {
     case FASTAR_OP_ANNSA: return annsa_ws_bytes(H, N, D, T);
     case FASTAR_OP_ANNSA_PARTS: return annsa_parts_ws_bytes(H, N, D, T);  // T = part_total
     case FASTAR_OP_BRANCH: return branch_ws_bytes(H, T, N, D);  // H = query heads, T = key/value heads
+    case FASTAR_OP_MASS: return mass_ws_bytes(H, T, N, D);      // H = query heads, N = tokens M, T = key/value heads
     case FASTAR_OP_QUANT: return quant_ws_bytes(H, N, C, D, T);  // N = Nq, T = bits, C = keys per head
     default: return 0;
   }
@@ -470,6 +471,35 @@ static int check_pages(const fastar_pages* p) {
   return FASTAR_OK;
 }
 
+static bool mass_ok(const fastar_mass* x) {
+  return x && x->mass && aligned16(x->mass) && aligned16(x->born) && (x->born == nullptr) == (x->total == nullptr);
+}
+// The checks of an attention call of branches; kRun: there is something to do.
+// A prefix without rows becomes none.
+constexpr int kRun = -1;
+static int check_branch(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* cu, const fastar_prefix** px,
+                        const fastar_pages* pages, float scale, int block, const void* out, const void* ws,
+                        size_t ws_bytes) {
+  const int rc = check_pages(pages);
+  if (rc != FASTAR_OK) return rc;
+  if (dt != pages->dt || N < 0 || Hq < 0 || Hq % pages->H || block < 0) return FASTAR_ERR_ARG;
+  if (!(scale > 0.f && scale < INFINITY)) return FASTAR_ERR_ARG;
+  if (N == 0 || Hq == 0 || pages->B == 0) return FASTAR_OK;
+  if ((int64_t)N * (Hq / pages->H) >= 0x7fffffff - 256) return FASTAR_ERR_UNSUPPORTED;
+  if (!q || !cu || !out || !aligned16(q) || !aligned16(out)) return FASTAR_ERR_ARG;
+  const fastar_prefix* prefix = *px;
+  if (prefix && prefix->C == 0) prefix = nullptr;
+  if (prefix) {
+    if (prefix->H != pages->H || prefix->D != pages->D || prefix->dt != dt || prefix->C < 0) return FASTAR_ERR_ARG;
+    if (!prefix->K || !prefix->V || !aligned16(prefix->K) || !aligned16(prefix->V)) return FASTAR_ERR_ARG;
+    if ((int64_t)prefix->H * prefix->C > 0x7fffffff) return FASTAR_ERR_UNSUPPORTED;
+  }
+  *px = prefix;
+  const size_t need = branch_ws_bytes(Hq, pages->H, N, pages->D);
+  if (!ws || ws_bytes < need || ((uintptr_t)ws & 255)) return FASTAR_ERR_WORKSPACE;
+  return kRun;
+}
+
 extern "C" {
 
 int fastar_rope_plan_init(fastar_rope_plan* plan, int D, int axes, const int* dims, int pairing, const double* freq) {
@@ -536,22 +566,64 @@ int fastar_branch_attention(fastar_dtype dt, const void* q, int Hq, int N, const
                             const fastar_prefix* prefix, const fastar_pages* pages, float scale, int block, void* out,
                             float* lse, void* ws, size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
   CallRange range("fastar_branch_attention");
-  int rc = check_pages(pages);
+  const int rc = check_branch(dt, q, Hq, N, cu, &prefix, pages, scale, block, out, ws, ws_bytes);
+  if (rc != kRun) return rc;
+  return launch_branch(dt, q, Hq, N, cu, nullptr, prefix, pages, scale, block, out, lse, ws, dev_status, stream);
+}
+
+int fastar_tree_attention(fastar_dtype dt, const void* q, int Hq, int N, const int32_t* cu, const int32_t* parent,
+                          const fastar_prefix* prefix, const fastar_pages* pages, float scale, void* out, float* lse,
+                          void* ws, size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
+  CallRange range("fastar_tree_attention");
+  const int rc = check_branch(dt, q, Hq, N, cu, &prefix, pages, scale, 1, out, ws, ws_bytes);
+  if (rc != kRun) return rc;
+  if (!parent) return FASTAR_ERR_ARG;
+  return launch_branch(dt, q, Hq, N, cu, parent, prefix, pages, scale, 1, out, lse, ws, dev_status, stream);
+}
+
+int fastar_page_keep(const fastar_pages* pages, const int32_t* cu, const int32_t* rows, int M,
+                     const int32_t* cu_keep, int32_t* dev_status, cudaStream_t stream) {
+  CallRange range("fastar_page_keep");
+  const int rc = check_pages(pages);
   if (rc != FASTAR_OK) return rc;
-  if (dt != pages->dt || N < 0 || Hq < 0 || Hq % pages->H || block < 0) return FASTAR_ERR_ARG;
-  if (!(scale > 0.f && scale < INFINITY)) return FASTAR_ERR_ARG;
-  if (N == 0 || Hq == 0 || pages->B == 0) return FASTAR_OK;
-  if ((int64_t)N * (Hq / pages->H) >= 0x7fffffff - 256) return FASTAR_ERR_UNSUPPORTED;
-  if (!q || !cu || !out || !aligned16(q) || !aligned16(out)) return FASTAR_ERR_ARG;
-  if (prefix && prefix->C == 0) prefix = nullptr;
-  if (prefix) {
-    if (prefix->H != pages->H || prefix->D != pages->D || prefix->dt != dt || prefix->C < 0) return FASTAR_ERR_ARG;
-    if (!prefix->K || !prefix->V || !aligned16(prefix->K) || !aligned16(prefix->V)) return FASTAR_ERR_ARG;
-    if ((int64_t)prefix->H * prefix->C > 0x7fffffff) return FASTAR_ERR_UNSUPPORTED;
-  }
-  const size_t need = branch_ws_bytes(Hq, pages->H, N, pages->D);
+  if (M < 0) return FASTAR_ERR_ARG;
+  if (M == 0 || pages->B == 0) return FASTAR_OK;
+  if (!cu || !rows || !cu_keep) return FASTAR_ERR_ARG;
+  if (pages->B > 65535) return FASTAR_ERR_UNSUPPORTED;
+  return launch_page_keep(pages, cu, rows, M, cu_keep, dev_status, stream);
+}
+
+int fastar_page_mass(const fastar_pages* pages, const void* q, const float* lse, int Hq, int N, const int32_t* rows,
+                     int M, const int32_t* cu, float scale, int block, float decay, const fastar_mass* mass, void* ws,
+                     size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
+  CallRange range("fastar_page_mass");
+  const int rc = check_pages(pages);
+  if (rc != FASTAR_OK) return rc;
+  if (N < 0 || M < 0 || Hq < 0 || Hq % pages->H || block < 0 || (!rows && M != N)) return FASTAR_ERR_ARG;
+  if (!(scale > 0.f && scale < INFINITY) || !(decay >= 0.f && decay < INFINITY) || !mass_ok(mass)) return FASTAR_ERR_ARG;
+  if (M == 0 || Hq == 0 || pages->B == 0) return FASTAR_OK;
+  if ((int64_t)M * (Hq / pages->H) >= 0x7fffffff - 256) return FASTAR_ERR_UNSUPPORTED;
+  if (!q || !lse || !cu || !aligned16(q)) return FASTAR_ERR_ARG;
+  const size_t need = mass_ws_bytes(Hq, pages->H, M, pages->D);
   if (!ws || ws_bytes < need || ((uintptr_t)ws & 255)) return FASTAR_ERR_WORKSPACE;
-  return launch_branch(dt, q, Hq, N, cu, prefix, pages, scale, block, out, lse, ws, dev_status, stream);
+  return launch_page_mass(pages, q, lse, Hq, N, rows, M, cu, scale, block, decay, mass, ws, dev_status, stream);
+}
+
+int fastar_page_evict(const fastar_pages* pages, const fastar_mass* mass, int budget, int first, int recent,
+                      const fastar_mass* out, int32_t* dev_status, cudaStream_t stream) {
+  CallRange range("fastar_page_evict");
+  const int rc = check_pages(pages);
+  if (rc != FASTAR_OK) return rc;
+  if (budget < 0 || first < 0 || recent < 0 || (int64_t)first + recent > budget || !mass_ok(mass)) return FASTAR_ERR_ARG;
+  if (out) {
+    if (!out->mass || !aligned16(out->mass) || !aligned16(out->born)) return FASTAR_ERR_ARG;
+    if ((out->born == nullptr) != (mass->born == nullptr)) return FASTAR_ERR_ARG;
+    // both in place, or both apart
+    if (mass->born && (out->born == mass->born) != (out->mass == mass->mass)) return FASTAR_ERR_ARG;
+  }
+  if ((int64_t)pages->max_pages * pages->page > (1 << 19)) return FASTAR_ERR_UNSUPPORTED;
+  if (pages->B == 0 || pages->max_pages == 0) return FASTAR_OK;
+  return launch_page_evict(pages, mass, budget, first, recent, out, dev_status, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,318 @@
+// fastar_page_evict: every branch and head keeps `budget` of its rows, those
+// that drew the most attention beside the first and the latest ones.
+//
+// The kept rows are the largest by (protected, mass, lower position first).  A
+// mass is compared as an unsigned integer of the same order, so the last kept
+// value is found bit by bit from the top: a bit stays set while at least `budget`
+// values reach the candidate, and the search ends as soon as exactly `budget` do.
+// The integers of a (branch, head) stay in registers over the rounds, a round is
+// a count over the CTA.  Ties at the last value go to the lower positions by a
+// prefix sum over words of 32 positions.  Kept rows from the budget on then move
+// into the holes before it, both in ascending order: sources and targets are
+// disjoint, rows below the budget that stay are not touched, and as few rows move
+// as can.
+//
+// A cluster of CTAs shares the moves of a (branch, head); each of its CTAs does
+// the selection for itself (a reduction across CTAs costs more than it saves) and
+// all of them have read the masses before any is overwritten.
+#include "common.cuh"
+
+namespace fastar {
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kList = 1024;  // moves listed at a time
+
+struct EvictArgs {
+  const int32_t* len;
+  const int32_t* table;
+  uint4* K;
+  uint4* V;
+  const float* mass;
+  const int32_t* born;   // or null: positions tell the age
+  const int32_t* total;
+  float* out_mass;       // may be mass and born
+  int32_t* out_born;
+  int H, max_pages, page_shift, n_pages, budget, first, recent, cluster, words, copies;
+};
+
+__device__ __forceinline__ int row_of(const EvictArgs& a, const int32_t* table, int h, int p) {
+  const int id = table[p >> a.page_shift];
+  if (id < 0 || id >= a.n_pages) return -1;
+  return ((id * a.H + h) << a.page_shift) + (p & ((1 << a.page_shift) - 1));
+}
+
+// The order of the rows as an unsigned integer: protected rows first, then by
+// mass; a mass that is not a number comes last.
+__device__ __forceinline__ uint32_t rank_of(const EvictArgs& a, int row, int p, int total) {
+  if (row < 0) return 0u;
+  const int age = a.born ? a.born[row] : p;
+  if (age < a.first || age >= total - a.recent) return 0xffffffffu;
+  const float x = a.mass[row] + 0.f;  // one zero
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x);
+  return u >> 31 ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// The lowest n set bits of w.
+__device__ __forceinline__ uint32_t lowest(uint32_t w, int n) {
+  if (n <= 0) return 0u;
+  if (n >= __popc(w)) return w;
+  uint32_t r = 0;
+  for (; n > 0; --n) {
+    r |= w & (0u - w);
+    w &= w - 1;
+  }
+  return r;
+}
+
+// Each thread's count summed over the CTA (one barrier; sum[round & 1] is in use).
+__device__ __forceinline__ int block_count(int c, int (*sum)[kWarps], int round) {
+  c = __reduce_add_sync(0xffffffffu, c);
+  if ((threadIdx.x & 31) == 0) sum[round & 1][threadIdx.x >> 5] = c;
+  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < kWarps ? sum[round & 1][threadIdx.x & 31] : 0);
+}
+
+// kKeys: integers in a thread's registers, for up to kThreads kKeys positions; 0:
+// they are made anew in every round (longer tables).  per: 16-byte vectors of a row.
+template <int kKeys, int per>
+__global__ void __launch_bounds__(kThreads) page_evict_kernel(const EvictArgs a, int32_t* st) {
+  extern __shared__ uint32_t words[];  // [words] kept, [words] ties, then counts
+  __shared__ int sum[2][kWarps], scan[33];
+  __shared__ int src[kList], dst[kList];
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int item = blockIdx.x / a.cluster, part = blockIdx.x % a.cluster;
+  const int b = item / a.H, h = item % a.H;
+  const int32_t* const table = a.table + (size_t)b * a.max_pages;
+  const int len = a.len[b], total = a.born ? a.total[b] : len;
+  // (a CTA that has left does not hold up its cluster's barrier)
+  if (block_status_bad(st)) return;
+  if (len < 0 || (long long)len > ((long long)a.max_pages << a.page_shift)) {
+    if (tid == 0) status_set(st, FASTAR_ERR_DEVICE_ARG);
+    return;
+  }
+  if (len <= a.budget) {
+    if (a.copies)
+      for (int p = part * kThreads + tid; p < len; p += a.cluster * kThreads) {
+        const int r = row_of(a, table, h, p);
+        if (r < 0) {
+          status_set(st, FASTAR_ERR_DEVICE_ARG);
+          continue;
+        }
+        a.out_mass[r] = a.mass[r];
+        if (a.born) a.out_born[r] = a.born[r];
+      }
+    return;
+  }
+  uint32_t* const kept = words;
+  uint32_t* const tied = words + a.words;
+  const int nw = (len + 31) / 32;
+  bool bad = false;
+  auto key_at = [&](int p) {
+    if (p >= len) return 0u;
+    const int r = row_of(a, table, h, p);
+    bad = bad || r < 0;
+    return rank_of(a, r, p, total);
+  };
+  uint32_t key[kKeys ? kKeys : 1];
+  const int rounds = kKeys ? kKeys : (len + kThreads - 1) / kThreads;
+  if (kKeys) {
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) key[i] = key_at(i * kThreads + tid);
+  }
+  auto count = [&](uint32_t least) {
+    int c = 0;
+    if (kKeys) {
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) c += key[i] >= least;
+    } else {
+      for (int i = 0; i < rounds; ++i) c += key_at(i * kThreads + tid) >= least;
+    }
+    return c;
+  };
+  // the last kept value: the largest that at least `budget` values reach (rows
+  // behind the length have the smallest value and come last among its ties)
+  uint32_t last = 0u;
+  bool exact = false;  // exactly `budget` values reach it
+  int round = 0;
+  if (a.budget == 0) {
+    last = 0xffffffffu;
+  } else {
+    for (uint32_t bit = 0x80000000u; bit && !exact; bit >>= 1) {
+      const int c = block_count(count(last | bit), sum, round++);
+      if (c >= a.budget) {
+        last |= bit;
+        exact = c == a.budget;
+      }
+    }
+  }
+  // how many of the ties at it stay
+  int quota = 0x7fffffff;
+  if (!exact && a.budget > 0) {
+    const int above = last == 0xffffffffu ? 0 : block_count(count(last + 1), sum, round++);
+    quota = a.budget - above;
+  } else if (a.budget == 0) {
+    quota = 0;
+  }
+  auto mark = [&](int i, uint32_t k) {
+    const uint32_t more = __ballot_sync(0xffffffffu, k > last), same = __ballot_sync(0xffffffffu, k == last);
+    const int w = i * kWarps + warp;
+    if (lane == 0 && w < nw) {
+      const int live = len - w * 32;
+      kept[w] = more;
+      tied[w] = live >= 32 ? same : same & ((1u << live) - 1u);
+    }
+  };
+  if (kKeys) {
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) mark(i, key[i]);
+  } else {
+    for (int i = 0; i < rounds; ++i) mark(i, key_at(i * kThreads + tid));
+  }
+  if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
+  __syncthreads();
+  // ties in order, then each word's holes (before the budget) or moving rows
+  // (from it on) and how many there are in the words before
+  int carry = 0;
+  for (int w0 = 0; w0 < nw; w0 += kThreads) {
+    const int w = w0 + tid;
+    const uint32_t t = w < nw ? tied[w] : 0u;
+    int all;
+    const int before = carry + block_excl_scan(__popc(t), scan, &all);
+    if (w < nw) kept[w] |= lowest(t, quota - before);
+    carry += all;
+  }
+  const int edge = a.budget >> 5;  // the word of the budget's own position
+  const uint32_t below = (1u << (a.budget & 31)) - 1u;
+  int holes = 0, moves = 0;
+  for (int w0 = 0; w0 < nw; w0 += kThreads) {
+    const int w = w0 + tid;
+    int nh = 0, nm = 0, all;
+    if (w < nw) {
+      const uint32_t k = kept[w];
+      nh = w < edge ? __popc(~k) : w == edge ? __popc(~k & below) : 0;
+      nm = w > edge ? __popc(k) : w == edge ? __popc(k & ~below) : 0;
+    }
+    const int h0 = holes + block_excl_scan(nh, scan, &all);
+    holes += all;
+    const int m0 = moves + block_excl_scan(nm, scan, &all);
+    moves += all;
+    if (w < nw) tied[w] = w <= edge ? h0 : m0;  // (the edge's own moving rows are the first)
+  }
+  __syncthreads();
+  if (a.cluster > 1) cluster_sync();
+  if (a.copies)
+    for (int p = part * kThreads + tid; p < a.budget; p += a.cluster * kThreads)
+      if (kept[p >> 5] >> (p & 31) & 1u) {
+        const int r = row_of(a, table, h, p);
+        if (r < 0) continue;
+        a.out_mass[r] = a.mass[r];
+        if (a.born) a.out_born[r] = a.born[r];
+      }
+  // this CTA's share of the moves
+  const int end = (int)((long long)moves * (part + 1) / a.cluster);
+  for (int m0 = (int)((long long)moves * part / a.cluster); m0 < end; m0 += kList) {
+    const int n = min(kList, end - m0);
+    for (int w = tid; w < nw; w += kThreads) {
+      const uint32_t k = kept[w];
+      auto list = [&](uint32_t bits, int at, int* to) {
+        if (at >= m0 + n || at + __popc(bits) <= m0) return;
+        for (; bits; bits &= bits - 1, ++at)
+          if (at >= m0 && at < m0 + n) to[at - m0] = row_of(a, table, h, w * 32 + __ffs(bits) - 1);
+      };
+      if (w <= edge) list(w < edge ? ~k : ~k & below, (int)tied[w], dst);
+      if (w >= edge) list(w > edge ? k : k & ~below, w > edge ? (int)tied[w] : 0, src);
+    }
+    __syncthreads();
+    constexpr int kAhead = 8;
+    for (int e0 = tid; e0 < n * 2 * per; e0 += kThreads * kAhead) {
+      uint4 v[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int e = e0 + q * kThreads, i = e / (2 * per), c = e % (2 * per);
+        if (e < n * 2 * per && src[i] >= 0) v[q] = (c < per ? a.K : a.V)[(size_t)src[i] * per + c % per];
+      }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int e = e0 + q * kThreads, i = e / (2 * per), c = e % (2 * per);
+        if (e < n * 2 * per && src[i] >= 0 && dst[i] >= 0) (c < per ? a.K : a.V)[(size_t)dst[i] * per + c % per] = v[q];
+      }
+    }
+    for (int i = tid; i < n; i += kThreads)
+      if (src[i] >= 0 && dst[i] >= 0) {
+        a.out_mass[dst[i]] = a.mass[src[i]];
+        if (a.born) a.out_born[dst[i]] = a.born[src[i]];
+      }
+    __syncthreads();
+  }
+  pdl_trigger();
+}
+
+template <int kKeys>
+int launch_keys(const EvictArgs& a, int items, int per, int32_t* st, cudaStream_t s) {
+  auto kernel = per == 8 ? page_evict_kernel<kKeys, 8> : per == 16 ? page_evict_kernel<kKeys, 16> : page_evict_kernel<kKeys, 32>;
+  const int smem = 2 * a.words * 4;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FASTAR_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(items * a.cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, a, st) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FASTAR_ERR_CUDA;
+  }
+  FASTAR_LAUNCHED(s, "page_evict");
+  return FASTAR_OK;
+}
+
+}  // namespace
+
+int launch_page_evict(const fastar_pages* pg, const fastar_mass* mass, int budget, int first, int recent,
+                      const fastar_mass* out, int32_t* st, cudaStream_t s) {
+  EvictArgs a = {};
+  a.len = pg->len;
+  a.table = pg->table;
+  a.K = (uint4*)pg->K;
+  a.V = (uint4*)pg->V;
+  a.mass = mass->mass;
+  a.born = mass->born;
+  a.total = mass->total;
+  a.out_mass = out ? out->mass : mass->mass;
+  a.out_born = out ? out->born : mass->born;
+  a.copies = a.out_mass != a.mass;
+  a.H = pg->H;
+  a.max_pages = pg->max_pages;
+  a.n_pages = pg->n_pages;
+  while ((1 << a.page_shift) < pg->page) ++a.page_shift;
+  a.budget = budget;
+  a.first = first;
+  a.recent = recent;
+  const int room = pg->max_pages * pg->page, items = pg->B * pg->H;
+  a.words = (room + 31) / 32;
+  a.cluster = items >= 304 ? 1 : items >= 152 ? 2 : items >= 76 ? 4 : 8;
+  const int per = pg->D * (pg->dt == FASTAR_BF16 ? 2 : 4) / 16;
+  if (room <= 4 * kThreads) return launch_keys<4>(a, items, per, st, s);
+  if (room <= 16 * kThreads) return launch_keys<16>(a, items, per, st, s);
+  if (room <= 64 * kThreads) return launch_keys<64>(a, items, per, st, s);
+  return launch_keys<0>(a, items, per, st, s);
+}
+
+}  // namespace fastar

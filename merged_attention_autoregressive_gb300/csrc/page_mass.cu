@@ -1,0 +1,240 @@
+// fastar_page_mass on the FP32 pipes, the join of cut items, and the dispatch.
+//
+// w(i, p) = exp(scale q_i . k_p - lse_i), summed over the rows i that see
+// position p.  A CTA of 256 threads holds 64 keys and takes 64 rows at a time:
+// 4 x 4 scores per thread, their weights added over the thread's four rows; at
+// the item's end the sums of the 16 threads of a key are joined.
+#include <math.h>
+
+#include "page_mass.cuh"
+
+namespace fastar {
+namespace {
+
+constexpr int kTK = 64, kTQ = 64, kThreads = 256, kCtas = 2 * 152;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Smem {
+  float K[kTK][D + 4];
+  float Q[kTQ][D + 4];
+  float base[kTQ];      // -lse log2 e
+  int limit[kTQ];       // positions that the row sees; 0: none, or nobody's row
+  int row[kTK];         // in the pages; -1: none
+  float old[kTK];
+  float sum[kThreads / 32][kTK];
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, int32_t* st) {
+  pdl_wait();
+  extern __shared__ uint4 raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
+  if (block_status_bad(st)) return;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  constexpr int VN = 16 / (int)sizeof(T), RV = D / VN;  // elements of a vector, vectors of a row
+  const float scale2 = a.scale * kLog2e;
+  MassWalk<kTK> walk;
+  int most;
+  bool ok = true, bad = false;
+  const long long items = walk.count(a, most, ok);
+  if (!ok) {
+    if (tid == 0) status_set(st, FASTAR_ERR_DEVICE_ARG);
+    return;
+  }
+  const int parts = mass_parts(a, items, most, kTQ);
+  for (long long it = blockIdx.x; it < items * parts; it += gridDim.x) {
+    const MassItem x = walk.find(a, it / parts);
+    const int part = (int)(it % parts), tiles = (x.rows + kTQ - 1) / kTQ;
+    const int t0 = (int)((long long)tiles * part / parts), t1 = (int)((long long)tiles * (part + 1) / parts);
+    if (tid < kTK) {
+      const int p = x.k0 + tid;
+      int row = -1;
+      if (p < x.len) {
+        row = mass_row(a, x.b, x.h, p);
+        bad = bad || row < 0;
+      }
+      sm.row[tid] = row;
+      sm.old[tid] = row >= 0 && parts == 1 ? a.mass[row] : 0.f;
+    }
+    __syncthreads();
+    for (int e = tid; e < kTK * RV; e += kThreads) {
+      const int r = e / RV, c = e % RV;
+      float v[VN];
+#pragma unroll
+      for (int i = 0; i < VN; ++i) v[i] = 0.f;
+      if (sm.row[r] >= 0) ld_vec<T, VN>((const T*)a.K + (size_t)sm.row[r] * D + c * VN, v);
+#pragma unroll
+      for (int i = 0; i < VN; i += 4) *reinterpret_cast<float4*>(&sm.K[r][c * VN + i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+    float drew[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int t = t0; t < t1; ++t) {
+      __syncthreads();
+      const int r0 = t * kTQ, live = min(kTQ, x.rows - r0);
+      for (int e = tid; e < kTQ * RV; e += kThreads) {
+        const int r = e / RV, c = e % RV;
+        float v[VN];
+#pragma unroll
+        for (int i = 0; i < VN; ++i) v[i] = 0.f;
+        float base = 0.f;
+        int limit = 0;
+        if (r < live) {
+          const int i = x.i0 + (r0 + r) / a.g, head = x.h * a.g + (r0 + r) % a.g;
+          const int at = a.rows ? a.rows[x.lo + i] : x.lo + i;
+          if (at < 0 || at >= a.N) {
+            bad = true;
+          } else {
+            const float lse = a.lse[(size_t)head * a.N + at];
+            if (lse != -INFINITY) {
+              ld_vec<T, VN>((const T*)a.q + ((size_t)head * a.N + at) * D + c * VN, v);
+              base = -lse * kLog2e;
+              limit = mass_limit(i, x.n, x.len, a.block);
+            }
+          }
+        }
+        if (c == 0) {
+          sm.base[r] = base;
+          sm.limit[r] = limit;
+        }
+#pragma unroll
+        for (int i = 0; i < VN; i += 4) *reinterpret_cast<float4*>(&sm.Q[r][c * VN + i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+      __syncthreads();
+      if ((ty & ~1) * 4 >= live) continue;  // no row of the warp
+      float s[4][4], s1[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = s1[i][j] = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < D; k += 4) {
+        float4 qv[4], kv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(&sm.Q[ty * 4 + i][k]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(&sm.K[tx + 16 * j][k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+            s1[i][j] = fmaf(qv[i].y, kv[j].y, s1[i][j]);
+            s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+            s1[i][j] = fmaf(qv[i].w, kv[j].w, s1[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float base = sm.base[ty * 4 + i];
+        const int limit = sm.limit[ty * 4 + i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (x.k0 + tx + 16 * j < limit) drew[j] += exp2f(fmaf(s[i][j] + s1[i][j], scale2, base));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      drew[j] += __shfl_xor_sync(0xffffffffu, drew[j], 16);
+      if ((tid & 31) < 16) sm.sum[tid >> 5][tx + 16 * j] = drew[j];
+    }
+    __syncthreads();
+    if (tid < kTK) {
+      float d = 0.f;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) d += sm.sum[w][tid];
+      const int row = sm.row[tid];
+      if (parts > 1)
+        a.part[it * kTK + tid] = d;
+      else if (row >= 0)
+        mass_write(a, x, x.k0 + tid, row, sm.old[tid], d);
+    }
+    __syncthreads();
+  }
+  if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
+  pdl_trigger();
+}
+
+// Adds the parts of the items that are cut, in order; a CTA per item.
+template <int TK, int TQ>
+__global__ void __launch_bounds__(TK) mass_join_kernel(const MassArgs a, int32_t* st) {
+  pdl_wait();
+  if (block_status_bad(st)) return;
+  MassWalk<TK> walk;
+  int most;
+  bool ok = true;
+  const long long items = walk.count(a, most, ok);
+  const int parts = ok ? mass_parts(a, items, most, TQ) : 1;
+  if (parts == 1 || blockIdx.x >= items) return;
+  const MassItem x = walk.find(a, blockIdx.x);
+  const int p = x.k0 + threadIdx.x;
+  if (p >= x.len) return;
+  const int row = mass_row(a, x.b, x.h, p);
+  if (row < 0) return;
+  const float old = a.mass[row];
+  float d = 0.f;
+  for (int i = 0; i < parts; ++i) d += a.part[((size_t)blockIdx.x * parts + i) * TK + threadIdx.x];
+  mass_write(a, x, p, row, old, d);
+}
+
+template <typename T, int D>
+int launch_t(const MassArgs& a, int32_t* st, cudaStream_t s) {
+  constexpr int smem = (int)sizeof(Smem<D>);
+  auto kernel = mass_simt_kernel<T, D>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, a, st) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FASTAR_ERR_CUDA;
+  }
+  FASTAR_LAUNCHED(s, "page_mass_simt");
+  if (!a.split) return FASTAR_OK;
+  if (launch_pdl(mass_join_kernel<kTK, kTQ>, dim3(a.G / 2), dim3(kTK), 0, s, a, st) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FASTAR_ERR_CUDA;
+  }
+  FASTAR_LAUNCHED(s, "page_mass_join");
+  return FASTAR_OK;
+}
+
+}  // namespace
+
+size_t mass_ws_bytes(int Hq, int H, int M, int D) {
+  if (Hq < 1 || H < 1 || M < 1 || D < 1 || Hq % H) return 0;
+  return (size_t)kCtas * 256 * 4;
+}
+
+int launch_page_mass(const fastar_pages* pg, const void* q, const float* lse, int Hq, int N, const int32_t* rows,
+                     int M, const int32_t* cu, float scale, int block, float decay, const fastar_mass* mass, void* ws,
+                     int32_t* st, cudaStream_t s) {
+  MassArgs a = {};
+  a.q = q;
+  a.lse = lse;
+  a.rows = rows;
+  a.cu = cu;
+  a.len = pg->len;
+  a.table = pg->table;
+  a.K = pg->K;
+  a.mass = mass->mass;
+  a.born = mass->born;
+  a.total = mass->total;
+  a.N = N;
+  a.M = M;
+  a.Hq = Hq;
+  a.H = pg->H;
+  a.g = Hq / pg->H;
+  a.B = pg->B;
+  a.max_pages = pg->max_pages;
+  while ((1 << a.page_shift) < pg->page) ++a.page_shift;
+  a.n_pages = pg->n_pages;
+  a.block = block;
+  a.scale = scale;
+  a.decay = decay;
+  a.part = (float*)ws;
+  a.G = kCtas;
+  // cut only where a branch may have rows for two tiles of them
+  a.split = (long long)M * a.g > kTQ;
+  const int D = pg->D;
+  if (pg->dt == FASTAR_BF16) return D == 128 ? launch_t<__nv_bfloat16, 128>(a, st, s) : launch_t<__nv_bfloat16, 64>(a, st, s);
+  return D == 128 ? launch_t<float, 128>(a, st, s) : launch_t<float, 64>(a, st, s);
+}
+
+}  // namespace fastar

@@ -1,0 +1,153 @@
+// Work of fastar_page_mass, shared by its kernels.
+//
+// An item is a tile of TK positions of one branch and one key/value head.  Its
+// rows are the queries of the branch's new tokens that see the tile, row r =
+// token i0 + r / g, head h g + r % g, TQ of them at a time: the scores of a tile
+// are summed over the rows, so an item is one pass over the queries with its keys
+// held, and its masses are written once.  Items follow one another branch by
+// branch, tile by tile, head by head (all heads of a page lie side by side, and
+// the first tiles, which most tokens see, come first); CTA c takes the items c,
+// c + G, c + 2 G, ...
+//
+// Where there are fewer items than CTAs and many rows, each item's rows are cut
+// into `parts` runs of tiles; each leaves its sums in the workspace and
+// page_mass_join adds them in order, so results do not change from run to run.
+//
+// The lengths live on the device: every CTA walks them, 32 branches at a time.
+#pragma once
+
+#include "common.cuh"
+
+namespace fastar {
+
+struct MassArgs {
+  const void* q;        // [Hq][N][D]
+  const float* lse;     // [Hq][N]
+  const int32_t* rows;  // [M] query row of each token, or null
+  const int32_t* cu;    // [B + 1]
+  const int32_t* len;   // [B]
+  const int32_t* table;
+  const void* K;
+  float* mass;
+  int32_t* born;        // or null
+  const int32_t* total;
+  int N, M, Hq, H, g, B, max_pages, page_shift, n_pages, block, G, split;
+  float scale, decay;
+  float* part;          // [G][TK] sums of cut items
+};
+
+// Keys of its branch that token i of n (branch length len) sees.
+__device__ __forceinline__ int mass_limit(int i, int n, int len, int block) {
+  if (block <= 0) return len;
+  const int t = len - n + i;
+  if (t < 0) return 0;
+  const int blocks = t / block + 1;
+  return blocks > len / block ? len : blocks * block;
+}
+
+struct MassItem {
+  int b, h, k0;    // branch, head, first position of the tile
+  int lo, n, len;  // first token, tokens, length of the branch
+  int i0, rows;    // first token that sees the tile, rows from it on
+};
+
+// Row of position p in the pages of branch b, head h; -1: its page is not there.
+__device__ __forceinline__ int mass_row(const MassArgs& a, int b, int h, int p) {
+  const int id = a.table[(size_t)b * a.max_pages + (p >> a.page_shift)];
+  if (id < 0 || id >= a.n_pages) return -1;
+  return ((id * a.H + h) << a.page_shift) + (p & ((1 << a.page_shift) - 1));
+}
+
+// A warp's place among the items; all lanes in step.
+template <int TK>
+struct MassWalk {
+  long long base, total;  // items before the 32 branches, and of them
+  int b0, lo, n, len;     // lane: branch b0 + lane
+  long long incl;         // items up to and with it
+
+  __device__ __forceinline__ void load(const MassArgs& a, bool& ok) {
+    const int b = b0 + (threadIdx.x & 31);
+    lo = n = len = 0;
+    if (b < a.B) {
+      lo = a.cu[b];
+      const int hi = a.cu[b + 1];
+      len = a.len[b];
+      ok = ok && lo >= 0 && hi >= lo && hi <= a.M && (b != 0 || lo == 0) && len >= 0 &&
+           (long long)len <= ((long long)a.max_pages << a.page_shift);
+      n = ok ? hi - lo : 0;
+    }
+    const int lane = threadIdx.x & 31;
+    incl = n > 0 ? (long long)((len + TK - 1LL) / TK) * a.H : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+  }
+  // Items of the call, and the most rows of one; ok: every length and offset holds.
+  __device__ __forceinline__ long long count(const MassArgs& a, int& most, bool& ok) {
+    long long items = 0;
+    most = 0;
+    for (b0 = 0; b0 < a.B; b0 += 32) {
+      load(a, ok);
+      items += total;
+      most = max(most, __reduce_max_sync(0xffffffffu, n));
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    base = 0;
+    b0 = 0;
+    if (a.B > 32) {
+      bool same = true;
+      load(a, same);
+    } else if (a.B == 0) {
+      total = 0;
+    }
+    return items;
+  }
+  // Item `it`, at or behind the last one asked for.
+  __device__ __forceinline__ MassItem find(const MassArgs& a, long long it) {
+    while (it >= base + total) {
+      base += total;
+      b0 += 32;
+      bool ok = true;
+      load(a, ok);
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, base + incl > it);
+    const int src = __ffs(m) - 1;
+    const long long mine = n > 0 ? (long long)((len + TK - 1LL) / TK) * a.H : 0;
+    const long long off = it - base - __shfl_sync(0xffffffffu, incl - mine, src);
+    MassItem x;
+    x.b = b0 + src;
+    x.h = (int)(off % a.H);
+    x.k0 = (int)(off / a.H) * TK;
+    x.lo = __shfl_sync(0xffffffffu, lo, src);
+    x.n = __shfl_sync(0xffffffffu, n, src);
+    x.len = __shfl_sync(0xffffffffu, len, src);
+    // the first token whose last block reaches the tile
+    const int past = x.len - x.n;
+    x.i0 = a.block > 0 ? min(x.n, max(0, x.k0 / a.block * a.block - past)) : 0;
+    x.rows = (x.n - x.i0) * a.g;
+    return x;
+  }
+};
+
+// Parts of each item.
+__device__ __forceinline__ int mass_parts(const MassArgs& a, long long items, int most, int TQ) {
+  if (!a.split || items == 0 || 2 * items > a.G) return 1;
+  const long long tiles = ((long long)most * a.g + TQ - 1) / TQ;
+  const int n = a.G / (int)items;
+  return tiles < n ? (int)max(1ll, tiles) : n;
+}
+
+// The mass of a position with what it drew in this call, and its token's number.
+__device__ __forceinline__ void mass_write(const MassArgs& a, const MassItem& x, int p, int row, float old, float drew) {
+  const int past = x.len - x.n;
+  a.mass[row] = p >= past ? drew : fmaf(a.decay, old, drew);
+  if (a.born && p >= past) a.born[row] = a.total[x.b] - x.len + p;
+}
+
+int launch_mass_simt(fastar_dtype dt, int D, const MassArgs& a, int32_t* st, cudaStream_t s);
+int launch_mass_tc(int D, const MassArgs& a, int32_t* st, cudaStream_t s);
+
+}  // namespace fastar

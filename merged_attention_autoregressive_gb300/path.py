@@ -13,10 +13,11 @@ from types import SimpleNamespace
 
 import torch
 
-from . import (Cache, OP_ANNCA, OP_ANNSA, OP_ANNSA_PARTS, OP_MERGE, PagedKV, Prefix, branch_workspace_size,
+from . import (Cache, OP_ANNCA, OP_ANNSA, OP_ANNSA_PARTS, OP_MERGE, PagedKV, PageMass, Prefix, branch_workspace_size,
                fastar_annca_attention, fastar_annca_prune, fastar_annsa_attention, fastar_annsa_attention_part,
                fastar_annsa_combine, fastar_branch_attention, fastar_bucket_csr, fastar_hash, fastar_hash_many,
-               fastar_page_append, fastar_tempcache_merge, fastar_workspace_size)
+               fastar_page_append, fastar_page_evict, fastar_page_keep, fastar_page_mass, fastar_tempcache_merge,
+               fastar_tree_attention, fastar_workspace_size, mass_workspace_size)
 
 DENSE_FRAC = 0.3  # sparse attention is off for this share of a chunk's denoising steps
 
@@ -435,12 +436,26 @@ class BranchRollout:
     earlier blocks of n positions (a frame's tokens, 1 for text).
 
     Branches are independent: infinities and NaN among the keys and values of
-    one reach no other's outputs."""
+    one reach no other's outputs.
+
+    Drafts: `extend(new, parents)` makes the next step's tokens of each branch a
+    tree, of which `accept` keeps one path.
+
+    budget: rows that a branch holds per head after `evict`.  Every step then adds
+    its tokens' attention weights to the masses of the rows (older ones fade by
+    `decay`), and `evict` keeps the rows of the first `first` and the last `recent`
+    tokens and those of the largest masses.  With block > 1 the budget is whole
+    blocks, so that later tokens' blocks begin where they did."""
+    budget = mass = drafts = _asked = None
 
     def __init__(self, B, H, D, tokens, max_len, prefix=None, Hq=None, page=64, n_pages=None, plan=None, block=0,
-                 scale=None, dtype=torch.bfloat16, device="cuda"):
+                 scale=None, dtype=torch.bfloat16, device="cuda", budget=None, first=0, recent=0, decay=1.0):
         dev = torch.device(device)
         most = -(-max_len // page)
+        if budget is not None and (first < 0 or recent < 0 or first + recent > budget or
+                                   (block > 1 and budget % block)):
+            raise ValueError("a budget holds the first and the recent rows, and whole blocks")
+        self.budget, self.first, self.recent, self.decay = budget, first, recent, decay
         self.B, self.H, self.D, self.Hq, self.max_len, self.tokens = B, H, D, Hq or H, max_len, tokens
         self.prefix, self.plan, self.block = prefix, plan, block
         self.scale = D ** -0.5 if scale is None else scale
@@ -451,16 +466,31 @@ class BranchRollout:
         self.lse = torch.zeros(self.Hq, tokens, dtype=torch.float32, device=dev)
         self.ws = torch.empty(branch_workspace_size(self.Hq, H, tokens, D), dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.parent = torch.zeros(tokens, dtype=torch.int32, device=dev)
+        self.drafts = self._asked = None             # parents of the step's tokens, branch by branch; its queries
+        if budget is not None:
+            self.mass = PageMass(self.pages)
+            self.ws_mass = torch.empty(max(1, mass_workspace_size(self.Hq, H, tokens, D)), dtype=torch.uint8, device=dev)
         self.lengths = [0] * B
+        self.totals = [0] * B                        # tokens that each branch has had
         self.held = [[] for _ in range(B)]           # page ids of each branch
         self.free = list(range(self.pages.n_pages))[::-1]
         # the fills above are over before another stream's `extend` or `step`
         torch.cuda.current_stream(dev).synchronize()
 
-    def extend(self, new, stream=None):
+    def extend(self, new, stream=None, parents=None):
         """Make room for new[b] more positions of each branch: the next step's
         tokens, laid out branch after branch.  The copies to the device go to
-        `stream` (default: the current one), which is also the next step's."""
+        `stream` (default: the current one), which is also the next step's.
+
+        parents: the tokens are drafts; parents[b][i] < i is the draft of branch b
+        that its draft i follows, -1: the branch's last position.  `accept` ends
+        their step."""
+        if self.drafts is not None:
+            raise ValueError("the drafts of the last step are not accepted yet")
+        if parents is not None and ([len(p) for p in parents] != list(new) or
+                                    any(not -1 <= q < i for p in parents for i, q in enumerate(p))):
+            raise ValueError("one parent per draft, an earlier one of its branch or -1")
         if len(new) != self.B or any(n < 0 for n in new) or sum(new) > self.tokens:
             raise ValueError("one count of new tokens per branch, at most `tokens` in all")
         lengths = [a + n for a, n in zip(self.lengths, new)]
@@ -484,11 +514,78 @@ class BranchRollout:
                 self.pages.table.copy_(torch.tensor(table, **i32).view(self.B, most))
             self.pages.len.copy_(torch.tensor(lengths, **i32))
             self.cu.copy_(torch.tensor(offsets, **i32))
+            if self.mass is not None:
+                self.totals = [a + n for a, n in zip(self.totals, new)]
+                self.mass.total.copy_(torch.tensor(self.totals, **i32))
+            if parents is not None:
+                self.drafts = [list(p) for p in parents]
+                flat = [q for p in parents for q in p]
+                self.parent[:len(flat)].copy_(torch.tensor(flat, **i32))
 
     def release(self, b):
         """Branch b starts again: its pages return to the pool."""
+        if self.drafts is not None:
+            raise ValueError("the drafts of the last step are not accepted yet")
         self.free.extend(self.held[b][::-1])
         self.held[b], self.lengths[b] = [], 0
+        if self.mass is not None:
+            self.totals[b] = 0
+
+    def _shrink(self, lengths):
+        """The branches hold `lengths` positions now; pages behind return to the
+        pool.  (Their entries of the table are not read any more.)"""
+        self.lengths = lengths
+        for held, n in zip(self.held, lengths):
+            while len(held) > -(-n // self.pages.page):
+                self.free.append(held.pop())
+        self.pages.len.copy_(torch.tensor(lengths, dtype=torch.int32))
+
+    def accept(self, leaves, stream=None):
+        """Ends a step of drafts: of each branch the draft leaves[b] and those
+        above it stay (-1: none), in the order of their positions.  Returns their
+        numbers within the step's rows, branch by branch."""
+        if self.drafts is None:
+            raise ValueError("the last step had no drafts")
+        if len(leaves) != self.B or any(not -1 <= x < len(p) for x, p in zip(leaves, self.drafts)):
+            raise ValueError("one draft per branch, or -1")
+        kept, first = [], 0
+        for x, p in zip(leaves, self.drafts):
+            path = []
+            while x >= 0:
+                path.append(first + x)
+                x = p[x]
+            kept.append(path[::-1])
+            first += len(p)
+        gone = [len(p) - len(k) for p, k in zip(self.drafts, kept)]
+        cu = [0]
+        for k in kept:
+            cu.append(cu[-1] + len(k))
+        i32 = dict(dtype=torch.int32, device=self.cu.device)
+        with torch.cuda.stream(None if stream is None else ChunkPath._main(stream)):
+            rows = torch.tensor([r for k in kept for r in k], **i32)
+            keep = torch.tensor(cu, **i32)
+            fastar_page_keep(self.pages, self.cu, rows, keep, status=self.status)
+            self._shrink([n - g for n, g in zip(self.lengths, gone)])
+            self.cu.copy_(keep)
+            if self.mass is not None:
+                self.totals = [n - g for n, g in zip(self.totals, gone)]
+                self.mass.total.copy_(torch.tensor(self.totals, dtype=torch.int32))
+                fastar_page_mass(self.pages, self._asked, self.lse, self.cu, self.scale, self.mass, block=1, rows=rows,
+                                 decay=self.decay, ws=self.ws_mass, status=self.status)
+        self.drafts = self._asked = None
+        return kept
+
+    def evict(self, stream=None):
+        """Every branch of more than `budget` positions keeps, in each head,
+        `budget` of its rows, and returns the pages behind."""
+        if self.budget is None:
+            raise ValueError("this rollout has no budget")
+        if self.drafts is not None:
+            raise ValueError("the drafts of the last step are not accepted yet")
+        with torch.cuda.stream(None if stream is None else ChunkPath._main(stream)):
+            fastar_page_evict(self.pages, self.mass, self.budget, first=self.first, recent=self.recent,
+                              status=self.status)
+            self._shrink([min(n, self.budget) for n in self.lengths])
 
     def step(self, q, k, v, pos=None, stream=None):
         """The new tokens of the last `extend`: q [Hq][tokens][D], k, v
@@ -499,6 +596,14 @@ class BranchRollout:
         fastar_page_append(self.pages, k, v, self.cu, pos=pos, plan=self.plan,
                            q=q if self.plan is not None else None, q_out=self.q if self.plan is not None else None,
                            status=self.status, stream=stream)
+        if self.drafts is not None:
+            self._asked = rotated  # `accept` weighs the tokens that stay
+            fastar_tree_attention(rotated, self.cu, self.parent, self.prefix, self.pages, self.scale, self.out,
+                                  lse=self.lse, ws=self.ws, status=self.status, stream=stream)
+            return self.out, self.lse
         fastar_branch_attention(rotated, self.cu, self.prefix, self.pages, self.scale, self.out, lse=self.lse,
                                 block=self.block, ws=self.ws, status=self.status, stream=stream)
+        if self.mass is not None:
+            fastar_page_mass(self.pages, rotated, self.lse, self.cu, self.scale, self.mass, block=self.block,
+                             decay=self.decay, ws=self.ws_mass, status=self.status, stream=stream)
         return self.out, self.lse
