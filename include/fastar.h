@@ -747,7 +747,8 @@ typedef struct {
  * fastar_workspace_size(FASTAR_OP_MASS, Hq, M, D, H, 0, 0) bytes; two calls that
  * may overlap need one each.  Pages whose masses are written must not be shared.
  * FASTAR_ERR_DEVICE_ARG: cu not ascending within 0..M, a length outside
- * 0..max_pages * page, a row outside 0..N-1, a page id outside the pool.
+ * 0..max_pages * page, a row outside 0..N-1, a page id outside the pool, branches
+ * that hold 2^31 rows and more over all heads.
  */
 #define FASTAR_OP_MASS 8
 int fastar_page_mass(const fastar_pages* pages, const void* q, const float* lse,

@@ -37,21 +37,20 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, i
   MassWalk<kTK> walk;
   int most;
   bool ok = true, bad = false;
-  const long long items = walk.count(a, most, ok);
+  const unsigned items = walk.count(a, most, ok);
   if (!ok) {
     if (tid == 0) status_set(st, FASTAR_ERR_DEVICE_ARG);
     return;
   }
   const int parts = mass_parts(a, items, most, kTQ);
-  for (long long it = blockIdx.x; it < items * parts; it += gridDim.x) {
+  for (unsigned it = blockIdx.x; it < items * parts; it += gridDim.x) {
     const MassItem x = walk.find(a, it / parts);
     const int part = (int)(it % parts), tiles = (x.rows + kTQ - 1) / kTQ;
     const int t0 = (int)((long long)tiles * part / parts), t1 = (int)((long long)tiles * (part + 1) / parts);
     if (tid < kTK) {
-      const int p = x.k0 + tid;
       int row = -1;
-      if (p < x.len) {
-        row = mass_row(a, x.b, x.h, p);
+      if (tid < x.len - x.k0) {
+        row = mass_row(a, x.b, x.h, x.k0 + tid);
         bad = bad || row < 0;
       }
       sm.row[tid] = row;
@@ -129,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, i
         const int limit = sm.limit[ty * 4 + i];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (x.k0 + tx + 16 * j < limit) drew[j] += exp2f(fmaf(s[i][j] + s1[i][j], scale2, base));
+          if (tx + 16 * j < limit - x.k0) drew[j] += exp2f(fmaf(s[i][j] + s1[i][j], scale2, base));
       }
     }
 #pragma unroll
@@ -144,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, i
       for (int w = 0; w < kThreads / 32; ++w) d += sm.sum[w][tid];
       const int row = sm.row[tid];
       if (parts > 1)
-        a.part[it * kTK + tid] = d;
+        a.part[(size_t)it * kTK + tid] = d;
       else if (row >= 0)
         mass_write(a, x, x.k0 + tid, row, sm.old[tid], d);
     }
@@ -162,12 +161,12 @@ __global__ void __launch_bounds__(TK) mass_join_kernel(const MassArgs a, int32_t
   MassWalk<TK> walk;
   int most;
   bool ok = true;
-  const long long items = walk.count(a, most, ok);
+  const unsigned items = walk.count(a, most, ok);
   const int parts = ok ? mass_parts(a, items, most, TQ) : 1;
   if (parts == 1 || blockIdx.x >= items) return;
   const MassItem x = walk.find(a, blockIdx.x);
+  if ((int)threadIdx.x >= x.len - x.k0) return;
   const int p = x.k0 + threadIdx.x;
-  if (p >= x.len) return;
   const int row = mass_row(a, x.b, x.h, p);
   if (row < 0) return;
   const float old = a.mass[row];
@@ -186,16 +185,21 @@ int launch_t(const MassArgs& a, int32_t* st, cudaStream_t s) {
     return FASTAR_ERR_CUDA;
   }
   FASTAR_LAUNCHED(s, "page_mass_simt");
-  if (!a.split) return FASTAR_OK;
-  if (launch_pdl(mass_join_kernel<kTK, kTQ>, dim3(a.G / 2), dim3(kTK), 0, s, a, st) != cudaSuccess) {
+  return a.split ? launch_mass_join(kTK, kTQ, a, st, s) : FASTAR_OK;
+}
+
+}  // namespace
+
+// Tiles of keys and rows as in the kernel that left the sums.
+int launch_mass_join(int TK, int TQ, const MassArgs& a, int32_t* st, cudaStream_t s) {
+  auto kernel = TK == 64 ? mass_join_kernel<64, 64> : mass_join_kernel<256, 128>;
+  if (launch_pdl(kernel, dim3(a.G / 2), dim3(TK), 0, s, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
   }
   FASTAR_LAUNCHED(s, "page_mass_join");
   return FASTAR_OK;
 }
-
-}  // namespace
 
 size_t mass_ws_bytes(int Hq, int H, int M, int D) {
   if (Hq < 1 || H < 1 || M < 1 || D < 1 || Hq % H) return 0;
@@ -233,7 +237,7 @@ int launch_page_mass(const fastar_pages* pg, const void* q, const float* lse, in
   // cut only where a branch may have rows for two tiles of them
   a.split = (long long)M * a.g > kTQ;
   const int D = pg->D;
-  if (pg->dt == FASTAR_BF16) return D == 128 ? launch_t<__nv_bfloat16, 128>(a, st, s) : launch_t<__nv_bfloat16, 64>(a, st, s);
+  if (pg->dt == FASTAR_BF16) return launch_mass_tc(D, a, st, s);
   return D == 128 ? launch_t<float, 128>(a, st, s) : launch_t<float, 64>(a, st, s);
 }
 

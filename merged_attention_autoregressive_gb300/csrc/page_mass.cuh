@@ -58,15 +58,18 @@ __device__ __forceinline__ int mass_row(const MassArgs& a, int b, int h, int p) 
   return ((id * a.H + h) << a.page_shift) + (p & ((1 << a.page_shift) - 1));
 }
 
+// Items of a call, and units of parts of them, fit an unsigned: more are refused.
+constexpr long long kMaxItems = 1 << 30;
+
 // A warp's place among the items; all lanes in step.
 template <int TK>
 struct MassWalk {
-  long long base, total;  // items before the 32 branches, and of them
-  int b0, lo, n, len;     // lane: branch b0 + lane
-  long long incl;         // items up to and with it
+  unsigned base, total;   // items before the 32 branches, and of them
+  unsigned mine, incl;    // lane: items of branch b0 + lane; items up to and with it
+  int b0, lo, n, len;
 
-  __device__ __forceinline__ void load(const MassArgs& a, bool& ok) {
-    const int b = b0 + (threadIdx.x & 31);
+  __device__ __forceinline__ long long load(const MassArgs& a, bool& ok) {
+    const int lane = threadIdx.x & 31, b = b0 + lane;
     lo = n = len = 0;
     if (b < a.B) {
       lo = a.cu[b];
@@ -76,25 +79,23 @@ struct MassWalk {
            (long long)len <= ((long long)a.max_pages << a.page_shift);
       n = ok ? hi - lo : 0;
     }
-    const int lane = threadIdx.x & 31;
-    incl = n > 0 ? (long long)((len + TK - 1LL) / TK) * a.H : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
+    const long long items = n > 0 ? (long long)(((unsigned)len + TK - 1u) / TK) * a.H : 0;
+    ok = ok && items < kMaxItems / 32;
+    mine = ok ? (unsigned)items : 0u;
+    incl = (unsigned)warp_incl_scan((int)mine);
     total = __shfl_sync(0xffffffffu, incl, 31);
+    return total;
   }
-  // Items of the call, and the most rows of one; ok: every length and offset holds.
-  __device__ __forceinline__ long long count(const MassArgs& a, int& most, bool& ok) {
+  // Items of the call, and the most tokens of a branch; ok: every length and
+  // offset holds.
+  __device__ __forceinline__ unsigned count(const MassArgs& a, int& most, bool& ok) {
     long long items = 0;
     most = 0;
     for (b0 = 0; b0 < a.B; b0 += 32) {
-      load(a, ok);
-      items += total;
+      items += load(a, ok);
       most = max(most, __reduce_max_sync(0xffffffffu, n));
     }
-    ok = __all_sync(0xffffffffu, ok);
+    ok = __all_sync(0xffffffffu, ok) && items < kMaxItems;
     base = 0;
     b0 = 0;
     if (a.B > 32) {
@@ -103,24 +104,22 @@ struct MassWalk {
     } else if (a.B == 0) {
       total = 0;
     }
-    return items;
+    return ok ? (unsigned)items : 0u;
   }
   // Item `it`, at or behind the last one asked for.
-  __device__ __forceinline__ MassItem find(const MassArgs& a, long long it) {
+  __device__ __forceinline__ MassItem find(const MassArgs& a, unsigned it) {
     while (it >= base + total) {
       base += total;
       b0 += 32;
       bool ok = true;
       load(a, ok);
     }
-    const unsigned m = __ballot_sync(0xffffffffu, base + incl > it);
-    const int src = __ffs(m) - 1;
-    const long long mine = n > 0 ? (long long)((len + TK - 1LL) / TK) * a.H : 0;
-    const long long off = it - base - __shfl_sync(0xffffffffu, incl - mine, src);
+    const int src = __ffs(__ballot_sync(0xffffffffu, base + incl > it)) - 1;
+    const unsigned off = it - base - __shfl_sync(0xffffffffu, incl - mine, src);
     MassItem x;
     x.b = b0 + src;
-    x.h = (int)(off % a.H);
-    x.k0 = (int)(off / a.H) * TK;
+    x.h = (int)(off % (unsigned)a.H);
+    x.k0 = (int)(off / (unsigned)a.H) * TK;
     x.lo = __shfl_sync(0xffffffffu, lo, src);
     x.n = __shfl_sync(0xffffffffu, n, src);
     x.len = __shfl_sync(0xffffffffu, len, src);
@@ -133,8 +132,8 @@ struct MassWalk {
 };
 
 // Parts of each item.
-__device__ __forceinline__ int mass_parts(const MassArgs& a, long long items, int most, int TQ) {
-  if (!a.split || items == 0 || 2 * items > a.G) return 1;
+__device__ __forceinline__ int mass_parts(const MassArgs& a, unsigned items, int most, int TQ) {
+  if (!a.split || items == 0 || 2 * items > (unsigned)a.G) return 1;
   const long long tiles = ((long long)most * a.g + TQ - 1) / TQ;
   const int n = a.G / (int)items;
   return tiles < n ? (int)max(1ll, tiles) : n;
@@ -147,7 +146,7 @@ __device__ __forceinline__ void mass_write(const MassArgs& a, const MassItem& x,
   if (a.born && p >= past) a.born[row] = a.total[x.b] - x.len + p;
 }
 
-int launch_mass_simt(fastar_dtype dt, int D, const MassArgs& a, int32_t* st, cudaStream_t s);
-int launch_mass_tc(int D, const MassArgs& a, int32_t* st, cudaStream_t s);
+int launch_mass_tc(int D, MassArgs a, int32_t* st, cudaStream_t s);
+int launch_mass_join(int TK, int TQ, const MassArgs& a, int32_t* st, cudaStream_t s);
 
 }  // namespace fastar
