@@ -602,7 +602,7 @@ int fastar_page_mass(const fastar_pages* pages, const void* q, const float* lse,
   if (N < 0 || M < 0 || Hq < 0 || Hq % pages->H || block < 0 || (!rows && M != N)) return FASTAR_ERR_ARG;
   if (!(scale > 0.f && scale < INFINITY) || !(decay >= 0.f && decay < INFINITY) || !mass_ok(mass)) return FASTAR_ERR_ARG;
   if (M == 0 || Hq == 0 || pages->B == 0) return FASTAR_OK;
-  if ((int64_t)M * (Hq / pages->H) >= 0x7fffffff - 256) return FASTAR_ERR_UNSUPPORTED;
+  if ((int64_t)M * (Hq / pages->H) >= 0x7fffffff - 256 || (int64_t)Hq * N > 0x7fffffff) return FASTAR_ERR_UNSUPPORTED;
   if (!q || !lse || !cu || !aligned16(q)) return FASTAR_ERR_ARG;
   const size_t need = mass_ws_bytes(Hq, pages->H, M, pages->D);
   if (!ws || ws_bytes < need || ((uintptr_t)ws & 255)) return FASTAR_ERR_WORKSPACE;

@@ -45,8 +45,9 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, i
   const int parts = mass_parts(a, items, most, kTQ);
   for (unsigned it = blockIdx.x; it < items * parts; it += gridDim.x) {
     const MassItem x = walk.find(a, it / parts);
-    const int part = (int)(it % parts), tiles = (x.rows + kTQ - 1) / kTQ;
-    const int t0 = (int)((long long)tiles * part / parts), t1 = (int)((long long)tiles * (part + 1) / parts);
+    const int part = (int)(it % parts), rows = (x.n - x.i0) * a.g, tiles = mass_tiles(a, x.n - x.i0, kTQ);
+    int t0, t1;
+    mass_share(tiles, part, parts, t0, t1);
     if (tid < kTK) {
       int row = -1;
       if (tid < x.len - x.k0) {
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, i
     float drew[4] = {0.f, 0.f, 0.f, 0.f};
     for (int t = t0; t < t1; ++t) {
       __syncthreads();
-      const int r0 = t * kTQ, live = min(kTQ, x.rows - r0);
+      const int r0 = t * kTQ, live = min(kTQ, rows - r0);
       for (int e = tid; e < kTQ * RV; e += kThreads) {
         const int r = e / RV, c = e % RV;
         float v[VN];
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, i
       if (parts > 1)
         a.part[(size_t)it * kTK + tid] = d;
       else if (row >= 0)
-        mass_write(a, x, x.k0 + tid, row, sm.old[tid], d);
+        mass_write(a, x.b, x.len - x.n, x.len, x.k0 + tid, row, sm.old[tid], d);
     }
     __syncthreads();
   }
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(TK) mass_join_kernel(const MassArgs a, int32_t
   const float old = a.mass[row];
   float d = 0.f;
   for (int i = 0; i < parts; ++i) d += a.part[((size_t)blockIdx.x * parts + i) * TK + threadIdx.x];
-  mass_write(a, x, p, row, old, d);
+  mass_write(a, x.b, x.len - x.n, x.len, p, row, old, d);
 }
 
 template <typename T, int D>
@@ -193,7 +194,7 @@ int launch_t(const MassArgs& a, int32_t* st, cudaStream_t s) {
 // Tiles of keys and rows as in the kernel that left the sums.
 int launch_mass_join(int TK, int TQ, const MassArgs& a, int32_t* st, cudaStream_t s) {
   auto kernel = TK == 64 ? mass_join_kernel<64, 64> : mass_join_kernel<256, 128>;
-  if (launch_pdl(kernel, dim3(a.G / 2), dim3(TK), 0, s, a, st) != cudaSuccess) {
+  if (launch_pdl(kernel, dim3(a.G * kMostParts / 2), dim3(TK), 0, s, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
   }
@@ -203,7 +204,7 @@ int launch_mass_join(int TK, int TQ, const MassArgs& a, int32_t* st, cudaStream_
 
 size_t mass_ws_bytes(int Hq, int H, int M, int D) {
   if (Hq < 1 || H < 1 || M < 1 || D < 1 || Hq % H) return 0;
-  return (size_t)kCtas * 256 * 4;
+  return (size_t)kMostParts * 152 * 256 * 4;  // (64-key tiles of twice the CTAs need half of it)
 }
 
 int launch_page_mass(const fastar_pages* pg, const void* q, const float* lse, int Hq, int N, const int32_t* rows,
@@ -236,8 +237,24 @@ int launch_page_mass(const fastar_pages* pg, const void* q, const float* lse, in
   a.G = kCtas;
   // cut only where a branch may have rows for two tiles of them
   a.split = (long long)M * a.g > kTQ;
+  a.rows_lo = 0;
+  a.rows_hi = 0x7fffffff;
   const int D = pg->D;
-  if (pg->dt == FASTAR_BF16) return launch_mass_tc(D, a, st, s);
+  if (pg->dt == FASTAR_BF16) {
+    // Branches of a few rows (single tokens) and of many each have their kernel.  The
+    // lengths are not known here: where only one kind can be expected, its kernel
+    // takes all.
+    const long long rows = (long long)M * a.g;
+    const bool many = rows > kMassFew, few = rows <= 64ll * pg->B;
+    int rc = FASTAR_OK;
+    if (few) {
+      a.rows_hi = kMassFew;
+      rc = launch_mass_few(D, a, st, s);
+      a.rows_lo = kMassFew;
+      a.rows_hi = 0x7fffffff;
+    }
+    return rc == FASTAR_OK && many ? launch_mass_tc(D, a, st, s) : rc;
+  }
   return D == 128 ? launch_t<float, 128>(a, st, s) : launch_t<float, 64>(a, st, s);
 }
 

@@ -9,8 +9,8 @@
 // the first tiles, which most tokens see, come first); CTA c takes the items c,
 // c + G, c + 2 G, ...
 //
-// Where there are fewer items than CTAs and many rows, each item's rows are cut
-// into `parts` runs of tiles; each leaves its sums in the workspace and
+// Where items do not fill the CTAs evenly, each item's rows are cut into `parts`
+// runs of tiles; each leaves its sums in the workspace and
 // page_mass_join adds them in order, so results do not change from run to run.
 //
 // The lengths live on the device: every CTA walks them, 32 branches at a time.
@@ -32,8 +32,9 @@ struct MassArgs {
   int32_t* born;        // or null
   const int32_t* total;
   int N, M, Hq, H, g, B, max_pages, page_shift, n_pages, block, G, split;
+  int rows_lo, rows_hi;  // the kernel takes branches of rows_lo < n g <= rows_hi rows
   float scale, decay;
-  float* part;          // [G][TK] sums of cut items
+  float* part;          // [kMostParts G][TK] sums of cut items
 };
 
 // Keys of its branch that token i of n (branch length len) sees.
@@ -45,10 +46,12 @@ __device__ __forceinline__ int mass_limit(int i, int n, int len, int block) {
   return blocks > len / block ? len : blocks * block;
 }
 
+constexpr int kMassFew = 32;  // rows of a branch, for one head, that are a few
+
 struct MassItem {
   int b, h, k0;    // branch, head, first position of the tile
   int lo, n, len;  // first token, tokens, length of the branch
-  int i0, rows;    // first token that sees the tile, rows from it on
+  int i0;          // first token that sees the tile
 };
 
 // Row of position p in the pages of branch b, head h; -1: its page is not there.
@@ -67,6 +70,8 @@ struct MassWalk {
   unsigned base, total;   // items before the 32 branches, and of them
   unsigned mine, incl;    // lane: items of branch b0 + lane; items up to and with it
   int b0, lo, n, len;
+  MassItem x;             // the item found last
+  unsigned left;          // items behind it in its branch
 
   __device__ __forceinline__ long long load(const MassArgs& a, bool& ok) {
     const int lane = threadIdx.x & 31, b = b0 + lane;
@@ -78,6 +83,7 @@ struct MassWalk {
       ok = ok && lo >= 0 && hi >= lo && hi <= a.M && (b != 0 || lo == 0) && len >= 0 &&
            (long long)len <= ((long long)a.max_pages << a.page_shift);
       n = ok ? hi - lo : 0;
+      if (n * a.g <= a.rows_lo || n * a.g > a.rows_hi) n = 0;
     }
     const long long items = n > 0 ? (long long)(((unsigned)len + TK - 1u) / TK) * a.H : 0;
     ok = ok && items < kMaxItems / 32;
@@ -98,6 +104,7 @@ struct MassWalk {
     ok = __all_sync(0xffffffffu, ok) && items < kMaxItems;
     base = 0;
     b0 = 0;
+    left = 0;
     if (a.B > 32) {
       bool same = true;
       load(a, same);
@@ -107,7 +114,7 @@ struct MassWalk {
     return ok ? (unsigned)items : 0u;
   }
   // Item `it`, at or behind the last one asked for.
-  __device__ __forceinline__ MassItem find(const MassArgs& a, unsigned it) {
+  __device__ __forceinline__ const MassItem& find(const MassArgs& a, unsigned it) {
     while (it >= base + total) {
       base += total;
       b0 += 32;
@@ -116,36 +123,88 @@ struct MassWalk {
     }
     const int src = __ffs(__ballot_sync(0xffffffffu, base + incl > it)) - 1;
     const unsigned off = it - base - __shfl_sync(0xffffffffu, incl - mine, src);
-    MassItem x;
+    left = __shfl_sync(0xffffffffu, mine, src) - off - 1u;
     x.b = b0 + src;
-    x.h = (int)(off % (unsigned)a.H);
-    x.k0 = (int)(off / (unsigned)a.H) * TK;
+    const unsigned tile = off / (unsigned)a.H;
+    x.h = (int)(off - tile * (unsigned)a.H);
+    x.k0 = (int)tile * TK;
     x.lo = __shfl_sync(0xffffffffu, lo, src);
     x.n = __shfl_sync(0xffffffffu, n, src);
     x.len = __shfl_sync(0xffffffffu, len, src);
-    // the first token whose last block reaches the tile
-    const int past = x.len - x.n;
-    x.i0 = a.block > 0 ? min(x.n, max(0, x.k0 / a.block * a.block - past)) : 0;
-    x.rows = (x.n - x.i0) * a.g;
+    first_token(a);
     return x;
+  }
+  // The item `by` behind the last one, or `it` where that is another's (the same
+  // item, found without a search while the branch has as many: with one unit per
+  // item the search is what every warp would do most of the time).  by_tiles, by_heads:
+  // by / H and by % H.
+  __device__ __forceinline__ const MassItem& next(const MassArgs& a, unsigned it, unsigned by, int by_tiles, int by_heads) {
+    if (by > left) return find(a, it);
+    left -= by;
+    x.h += by_heads;
+    x.k0 += by_tiles * TK;
+    if (x.h >= a.H) {
+      x.h -= a.H;
+      x.k0 += TK;
+    }
+    first_token(a);
+    return x;
+  }
+  // the first token whose last block reaches the tile
+  __device__ __forceinline__ void first_token(const MassArgs& a) {
+    x.i0 = a.block > 0 ? min(x.n, max(0, x.k0 / a.block * a.block - (x.len - x.n))) : 0;
   }
 };
 
-// Parts of each item.
+// Tiles of TQ rows of an item that `tokens` tokens see.  On the tensor cores
+// (TQ 128) the rows of many tokens that lie in order go head by head, so that a
+// tile is one run of memory; otherwise a token's heads follow one another and few
+// tokens fill few tiles.
+__device__ __forceinline__ bool mass_by_head(const MassArgs& a, int tokens, int TQ) {
+  return TQ == 128 && !a.rows && tokens >= 64;
+}
+__device__ __forceinline__ int mass_tiles(const MassArgs& a, int tokens, int TQ) {
+  return mass_by_head(a, tokens, TQ) ? (tokens + TQ - 1) / TQ * a.g : (tokens * a.g + TQ - 1) / TQ;
+}
+
+// Parts of each item (whole warp): the number that makes the fullest CTA's share
+// least, in tiles of rows, of which an item's begin and end cost about one more
+// and the join's launch three.
+constexpr int kMostParts = 8;  // parts per CTA
 __device__ __forceinline__ int mass_parts(const MassArgs& a, unsigned items, int most, int TQ) {
-  if (!a.split || items == 0 || 2 * items > (unsigned)a.G) return 1;
-  const long long tiles = ((long long)most * a.g + TQ - 1) / TQ;
-  const int n = a.G / (int)items;
-  return tiles < n ? (int)max(1ll, tiles) : n;
+  const unsigned G = a.G;
+  if (!a.split || items == 0 || items > G * kMostParts / 2) return 1;
+  const unsigned tiles = mass_tiles(a, most, TQ), limit = min(tiles, G * kMostParts / items);
+  unsigned best = 0xffffffffu, at = 1;
+  for (unsigned p = 1 + (threadIdx.x & 31); p <= limit; p += 32) {
+    const unsigned cost = (items * p + G - 1) / G * ((tiles + p - 1) / p + 1) + (p > 1 ? 3 : 0);
+    if (cost < best) {
+      best = cost;
+      at = p;
+    }
+  }
+  const unsigned least = __reduce_min_sync(0xffffffffu, best);
+  return (int)__reduce_min_sync(0xffffffffu, best == least ? at : 0xffffffffu);
+}
+
+// Tiles t0 .. t1 - 1 of an item's are those of part `part`.
+__device__ __forceinline__ void mass_share(int tiles, unsigned part, unsigned parts, int& t0, int& t1) {
+  t0 = 0;
+  t1 = tiles;
+  if (parts > 1) {
+    const unsigned each = (unsigned)tiles / parts, more = (unsigned)tiles - each * parts;
+    t0 = (int)(part * each + min(part, more));
+    t1 = t0 + (int)(each + (part < more ? 1u : 0u));
+  }
 }
 
 // The mass of a position with what it drew in this call, and its token's number.
-__device__ __forceinline__ void mass_write(const MassArgs& a, const MassItem& x, int p, int row, float old, float drew) {
-  const int past = x.len - x.n;
+__device__ __forceinline__ void mass_write(const MassArgs& a, int b, int past, int len, int p, int row, float old, float drew) {
   a.mass[row] = p >= past ? drew : fmaf(a.decay, old, drew);
-  if (a.born && p >= past) a.born[row] = a.total[x.b] - x.len + p;
+  if (a.born && p >= past) a.born[row] = a.total[b] - len + p;
 }
 
+int launch_mass_few(int D, MassArgs a, int32_t* st, cudaStream_t s);
 int launch_mass_tc(int D, MassArgs a, int32_t* st, cudaStream_t s);
 int launch_mass_join(int TK, int TQ, const MassArgs& a, int32_t* st, cudaStream_t s);
 

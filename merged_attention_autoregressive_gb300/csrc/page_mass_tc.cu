@@ -4,14 +4,26 @@
 // rows at a time.  The scores are taken transposed, S^T = K Q^T: a key is a TMEM
 // lane and a row a column, so that a thread sums the weights of its key in a
 // register, and nothing but 256 sums leaves an item.
+// The rows' log-sum-exps enter as one more step of the product: 16 channels of the
+// keys hold 1, 1, 1, 0, ... and those of a row the three bf16 parts of -lse / scale
+// (24 bits), so that a column's score comes out ready for the exponential.  Read
+// from shared memory instead they cost every thread 32 loads a unit in the way of
+// the products' operands.
 //   warps 0-15   weights: warp w takes the keys of lane quarter w % 4 of key tile
-//                w / 4 % 2, and half w / 8 of the columns;
+//                w / 4 % 2 and half w / 8 of the columns (eight warps a unit in turn
+//                idled while their half of TMEM was filled); at an item's end the
+//                second halves' sums are handed over.  Without a decay the masses
+//                are added to in L2, each by one thread once;
 //   warp 16      keys: a page box per lane and column half by TMA;
-//   warp 17      products: two of M 128, N = the live rows, K = D per unit, into
-//                one of two halves of TMEM;
-//   warps 18-21  rows: two warps per query tile in turn gather the rows, their
-//                log-sum-exps and limits, and at an item's begin the places and old
-//                masses of its keys, ahead of the products.
+//   warps 17, 18 products: two of M 128, N = the live rows, K = D per unit, into
+//                one of two halves of TMEM, even units by one warp and odd ones by the
+//                other.  The queue of products is a few deep and a look at a barrier
+//                in shared memory takes long beside them, so that one warp for all
+//                left the tensor core idle for as long as it worked;
+//   warps 19-22  rows: a unit each in turn.  The rows' log-sum-exps and limits are
+//                read while the units before are worked on; once the query tile's
+//                place is free a run of rows is fetched by TMA, others 16 bytes a
+//                lane.
 // Waits are bounded: one that runs out sets the status word, and every warp
 // leaves its loop by its own bounded waits.
 #include <math.h>
@@ -23,33 +35,34 @@ namespace fastar {
 namespace {
 
 constexpr int kTK = 256, kTQ = 128, kCtas = 152;
-constexpr int kWeights = 16, kKeys = 16, kProducts = 17, kRows = 18, kThreads = 22 * 32;
-constexpr int kMeta = 4;  // units described ahead: the rows' warps fill unit u + 4 only after unit u + 2's products, so after unit u's weights
+constexpr int kWeights = 16, kKeys = 16, kProducts = 17, kRows = 19, kThreads = 23 * 32;
+// A unit's log-sum-exps and limits are written after the products of the unit four
+// before it, the last turn of the same warp, so after the weights of the unit six
+// before it: its description has one of eight places.  Its query tile waits for the
+// products of the last unit in the same place.
+constexpr int kTurns = 4, kMeta = 8;
+constexpr int kPlaces = 16;  // items whose page ids are kept: the keys are at most 8 items ahead of the products, and these 3 units of the weights
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Unit {
-  int flags;       // kFirst, kLast of the item; kMasked: some row does not see every key; kEnd: none
-  int cols;        // live rows
-  int keys;        // live keys of the item
-  int k0, past, born;
-  int slot;        // of the item's rows, old masses and sums
-  int part;        // of the workspace, -1: the item is whole
+  int cols;    // live rows
+  int masked;  // some row does not see every key, or is nobody's
 };
-constexpr int kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8;
 
-template <int D>
+template <int D, int kPlacesQ>
 struct Smem {
   static constexpr int kTile = 128 * D * 2;       // bytes of 128 keys or rows
-  static constexpr int kSlots = D == 128 ? 2 : 4; // items' keys
-  uint8_t K[kSlots][2][kTile];
-  uint8_t Q[2][kTile];
-  float base[kMeta][kTQ];   // -lse log2 e; -inf: nobody's row
+  static constexpr int kQ = kPlacesQ;                              // query tiles
+  static constexpr int kSlots = (D == 128 ? 6 : 12) - kPlacesQ;    // key tiles, an item has two
+  uint8_t K[kSlots][kTile];
+  uint8_t Q[kQ][kTile];
+  uint4 ones[256];          // the keys' channels for the log-sum-exps: cores of 8 rows x 16 bytes
+  uint4 base[kTurns][256];       // the rows': -lse / scale in three parts; -inf: nobody's row
   int limit[kMeta][kTQ];    // positions that the row sees
   Unit unit[kMeta];
-  int row[kMeta][kTK];      // place in the pages; -1: none
-  float old[kMeta][kTK];
-  float sum[kMeta][kTK];    // of the second half of the columns
-  uint64_t kfull[kSlots], kempty[kSlots], ufull[kMeta], qempty[2], sfull[2], sempty[2], summed[kMeta][8], fin;
+  float sum[2][kTK];        // of the second halves of the columns
+  int ids[kPlaces][kTK / 16];  // page of each box of an item's keys
+  uint64_t kfull[kSlots], kempty[kSlots], ufull[kMeta], qempty[kQ], uempty[kTurns], sfull[2][2], sempty[2][2], summed[2][8], taken[2][8], placed[kPlaces], fin[2];
   uint32_t tmem;
 };
 
@@ -59,31 +72,52 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_constant__ CUtensorMap mapK, const MassArgs a,
+// x as the sum of three bf16 numbers, side by side.
+__device__ __forceinline__ uint2 three_parts(float x) {
+  const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+  const float r = x - __bfloat162float(hi);
+  const bool fine = r - r == 0.f;  // (an infinity has one part)
+  const __nv_bfloat16 mid = __float2bfloat16_rn(fine ? r : 0.f);
+  const __nv_bfloat16 lo = __float2bfloat16_rn(fine ? r - __bfloat162float(mid) : 0.f);
+  const auto bits = [](__nv_bfloat16 y) { return (uint32_t)__bfloat16_as_ushort(y); };
+  return make_uint2(bits(hi) | bits(mid) << 16, bits(lo));
+}
+
+template <int D, int kPlacesQ>
+__global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_constant__ CUtensorMap mapK,
+                                                             const __grid_constant__ CUtensorMap mapQ, const MassArgs a,
                                                              int32_t* st) {
-  using S = Smem<D>;
+  using S = Smem<D, kPlacesQ>;
   extern __shared__ __align__(1024) uint8_t raw[];
   S& sm = *reinterpret_cast<S*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
       tc::mbar_init(&sm.kfull[i], 1);
-      tc::mbar_init(&sm.kempty[i], 1);
+      tc::mbar_init(&sm.kempty[i], 2);
     }
-    for (int i = 0; i < kMeta; ++i) {
-      tc::mbar_init(&sm.ufull[i], 2);
-      for (int k = 0; k < 8; ++k) tc::mbar_init(&sm.summed[i][k], 1);
+    for (int i = 0; i < kMeta; ++i) tc::mbar_init(&sm.ufull[i], 1);
+    for (int i = 0; i < S::kQ; ++i) tc::mbar_init(&sm.qempty[i], 1);
+    for (int i = 0; i < kTurns; ++i) {
+      tc::mbar_init(&sm.uempty[i], 1);
+      tc::mbar_init(&sm.sfull[i >> 1][i & 1], 1);
+      tc::mbar_init(&sm.sempty[i >> 1][i & 1], kWeights / 2);
     }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sm.qempty[i], 1);
-      tc::mbar_init(&sm.sfull[i], 1);
-      tc::mbar_init(&sm.sempty[i], kWeights);
+    for (int i = 0; i < 16; ++i) {
+      tc::mbar_init(&sm.summed[i >> 3][i & 7], 1);
+      tc::mbar_init(&sm.taken[i >> 3][i & 7], 1);
     }
-    tc::mbar_init(&sm.fin, 1);
+    for (int i = 0; i < kPlaces; ++i) tc::mbar_init(&sm.placed[i], 1);
+    tc::mbar_init(&sm.fin[0], 1);
+    tc::mbar_init(&sm.fin[1], 1);
     tc::fence_mbar_init();
   }
-  if (warp == kKeys && lane == 0) tc::prefetch_tensormap(&mapK);
+  if (tid < 256) sm.ones[tid] = tid & 8 ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);
+  tc::fence_proxy_async_smem();
+  if (warp == kKeys && lane == 0) {
+    tc::prefetch_tensormap(&mapK);
+    tc::prefetch_tensormap(&mapQ);
+  }
   pdl_wait();
   const bool odd = (tc::smem_u32(raw) & 1023u) != 0;  // (the products' tiles lie on 1024 bytes)
   if (odd && tid == 0) status_set(st, FASTAR_ERR_CUDA);
@@ -97,10 +131,10 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
   unsigned items = 0;
   int parts = 1;
   bool ok = true;
-  if (warp == kKeys || warp >= kRows) {
+  {
     int most;
     items = walk.count(a, most, ok);
-    if (!ok && lane == 0) status_set(st, FASTAR_ERR_DEVICE_ARG);
+    if (!ok && tid == 0) status_set(st, FASTAR_ERR_DEVICE_ARG);
     if (!ok) items = 0;
     parts = mass_parts(a, items, most, kTQ);
   }
@@ -114,38 +148,62 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
   const uint32_t tmem = sm.tmem;
   ok = true;
   bool bad = false;
+  // (items that are not cut are G apart)
+  const int by_tiles = (int)gridDim.x / a.H, by_heads = (int)gridDim.x - by_tiles * a.H;
+  auto item = [&](unsigned it) -> const MassItem& {
+    return parts > 1 ? walk.find(a, it / parts) : walk.next(a, it, gridDim.x, by_tiles, by_heads);
+  };
 
   if (warp == kKeys) {
     // ================================================= keys
     const int box = min(1 << a.page_shift, 128);
-    unsigned slot = 0, round = 0;
-    for (unsigned it = blockIdx.x; it < items * parts && ok; it += gridDim.x) {
-      const MassItem x = walk.find(a, it / parts);
-      const int tiles = (x.rows + kTQ - 1) / kTQ, part = it % parts;
-      if ((long long)tiles * part / parts == (long long)tiles * (part + 1) / parts) continue;
+    unsigned slot = 0, round = 0, count = 0;
+    // an item's place and page ids are read one item ahead
+    MassItem next;
+    int next_id = -1;
+    auto look = [&](unsigned it) {
+      if (it >= items * parts) return;
+      next = item(it);
+      const int p = next.k0 + lane * box;
+      next_id = lane * box < min(kTK, next.len - next.k0) ? a.table[(size_t)next.b * a.max_pages + (p >> a.page_shift)] : -1;
+    };
+    look(blockIdx.x);
+    for (unsigned it = blockIdx.x; it < items * parts && ok; it += gridDim.x, ++count) {
+      const MassItem x = next;
+      int id = next_id;
+      look(it + gridDim.x);
+      int t0, t1;
+      mass_share(mass_tiles(a, x.n - x.i0, kTQ), it % parts, parts, t0, t1);
+      if (t0 == t1) continue;
       const int p = x.k0 + lane * box;
-      int id = -1;
-      if (lane * box < min(kTK, x.len - x.k0)) {
-        id = a.table[(size_t)x.b * a.max_pages + (p >> a.page_shift)];
-        if (id < 0 || id >= a.n_pages) {
-          bad = true;
-          id = -1;
+      if (lane * box < min(kTK, x.len - x.k0) && (id < 0 || id >= a.n_pages)) {
+        bad = true;
+        id = -1;
+      }
+      bool told = parts > 1;  // (the masses of cut items are the join's)
+      for (int j = 0; j < (x.len - x.k0 > 128 ? 2 : 1) && ok; ++j) {
+        if (round > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.kempty[slot], (round - 1) & 1u));
+        if (!ok) break;
+        if (!told) {
+          if (lane * box < kTK) sm.ids[count % kPlaces][lane] = id;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.placed[count % kPlaces]);
+          told = true;
         }
-      }
-      if (round > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.kempty[slot], (round - 1) & 1u));
-      if (!ok) break;
-      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, id >= 0)) * box * D * 2;
-      if (lane == 0) tc::mbar_arrive_expect_tx(&sm.kfull[slot], bytes);
-      __syncwarp();
-      if (id >= 0) {
-        const int at = lane * box, row = ((id * a.H + x.h) << a.page_shift) + (p & ((1 << a.page_shift) - 1));
-        uint8_t* dst = sm.K[slot][at >> 7] + (at & 127) * 128;
+        const bool mine = id >= 0 && (lane * box) >> 7 == j;
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box * D * 2;
+        if (lane == 0) tc::mbar_arrive_expect_tx(&sm.kfull[slot], bytes);
+        __syncwarp();
+        if (mine) {
+          const int row = ((id * a.H + x.h) << a.page_shift) + (p & ((1 << a.page_shift) - 1));
+          uint8_t* dst = sm.K[slot] + (lane * box & 127) * 128;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) tc::tma_load_2d(dst + c * 128 * 128, &mapK, &sm.kfull[slot], c * 64, row);
-      }
-      if (++slot == S::kSlots) {
-        slot = 0;
-        ++round;
+          for (int c = 0; c < D / 64; ++c) tc::tma_load_2d(dst + c * 128 * 128, &mapK, &sm.kfull[slot], c * 64, row);
+        }
+        if (++slot == S::kSlots) {
+          slot = 0;
+          ++round;
+        }
       }
     }
     // the copies have landed before the CTA exits, also when nobody takes them
@@ -153,233 +211,301 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
       const unsigned n = round + (i < slot);
       if (n && !tc::mbar_wait(&sm.kfull[i], (n - 1) & 1u)) ok = false;
     }
-  } else if (warp == kProducts) {
+  } else if (warp == kProducts || warp == kProducts + 1) {
     // ================================================= products
-    unsigned slot = 0, kphase = 0;
+    const int me = warp - kProducts;
+    unsigned u = 0, slot = 0, phase = 0;  // of the item: first unit, first key tile
     bool issued = false;
-    for (unsigned u = 0; ok; ++u) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.ufull[u % kMeta], (u / kMeta) & 1u));
-      if (!ok) break;
-      const Unit d = sm.unit[u % kMeta];
-      if (d.flags & kEnd) break;
-      if (u >= 2) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sempty[u & 1], ((u >> 1) - 1) & 1u));
-      if (ok && (d.flags & kFirst) && d.cols) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.kfull[slot], kphase));
-      if (!ok) break;
-      tc::tc_fence_after();
-      const int n = (d.cols + 15) & ~15;
-      const uint32_t idesc = tc::idesc_bf16_f32(128, n, 0, 0);
-      const uint32_t kd = tc::desc_low(tc::smem_u32(sm.K[slot][0]), 16), qd = tc::desc_low(tc::smem_u32(sm.Q[u & 1]), 16);
-      const uint32_t dS = tmem + (u & 1) * 256;
-      const int two = d.keys > 128 ? 2 : 1;
-      if (tc::elect_one()) {
-        if (d.cols) {
-          for (int j = 0; j < two; ++j)
+    const uint64_t ones = tc::sdesc_kmajor_plain(tc::smem_u32(sm.ones), 128, 256);
+    const uint32_t k0 = tc::smem_u32(sm.K), dS = tmem + me * 256;
+    for (unsigned it = blockIdx.x; it < items * parts && ok; it += gridDim.x) {
+      const MassItem& x = item(it);
+      int t0, t1;
+      mass_share(mass_tiles(a, x.n - x.i0, kTQ), it % parts, parts, t0, t1);
+      const int units = max(1, t1 - t0), tiles = t0 == t1 ? 0 : x.len - x.k0 > 128 ? 2 : 1;
+      const unsigned slot1 = slot + 1 == S::kSlots ? 0 : slot + 1, phase1 = slot + 1 == S::kSlots ? phase ^ 1u : phase;
+      // (also where none of its units is this warp's: it sees every phase)
+      if (tiles > 0) ok = tc::mbar_wait(&sm.kfull[slot], phase);
+      bool both = tiles < 2;
+      ok = __all_sync(0xffffffffu, ok);
+      int k = (int)(u + me & 1);
+      const bool none = k >= units;
+      for (; k < units && ok; k += 2) {
+        const unsigned n = u + k;
+        const uint32_t back = ((n >> 1) - 1) & 1u;  // parity of the weights of unit n - 2
+        if (n >= 2) ok = tc::mbar_wait(&sm.sempty[me][0], back);
+        ok = ok && tc::mbar_wait(&sm.ufull[n % kMeta], (n / kMeta) & 1u);
+        const Unit d = sm.unit[n % kMeta];
+        const uint32_t idesc = tc::idesc_bf16_f32(128, (d.cols + 15) & ~15, 0, 0);
+        const int q = n % S::kQ;
+        const uint32_t qd = tc::desc_low(tc::smem_u32(sm.Q[q]), 16);
+        const uint64_t base = tc::sdesc_kmajor_plain(tc::smem_u32(sm.base[n % kTurns]), 128, 256);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = ((k >> 2) * 128 * 128 + (k & 3) * 32) / 16;
-              tc::mma_bf16_low(dS + j * 128, kd + j * (S::kTile / 16) + off, qd + off, idesc, k > 0 ? 1u : 0u);
+        for (int j = 0; j < 2; ++j) {
+          if (j == 1 && n >= 2) ok = tc::mbar_wait(&sm.sempty[me][1], back);
+          if (j == 1 && !both) {
+            ok = ok && tc::mbar_wait(&sm.kfull[slot1], phase1);
+            both = true;
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t kd = tc::desc_low(k0 + (j ? slot1 : slot) * S::kTile, 16);
+          if (tc::elect_one()) {
+            if (j < tiles) {
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                const uint32_t off = ((c >> 2) * 128 * 128 + (c & 3) * 32) / 16;
+                tc::mma_bf16_low(dS + j * 128, kd + off, qd + off, idesc, c > 0 ? 1u : 0u);
+              }
+              // (the largest term last: it is rounded once)
+              tc::mma_bf16(dS + j * 128, ones, base, idesc, 1u);
+              if (k + 2 >= units) tc::mma_commit(&sm.kempty[j ? slot1 : slot]);
             }
+            tc::mma_commit(&sm.sfull[me][j]);
+            if (j == 1) {
+              tc::mma_commit(&sm.qempty[q]);
+              tc::mma_commit(&sm.uempty[n % kTurns]);
+            }
+          }
+          __syncwarp();
+          issued = true;
         }
-        tc::mma_commit(&sm.qempty[u & 1]);
-        tc::mma_commit(&sm.sfull[u & 1]);
-        if ((d.flags & kLast) && d.cols) tc::mma_commit(&sm.kempty[slot]);
       }
-      __syncwarp();
-      issued = true;
-      if ((d.flags & kLast) && d.cols && ++slot == S::kSlots) {
-        slot = 0;
-        kphase ^= 1u;
+      if (!both) ok = ok && tc::mbar_wait(&sm.kfull[slot1], phase1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (none && lane == 0) {
+        if (tiles > 0) tc::mbar_arrive(&sm.kempty[slot]);
+        if (tiles > 1) tc::mbar_arrive(&sm.kempty[slot1]);
       }
+      u += units;
+      for (int j = 0; j < tiles; ++j)
+        if (++slot == S::kSlots) {
+          slot = 0;
+          phase ^= 1u;
+        }
     }
     if (issued) {
       // every product has finished before TMEM is freed
-      if (tc::elect_one()) tc::mma_commit(&sm.fin);
+      if (tc::elect_one()) tc::mma_commit(&sm.fin[me]);
       __syncwarp();
-      if (!tc::mbar_wait(&sm.fin, 0)) ok = false;
+      if (!tc::mbar_wait(&sm.fin[me], 0)) ok = false;
     }
   } else if (warp >= kRows) {
     // ================================================= rows
-    const int group = (warp - kRows) >> 1, half = (warp - kRows) & 1;
+    const unsigned me = warp - kRows;
     constexpr int per = D / 8;  // 16-byte pieces of a row
-    unsigned u = 0, count = 0;
-    for (unsigned it = blockIdx.x; it < items * parts && ok; it += gridDim.x, ++count) {
-      const MassItem x = walk.find(a, it / parts);
-      const int tiles = (x.rows + kTQ - 1) / kTQ, part = it % parts;
-      const int t0 = (int)((long long)tiles * part / parts), t1 = (int)((long long)tiles * (part + 1) / parts);
+    unsigned u = 0;
+    for (unsigned it = blockIdx.x; it < items * parts && ok; it += gridDim.x) {
+      const MassItem& x = item(it);
+      const int tokens = x.n - x.i0, rows = tokens * a.g;
+      const bool by_head = mass_by_head(a, tokens, kTQ);
+      const int of_head = (tokens + kTQ - 1) / kTQ;
+      int t0, t1;
+      mass_share(mass_tiles(a, tokens, kTQ), it % parts, parts, t0, t1);
       const int units = max(1, t1 - t0);  // an empty part has a unit too, of no rows
-      for (int t = 0; t < units; ++t, ++u) {
-        if ((int)(u & 1) != group) continue;
-        if (u >= 2) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.qempty[group], ((u >> 1) - 1) & 1u));
-        if (!ok) break;
-        const int ms = u % kMeta, slot = count % kMeta;
-        const int r0 = (t0 + t) * kTQ, live = t1 > t0 ? min(kTQ, x.rows - r0) : 0, padded = (live + 15) & ~15;
-        // two rows per lane: their place, log-sum-exp and limit
-        uint32_t from[2];
+      for (int t = (int)((me - u) % kTurns); t < units; t += kTurns) {
+        const unsigned n = u + t;  // the unit
+        const int ms = n % kMeta, q = n % S::kQ;
+        // first row, of the item or of head `head`
+        const int head = by_head ? (t0 + t) / of_head : 0, r0 = (by_head ? t0 + t - head * of_head : t0 + t) * kTQ;
+        const int live = t1 > t0 ? min(kTQ, (by_head ? tokens : rows) - r0) : 0, padded = (live + 15) & ~15;
+        const int first = x.i0 + (by_head ? r0 : r0 / a.g);  // first token, which sees the fewest keys
+        const int sees = live ? mass_limit(first, x.n, x.len, a.block) : 0;
+        bool masked = sees - x.k0 < min(x.len - x.k0, kTK);
+        // rows e * 32 + lane: their place, log-sum-exp and limit
+        uint32_t from[4];
+        float lse[4];
+        int limit[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = half * 64 + e * 32 + lane;
+        for (int e = 0; e < 4; ++e) {
+          const int r = e * 32 + lane;
           from[e] = 0xffffffffu;
-          float base = -INFINITY;
-          int limit = 0;
+          limit[e] = 0;
           if (r < live) {
-            const int i = (r0 + r) / a.g, head = x.h * a.g + (r0 + r) - i * a.g;
+            const int i = by_head ? r0 + r : (r0 + r) / a.g;
+            const int of = x.h * a.g + (by_head ? head : (r0 + r) - i * a.g);
             const int at = a.rows ? a.rows[x.lo + x.i0 + i] : x.lo + x.i0 + i;
-            if (at < 0 || at >= a.N) {
+            if (at < 0 || at >= a.N)
               bad = true;
-            } else {
-              const uint32_t y = (uint32_t)head * a.N + at;
-              const float lse = a.lse[y];
-              if (lse != -INFINITY) {
-                from[e] = y;
-                base = -lse * kLog2e;
-                limit = mass_limit(x.i0 + i, x.n, x.len, a.block);
-              }
-            }
+            else
+              from[e] = (uint32_t)of * a.N + at;
+            limit[e] = masked ? mass_limit(x.i0 + i, x.n, x.len, a.block) : x.len;
           }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lse[e] = from[e] != 0xffffffffu ? a.lse[from[e]] : -INFINITY;
+        uint2 base[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (lse[e] == -INFINITY) {
+            from[e] = 0xffffffffu;  // it adds nothing, whatever its query
+            limit[e] = 0;
+          }
+          base[e] = three_parts(from[e] == 0xffffffffu ? -INFINITY : -lse[e] / a.scale);
+          masked = masked || (e * 32 + lane < padded && limit[e] == 0);
+        }
+        masked = __any_sync(0xffffffffu, masked);
+        // What goes beside the queries, once the products of unit n - 4 are done, the
+        // last turn of this warp (which sees every phase of the barrier).
+        ok = __all_sync(0xffffffffu, n < kTurns || tc::mbar_wait(&sm.uempty[n % kTurns], (n / kTurns - 1) & 1u));
+        if (!ok) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = e * 32 + lane;
           if (r < padded) {
-            sm.base[ms][r] = base;
-            sm.limit[ms][r] = limit;
+            uint4* const to = sm.base[n % kTurns] + (r >> 3) * 16 + (r & 7);
+            to[0] = make_uint4(base[e].x, base[e].y, 0u, 0u);
+            to[8] = make_uint4(0u, 0u, 0u, 0u);
+            sm.limit[ms][r] = limit[e];
           }
         }
-        // their queries, 16 bytes per lane
-        const uint32_t q0 = tc::smem_u32(sm.Q[group]);
-        const int end = min(64, padded - half * 64);
-        for (int k = 0; k < end; k += 32 / per) {
-          const int r = k + lane / per, c = lane % per;
-          const uint32_t src = __shfl_sync(0xffffffffu, k & 32 ? from[1] : from[0], r & 31);
-          const bool there = src != 0xffffffffu;
-          tc::cp_async16(q0 + tc::sw128_offset(half * 64 + r, c, 128),
-                         (const char*)a.q + (there ? (size_t)src * (D * 2) + c * 16 : 0), there ? 16u : 0u);
-        }
-        if (t == 0) {
-          // the item's keys: four per lane
-          int row[4];
+        if (lane == 0) sm.unit[ms] = {live, masked};
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        // The queries, once the products of unit n - kQ are done, the last one in
+        // their place.  (The phase before it, unit n - 2 kQ's, is over: that unit is n -
+        // 4 or older, and as odd or even as n - 4; the phase behind it is unit n's.)
+        ok = __all_sync(0xffffffffu, n < S::kQ || tc::mbar_wait(&sm.qempty[q], (n / S::kQ - 1) & 1u));
+        if (!ok) break;
+        if (by_head) {
+          // (a box past the branch's rows brings others': nobody's columns)
+          if (lane == 0 && live) {
+            tc::mbar_arrive_expect_tx(&sm.ufull[ms], kTQ * D * 2);
+            const int y = (int)((uint32_t)(x.h * a.g + head) * a.N + x.lo + first);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = (half * 4 + e) * 32 + lane;
-            row[e] = k < x.len - x.k0 ? mass_row(a, x.b, x.h, x.k0 + k) : -1;
-            bad = bad || (k < x.len - x.k0 && row[e] < 0);
+            for (int c = 0; c < D / 64; ++c) tc::tma_load_2d(sm.Q[q] + c * 128 * 128, &mapQ, &sm.ufull[ms], c * 64, y);
+          } else if (lane == 0) {
+            tc::mbar_arrive(&sm.ufull[ms]);
           }
-          float old[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) old[e] = row[e] >= 0 && parts == 1 ? a.mass[row[e]] : 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            sm.row[slot][(half * 4 + e) * 32 + lane] = row[e];
-            sm.old[slot][(half * 4 + e) * 32 + lane] = old[e];
-          }
+          continue;
         }
-        if (half == 0 && lane == 0) {
-          Unit d;
-          // the tile's first row sees the fewest keys
-          const int first = live ? mass_limit(x.i0 + r0 / a.g, x.n, x.len, a.block) : 0;
-          d.flags = (t == 0 ? kFirst : 0) | (t == units - 1 ? kLast : 0) | (first - x.k0 < min(x.len - x.k0, kTK) ? kMasked : 0);
-          d.cols = live;
-          d.keys = x.len - x.k0;
-          d.k0 = x.k0;
-          d.past = x.len - x.n;
-          d.born = a.born ? a.total[x.b] - x.len : 0;
-          d.slot = slot;
-          d.part = parts > 1 ? (int)it : -1;
-          sm.unit[ms] = d;
+        const uint32_t q0 = tc::smem_u32(sm.Q[q]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (e * 32 >= padded) break;
+          for (int k = 0; k < 32; k += 32 / per) {
+            const int r = k + lane / per, c = lane % per;
+            const uint32_t src = __shfl_sync(0xffffffffu, from[e], r);
+            const bool there = src != 0xffffffffu;
+            tc::cp_async16(q0 + tc::sw128_offset(e * 32 + r, c, 128),
+                           (const char*)a.q + (there ? (size_t)src * (D * 2) + c * 16 : 0), there ? 16u : 0u);
+          }
         }
         tc::cp_async_wait_all();
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sm.ufull[ms]);
       }
-    }
-    // no unit: the end (the group whose turn it is)
-    if (ok && (int)(u & 1) == group) {
-      if (u >= 2) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.qempty[group], ((u >> 1) - 1) & 1u));
-      if (ok && lane == 0) {
-        if (half == 0) sm.unit[u % kMeta].flags = kEnd;
-        tc::mbar_arrive(&sm.ufull[u % kMeta]);
-      }
+      u += units;
     }
     tc::cp_async_wait_all();
   } else {
     // ================================================= weights
-    const int tile = (warp >> 2) & 1, half = warp >> 3;
-    const int key = tile * 128 + (warp & 3) * 32 + lane;
+    const int half = warp >> 3, tile = (warp >> 2) & 1, key = (warp & 7) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + tile * 128 + half * 64;
     const float scale2 = a.scale * kLog2e;
-    float sum[8];
-    unsigned count = 0;
-    for (unsigned u = 0; ok; ++u) {
-      const int ms = u % kMeta;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.ufull[ms], (u / kMeta) & 1u));
-      if (!ok) break;
-      const Unit d = sm.unit[ms];
-      if (d.flags & kEnd) break;
-      if (d.flags & kFirst) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+    unsigned u = 0, count = 0;
+    unsigned shared = 0;  // items so far that both halves have columns of
+    for (unsigned it = blockIdx.x; it < items * parts && ok; it += gridDim.x, ++count) {
+      const MassItem& x = item(it);
+      const int tokens = x.n - x.i0;
+      int t0, t1;
+      mass_share(mass_tiles(a, tokens, kTQ), it % parts, parts, t0, t1);
+      const int units = max(1, t1 - t0);
+      const bool both = units > 1 || (t1 > t0 && min(kTQ, mass_by_head(a, tokens, kTQ) ? tokens : tokens * a.g - t0 * kTQ) > 64);
+      const int p = x.k0 + key;  // (behind the branch's end nothing is done with it)
+      int row = -1;
+      float old = 0.f;
+      if (half == 0 && parts == 1) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.placed[count % kPlaces], (count / kPlaces) & 1u));
+        if (!ok) break;
+        const int id = sm.ids[count % kPlaces][key >> min(a.page_shift, 7)];
+        if (key < x.len - x.k0 && id >= 0) row = ((id * a.H + x.h) << a.page_shift) + (p & ((1 << a.page_shift) - 1));
+        if (row >= 0 && a.decay != 1.f) old = a.mass[row];
       }
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sfull[u & 1], (u >> 1) & 1u));
-      if (!ok) break;
-      tc::tc_fence_after();
-      const int cols = min(64, ((d.cols + 15) & ~15) - half * 64);
-      if (tile * 128 < d.keys) {
-        const uint32_t t = tl + (u & 1) * 256;
-        const float* base = sm.base[ms] + half * 64;
-        const int* limit = sm.limit[ms] + half * 64;
-        const int p = d.k0 + key;
-        int c = 0;
-        for (; c + 32 <= cols; c += 32) {
-          float v[32];
-          tc::tmem_ld32(t + c, v);
+      float sum[2] = {0.f, 0.f};
+      for (int k = 0; k < units; ++k, ++u) {
+        const int ms = u % kMeta, side = u & 1;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.ufull[ms], (u / kMeta) & 1u));
+        if (!ok) break;
+        const Unit d = sm.unit[ms];
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sfull[side][tile], (u >> 1) & 1u));
+        if (!ok) break;
+        tc::tc_fence_after();
+        const int cols = min(64, ((d.cols + 15) & ~15) - half * 64);
+        if (cols > 0 && tile * 128 < x.len - x.k0) {
+          const int* limit = sm.limit[ms] + half * 64;
+          const uint32_t t = tl + side * 256;
+          auto weigh = [&](uint32_t* raw, int c) {
+            float* const v = reinterpret_cast<float*>(raw);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 b = *reinterpret_cast<const float4*>(base + c + i);
-            tc::fma2(v[i], v[i + 1], scale2, scale2, b.x, b.y);
-            tc::fma2(v[i + 2], v[i + 3], scale2, scale2, b.z, b.w);
-          }
-          if (d.flags & kMasked) {
+            for (int i = 0; i < 16; i += 2) tc::mul2(v[i], v[i + 1], scale2, scale2);
+            if (d.masked) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const int4 l = *reinterpret_cast<const int4*>(limit + c + i);
-              v[i] = p < l.x ? v[i] : -INFINITY;
-              v[i + 1] = p < l.y ? v[i + 1] : -INFINITY;
-              v[i + 2] = p < l.z ? v[i + 2] : -INFINITY;
-              v[i + 3] = p < l.w ? v[i + 3] : -INFINITY;
+              for (int i = 0; i < 16; i += 4) {
+                const int4 l = *reinterpret_cast<const int4*>(limit + c + i);
+                v[i] = p < l.x ? v[i] : -INFINITY;
+                v[i + 1] = p < l.y ? v[i + 1] : -INFINITY;
+                v[i + 2] = p < l.z ? v[i + 2] : -INFINITY;
+                v[i + 3] = p < l.w ? v[i + 3] : -INFINITY;
+              }
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = ex2(v[i]);
+            // (a tree: one long chain of sums would hold the next exponentials up)
+#pragma unroll
+            for (int o = 8; o > 1; o >>= 1)
+#pragma unroll
+              for (int i = 0; i < o; i += 2) tc::add2(v[i], v[i + 1], v[i + o], v[i + o + 1]);
+            tc::add2(sum[0], sum[1], v[0], v[1]);
+          };
+          // 16 columns while the next 16 are on their way
+          uint32_t v0[16], v1[16];
+          tc::tmem_ld16_async(t, v0);
+          for (int c = 0; c < cols; c += 32) {
+            tc::tmem_wait16(v0);
+            if (c + 16 < cols) tc::tmem_ld16_async(t + c + 16, v1);
+            weigh(v0, c);
+            if (c + 16 >= cols) break;
+            tc::tmem_wait16(v1);
+            if (c + 32 < cols) tc::tmem_ld16_async(t + c + 32, v0);
+            weigh(v1, c + 16);
           }
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) tc::add2(sum[i & 7], sum[(i & 7) + 1], ex2(v[i]), ex2(v[i + 1]));
         }
-        for (; c < cols; c += 8) {
-          float v[8];
-          tc::tmem_ld8(t + c, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            sum[i] += p < limit[c + i] ? ex2(fmaf(v[i], scale2, base[c + i])) : 0.f;
-        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.sempty[side][tile]);
       }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.sempty[u & 1]);
-      if (d.flags & kLast) {
-        float drew = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
-        const int pair = warp & 7;
-        // the second half's sums; a slot is free again two units later
+      if (!ok) break;
+      float drew = sum[0] + sum[1];
+      if (both) {
+        const int slot = shared & 1;
         if (half == 1) {
-          sm.sum[d.slot][key] = drew;
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm.summed[d.slot][pair]);
-        } else {
-          ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.summed[d.slot][pair], (count / kMeta) & 1u));
+          if (shared >= 2) ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.taken[slot][warp & 7], ((shared >> 1) - 1) & 1u));
           if (!ok) break;
-          drew += sm.sum[d.slot][key];
-          const int row = sm.row[d.slot][key], p = d.k0 + key;
-          if (d.part >= 0) {
-            a.part[(size_t)d.part * kTK + key] = drew;
-          } else if (row >= 0) {
-            a.mass[row] = p >= d.past ? drew : fmaf(a.decay, sm.old[d.slot][key], drew);
-            if (a.born && p >= d.past) a.born[row] = d.born + p;
-          }
+          sm.sum[slot][key] = drew;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.summed[slot][warp & 7]);
+        } else {
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.summed[slot][warp & 7], (shared >> 1) & 1u));
+          if (!ok) break;
+          drew += sm.sum[slot][key];
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.taken[slot][warp & 7]);
         }
-        ++count;
+        ++shared;
+      }
+      if (half == 1) continue;
+      if (parts > 1) {
+        a.part[(size_t)it * kTK + key] = drew;
+      } else if (row >= 0) {
+        const int past = x.len - x.n;
+        if (p < past && a.decay == 1.f)
+          atomicAdd(a.mass + row, drew);  // (nobody else's: the sum is old + drew, rounded once)
+        else
+          mass_write(a, x.b, past, x.len, p, row, old, drew);
       }
     }
   }
@@ -392,19 +518,20 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
   pdl_trigger();
 }
 
-template <int D>
+template <int D, int kPlacesQ>
 int launch_t(const MassArgs& a, int32_t* st, cudaStream_t s) {
-  CUtensorMap k;
+  CUtensorMap k, q;
   const uint32_t box = (1u << a.page_shift) < 128u ? (1u << a.page_shift) : 128u;
   const uint64_t rows = ((uint64_t)a.n_pages * a.H) << a.page_shift;
   // without pages nothing is loaded; the map then describes the queries
-  const int rc = make_tmap_bf16_2d(&k, rows ? a.K : a.q, rows ? rows : 1, D, box, 64);
+  int rc = make_tmap_bf16_2d(&k, rows ? a.K : a.q, rows ? rows : 1, D, box, 64);
+  if (rc == FASTAR_OK) rc = make_tmap_bf16_2d(&q, a.q, (uint64_t)a.Hq * a.N, D, kTQ, 64);
   if (rc != FASTAR_OK) return rc;
-  constexpr int smem = (int)sizeof(Smem<D>);
+  constexpr int smem = (int)sizeof(Smem<D, kPlacesQ>);
   static_assert(smem <= 227 * 1024, "shared memory");
-  auto kernel = mass_tc_kernel<D>;
+  auto kernel = mass_tc_kernel<D, kPlacesQ>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-      launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, k, a, st) != cudaSuccess) {
+      launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, k, q, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
   }
@@ -418,7 +545,7 @@ int launch_mass_tc(int D, MassArgs a, int32_t* st, cudaStream_t s) {
   a.G = kCtas;
   // cut only where a branch may have rows for two tiles of them
   a.split = (long long)a.M * a.g > kTQ;
-  const int rc = D == 128 ? launch_t<128>(a, st, s) : launch_t<64>(a, st, s);
+  const int rc = D == 128 ? launch_t<128, 3>(a, st, s) : launch_t<64, 4>(a, st, s);
   return rc == FASTAR_OK && a.split ? launch_mass_join(kTK, kTQ, a, st, s) : rc;
 }
 

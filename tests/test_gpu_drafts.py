@@ -179,7 +179,15 @@ MASSES = [
     (BF, 128, 2, 8, 64, [24, 3, 17], [700, 0, 31], 1, True, 1.0, True, 40),
     (BF, 64, 1, 1, 256, [1, 2], [2000, 255], 0, True, 0.0, False, 1),
     (BF, 128, 1, 1, 64, [1300], [100], 0, False, 1.0, True, 0),
+    # several items, and tiles of rows, one after the other on every SM
+    (BF, 128, 8, 1, 64, [1] * 40, list(range(300, 700, 10)), 0, False, 1.0, True, 0),
+    (BF, 64, 16, 1, 128, [400, 100, 399, 1, 300, 128], [700, 0, 37, 600, 1000, 128], 1, False, 0.9, True, 0),
+    (BF, 128, 12, 3, 32, [40, 21, 64, 33], [1500, 2000, 900, 1111], 5, True, 1.0, True, 10),
+    # branches of a few rows beside some of many
+    (BF, 128, 3, 1, 64, [40, 1, 0, 1, 33, 2, 32], [100, 500, 3, 64, 300, 0, 129], 1, False, 0.7, True, 3),
+    (BF, 64, 2, 4, 16, [8, 1, 30, 9, 3, 2, 1, 1], [77, 500, 3, 64, 300, 1, 128, 129], 3, True, 1.0, True, 3),
     (F32, 64, 2, 1, 32, [1, 1], [256, 1], 0, False, 1.0, True, 0),
+    (F32, 64, 12, 1, 32, [90] * 5, [700] * 5, 1, False, 1.0, True, 0),
     (F32, 128, 1, 3, 16, [40, 0, 9], [0, 5, 77], 1, True, 0.9, True, 11),
     (F32, 64, 1, 2, 64, [400], [63], 13, False, 1.0, True, 0),
 ]
