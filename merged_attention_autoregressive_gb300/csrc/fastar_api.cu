@@ -622,6 +622,7 @@ int fastar_page_evict(const fastar_pages* pages, const fastar_mass* mass, int bu
     if (mass->born && (out->born == mass->born) != (out->mass == mass->mass)) return FASTAR_ERR_ARG;
   }
   if ((int64_t)pages->max_pages * pages->page > (1 << 19)) return FASTAR_ERR_UNSUPPORTED;
+  if ((int64_t)pages->B * pages->H > (1 << 27)) return FASTAR_ERR_UNSUPPORTED;
   if (pages->B == 0 || pages->max_pages == 0) return FASTAR_OK;
   return launch_page_evict(pages, mass, budget, first, recent, out, dev_status, stream);
 }

@@ -20,8 +20,7 @@
 namespace fastar {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kList = 1024;  // moves listed at a time
+constexpr int kList = 512;  // moves listed at a time
 
 struct EvictArgs {
   const int32_t* len;
@@ -44,11 +43,9 @@ __device__ __forceinline__ int row_of(const EvictArgs& a, const int32_t* table, 
 
 // The order of the rows as an unsigned integer: protected rows first, then by
 // mass; a mass that is not a number comes last.
-__device__ __forceinline__ uint32_t rank_of(const EvictArgs& a, int row, int p, int total) {
-  if (row < 0) return 0u;
-  const int age = a.born ? a.born[row] : p;
+__device__ __forceinline__ uint32_t rank_of(const EvictArgs& a, int age, float mass, int total) {
   if (age < a.first || age >= total - a.recent) return 0xffffffffu;
-  const float x = a.mass[row] + 0.f;  // one zero
+  const float x = mass + 0.f;  // one zero
   if (x != x) return 0u;
   const uint32_t u = __float_as_uint(x);
   return u >> 31 ? ~u : u | 0x80000000u;
@@ -71,6 +68,7 @@ __device__ __forceinline__ uint32_t lowest(uint32_t w, int n) {
 }
 
 // Each thread's count summed over the CTA (one barrier; sum[round & 1] is in use).
+template <int kWarps>
 __device__ __forceinline__ int block_count(int c, int (*sum)[kWarps], int round) {
   c = __reduce_add_sync(0xffffffffu, c);
   if ((threadIdx.x & 31) == 0) sum[round & 1][threadIdx.x >> 5] = c;
@@ -80,8 +78,10 @@ __device__ __forceinline__ int block_count(int c, int (*sum)[kWarps], int round)
 
 // kKeys: integers in a thread's registers, for up to kThreads kKeys positions; 0:
 // they are made anew in every round (longer tables).  per: 16-byte vectors of a row.
-template <int kKeys, int per>
-__global__ void __launch_bounds__(kThreads) page_evict_kernel(const EvictArgs a, int32_t* st) {
+template <int kThreads, int kKeys, int per>
+__global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : kKeys > 8 ? 3 : 4)
+    page_evict_kernel(const EvictArgs a, int32_t* st) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ uint32_t words[];  // [words] kept, [words] ties, then counts
   __shared__ int sum[2][kWarps], scan[33];
   __shared__ int src[kList], dst[kList];
@@ -97,34 +97,73 @@ __global__ void __launch_bounds__(kThreads) page_evict_kernel(const EvictArgs a,
     if (tid == 0) status_set(st, FASTAR_ERR_DEVICE_ARG);
     return;
   }
-  if (len <= a.budget) {
-    if (a.copies)
-      for (int p = part * kThreads + tid; p < len; p += a.cluster * kThreads) {
-        const int r = row_of(a, table, h, p);
-        if (r < 0) {
-          status_set(st, FASTAR_ERR_DEVICE_ARG);
-          continue;
-        }
-        a.out_mass[r] = a.mass[r];
-        if (a.born) a.out_born[r] = a.born[r];
+  // masses and stamps of the positions below n that stay, four at a time
+  auto copy = [&](int n, auto stays) {
+    for (int p0 = part * kThreads + tid; p0 < n; p0 += 4 * a.cluster * kThreads) {
+      int row[4], age[4];
+      float mass[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p = p0 + i * a.cluster * kThreads;
+        row[i] = p < n && stays(p) ? row_of(a, table, h, p) : -2;
+        if (row[i] == -1) status_set(st, FASTAR_ERR_DEVICE_ARG);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mass[i] = row[i] >= 0 ? a.mass[row[i]] : 0.f;
+        age[i] = row[i] >= 0 && a.born ? a.born[row[i]] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (row[i] >= 0) {
+          a.out_mass[row[i]] = mass[i];
+          if (a.born) a.out_born[row[i]] = age[i];
+        }
+    }
+  };
+  if (len <= a.budget) {
+    if (a.copies) copy(len, [](int) { return true; });
     return;
   }
   uint32_t* const kept = words;
   uint32_t* const tied = words + a.words;
   const int nw = (len + 31) / 32;
   bool bad = false;
-  auto key_at = [&](int p) {
-    if (p >= len) return 0u;
-    const int r = row_of(a, table, h, p);
-    bad = bad || r < 0;
-    return rank_of(a, r, p, total);
+  // the ranks of positions (i0 + i) kThreads + tid, their loads side by side
+  auto keys_at = [&](int i0, auto many, uint32_t* key) {
+    constexpr int n = decltype(many)::value;
+    int row[n], age[n];
+    float mass[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const int p = (i0 + i) * kThreads + tid;
+      row[i] = p < len ? row_of(a, table, h, p) : -1;
+      bad = bad || (p < len && row[i] < 0);
+    }
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      age[i] = row[i] >= 0 && a.born ? a.born[row[i]] : (i0 + i) * kThreads + tid;
+      mass[i] = row[i] >= 0 ? a.mass[row[i]] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < n; ++i) key[i] = row[i] >= 0 ? rank_of(a, age[i], mass[i], total) : 0u;
+  };
+  auto key_at = [&](int i) {
+    uint32_t k;
+    keys_at(i, std::integral_constant<int, 1>(), &k);
+    return k;
   };
   uint32_t key[kKeys ? kKeys : 1];
   const int rounds = kKeys ? kKeys : (len + kThreads - 1) / kThreads;
   if (kKeys) {
 #pragma unroll
-    for (int i = 0; i < kKeys; ++i) key[i] = key_at(i * kThreads + tid);
+    for (int i = 0; i < kKeys; i += 8)
+      if (i == 0 || i * kThreads < len) {
+        keys_at(i, std::integral_constant<int, 8>(), key + i);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) key[i + e] = 0u;
+      }
   }
   auto count = [&](uint32_t least) {
     int c = 0;
@@ -132,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) page_evict_kernel(const EvictArgs a,
 #pragma unroll
       for (int i = 0; i < kKeys; ++i) c += key[i] >= least;
     } else {
-      for (int i = 0; i < rounds; ++i) c += key_at(i * kThreads + tid) >= least;
+      for (int i = 0; i < rounds; ++i) c += key_at(i) >= least;
     }
     return c;
   };
@@ -145,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) page_evict_kernel(const EvictArgs a,
     last = 0xffffffffu;
   } else {
     for (uint32_t bit = 0x80000000u; bit && !exact; bit >>= 1) {
-      const int c = block_count(count(last | bit), sum, round++);
+      const int c = block_count<kWarps>(count(last | bit), sum, round++);
       if (c >= a.budget) {
         last |= bit;
         exact = c == a.budget;
@@ -155,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) page_evict_kernel(const EvictArgs a,
   // how many of the ties at it stay
   int quota = 0x7fffffff;
   if (!exact && a.budget > 0) {
-    const int above = last == 0xffffffffu ? 0 : block_count(count(last + 1), sum, round++);
+    const int above = last == 0xffffffffu ? 0 : block_count<kWarps>(count(last + 1), sum, round++);
     quota = a.budget - above;
   } else if (a.budget == 0) {
     quota = 0;
@@ -173,48 +212,45 @@ __global__ void __launch_bounds__(kThreads) page_evict_kernel(const EvictArgs a,
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) mark(i, key[i]);
   } else {
-    for (int i = 0; i < rounds; ++i) mark(i, key_at(i * kThreads + tid));
+    for (int i = 0; i < rounds; ++i) mark(i, key_at(i));
   }
   if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
   __syncthreads();
-  // ties in order, then each word's holes (before the budget) or moving rows
-  // (from it on) and how many there are in the words before
-  int carry = 0;
-  for (int w0 = 0; w0 < nw; w0 += kThreads) {
-    const int w = w0 + tid;
-    const uint32_t t = w < nw ? tied[w] : 0u;
-    int all;
-    const int before = carry + block_excl_scan(__popc(t), scan, &all);
-    if (w < nw) kept[w] |= lowest(t, quota - before);
-    carry += all;
+  // the ties that stay, in order
+  if (!exact) {
+    int carry = 0;
+    for (int w0 = 0; w0 < nw; w0 += kThreads) {
+      const int w = w0 + tid;
+      const uint32_t t = w < nw ? tied[w] : 0u;
+      int all;
+      const int before = carry + block_excl_scan(__popc(t), scan, &all);
+      if (w < nw) kept[w] |= lowest(t, quota - before);
+      carry += all;
+    }
+    __syncthreads();
+  } else {
+    for (int w = tid; w < nw; w += kThreads) kept[w] |= tied[w];
+    __syncthreads();
   }
+  // how many holes (before the budget) or moving rows (behind its word) are in the
+  // words before each; there are as many of them as of the others
   const int edge = a.budget >> 5;  // the word of the budget's own position
   const uint32_t below = (1u << (a.budget & 31)) - 1u;
-  int holes = 0, moves = 0;
+  const int first_moves = __popc(kept[edge] & ~below);
+  int all_words = 0;
   for (int w0 = 0; w0 < nw; w0 += kThreads) {
     const int w = w0 + tid;
-    int nh = 0, nm = 0, all;
-    if (w < nw) {
-      const uint32_t k = kept[w];
-      nh = w < edge ? __popc(~k) : w == edge ? __popc(~k & below) : 0;
-      nm = w > edge ? __popc(k) : w == edge ? __popc(k & ~below) : 0;
-    }
-    const int h0 = holes + block_excl_scan(nh, scan, &all);
-    holes += all;
-    const int m0 = moves + block_excl_scan(nm, scan, &all);
-    moves += all;
-    if (w < nw) tied[w] = w <= edge ? h0 : m0;  // (the edge's own moving rows are the first)
+    const uint32_t k = w < nw ? kept[w] : 0u;
+    const int n = w >= nw ? 0 : w < edge ? __popc(~k) : w == edge ? __popc(~k & below) : __popc(k);
+    int all;
+    const int before = all_words + block_excl_scan(n, scan, &all);
+    if (w < nw) tied[w] = before;
+    all_words += all;
   }
+  const int moves = (all_words + first_moves) / 2;
   __syncthreads();
   if (a.cluster > 1) cluster_sync();
-  if (a.copies)
-    for (int p = part * kThreads + tid; p < a.budget; p += a.cluster * kThreads)
-      if (kept[p >> 5] >> (p & 31) & 1u) {
-        const int r = row_of(a, table, h, p);
-        if (r < 0) continue;
-        a.out_mass[r] = a.mass[r];
-        if (a.born) a.out_born[r] = a.born[r];
-      }
+  if (a.copies) copy(a.budget, [&](int p) { return kept[p >> 5] >> (p & 31) & 1u; });
   // this CTA's share of the moves
   const int end = (int)((long long)moves * (part + 1) / a.cluster);
   for (int m0 = (int)((long long)moves * part / a.cluster); m0 < end; m0 += kList) {
@@ -227,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) page_evict_kernel(const EvictArgs a,
           if (at >= m0 && at < m0 + n) to[at - m0] = row_of(a, table, h, w * 32 + __ffs(bits) - 1);
       };
       if (w <= edge) list(w < edge ? ~k : ~k & below, (int)tied[w], dst);
-      if (w >= edge) list(w > edge ? k : k & ~below, w > edge ? (int)tied[w] : 0, src);
+      if (w >= edge) list(w > edge ? k : k & ~below, w > edge ? (int)tied[w] - moves + first_moves : 0, src);
     }
     __syncthreads();
     constexpr int kAhead = 8;
@@ -236,12 +272,12 @@ __global__ void __launch_bounds__(kThreads) page_evict_kernel(const EvictArgs a,
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         const int e = e0 + q * kThreads, i = e / (2 * per), c = e % (2 * per);
-        if (e < n * 2 * per && src[i] >= 0) v[q] = (c < per ? a.K : a.V)[(size_t)src[i] * per + c % per];
+        if (e < n * 2 * per && src[i] >= 0) v[q] = __ldcs((c < per ? a.K : a.V) + (size_t)src[i] * per + c % per);
       }
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         const int e = e0 + q * kThreads, i = e / (2 * per), c = e % (2 * per);
-        if (e < n * 2 * per && src[i] >= 0 && dst[i] >= 0) (c < per ? a.K : a.V)[(size_t)dst[i] * per + c % per] = v[q];
+        if (e < n * 2 * per && src[i] >= 0 && dst[i] >= 0) __stcs((c < per ? a.K : a.V) + (size_t)dst[i] * per + c % per, v[q]);
       }
     }
     for (int i = tid; i < n; i += kThreads)
@@ -254,10 +290,18 @@ __global__ void __launch_bounds__(kThreads) page_evict_kernel(const EvictArgs a,
   pdl_trigger();
 }
 
-template <int kKeys>
-int launch_keys(const EvictArgs& a, int items, int per, int32_t* st, cudaStream_t s) {
-  auto kernel = per == 8 ? page_evict_kernel<kKeys, 8> : per == 16 ? page_evict_kernel<kKeys, 16> : page_evict_kernel<kKeys, 32>;
+template <int kThreads, int kKeys>
+int launch_keys(EvictArgs a, int items, int per, int32_t* st, cudaStream_t s) {
+  auto kernel = per == 8    ? page_evict_kernel<kThreads, kKeys, 8>
+                : per == 16 ? page_evict_kernel<kThreads, kKeys, 16>
+                            : page_evict_kernel<kThreads, kKeys, 32>;
   const int smem = 2 * a.words * 4;
+  // CTAs of a (branch, head): as many as are resident at once and have 64 rows each
+  // to move, if the tables are as long as they may be
+  const int resident = 152 * (kThreads == 1024 ? 1 : kKeys > 8 ? 3 : 4);
+  const int room = a.max_pages << a.page_shift, moves = min(a.budget, room - a.budget);
+  a.cluster = 1;
+  while (a.cluster < 8 && 2 * a.cluster * items <= resident && 128 * a.cluster <= moves) a.cluster *= 2;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
@@ -307,12 +351,11 @@ int launch_page_evict(const fastar_pages* pg, const fastar_mass* mass, int budge
   a.recent = recent;
   const int room = pg->max_pages * pg->page, items = pg->B * pg->H;
   a.words = (room + 31) / 32;
-  a.cluster = items >= 304 ? 1 : items >= 152 ? 2 : items >= 76 ? 4 : 8;
   const int per = pg->D * (pg->dt == FASTAR_BF16 ? 2 : 4) / 16;
-  if (room <= 4 * kThreads) return launch_keys<4>(a, items, per, st, s);
-  if (room <= 16 * kThreads) return launch_keys<16>(a, items, per, st, s);
-  if (room <= 64 * kThreads) return launch_keys<64>(a, items, per, st, s);
-  return launch_keys<0>(a, items, per, st, s);
+  if (room <= 2048) return launch_keys<256, 8>(a, items, per, st, s);
+  if (room <= 8192) return launch_keys<256, 32>(a, items, per, st, s);
+  if (room <= 32768) return launch_keys<1024, 32>(a, items, per, st, s);
+  return launch_keys<1024, 0>(a, items, per, st, s);
 }
 
 }  // namespace fastar
