@@ -6,6 +6,10 @@
 // read lies behind, so a chunk of ascending tokens is read into registers, the
 // threads of the (branch, head) meet, and the chunk is written.
 //
+// A CTA takes 128 bytes of every row of a (branch, head): columns do not meet, so
+// that is where the work is split when rows are long or heads few.  The next chunk
+// is read before the present one is written, for its rows lie behind all of those.
+//
 // What bounds it: memory where many rows move, a launch and three dependent
 // reads (offsets, page ids, rows) where a path of a few drafts does.
 #include "common.cuh"
@@ -13,7 +17,8 @@
 namespace fastar {
 namespace {
 
-constexpr int kThreads = 256, kVecs = 4;  // 16-byte vectors in flight per thread
+constexpr int kVecs = 4;   // 16-byte vectors of a thread in a chunk
+constexpr int kSlice = 8;  // of a row in a CTA
 
 struct KeepArgs {
   const int32_t* cu;
@@ -23,7 +28,7 @@ struct KeepArgs {
   const int32_t* table;
   uint4* K;
   uint4* V;
-  int M, H, max_pages, page_shift, n_pages;
+  int M, H, max_pages, page_shift, n_pages, per;  // per: 16-byte vectors of a row
 };
 
 // Row of position p of branch b and head h in the pages; -1: there is none.
@@ -35,12 +40,12 @@ __device__ __forceinline__ int row_of(const KeepArgs& a, int b, int h, int p) {
   return ((id * a.H + h) << a.page_shift) + (p & ((1 << a.page_shift) - 1));
 }
 
-// grid (H, B, keys and values); per: 16-byte vectors of a row.
-template <int per>
+// grid (H slices, B, keys and values).
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) page_keep_kernel(const KeepArgs a, int32_t* st) {
   pdl_wait();
-  const int b = blockIdx.y, h = blockIdx.x;
-  uint4* const x = blockIdx.z ? a.V : a.K;
+  const int b = blockIdx.y, slices = a.per / kSlice, h = blockIdx.x / slices, slice = blockIdx.x - h * slices;
+  uint4* const x = (blockIdx.z ? a.V : a.K) + slice * kSlice + threadIdx.x % kSlice;
   if (block_status_bad(st)) return;
   const int lo = a.cu[b], hi = a.cu[b + 1], k0 = a.cu_keep[b], k1 = a.cu_keep[b + 1], len = a.len[b];
   const long long room = (long long)a.max_pages << a.page_shift;
@@ -49,35 +54,55 @@ __global__ void __launch_bounds__(kThreads) page_keep_kernel(const KeepArgs a, i
   if (!ok && threadIdx.x == 0) status_set(st, FASTAR_ERR_DEVICE_ARG);
   if (!ok) return;
   const int past = len - (hi - lo), n = k1 - k0;  // (past may be negative: those positions have no row)
-  constexpr int kRows = kThreads / per;  // rows of one vector per thread
-  const int c = threadIdx.x % per, t = threadIdx.x / per;
-  for (int j0 = 0; j0 < n; j0 += kRows * kVecs) {
-    uint4 v[kVecs];
-    int to[kVecs];
+  constexpr int kRows = kThreads / kSlice;        // rows of one vector per thread
+  const int t = threadIdx.x / kSlice;
+  // where the vectors of the chunk from j0 on are and where they go (-1: nowhere)
+  auto place = [&](int j0, int (&from)[kVecs], int (&to)[kVecs]) {
+int r[kVecs], before[kVecs];
 #pragma unroll
     for (int e = 0; e < kVecs; ++e) {
       const int j = j0 + e * kRows + t;
-      to[e] = -1;
-      if (j >= n) continue;
-      const int r = a.rows[k0 + j], before = j > 0 ? a.rows[k0 + j - 1] : lo - 1;
-      if (r <= before || r < lo || r >= hi) {
-        status_set(st, FASTAR_ERR_DEVICE_ARG);
-        continue;
-      }
-      if (r - lo == j) continue;  // it stays where it is
-      const int from = row_of(a, b, h, past + r - lo);
-      to[e] = row_of(a, b, h, past + j);
-      if (from < 0 || to[e] < 0) {
+      r[e] = j < n ? a.rows[k0 + j] : -1;
+      before[e] = j < n && j > 0 ? a.rows[k0 + j - 1] : lo - 1;
+    }
+#pragma unroll
+    for (int e = 0; e < kVecs; ++e) {
+      const int j = j0 + e * kRows + t;
+      const bool fine = r[e] > before[e] && r[e] >= lo && r[e] < hi, moves = j < n && fine && r[e] - lo != j;
+      if (j < n && !fine) status_set(st, FASTAR_ERR_DEVICE_ARG);
+      from[e] = moves ? row_of(a, b, h, past + r[e] - lo) : -1;
+      to[e] = moves ? row_of(a, b, h, past + j) : -1;
+      if (moves && (from[e] < 0 || to[e] < 0)) {
         status_set(st, FASTAR_ERR_DEVICE_ARG);
         to[e] = -1;
-        continue;
       }
-      v[e] = x[(size_t)from * per + c];
+    }
+  };
+  constexpr int kChunk = kRows * kVecs;
+  int from[kVecs], to[kVecs];
+  uint4 v[kVecs];
+  auto read = [&](uint4 (&v)[kVecs]) {
+#pragma unroll
+    for (int e = 0; e < kVecs; ++e)
+      if (to[e] >= 0) v[e] = __ldcs(x + (size_t)from[e] * a.per);
+  };
+  place(0, from, to);
+  read(v);
+  for (int j0 = 0; j0 < n; j0 += kChunk) {
+    int at[kVecs];
+#pragma unroll
+    for (int e = 0; e < kVecs; ++e) at[e] = to[e];
+    uint4 next[kVecs];
+    if (j0 + kChunk < n) {
+      place(j0 + kChunk, from, to);
+      read(next);
     }
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < kVecs; ++e)
-      if (to[e] >= 0) x[(size_t)to[e] * per + c] = v[e];
+      if (at[e] >= 0) __stcs(x + (size_t)at[e] * a.per, v[e]);
+#pragma unroll
+    for (int e = 0; e < kVecs; ++e) v[e] = next[e];
   }
   pdl_trigger();
 }
@@ -87,11 +112,12 @@ __global__ void __launch_bounds__(kThreads) page_keep_kernel(const KeepArgs a, i
 int launch_page_keep(const fastar_pages* pg, const int32_t* cu, const int32_t* rows, int M,
                      const int32_t* cu_keep, int32_t* st, cudaStream_t s) {
   KeepArgs a = {cu, rows, cu_keep, pg->len, pg->table, (uint4*)pg->K, (uint4*)pg->V, M, pg->H,
-                pg->max_pages, 0, pg->n_pages};
+                pg->max_pages, 0, pg->n_pages, pg->D * (pg->dt == FASTAR_BF16 ? 2 : 4) / 16};
   while ((1 << a.page_shift) < pg->page) ++a.page_shift;
-  const int per = pg->D * (pg->dt == FASTAR_BF16 ? 2 : 4) / 16;
-  auto kernel = per == 8 ? page_keep_kernel<8> : per == 16 ? page_keep_kernel<16> : page_keep_kernel<32>;
-  const cudaError_t rc = launch_pdl(kernel, dim3(a.H, pg->B, 2), dim3(kThreads), 0, s, a, st);
+  // a chunk of 256 rows where a branch keeps more than one of 128, of 64 for a path of drafts
+  const bool many = M > 128ll * pg->B;
+  const cudaError_t rc = many ? launch_pdl(page_keep_kernel<512>, dim3(a.H * (a.per / kSlice), pg->B, 2), dim3(512), 0, s, a, st)
+                              : launch_pdl(page_keep_kernel<128>, dim3(a.H * (a.per / kSlice), pg->B, 2), dim3(128), 0, s, a, st);
   if (rc != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
