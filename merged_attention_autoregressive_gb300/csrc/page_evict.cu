@@ -20,7 +20,7 @@
 namespace fastar {
 namespace {
 
-constexpr int kList = 512;  // moves listed at a time
+constexpr int kList = 1024;  // moves listed at a time
 
 struct EvictArgs {
   const int32_t* len;
@@ -193,12 +193,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : kKeys > 8 ? 3
   }
   // how many of the ties at it stay
   int quota = 0x7fffffff;
-  if (!exact && a.budget > 0) {
-    const int above = last == 0xffffffffu ? 0 : block_count<kWarps>(count(last + 1), sum, round++);
-    quota = a.budget - above;
-  } else if (a.budget == 0) {
+  if (!exact && a.budget > 0)
+    quota = a.budget - (last == 0xffffffffu ? 0 : block_count<kWarps>(count(last + 1), sum, round++));
+  else if (a.budget == 0)
     quota = 0;
-  }
   auto mark = [&](int i, uint32_t k) {
     const uint32_t more = __ballot_sync(0xffffffffu, k > last), same = __ballot_sync(0xffffffffu, k == last);
     const int w = i * kWarps + warp;
@@ -255,15 +253,45 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : kKeys > 8 ? 3
   const int end = (int)((long long)moves * (part + 1) / a.cluster);
   for (int m0 = (int)((long long)moves * part / a.cluster); m0 < end; m0 += kList) {
     const int n = min(kList, end - m0);
-    for (int w = tid; w < nw; w += kThreads) {
-      const uint32_t k = kept[w];
-      auto list = [&](uint32_t bits, int at, int* to) {
-        if (at >= m0 + n || at + __popc(bits) <= m0) return;
-        for (; bits; bits &= bits - 1, ++at)
-          if (at >= m0 && at < m0 + n) to[at - m0] = row_of(a, table, h, w * 32 + __ffs(bits) - 1);
-      };
-      if (w <= edge) list(w < edge ? ~k : ~k & below, (int)tied[w], dst);
-      if (w >= edge) list(w > edge ? k : k & ~below, w > edge ? (int)tied[w] - moves + first_moves : 0, src);
+    // move m: the m-th hole and the m-th moving row, found among the words' counts
+    auto find = [&](int m, int w0, int w1, int less) {  // last word of w0 .. w1 - 1 whose count is <= m
+      while (w1 - w0 > 1) {
+        const int mid = (w0 + w1) >> 1;
+        if ((int)tied[mid] - less <= m)
+          w0 = mid;
+        else
+          w1 = mid;
+      }
+      return w0;
+    };
+    auto nth = [](uint32_t bits, int k) {  // place of the k-th set bit
+      int at = 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const int c = __popc(bits & ((1u << o) - 1u));
+        if (k >= c) {
+          k -= c;
+          bits >>= o;
+          at += o;
+        }
+      }
+      return at;
+    };
+    for (int i = tid; i < n; i += kThreads) {
+      const int m = m0 + i, less = moves - first_moves;
+      const int w = find(m, 0, edge + 1, 0);
+      const int to = w * 32 + nth(w < edge ? ~kept[w] : ~kept[w] & below, m - (int)tied[w]);
+      // (the edge's own moving rows come before those of the words behind it)
+      const int y = m < first_moves ? edge : find(m, edge + 1, nw, less);
+      const int from = y * 32 + nth(y > edge ? kept[y] : kept[y] & ~below, y > edge ? m - ((int)tied[y] - less) : m);
+      const int s = row_of(a, table, h, from), d = row_of(a, table, h, to);
+      const bool there = s >= 0 && d >= 0;
+      src[i] = there ? s : -1;
+      dst[i] = d;
+      if (there) {
+        a.out_mass[d] = a.mass[s];
+        if (a.born) a.out_born[d] = a.born[s];
+      }
     }
     __syncthreads();
     constexpr int kAhead = 8;
@@ -277,14 +305,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : kKeys > 8 ? 3
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         const int e = e0 + q * kThreads, i = e / (2 * per), c = e % (2 * per);
-        if (e < n * 2 * per && src[i] >= 0 && dst[i] >= 0) __stcs((c < per ? a.K : a.V) + (size_t)dst[i] * per + c % per, v[q]);
+        if (e < n * 2 * per && src[i] >= 0) __stcs((c < per ? a.K : a.V) + (size_t)dst[i] * per + c % per, v[q]);
       }
     }
-    for (int i = tid; i < n; i += kThreads)
-      if (src[i] >= 0 && dst[i] >= 0) {
-        a.out_mass[dst[i]] = a.mass[src[i]];
-        if (a.born) a.out_born[dst[i]] = a.born[src[i]];
-      }
     __syncthreads();
   }
   pdl_trigger();
