@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, i
             if (lse != -INFINITY) {
               ld_vec<T, VN>((const T*)a.q + ((size_t)head * a.N + at) * D + c * VN, v);
               base = -lse * kLog2e;
-              limit = mass_limit(i, x.n, x.len, a.block);
+              limit = branch_limit(i, x.n, x.len, a.block);
             }
           }
         }

@@ -16,7 +16,7 @@
 // The lengths live on the device: every CTA walks them, 32 branches at a time.
 #pragma once
 
-#include "common.cuh"
+#include "branch.cuh"
 
 namespace fastar {
 
@@ -36,15 +36,6 @@ struct MassArgs {
   float scale, decay;
   float* part;          // [kMostParts G][TK] sums of cut items
 };
-
-// Keys of its branch that token i of n (branch length len) sees.
-__device__ __forceinline__ int mass_limit(int i, int n, int len, int block) {
-  if (block <= 0) return len;
-  const int t = len - n + i;
-  if (t < 0) return 0;
-  const int blocks = t / block + 1;
-  return blocks > len / block ? len : blocks * block;
-}
 
 constexpr int kMassFew = 32;  // rows of a branch, for one head, that are a few
 

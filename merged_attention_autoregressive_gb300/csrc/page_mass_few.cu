@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mass_few_kernel(const MassAr
         const long long f = place(i);
         const float lse = f >= 0 ? a.lse[f] : -INFINITY;
         base[e] = -lse * kLog2e;
-        limit[e] = lse == -INFINITY ? 0 : mass_limit(i / a.g, x.n, x.len, a.block);
+        limit[e] = lse == -INFINITY ? 0 : branch_limit(i / a.g, x.n, x.len, a.block);
       }
       float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     // ================================================= rows
     const unsigned me = warp - kRows;
     constexpr int per = D / 8;  // 16-byte pieces of a row
-    unsigned u = 0;
+    unsigned u = 0, sent = 0;   // sent: one behind the last unit that the lane has sent for
     for (unsigned it = blockIdx.x; it < items * parts && ok; it += gridDim.x) {
       const MassItem& x = item(it);
       const int tokens = x.n - x.i0, rows = tokens * a.g;
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
         const int head = by_head ? (t0 + t) / of_head : 0, r0 = (by_head ? t0 + t - head * of_head : t0 + t) * kTQ;
         const int live = t1 > t0 ? min(kTQ, (by_head ? tokens : rows) - r0) : 0, padded = (live + 15) & ~15;
         const int first = x.i0 + (by_head ? r0 : r0 / a.g);  // first token, which sees the fewest keys
-        const int sees = live ? mass_limit(first, x.n, x.len, a.block) : 0;
+        const int sees = live ? branch_limit(first, x.n, x.len, a.block) : 0;
         bool masked = sees - x.k0 < min(x.len - x.k0, kTK);
         // rows e * 32 + lane: their place, log-sum-exp and limit
         uint32_t from[4];
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
               bad = true;
             else
               from[e] = (uint32_t)of * a.N + at;
-            limit[e] = masked ? mass_limit(x.i0 + i, x.n, x.len, a.block) : x.len;
+            limit[e] = masked ? branch_limit(x.i0 + i, x.n, x.len, a.block) : x.len;
           }
         }
 #pragma unroll
@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
             const int y = (int)((uint32_t)(x.h * a.g + head) * a.N + x.lo + first);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) tc::tma_load_2d(sm.Q[q] + c * 128 * 128, &mapQ, &sm.ufull[ms], c * 64, y);
+            sent = n + 1;
           } else if (lane == 0) {
             tc::mbar_arrive(&sm.ufull[ms]);
           }
@@ -401,6 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
       u += units;
     }
     tc::cp_async_wait_all();
+    // the copies have landed before the CTA exits, also when nobody takes them
+    if (sent && !tc::mbar_wait(&sm.ufull[(sent - 1) % kMeta], ((sent - 1) / kMeta) & 1u)) ok = false;
   } else {
     // ================================================= weights
     const int half = warp >> 3, tile = (warp >> 2) & 1, key = (warp & 7) * 32 + lane;
