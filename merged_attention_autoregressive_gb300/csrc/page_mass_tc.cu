@@ -44,10 +44,8 @@ constexpr int kTurns = 4, kMeta = 8;
 constexpr int kPlaces = 16;  // items whose page ids are kept: the keys are at most 8 items ahead of the products, and these 3 units of the weights
 constexpr float kLog2e = 1.4426950408889634f;
 
-struct Unit {
-  int cols;    // live rows
-  int masked;  // some row does not see every key, or is nobody's
-};
+// A unit: its live rows, and whether some row does not see every key, or is nobody's.
+constexpr int kMasked = 256;
 
 template <int D, int kPlacesQ>
 struct Smem {
@@ -59,10 +57,10 @@ struct Smem {
   uint4 ones[256];          // the keys' channels for the log-sum-exps: cores of 8 rows x 16 bytes
   uint4 base[kTurns][256];       // the rows': -lse / scale in three parts; -inf: nobody's row
   int limit[kMeta][kTQ];    // positions that the row sees
-  Unit unit[kMeta];
+  int unit[kMeta];
   float sum[2][kTK];        // of the second halves of the columns
   int ids[kPlaces][kTK / 16];  // page of each box of an item's keys
-  uint64_t kfull[kSlots], kempty[kSlots], ufull[kMeta], qempty[kQ], uempty[kTurns], sfull[2][2], sempty[2][2], summed[2][8], taken[2][8], placed[kPlaces], fin[2];
+  uint64_t kfull[kSlots], kempty[kSlots], ufull[kMeta], qempty[kQ], uempty[kTurns], sfull[2][2], sempty[2][2], turn[2], summed[2][8], taken[2][8], placed[kPlaces], fin[2];
   uint32_t tmem;
 };
 
@@ -100,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
     for (int i = 0; i < S::kQ; ++i) tc::mbar_init(&sm.qempty[i], 1);
     for (int i = 0; i < kTurns; ++i) {
       tc::mbar_init(&sm.uempty[i], 1);
-      tc::mbar_init(&sm.sfull[i >> 1][i & 1], 1);
+      tc::mbar_init(&sm.sfull[i >> 1][i & 1], 2);  // the products, and who has seen the unit's description
       tc::mbar_init(&sm.sempty[i >> 1][i & 1], kWeights / 2);
     }
     for (int i = 0; i < 16; ++i) {
@@ -108,6 +106,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
       tc::mbar_init(&sm.taken[i >> 3][i & 7], 1);
     }
     for (int i = 0; i < kPlaces; ++i) tc::mbar_init(&sm.placed[i], 1);
+    tc::mbar_init(&sm.turn[0], 1);
+    tc::mbar_init(&sm.turn[1], 1);
     tc::mbar_init(&sm.fin[0], 1);
     tc::mbar_init(&sm.fin[1], 1);
     tc::fence_mbar_init();
@@ -233,28 +233,32 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
       for (; k < units && ok; k += 2) {
         const unsigned n = u + k;
         const uint32_t back = ((n >> 1) - 1) & 1u;  // parity of the weights of unit n - 2
-        if (n >= 2) ok = tc::mbar_wait(&sm.sempty[me][0], back);
+        if (n >= 2) ok = tc::mbar_wait(&sm.sempty[me][0], back) && tc::mbar_wait(&sm.sempty[me][1], back);
         ok = ok && tc::mbar_wait(&sm.ufull[n % kMeta], (n / kMeta) & 1u);
-        const Unit d = sm.unit[n % kMeta];
-        const uint32_t idesc = tc::idesc_bf16_f32(128, (d.cols + 15) & ~15, 0, 0);
+        const int cols = sm.unit[n % kMeta] & 255;
+        const uint32_t idesc = tc::idesc_bf16_f32(128, (cols + 15) & ~15, 0, 0);
         const int q = n % S::kQ;
         const uint32_t qd = tc::desc_low(tc::smem_u32(sm.Q[q]), 16);
         const uint64_t base = tc::sdesc_kmajor_plain(tc::smem_u32(sm.base[n % kTurns]), 128, 256);
+        if (!both) {
+          ok = ok && tc::mbar_wait(&sm.kfull[slot1], phase1);
+          both = true;
+        }
+        // The units' products go out one after the other: side by side each would
+        // take as long as both.
+        if (n > 0) ok = ok && tc::mbar_wait(&sm.turn[me], me ? (n >> 1) & 1u : back);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc::tc_fence_after();
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          if (j == 1 && n >= 2) ok = tc::mbar_wait(&sm.sempty[me][1], back);
-          if (j == 1 && !both) {
-            ok = ok && tc::mbar_wait(&sm.kfull[slot1], phase1);
-            both = true;
-          }
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc::tc_fence_after();
           const uint32_t kd = tc::desc_low(k0 + (j ? slot1 : slot) * S::kTile, 16);
           if (tc::elect_one()) {
             if (j < tiles) {
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) {
+                // (the other warp needs a while to begin)
+                if (j == tiles - 1 && c == D / 32) tc::mbar_arrive(&sm.turn[me ^ 1]);
                 const uint32_t off = ((c >> 2) * 128 * 128 + (c & 3) * 32) / 16;
                 tc::mma_bf16_low(dS + j * 128, kd + off, qd + off, idesc, c > 0 ? 1u : 0u);
               }
@@ -263,14 +267,16 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
               if (k + 2 >= units) tc::mma_commit(&sm.kempty[j ? slot1 : slot]);
             }
             tc::mma_commit(&sm.sfull[me][j]);
+            tc::mbar_arrive(&sm.sfull[me][j]);
             if (j == 1) {
               tc::mma_commit(&sm.qempty[q]);
               tc::mma_commit(&sm.uempty[n % kTurns]);
             }
           }
           __syncwarp();
-          issued = true;
         }
+        if (tiles == 0 && lane == 0) tc::mbar_arrive(&sm.turn[me ^ 1]);
+        issued = true;
       }
       if (!both) ok = ok && tc::mbar_wait(&sm.kfull[slot1], phase1);
       ok = __all_sync(0xffffffffu, ok);
@@ -361,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
             sm.limit[ms][r] = limit[e];
           }
         }
-        if (lane == 0) sm.unit[ms] = {live, masked};
+        if (lane == 0) sm.unit[ms] = live | (masked ? kMasked : 0);
         tc::fence_proxy_async_smem();
         __syncwarp();
         // The queries, once the products of unit n - kQ are done, the last one in
@@ -431,21 +437,19 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
       float sum[2] = {0.f, 0.f};
       for (int k = 0; k < units; ++k, ++u) {
         const int ms = u % kMeta, side = u & 1;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.ufull[ms], (u / kMeta) & 1u));
-        if (!ok) break;
-        const Unit d = sm.unit[ms];
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.sfull[side][tile], (u >> 1) & 1u));
         if (!ok) break;
+        const int unit = sm.unit[ms];
         tc::tc_fence_after();
-        const int cols = min(64, ((d.cols + 15) & ~15) - half * 64);
+        const int cols = min(64, (((unit & 255) + 15) & ~15) - half * 64);
         if (cols > 0 && tile * 128 < x.len - x.k0) {
           const int* limit = sm.limit[ms] + half * 64;
           const uint32_t t = tl + side * 256;
-          auto weigh = [&](uint32_t* raw, int c) {
+          auto weigh = [&](uint32_t* raw, auto masked, int c) {
             float* const v = reinterpret_cast<float*>(raw);
 #pragma unroll
             for (int i = 0; i < 16; i += 2) tc::mul2(v[i], v[i + 1], scale2, scale2);
-            if (d.masked) {
+            if (decltype(masked)::value) {
 #pragma unroll
               for (int i = 0; i < 16; i += 4) {
                 const int4 l = *reinterpret_cast<const int4*>(limit + c + i);
@@ -467,14 +471,27 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
           // 16 columns while the next 16 are on their way
           uint32_t v0[16], v1[16];
           tc::tmem_ld16_async(t, v0);
-          for (int c = 0; c < cols; c += 32) {
-            tc::tmem_wait16(v0);
-            if (c + 16 < cols) tc::tmem_ld16_async(t + c + 16, v1);
-            weigh(v0, c);
-            if (c + 16 >= cols) break;
-            tc::tmem_wait16(v1);
-            if (c + 32 < cols) tc::tmem_ld16_async(t + c + 32, v0);
-            weigh(v1, c + 16);
+          if (unit == kTQ) {
+            // every row and key: without a branch (240 us, 201 us of two chunks of 4,680 tokens)
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+              tc::tmem_wait16(v0);
+              tc::tmem_ld16_async(t + c + 16, v1);
+              weigh(v0, std::false_type(), c);
+              tc::tmem_wait16(v1);
+              if (c == 0) tc::tmem_ld16_async(t + 32, v0);
+              weigh(v1, std::false_type(), c + 16);
+            }
+          } else {
+            for (int c = 0; c < cols; c += 32) {
+              tc::tmem_wait16(v0);
+              if (c + 16 < cols) tc::tmem_ld16_async(t + c + 16, v1);
+              weigh(v0, std::true_type(), c);
+              if (c + 16 >= cols) break;
+              tc::tmem_wait16(v1);
+              if (c + 32 < cols) tc::tmem_ld16_async(t + c + 32, v0);
+              weigh(v1, std::true_type(), c + 16);
+            }
           }
         }
         tc::tc_fence_before();
