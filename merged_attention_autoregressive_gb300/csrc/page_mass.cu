@@ -7,11 +7,12 @@
 #include <math.h>
 
 #include "page_mass.cuh"
+#include "tc.cuh"
 
 namespace fastar {
 namespace {
 
-constexpr int kTK = 64, kTQ = 64, kThreads = 256, kCtas = 2 * 152;
+constexpr int kTK = 64, kTQ = 64, kThreads = 256, kPerSm = 3, kCtas = kPerSm * 152;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -20,19 +21,20 @@ struct Smem {
   float Q[kTQ][D + 4];
   float base[kTQ];      // -lse log2 e
   int limit[kTQ];       // positions that the row sees; 0: none, or nobody's row
+  long long from[kTQ];  // place in q; -1: its score does not matter
   int row[kTK];         // in the pages; -1: none
   float old[kTK];
   float sum[kThreads / 32][kTK];
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, int32_t* st) {
+template <int D>
+__global__ void __launch_bounds__(kThreads, kPerSm) mass_simt_kernel(const MassArgs a, int32_t* st) {
   pdl_wait();
   extern __shared__ uint4 raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(raw);
   if (block_status_bad(st)) return;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  constexpr int VN = 16 / (int)sizeof(T), RV = D / VN;  // elements of a vector, vectors of a row
+  constexpr int RV = D / 4;  // vectors of a row
   const float scale2 = a.scale * kLog2e;
   MassWalk<kTK> walk;
   int most;
@@ -48,6 +50,47 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, i
     const int part = (int)(it % parts), rows = (x.n - x.i0) * a.g, tiles = mass_tiles(a, x.n - x.i0, kTQ);
     int t0, t1;
     mass_share(tiles, part, parts, t0, t1);
+    // what belongs to the rows of tile t (64 threads)
+    auto describe = [&](int r, int t) {
+      const int i = t * kTQ + r;
+      long long from = -1;
+      float base = 0.f;
+      int limit = 0;
+      if (i < rows && t < t1) {
+        const int token = x.i0 + i / a.g, head = x.h * a.g + i % a.g;
+        const int at = a.rows ? a.rows[x.lo + token] : x.lo + token;
+        if (at < 0 || at >= a.N) {
+          bad = true;
+        } else {
+          const float lse = a.lse[(size_t)head * a.N + at];
+          if (lse != -INFINITY) {
+            from = (long long)head * a.N + at;
+            base = -lse * kLog2e;
+            limit = branch_limit(token, x.n, x.len, a.block);
+          }
+        }
+      }
+      sm.from[r] = from;
+      sm.base[r] = base;
+      sm.limit[r] = limit;
+    };
+    // 64 rows into shared memory, a thread's loads side by side
+    constexpr int kLoads = kTK * RV / kThreads;
+    auto fetch = [&](const float* src, auto place, float (*dst)[D + 4]) {
+      float4 v[kLoads];
+#pragma unroll
+      for (int e = 0; e < kLoads; ++e) {
+        const int r = (e * kThreads + tid) / RV, c = (e * kThreads + tid) % RV;
+        const long long at = place(r);
+        v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (at >= 0) v[e] = *(reinterpret_cast<const float4*>(src + (size_t)at * D) + c);
+      }
+#pragma unroll
+      for (int e = 0; e < kLoads; ++e) {
+        const int r = (e * kThreads + tid) / RV, c = (e * kThreads + tid) % RV;
+        *reinterpret_cast<float4*>(&dst[r][c * 4]) = v[e];
+      }
+    };
     if (tid < kTK) {
       int row = -1;
       if (tid < x.len - x.k0) {
@@ -56,49 +99,20 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, i
       }
       sm.row[tid] = row;
       sm.old[tid] = row >= 0 && parts == 1 ? a.mass[row] : 0.f;
+    } else if (tid < kTK + kTQ) {
+      describe(tid - kTK, t0);
     }
     __syncthreads();
-    for (int e = tid; e < kTK * RV; e += kThreads) {
-      const int r = e / RV, c = e % RV;
-      float v[VN];
-#pragma unroll
-      for (int i = 0; i < VN; ++i) v[i] = 0.f;
-      if (sm.row[r] >= 0) ld_vec<T, VN>((const T*)a.K + (size_t)sm.row[r] * D + c * VN, v);
-#pragma unroll
-      for (int i = 0; i < VN; i += 4) *reinterpret_cast<float4*>(&sm.K[r][c * VN + i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    }
+    fetch((const float*)a.K, [&](int r) { return (long long)sm.row[r]; }, sm.K);
     float drew[4] = {0.f, 0.f, 0.f, 0.f};
     for (int t = t0; t < t1; ++t) {
-      __syncthreads();
-      const int r0 = t * kTQ, live = min(kTQ, rows - r0);
-      for (int e = tid; e < kTQ * RV; e += kThreads) {
-        const int r = e / RV, c = e % RV;
-        float v[VN];
-#pragma unroll
-        for (int i = 0; i < VN; ++i) v[i] = 0.f;
-        float base = 0.f;
-        int limit = 0;
-        if (r < live) {
-          const int i = x.i0 + (r0 + r) / a.g, head = x.h * a.g + (r0 + r) % a.g;
-          const int at = a.rows ? a.rows[x.lo + i] : x.lo + i;
-          if (at < 0 || at >= a.N) {
-            bad = true;
-          } else {
-            const float lse = a.lse[(size_t)head * a.N + at];
-            if (lse != -INFINITY) {
-              ld_vec<T, VN>((const T*)a.q + ((size_t)head * a.N + at) * D + c * VN, v);
-              base = -lse * kLog2e;
-              limit = branch_limit(i, x.n, x.len, a.block);
-            }
-          }
-        }
-        if (c == 0) {
-          sm.base[r] = base;
-          sm.limit[r] = limit;
-        }
-#pragma unroll
-        for (int i = 0; i < VN; i += 4) *reinterpret_cast<float4*>(&sm.Q[r][c * VN + i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      if (t > t0) {
+        __syncthreads();
+        if (tid < kTQ) describe(tid, t);
+        __syncthreads();
       }
+      const int live = min(kTQ, rows - t * kTQ);
+      fetch((const float*)a.q, [&](int r) { return sm.from[r]; }, sm.Q);
       __syncthreads();
       if ((ty & ~1) * 4 >= live) continue;  // no row of the warp
       float s[4][4], s1[4][4];
@@ -106,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, i
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = s1[i][j] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
       for (int k = 0; k < D; k += 4) {
         float4 qv[4], kv[4];
 #pragma unroll
@@ -117,10 +131,12 @@ __global__ void __launch_bounds__(kThreads) mass_simt_kernel(const MassArgs a, i
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
-            s1[i][j] = fmaf(qv[i].y, kv[j].y, s1[i][j]);
-            s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
-            s1[i][j] = fmaf(qv[i].w, kv[j].w, s1[i][j]);
+            // even and odd channels have a sum each
+            float x0 = qv[i].x, x1 = qv[i].y, x2 = qv[i].z, x3 = qv[i].w;
+            tc::fma2(x0, x1, kv[j].x, kv[j].y, s[i][j], s1[i][j]);
+            tc::fma2(x2, x3, kv[j].z, kv[j].w, x0, x1);
+            s[i][j] = x2;
+            s1[i][j] = x3;
           }
       }
 #pragma unroll
@@ -176,10 +192,10 @@ __global__ void __launch_bounds__(TK) mass_join_kernel(const MassArgs a, int32_t
   mass_write(a, x.b, x.len - x.n, x.len, p, row, old, d);
 }
 
-template <typename T, int D>
+template <int D>
 int launch_t(const MassArgs& a, int32_t* st, cudaStream_t s) {
   constexpr int smem = (int)sizeof(Smem<D>);
-  auto kernel = mass_simt_kernel<T, D>;
+  auto kernel = mass_simt_kernel<D>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
       launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -204,7 +220,7 @@ int launch_mass_join(int TK, int TQ, const MassArgs& a, int32_t* st, cudaStream_
 
 size_t mass_ws_bytes(int Hq, int H, int M, int D) {
   if (Hq < 1 || H < 1 || M < 1 || D < 1 || Hq % H) return 0;
-  return (size_t)kMostParts * 152 * 256 * 4;  // (64-key tiles of twice the CTAs need half of it)
+  return (size_t)kMostParts * 152 * 256 * 4;  // (64-key tiles of three times the CTAs need less)
 }
 
 int launch_page_mass(const fastar_pages* pg, const void* q, const float* lse, int Hq, int N, const int32_t* rows,
@@ -255,7 +271,7 @@ int launch_page_mass(const fastar_pages* pg, const void* q, const float* lse, in
     }
     return rc == FASTAR_OK && many ? launch_mass_tc(D, a, st, s) : rc;
   }
-  return D == 128 ? launch_t<float, 128>(a, st, s) : launch_t<float, 64>(a, st, s);
+  return D == 128 ? launch_t<128>(a, st, s) : launch_t<64>(a, st, s);
 }
 
 }  // namespace fastar
