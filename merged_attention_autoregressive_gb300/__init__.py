@@ -589,7 +589,7 @@ class PagedKV(_Bound):
     place, or by assigning another tensor (a tensor whose own storage is
     replaced, as by resize_, has to be assigned again)."""
     _tensors = ("K", "V", "table", "len")
-    _derived = ("n_pages", "H", "page", "D", "B", "max_pages", "dtype", "device", "struct", "addr")
+    _derived = ("n_pages", "H", "page", "D", "B", "max_pages", "rows", "dtype", "device", "struct", "addr")
 
     def __init__(self, H, D, page, n_pages, B, max_pages, dtype=torch.bfloat16, device="cuda"):
         dev = torch.device(device)
@@ -619,6 +619,7 @@ class PagedKV(_Bound):
         struct = PagesStruct(H, D, page, n_pages, B, max_pages, _dt(K), _at(K, dev), _at(V, dev),
                              _int32(table, table.numel(), dev, "the table"), _int32(length, B, dev, "the lengths"))
         self.n_pages, self.H, self.page, self.D, self.B, self.max_pages = n_pages, H, page, D, B, max_pages
+        self.rows = (n_pages, H, page)
         self.dtype, self.device, self.struct, self.addr = K.dtype, dev, struct, ctypes.addressof(struct)
 
     def nbytes(self) -> int:
@@ -774,7 +775,7 @@ class PageMass(_Bound):
     row's token in its branch, with total [B] int32, the tokens that each branch
     has had so far (the caller counts them, the new ones of a call included)."""
     _tensors = ("mass", "born", "total")
-    _derived = ("device", "struct", "addr")
+    _derived = ("rows", "branches", "device", "struct", "addr")
 
     def __init__(self, pages: PagedKV, born=True):
         dev = pages.K.device
@@ -803,12 +804,13 @@ class PageMass(_Bound):
         dev = _gpu(mass)
         struct = MassStruct(_at(mass, dev), None if born is None else _int32(born, mass.numel(), dev, "born"),
                             None if total is None else _int32(total, total.numel(), dev, "total"))
+        self.rows, self.branches = tuple(mass.shape), None if total is None else total.numel()
         self.device, self.struct, self.addr = dev, struct, ctypes.addressof(struct)
 
     def _fits(self, pages):
-        if self.mass.shape != (pages.n_pages, pages.H, pages.page) or self.device != pages.device:
+        if self.rows != pages.rows or self.device != pages.device:
             raise ValueError("the masses do not fit the pages")
-        if self.total is not None and self.total.numel() != pages.B:
+        if self.branches is not None and self.branches != pages.B:
             raise ValueError("total has an entry per branch")
         return self.addr
 

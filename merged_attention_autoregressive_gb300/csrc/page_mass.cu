@@ -251,20 +251,20 @@ int launch_page_mass(const fastar_pages* pg, const void* q, const float* lse, in
   a.decay = decay;
   a.part = (float*)ws;
   a.G = kCtas;
-  // cut only where a branch may have rows for two tiles of them
-  a.split = (long long)M * a.g > kTQ;
+  a.split = mass_split(a, kTQ);
   a.rows_lo = 0;
   a.rows_hi = 0x7fffffff;
   const int D = pg->D;
   if (pg->dt == FASTAR_BF16) {
     // Branches of a few rows (single tokens) and of many each have their kernel.  The
-    // lengths are not known here: where only one kind can be expected, its kernel
-    // takes all.
+    // lengths are not known here: where only one kind is to be expected, its kernel
+    // takes all (a launch for nothing costs 3 us; the kernel for a few is right for any
+    // number).
     const long long rows = (long long)M * a.g;
-    const bool many = rows > kMassFew, few = rows <= 64ll * pg->B;
+    const bool many = rows > 64 + 4ll * pg->B, few = !many || rows <= 64ll * pg->B;
     int rc = FASTAR_OK;
     if (few) {
-      a.rows_hi = kMassFew;
+      if (many) a.rows_hi = kMassFew;
       rc = launch_mass_few(D, a, st, s);
       a.rows_lo = kMassFew;
       a.rows_hi = 0x7fffffff;

@@ -158,6 +158,10 @@ __device__ __forceinline__ int mass_tiles(const MassArgs& a, int tokens, int TQ)
   return mass_by_head(a, tokens, TQ) ? (tokens + TQ - 1) / TQ * a.g : (tokens * a.g + TQ - 1) / TQ;
 }
 
+// Whether items may be cut: where a branch can be expected to have rows for two
+// tiles (the join's launch for nothing costs 2 us of a small call).
+inline bool mass_split(const MassArgs& a, int TQ) { return (long long)a.M * a.g > TQ + 4ll * a.B; }
+
 // Parts of each item (whole warp): the number that makes the fullest CTA's share
 // least, in tiles of rows, of which an item's begin and end cost about one more
 // and the join's launch three.

@@ -563,8 +563,7 @@ int launch_t(const MassArgs& a, int32_t* st, cudaStream_t s) {
 
 int launch_mass_tc(int D, MassArgs a, int32_t* st, cudaStream_t s) {
   a.G = kCtas;
-  // cut only where a branch may have rows for two tiles of them
-  a.split = (long long)a.M * a.g > kTQ;
+  a.split = mass_split(a, kTQ);
   const int rc = D == 128 ? launch_t<128, 3>(a, st, s) : launch_t<64, 4>(a, st, s);
   return rc == FASTAR_OK && a.split ? launch_mass_join(kTK, kTQ, a, st, s) : rc;
 }
