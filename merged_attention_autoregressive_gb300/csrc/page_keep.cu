@@ -6,8 +6,8 @@
 // read lies behind, so a chunk of ascending tokens is read into registers, the
 // threads of the (branch, head) meet, and the chunk is written.
 //
-// A CTA takes 128 bytes of every row of a (branch, head): columns do not meet, so
-// that is where the work is split when rows are long or heads few.  The next chunk
+// A CTA takes 128 bytes (or less) of every row of a (branch, head): columns do not
+// meet, so that is where the work is split when rows are long or heads few.  The next chunk
 // is read before the present one is written, for its rows lie behind all of those.
 //
 // What bounds it: memory where many rows move, a launch and three dependent
@@ -18,7 +18,6 @@ namespace fastar {
 namespace {
 
 constexpr int kVecs = 4;   // 16-byte vectors of a thread in a chunk
-constexpr int kSlice = 8;  // of a row in a CTA
 
 struct KeepArgs {
   const int32_t* cu;
@@ -40,8 +39,8 @@ __device__ __forceinline__ int row_of(const KeepArgs& a, int b, int h, int p) {
   return ((id * a.H + h) << a.page_shift) + (p & ((1 << a.page_shift) - 1));
 }
 
-// grid (H slices, B, keys and values).
-template <int kThreads>
+// grid (H slices, B, keys and values); kSlice: vectors of a row in a CTA.
+template <int kThreads, int kSlice>
 __global__ void __launch_bounds__(kThreads) page_keep_kernel(const KeepArgs a, int32_t* st) {
   pdl_wait();
   const int b = blockIdx.y, slices = a.per / kSlice, h = blockIdx.x / slices, slice = blockIdx.x - h * slices;
@@ -114,10 +113,23 @@ int launch_page_keep(const fastar_pages* pg, const int32_t* cu, const int32_t* r
   KeepArgs a = {cu, rows, cu_keep, pg->len, pg->table, (uint4*)pg->K, (uint4*)pg->V, M, pg->H,
                 pg->max_pages, 0, pg->n_pages, pg->D * (pg->dt == FASTAR_BF16 ? 2 : 4) / 16};
   while ((1 << a.page_shift) < pg->page) ++a.page_shift;
-  // a chunk of 256 rows where a branch keeps more than one of 128, of 64 for a path of drafts
-  const bool many = M > 128ll * pg->B;
-  const cudaError_t rc = many ? launch_pdl(page_keep_kernel<512>, dim3(a.H * (a.per / kSlice), pg->B, 2), dim3(512), 0, s, a, st)
-                              : launch_pdl(page_keep_kernel<128>, dim3(a.H * (a.per / kSlice), pg->B, 2), dim3(128), 0, s, a, st);
+  // 128-byte slices, chunks of 64 rows for a path of drafts; of 256 rows where a branch
+  // keeps many, and then slices of 64 or 32 bytes where that leaves SMs without a CTA
+  // (5,550 of 6,142 tokens of one branch, 4 heads of 512 bytes: 16 us, 37 us at 128
+  // bytes)
+  cudaError_t rc;
+  auto launch = [&](auto kernel, int threads, int slice) {
+    rc = launch_pdl(kernel, dim3(a.H * (a.per / slice), pg->B, 2), dim3(threads), 0, s, a, st);
+  };
+  const long long ctas = 2ll * pg->B * a.H * a.per;
+  if (M <= 128ll * pg->B)
+    launch(page_keep_kernel<128, 8>, 128, 8);
+  else if (ctas / 8 >= 152)
+    launch(page_keep_kernel<512, 8>, 512, 8);
+  else if (ctas / 4 >= 152)
+    launch(page_keep_kernel<512, 4>, 512, 4);
+  else
+    launch(page_keep_kernel<512, 2>, 512, 2);
   if (rc != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;

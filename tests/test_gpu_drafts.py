@@ -139,6 +139,8 @@ KEEPS = [
     (F32, 128, 1, 32, [500], [17], [list(range(250, 500))]),
     (F32, 64, 5, 256, [1, 2000], [255, 1], [[0], list(range(1, 2000))]),
     (BF, 128, 2, 128, [4680], [4680], [list(range(1, 4680, 2))]),
+    (F32, 128, 2, 64, [3000], [1], [list(range(100, 3000))]),
+    (F32, 128, 20, 64, [500, 600], [1, 9], [list(range(100, 500)), list(range(0, 600, 2))]),
 ]
 
 
