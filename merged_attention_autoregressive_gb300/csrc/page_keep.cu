@@ -7,11 +7,14 @@
 // threads of the (branch, head) meet, and the chunk is written.
 //
 // A CTA takes 128 bytes (or less) of every row of a (branch, head): columns do not
-// meet, so that is where the work is split when rows are long or heads few.  The next chunk
-// is read before the present one is written, for its rows lie behind all of those.
+// meet, so that is where the work is split when rows are long or heads few.  The
+// next chunk is read before the present one is written, for its rows lie behind all
+// of those.
 //
-// What bounds it: memory where many rows move, a launch and three dependent
-// reads (offsets, page ids, rows) where a path of a few drafts does.
+// What bounds it: memory where many rows move (half of 4 x 4,680 tokens of 12 heads:
+// 29 us, 3.9 TB/s; 100 us with chunks of 64 rows, one after the other), a launch and
+// four dependent reads (offsets, ids, pages, rows) where a path of a few drafts does
+// (6 of 31 drafts of 16 branches: 4.6 us, 3.3 us in a graph).
 #include "common.cuh"
 
 namespace fastar {

@@ -3,7 +3,12 @@
 // w(i, p) = exp(scale q_i . k_p - lse_i), summed over the rows i that see
 // position p.  A CTA of 256 threads holds 64 keys and takes 64 rows at a time:
 // 4 x 4 scores per thread, their weights added over the thread's four rows; at
-// the item's end the sums of the 16 threads of a key are joined.
+// the item's end the sums of the 16 threads of a key are joined.  A thread's loads
+// go out side by side (drafts of 9 branches, up to 24 tokens of 3 heads a group,
+// D 64: 13.1 us; one after the other 17.3 us), three CTAs fit on an SM.
+//
+// What bounds it: latency where rows are few (that call: two items per CTA, each a
+// chain of page id, key and row reads), the FP32 pipes where they are many.
 #include <math.h>
 
 #include "page_mass.cuh"

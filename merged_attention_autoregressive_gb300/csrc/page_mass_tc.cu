@@ -7,8 +7,8 @@
 // The rows' log-sum-exps enter as one more step of the product: 16 channels of the
 // keys hold 1, 1, 1, 0, ... and those of a row the three bf16 parts of -lse / scale
 // (24 bits), so that a column's score comes out ready for the exponential.  Read
-// from shared memory instead they cost every thread 32 loads a unit in the way of
-// the products' operands.
+// from shared memory instead they were 900 passes through it a unit, beside the
+// 1,150 cycles that the products' operands take.
 //   warps 0-15   weights: warp w takes the keys of lane quarter w % 4 of key tile
 //                w / 4 % 2 and half w / 8 of the columns (eight warps a unit in turn
 //                idled while their half of TMEM was filled); at an item's end the
@@ -24,6 +24,17 @@
 //                read while the units before are worked on; once the query tile's
 //                place is free a run of rows is fetched by TMA, others 16 bytes a
 //                lane.
+//
+// What bounds it: the handovers between products and weights.  Two chunks of 4,680
+// tokens by frames over 9,360 keys, 12 heads: 215 us, 1.04 PFLOP/s, the tensor
+// pipe busy 54 % of the time and the exponentials' 50 %; without the weights' work
+// the same products take 147 us, without the exponentials 186 us.  On the way there:
+// query rows by 16-byte copies 448 us, by TMA 284 us; one warp for the products 255
+// us; their inputs a unit less ahead 242 us; every unit through the masked loop 234
+// us.  256 keys by 128 rows, because every tile of queries out of L2 then feeds two
+// products; N 256 would read the keys' tile half as often, but leaves no second half
+// of TMEM.
+//
 // Waits are bounded: one that runs out sets the status word, and every warp
 // leaves its loop by its own bounded waits.
 #include <math.h>
@@ -41,21 +52,21 @@ constexpr int kWeights = 16, kKeys = 16, kProducts = 17, kRows = 19, kThreads = 
 // before it: its description has one of eight places.  Its query tile waits for the
 // products of the last unit in the same place.
 constexpr int kTurns = 4, kMeta = 8;
-constexpr int kPlaces = 16;  // items whose page ids are kept: the keys are at most 8 items ahead of the products, and these 3 units of the weights
+constexpr int kPlaces = 16;  // items whose page ids are kept: the keys are at most 8 items ahead of the products, and these a few units of the weights
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A unit: its live rows, and whether some row does not see every key, or is nobody's.
 constexpr int kMasked = 256;
 
-template <int D, int kPlacesQ>
+template <int D>
 struct Smem {
-  static constexpr int kTile = 128 * D * 2;       // bytes of 128 keys or rows
-  static constexpr int kQ = kPlacesQ;                              // query tiles
-  static constexpr int kSlots = (D == 128 ? 6 : 12) - kPlacesQ;    // key tiles, an item has two
+  static constexpr int kTile = 128 * D * 2;                        // bytes of 128 keys or rows
+  static constexpr int kQ = D == 128 ? 3 : 4;                      // query tiles (two of 128 channels: 224 us, three: 215 us)
+  static constexpr int kSlots = (D == 128 ? 6 : 12) - kQ;         // key tiles, an item has two
   uint8_t K[kSlots][kTile];
   uint8_t Q[kQ][kTile];
   uint4 ones[256];          // the keys' channels for the log-sum-exps: cores of 8 rows x 16 bytes
-  uint4 base[kTurns][256];       // the rows': -lse / scale in three parts; -inf: nobody's row
+  uint4 base[kTurns][256];  // the rows': -lse / scale in three parts; -inf: nobody's row
   int limit[kMeta][kTQ];    // positions that the row sees
   int unit[kMeta];
   float sum[2][kTK];        // of the second halves of the columns
@@ -81,11 +92,11 @@ __device__ __forceinline__ uint2 three_parts(float x) {
   return make_uint2(bits(hi) | bits(mid) << 16, bits(lo));
 }
 
-template <int D, int kPlacesQ>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_constant__ CUtensorMap mapK,
                                                              const __grid_constant__ CUtensorMap mapQ, const MassArgs a,
                                                              int32_t* st) {
-  using S = Smem<D, kPlacesQ>;
+  using S = Smem<D>;
   extern __shared__ __align__(1024) uint8_t raw[];
   S& sm = *reinterpret_cast<S*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -472,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
           uint32_t v0[16], v1[16];
           tc::tmem_ld16_async(t, v0);
           if (unit == kTQ) {
-            // every row and key: without a branch (240 us, 201 us of two chunks of 4,680 tokens)
+            // every row and key: without a branch (two chunks of 4,680 tokens 234 -> 215 us)
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
               tc::tmem_wait16(v0);
@@ -538,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_tc_kernel(const __grid_const
   pdl_trigger();
 }
 
-template <int D, int kPlacesQ>
+template <int D>
 int launch_t(const MassArgs& a, int32_t* st, cudaStream_t s) {
   CUtensorMap k, q;
   const uint32_t box = (1u << a.page_shift) < 128u ? (1u << a.page_shift) : 128u;
@@ -547,9 +558,9 @@ int launch_t(const MassArgs& a, int32_t* st, cudaStream_t s) {
   int rc = make_tmap_bf16_2d(&k, rows ? a.K : a.q, rows ? rows : 1, D, box, 64);
   if (rc == FASTAR_OK) rc = make_tmap_bf16_2d(&q, a.q, (uint64_t)a.Hq * a.N, D, kTQ, 64);
   if (rc != FASTAR_OK) return rc;
-  constexpr int smem = (int)sizeof(Smem<D, kPlacesQ>);
+  constexpr int smem = (int)sizeof(Smem<D>);
   static_assert(smem <= 227 * 1024, "shared memory");
-  auto kernel = mass_tc_kernel<D, kPlacesQ>;
+  auto kernel = mass_tc_kernel<D>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
       launch_pdl(kernel, dim3(a.G), dim3(kThreads), smem, s, k, q, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -564,7 +575,7 @@ int launch_t(const MassArgs& a, int32_t* st, cudaStream_t s) {
 int launch_mass_tc(int D, MassArgs a, int32_t* st, cudaStream_t s) {
   a.G = kCtas;
   a.split = mass_split(a, kTQ);
-  const int rc = D == 128 ? launch_t<128, 3>(a, st, s) : launch_t<64, 4>(a, st, s);
+  const int rc = D == 128 ? launch_t<128>(a, st, s) : launch_t<64>(a, st, s);
   return rc == FASTAR_OK && a.split ? launch_mass_join(kTK, kTQ, a, st, s) : rc;
 }
 
