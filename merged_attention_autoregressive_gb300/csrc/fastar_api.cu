@@ -599,9 +599,10 @@ int fastar_page_mass(const fastar_pages* pages, const void* q, const float* lse,
   CallRange range("fastar_page_mass");
   const int rc = check_pages(pages);
   if (rc != FASTAR_OK) return rc;
-  if (N < 0 || M < 0 || Hq < 0 || Hq % pages->H || block < 0 || (!rows && M != N)) return FASTAR_ERR_ARG;
+  if (N < 0 || M < 0 || Hq < 0 || Hq % pages->H || block < 0) return FASTAR_ERR_ARG;
   if (!(scale > 0.f && scale < INFINITY) || !(decay >= 0.f && decay < INFINITY) || !mass_ok(mass)) return FASTAR_ERR_ARG;
   if (M == 0 || Hq == 0 || pages->B == 0) return FASTAR_OK;
+  if (!rows && M != N) return FASTAR_ERR_ARG;
   if ((int64_t)M * (Hq / pages->H) >= 0x7fffffff - 256 || (int64_t)Hq * N > 0x7fffffff) return FASTAR_ERR_UNSUPPORTED;
   if (!q || !lse || !cu || !aligned16(q)) return FASTAR_ERR_ARG;
   const size_t need = mass_ws_bytes(Hq, pages->H, M, pages->D);

@@ -543,9 +543,12 @@ class BranchRollout:
     def accept(self, leaves, stream=None):
         """Ends a step of drafts: of each branch the draft leaves[b] and those
         above it stay (-1: none), in the order of their positions.  Returns their
-        numbers within the step's rows, branch by branch."""
+        numbers within the step's rows, branch by branch.  (Under a budget their
+        queries are read again: without a plan, the step's q is as it was.)"""
         if self.drafts is None:
             raise ValueError("the last step had no drafts")
+        if self._asked is None:
+            raise ValueError("the drafts have not been attended yet")
         if len(leaves) != self.B or any(not -1 <= x < len(p) for x, p in zip(leaves, self.drafts)):
             raise ValueError("one draft per branch, or -1")
         kept, first = [], 0
@@ -572,7 +575,7 @@ class BranchRollout:
                 self.mass.total.copy_(torch.tensor(self.totals, dtype=torch.int32))
                 fastar_page_mass(self.pages, self._asked, self.lse, self.cu, self.scale, self.mass, block=1, rows=rows,
                                  decay=self.decay, ws=self.ws_mass, status=self.status)
-        self.drafts = self._asked = None
+        self.drafts = None
         return kept
 
     def evict(self, stream=None):
@@ -597,7 +600,7 @@ class BranchRollout:
                            q=q if self.plan is not None else None, q_out=self.q if self.plan is not None else None,
                            status=self.status, stream=stream)
         if self.drafts is not None:
-            self._asked = rotated  # `accept` weighs the tokens that stay
+            self._asked = rotated  # `accept` weighs the tokens that stay (a replayed step asks the same rows)
             fastar_tree_attention(rotated, self.cu, self.parent, self.prefix, self.pages, self.scale, self.out,
                                   lse=self.lse, ws=self.ws, status=self.status, stream=stream)
             return self.out, self.lse

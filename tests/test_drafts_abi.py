@@ -74,6 +74,7 @@ def test_nothing_to_do(m):
     assert _tree(m, _pages(m), N=0, q=None, parent=None) == OK
     assert _keep(m, _pages(m), M=0, rows=None) == OK
     assert _mass(m, _pages(m), M=0, N=0, q=None) == OK
+    assert _mass(m, _pages(m), M=0, N=10, rows=None) == OK  # (an empty tensor of rows is NULL)
     assert _evict(m, _pages(m, max_pages=0, table=None)) == OK
 
 
@@ -174,6 +175,10 @@ def test_rollout_counts_drafts_and_accepted_paths(m, monkeypatch):
     r.extend([30, 0, 5])
     trees = [[-1, 0, 0, 1, 3], [-1, -1], [0 - 1]]
     r.extend([5, 2, 1], parents=trees)
+    r._asked = None
+    with pytest.raises(ValueError, match="attended"):
+        r.accept([0, 0, 0])
+    r._asked = "q"
     assert r.parent[:8].tolist() == [-1, 0, 0, 1, 3, -1, -1, -1] and r.lengths == [35, 2, 6] and len(r.held[0]) == 2
     for call in (lambda: r.extend([1, 1, 1]), lambda: r.release(0), r.evict):
         with pytest.raises(ValueError, match="accepted"):

@@ -289,3 +289,22 @@ def test_graph_of_a_budgeted_step(m):
     torch.cuda.synchronize()
     assert torch.equal(rolls[0].mass.mass, rolls[1].mass.mass) and torch.equal(rolls[0].out, rolls[1].out)
     assert torch.equal(rolls[0].mass.born, rolls[1].mass.born)
+
+
+def test_a_rollout_may_keep_no_draft(m):
+    from merged_attention_autoregressive_gb300.path import BranchRollout
+    gen = torch.Generator().manual_seed(9)
+    r = BranchRollout(2, 2, 64, 20, 64, page=16, block=1, budget=32, recent=8)
+    q, k, v = (_randn(gen, 2, 20, 64) for _ in range(3))
+    r.extend([10, 7])
+    r.step(q, k, v)
+    before = r.mass.mass.clone()
+    r.extend([4, 3], parents=[[-1, 0, 0, 1], [-1, -1, 1]])
+    out = r.step(q, k, v)[0].clone()
+    assert r.accept([-1, -1]) == [[], []] and r.lengths == [10, 7] == r.pages.len.tolist()
+    assert torch.equal(r.mass.mass, before)
+    r.extend([4, 3], parents=[[-1, 0, 0, 1], [-1, -1, 1]])  # again, as if nothing had been
+    assert torch.equal(r.step(q, k, v)[0][:, :7], out[:, :7])
+    assert r.accept([3, 2]) == [[0, 1, 3], [5, 6]] and int(r.status) == 0
+    r.evict()
+    assert r.lengths == [13, 9]
