@@ -308,3 +308,59 @@ def test_a_rollout_may_keep_no_draft(m):
     assert r.accept([3, 2]) == [[0, 1, 3], [5, 6]] and int(r.status) == 0
     r.evict()
     assert r.lengths == [13, 9]
+
+
+# tables longer than the branches, so that each way of sharing a head's rows is taken:
+# heads, room of a table, lengths, budget
+LONG = [
+    (2, 3008, [3000, 20], 1500),
+    (80, 8192, [4500, 10], 1999),
+    (350, 8192, [300, 4], 97),
+    (1, 16384, [9000], 4096),
+    (38, 32768, [9000, 5], 8999),
+    (38, 65536, [3000, 5], 1),
+    (80, 16384, [2500, 31], 1250),
+    (80, 65536, [2500, 31], 640),
+]
+
+
+@pytest.mark.parametrize("H,room,lengths,budget", LONG)
+@pytest.mark.parametrize("kind", ["random", "ties"])
+def test_eviction_of_long_tables(m, H, room, lengths, budget, kind):
+    rng, gen, page, D = np.random.default_rng(H + budget), torch.Generator().manual_seed(H), 64, 64
+    _, length, table, pool = _layout(rng, lengths, [0] * len(lengths), page)
+    table = np.concatenate((table, np.full((len(lengths), room // page - table.shape[1]), -1, np.int32)), 1)
+    K, V, pages = _pages(m, gen, pool, H, page, D, BF, table, length)
+    x = rng.random((pool, H, page)).astype(np.float32)
+    if kind == "ties":
+        x = np.floor(x * 3).astype(np.float32)
+    born = rng.integers(0, max(lengths) + 50, (pool, H, page)).astype(np.int32)
+    total = length + 50
+    mass, stamp = torch.from_numpy(x).cuda(), torch.from_numpy(born).cuda()
+    want = [K.float().cpu().numpy(), V.float().cpu().numpy(), x.copy(), born.copy()]
+    O.page_evict(want, x, born, total, table, length, budget, 0, min(40, budget // 2))
+    held, st = m.PageMass.view(mass, stamp, _ints(total)), _status()
+    # an earlier error, and a length that the table has no room for: nothing is written
+    for spoil in ("status", "long", "negative"):
+        st.fill_(5 if spoil == "status" else 0)
+        if spoil != "status":
+            pages.len[0] = room + 1 if spoil == "long" else -1
+        before = [y.clone() for y in (K, V, mass, stamp)] if spoil == "status" else before
+        m.fastar_page_evict(pages, held, budget, first=0, recent=min(40, budget // 2), status=st)
+        assert int(st) == (5 if spoil == "status" else 18)
+        pages.len.copy_(_ints(length))
+        if spoil == "status" or len(lengths) == 1 or max(lengths[1:]) <= budget:
+            assert all(torch.equal(a, b) for a, b in zip(before, (K, V, mass, stamp)))
+    for y, y0 in zip((K, V, mass, stamp), before):
+        y.copy_(y0)
+    st.zero_()
+    m.fastar_page_evict(pages, held, budget, first=0, recent=min(40, budget // 2), status=st)
+    assert int(st) == 0
+    kept = np.zeros((pool, page), bool)
+    for b, n in enumerate(lengths):
+        for p in range(min(n, budget)):
+            kept[table[b, p // page], p % page] = True
+    for y, w, y0 in zip((K, V, mass, stamp), want, before):
+        y, y0 = (t.float().cpu().numpy() if t.is_floating_point() else t.cpu().numpy() for t in (y, y0))
+        assert np.array_equal(y.swapaxes(1, 2)[kept], w.swapaxes(1, 2)[kept])
+        assert np.array_equal(y.swapaxes(1, 2)[~kept], y0.swapaxes(1, 2)[~kept])
