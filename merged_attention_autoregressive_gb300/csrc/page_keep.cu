@@ -6,13 +6,14 @@
 // read lies behind, so a chunk of ascending tokens is read into registers, the
 // threads of the (branch, head) meet, and the chunk is written.
 //
-// A CTA takes 128 bytes (or less) of every row of a (branch, head): columns do not
+// A CTA takes 128 bytes or less of every row of a (branch, head): columns do not
 // meet, so that is where the work is split when rows are long or heads few.  The
 // next chunk is read before the present one is written, for its rows lie behind all
 // of those.
 //
 // What bounds it: memory where many rows move (half of 4 x 4,680 tokens of 12 heads:
-// 29 us, 3.9 TB/s; 100 us with chunks of 64 rows, one after the other), a launch and
+// 28 us, 4.1 TB/s; 100 us with chunks of 64 rows, one after the other; chunks of 512
+// rows 40 us, ids read two chunks ahead 30 us), a launch and
 // four dependent reads (offsets, ids, pages, rows) where a path of a few drafts does
 // (6 of 31 drafts of 16 branches: 4.6 us, 3.3 us in a graph).
 #include "common.cuh"
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) page_keep_kernel(const KeepArgs a, i
   const int t = threadIdx.x / kSlice;
   // where the vectors of the chunk from j0 on are and where they go (-1: nowhere)
   auto place = [&](int j0, int (&from)[kVecs], int (&to)[kVecs]) {
-int r[kVecs], before[kVecs];
+    int r[kVecs], before[kVecs];
 #pragma unroll
     for (int e = 0; e < kVecs; ++e) {
       const int j = j0 + e * kRows + t;
@@ -117,7 +118,9 @@ int launch_page_keep(const fastar_pages* pg, const int32_t* cu, const int32_t* r
                 pg->max_pages, 0, pg->n_pages, pg->D * (pg->dt == FASTAR_BF16 ? 2 : 4) / 16};
   while ((1 << a.page_shift) < pg->page) ++a.page_shift;
   // 128-byte slices, chunks of 64 rows for a path of drafts; of 256 rows where a branch
-  // keeps many, and then slices of 64 or 32 bytes where that leaves SMs without a CTA
+  // keeps many, by 256 threads in slices of 64 bytes (half of 4 x 4,680 tokens of 12
+  // heads: 28 us, 30 us by 512 threads in slices of 128; 16 branches of 40 heads: 272
+  // and 267 us), or by 512 in slices of 64 or 32 where that leaves SMs without a CTA
   // (5,550 of 6,142 tokens of one branch, 4 heads of 512 bytes: 16 us, 37 us at 128
   // bytes)
   cudaError_t rc;
@@ -128,7 +131,7 @@ int launch_page_keep(const fastar_pages* pg, const int32_t* cu, const int32_t* r
   if (M <= 128ll * pg->B)
     launch(page_keep_kernel<128, 8>, 128, 8);
   else if (ctas / 8 >= 152)
-    launch(page_keep_kernel<512, 8>, 512, 8);
+    launch(page_keep_kernel<256, 4>, 256, 4);
   else if (ctas / 4 >= 152)
     launch(page_keep_kernel<512, 4>, 512, 4);
   else
