@@ -240,12 +240,16 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
         *reinterpret_cast<float4*>(&sm.V[g][tid >> 2][c * VN]) = make_float4(0.f, 0.f, 0.f, 0.f);
     int sees = 0;  // rows that see a key of the unit, or are nobody's
     if (busy) {
+      uint64_t mine = ~0ull;  // tree: what row ty * 4 + tx % 4 sees
+      if (tree && !(x.flags & 16)) {
+        const int r = r0 + ty * 4 + (tx & 3);
+        if (r < rows && branch_row_keys(a, x, r) > 0) mine = tree_row_keys(a, x, r, 0, bad);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = r0 + ty * 4 + i;
         const int seen = x.flags & 16 ? kTN : r < rows ? branch_row_keys(a, x, r) : 0;
-        uint64_t which = ~0ull;
-        if (tree && seen > 0 && !(x.flags & 16)) which = tree_row_keys(a, x, r, 0, bad);
+        const uint64_t which = tree ? __shfl_sync(0xffffffffu, mine, i, 16) : ~0ull;
         sees |= ((seen > 0 && which) || r >= rows ? 1 : 0) << i;
         float top = -INFINITY;
 #pragma unroll
