@@ -547,8 +547,8 @@ __device__ __forceinline__ int branch_row_keys(const BranchArgs& a, const Branch
 // tokens differ.  There a row walks up from its token, which is a read of L1 per
 // step (the rows of a warp share the list) and ends with the unit; no mask is
 // stored, and a branch may have any number of drafts.  Against a plain row of tokens
-// it costs 0 to 5 % (31 drafts of 16 branches, 40 heads, 11,900 + 1,591 keys: 250
-// and 238 us).
+// it costs 0 to 4 % (31 drafts of 16 branches, 40 heads, 11,900 + 1,591 keys: 247
+// and 238 us; 250 without the list's prefetch).
 //
 // The keys from..from + 63 of unit x (from: 0 or 64) that row r of its item sees,
 // a bit each.  bad: a parent is not below its token; the walk ends there.

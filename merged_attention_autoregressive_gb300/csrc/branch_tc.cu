@@ -701,6 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1) branch_tc_kernel(const __grid_con
 #pragma unroll
         for (int c = 0; c < per; ++c)
           tc::cp_async16(q0 + tc::sw128_offset(wr, c0 + c, kM), src + (n ? (c0 + c) * 16 : 0), n);
+        // the first step up the tree, for the units of drafts to come
+        if (tree && r < rows) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.parent + r / a.g));
         tc::cp_async_wait_all();
         tc::fence_proxy_async_smem();
         __syncwarp();
