@@ -21,17 +21,6 @@ namespace {
 constexpr int kTM = 64, kTN = 64, kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// (a0, a1) += (x0 y0, x1 y1), one instruction, each as fmaf rounds it.
-__device__ __forceinline__ void fma_pair(float& a0, float& a1, float x0, float x1, float y0, float y1) {
-  asm("{\n\t.reg .b64 a, x, y;\n\t"
-      "mov.b64 a, {%0, %1};\n\t"
-      "mov.b64 x, {%2, %3};\n\t"
-      "mov.b64 y, {%4, %5};\n\t"
-      "fma.rn.f32x2 a, x, y, a;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}\n"
-      : "+f"(a0), "+f"(a1)
-      : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // relative error about 2^-22
@@ -228,8 +217,8 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            fma_pair(s[i][j], s1[i][j], qv[i].x, qv[i].y, kv[j].x, kv[j].y);
-            fma_pair(s[i][j], s1[i][j], qv[i].z, qv[i].w, kv[j].z, kv[j].w);
+            tc::fma_pair(s[i][j], s1[i][j], qv[i].x, qv[i].y, kv[j].x, kv[j].y);
+            tc::fma_pair(s[i][j], s1[i][j], qv[i].z, qv[i].w, kv[j].z, kv[j].w);
           }
       }
     }
@@ -295,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
-              fma_pair(o[i][4 * c], o[i][4 * c + 1], p, p, v.x, v.y);
-              fma_pair(o[i][4 * c + 2], o[i][4 * c + 3], p, p, v.z, v.w);
+              tc::fma_pair(o[i][4 * c], o[i][4 * c + 1], p, p, v.x, v.y);
+              tc::fma_pair(o[i][4 * c + 2], o[i][4 * c + 3], p, p, v.z, v.w);
             }
           }
         }
@@ -316,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, 2) branch_simt_kernel(BranchArgs a, 
               for (int kk = 0; kk < 4; ++kk) {
                 const float4 v = *reinterpret_cast<const float4*>(&sm.V[g][k + kk][tx * 4 + 64 * c]);
                 const float p = kk == 0 ? pv.x : kk == 1 ? pv.y : kk == 2 ? pv.z : pv.w;
-                fma_pair(o[i][4 * c], o[i][4 * c + 1], p, p, v.x, v.y);
-                fma_pair(o[i][4 * c + 2], o[i][4 * c + 3], p, p, v.z, v.w);
+                tc::fma_pair(o[i][4 * c], o[i][4 * c + 1], p, p, v.x, v.y);
+                tc::fma_pair(o[i][4 * c + 2], o[i][4 * c + 3], p, p, v.z, v.w);
               }
             }
           }

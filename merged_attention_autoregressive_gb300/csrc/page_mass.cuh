@@ -37,7 +37,7 @@ struct MassArgs {
   float* part;          // [kMostParts G][TK] sums of cut items
 };
 
-constexpr int kMassFew = 32;  // rows of a branch, for one head, that are a few
+constexpr int kMassFew = 32, kMassFew32 = 16;  // rows of a branch, for one head, that are a few: bf16, fp32
 
 struct MassItem {
   int b, h, k0;    // branch, head, first position of the tile
@@ -199,7 +199,7 @@ __device__ __forceinline__ void mass_write(const MassArgs& a, int b, int past, i
   if (a.born && p >= past) a.born[row] = a.total[b] - len + p;
 }
 
-int launch_mass_few(int D, MassArgs a, int32_t* st, cudaStream_t s);
+int launch_mass_few(int D, bool bf16, MassArgs a, int32_t* st, cudaStream_t s);
 int launch_mass_tc(int D, MassArgs a, int32_t* st, cudaStream_t s);
 int launch_mass_join(int TK, int TQ, const MassArgs& a, int32_t* st, cudaStream_t s);
 

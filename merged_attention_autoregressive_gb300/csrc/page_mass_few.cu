@@ -1,6 +1,6 @@
-// fastar_page_mass for branches of a few rows (bf16): single tokens, short drafts.
+// fastar_page_mass for branches of a few rows: single tokens, short drafts.
 //
-// The keys pass through once and nothing is done twice with them, so they go
+// bf16: the keys pass through once and nothing is done twice with them, so they go
 // from memory straight into the registers of warp-level products (m 16 keys, n 8
 // rows, k 16 channels): a warp takes 16 keys, lane 4 r + t the 16-byte pieces t, t +
 // 4, ... of keys r and r + 8, and the same pieces of row r.  A piece is two steps'
@@ -21,6 +21,8 @@ namespace fastar {
 namespace {
 
 constexpr int kTK = 128, kThreads = 256, kPerSm = 3;
+constexpr int kTK32 = 64, kThreads32 = 128;
+constexpr int per_sm32(int D) { return D == 128 ? 3 : 4; }  // (4 of 128 channels spill: single tokens 75 us for 70)
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -141,11 +143,139 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mass_few_kernel(const MassAr
   pdl_trigger();
 }
 
+// The same in 32 bits, on the FP32 pipes: eight lanes share a key, lane t its 16-byte
+// pieces t, t + 8, ..., and hold four keys each; two rows at a time come out of L1, and
+// the partial sums of four keys and two rows are added over the eight lanes so that
+// each ends with the score of one key and one row.
+//
+// What bounds it: HBM for single tokens (16 of 12 heads over 4,681 keys: 70 us, 6.7
+// TB/s, by the kernel for many rows 202 us; D 64 40 and 122 us), reads of rows and
+// shuffles for more (16 tokens a branch 164 and 231 us, 32 tokens 287 and 278 us).
+template <int D>
+__global__ void __launch_bounds__(kThreads32, per_sm32(D)) mass_few32_kernel(const MassArgs a, int32_t* st) {
+  pdl_wait();
+  if (block_status_bad(st)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 3, t = lane & 7;
+  constexpr int kPieces = D / 32, kKeys = 4;  // 16-byte pieces of a key that a lane takes, and its keys
+  const float scale2 = a.scale * kLog2e;
+  MassWalk<kTK32> walk;
+  int most;
+  bool ok = true, bad = false;
+  const unsigned items = walk.count(a, most, ok);
+  if (!ok) {
+    if (threadIdx.x == 0) status_set(st, FASTAR_ERR_DEVICE_ARG);
+    return;
+  }
+  const int by_tiles = (int)gridDim.x / a.H, by_heads = (int)gridDim.x - by_tiles * a.H;
+  // the page ids of the lane's keys, warp * 16 + r + 4 e, are read one item ahead
+  int id[kKeys];
+  MassItem y = {};
+  auto look = [&](unsigned it) {
+    if (it >= items) return;
+    y = walk.next(a, it, gridDim.x, by_tiles, by_heads);
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e) {
+      const int k = warp * 16 + r + 4 * e;
+      id[e] = k < y.len - y.k0 ? a.table[(size_t)y.b * a.max_pages + ((y.k0 + k) >> a.page_shift)] : -2;
+    }
+  };
+  look(blockIdx.x);
+  for (unsigned it = blockIdx.x; it < items; it += gridDim.x) {
+    const MassItem x = y;
+    const int p0 = x.k0 + warp * 16 + r;
+    int mine = -1;  // the row of the lane's own key, whose score it gets
+    float4 key[kKeys][kPieces];
+    const int own = 2 * (t & 1) + (t >> 1 & 1);
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e) {
+      int row = -1;
+      if (id[e] >= 0 && id[e] < a.n_pages)
+        row = ((id[e] * a.H + x.h) << a.page_shift) + ((p0 + 4 * e) & ((1 << a.page_shift) - 1));
+      else if (id[e] != -2)
+        bad = true;
+      if (e == own) mine = row;
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        key[e][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row >= 0) key[e][j] = __ldcs(reinterpret_cast<const float4*>((const float*)a.K + (size_t)row * D) + t + 8 * j);
+      }
+    }
+    look(it + gridDim.x);
+    if (x.k0 + warp * 16 >= x.len) continue;  // (no key of the warp's is there)
+    const int p = p0 + 4 * own;
+    const int end = (x.n - x.i0) * a.g;
+    const float old = mine >= 0 && t < 4 ? a.mass[mine] : 0.f;
+    float drew = 0.f;
+    for (int i0 = 0; i0 < end; i0 += 32) {
+      // a row per lane: its place in q, its log-sum-exp, the positions that it sees
+      int from = -1, limit = 0;
+      float base = 0.f;
+      if (i0 + lane < end) {
+        const int token = x.i0 + (i0 + lane) / a.g, head = x.h * a.g + (i0 + lane) % a.g;
+        const int at = a.rows ? a.rows[x.lo + token] : x.lo + token;
+        if (at < 0 || at >= a.N) {
+          bad = true;
+        } else {
+          const float lse = a.lse[(size_t)head * a.N + at];
+          if (lse != -INFINITY) {
+            from = head * a.N + at;
+            base = -lse * kLog2e;
+            limit = branch_limit(token, x.n, x.len, a.block);
+          }
+        }
+      }
+      const int n = min(32, end - i0);
+      for (int i = 0; i < n; i += 2) {
+        float s[2][kKeys], s1[2][kKeys];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const int f = __shfl_sync(0xffffffffu, from, i + w);  // (i + 1 <= 31)
+          float4 q[kPieces];
+#pragma unroll
+          for (int j = 0; j < kPieces; ++j) {
+            q[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (f >= 0) q[j] = *(reinterpret_cast<const float4*>((const float*)a.q + (size_t)f * D) + t + 8 * j);
+          }
+#pragma unroll
+          for (int e = 0; e < kKeys; ++e) {
+            s[w][e] = s1[w][e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+              tc::fma_pair(s[w][e], s1[w][e], q[j].x, q[j].y, key[e][j].x, key[e][j].y);
+              tc::fma_pair(s[w][e], s1[w][e], q[j].z, q[j].w, key[e][j].z, key[e][j].w);
+            }
+            s[w][e] += s1[w][e];
+          }
+        }
+        // the eight lanes of a key add up, and share out keys and rows
+        float v[2];
+        const bool b0 = t & 1, b1 = t & 2, b2 = t & 4;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const float u0 = (b0 ? s[w][2] : s[w][0]) + __shfl_xor_sync(0xffffffffu, b0 ? s[w][0] : s[w][2], 1);
+          const float u1 = (b0 ? s[w][3] : s[w][1]) + __shfl_xor_sync(0xffffffffu, b0 ? s[w][1] : s[w][3], 1);
+          v[w] = (b1 ? u1 : u0) + __shfl_xor_sync(0xffffffffu, b1 ? u0 : u1, 2);
+        }
+        const float score = (b2 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, b2 ? v[0] : v[1], 4);
+        const float off = __shfl_sync(0xffffffffu, base, i + (t >> 2));
+        const int lim = __shfl_sync(0xffffffffu, limit, i + (t >> 2));
+        if (p < lim) drew += exp2f(fmaf(score, scale2, off));
+      }
+    }
+    drew += __shfl_xor_sync(0xffffffffu, drew, 4);
+    if (t < 4 && mine >= 0) mass_write(a, x.b, x.len - x.n, x.len, p, mine, old, drew);
+  }
+  if (bad) status_set(st, FASTAR_ERR_DEVICE_ARG);
+  pdl_trigger();
+}
+
 }  // namespace
 
-int launch_mass_few(int D, MassArgs a, int32_t* st, cudaStream_t s) {
-  auto kernel = D == 128 ? mass_few_kernel<128> : mass_few_kernel<64>;
-  if (launch_pdl(kernel, dim3(152 * kPerSm), dim3(kThreads), 0, s, a, st) != cudaSuccess) {
+int launch_mass_few(int D, bool bf16, MassArgs a, int32_t* st, cudaStream_t s) {
+  auto kernel = bf16 ? D == 128 ? mass_few_kernel<128> : mass_few_kernel<64>
+                     : D == 128 ? mass_few32_kernel<128> : mass_few32_kernel<64>;
+  const int ctas = 152 * (bf16 ? kPerSm : per_sm32(D));
+  if (launch_pdl(kernel, dim3(ctas), dim3(bf16 ? kThreads : kThreads32), 0, s, a, st) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
   }

@@ -430,6 +430,17 @@ __device__ __forceinline__ void tmem_wait16(uint32_t* r) {
       :
       : "memory");
 }
+// (a0, a1) += (x0 y0, x1 y1), one instruction, each as fmaf rounds it.
+__device__ __forceinline__ void fma_pair(float& a0, float& a1, float x0, float x1, float y0, float y1) {
+  asm("{\n\t.reg .b64 a, x, y;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "fma.rn.f32x2 a, x, y, a;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
+}
 // Two fp32 fused multiply-adds, or additions, in one instruction, each
 // rounded as a separate one would be: x = x m + a, s = s + x.
 __device__ __forceinline__ void fma2(float& x0, float& x1, float m0, float m1, float a0, float a1) {

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_drafts as T
 from oracle import draft_oracle as O
 from test_gpu_drafts import BF, F32, _f64, _ints, _layout, _pages, _randn, _status, _tree
 
@@ -364,3 +365,49 @@ def test_eviction_of_long_tables(m, H, room, lengths, budget, kind):
         y, y0 = (t.float().cpu().numpy() if t.is_floating_point() else t.cpu().numpy() for t in (y, y0))
         assert np.array_equal(y.swapaxes(1, 2)[kept], w.swapaxes(1, 2)[kept])
         assert np.array_equal(y.swapaxes(1, 2)[~kept], y0.swapaxes(1, 2)[~kept])
+
+
+FEW32 = [
+    # D, H, g, page, new, past, block, rows, decay, born, pad
+    (128, 2, 1, 64, [1, 1, 1, 1], [300, 0, 63, 1000], 0, False, 1.0, True, 0),
+    (128, 3, 5, 16, [1, 0, 1], [500, 7, 255], 1, False, 0.9, True, 4),
+    (64, 2, 8, 256, [2, 1, 1], [2000, 255, 0], 0, True, 0.0, False, 1),
+    (128, 8, 1, 64, [1] * 40, list(range(300, 700, 10)), 0, False, 1.0, True, 0),
+    (64, 12, 1, 16, [1] * 40, list(range(300, 700, 10)), 1, False, 1.0, True, 5),
+    (128, 1, 1, 128, [15], [200], 7, False, 1.0, True, 0),
+    # many rows where few are to be expected
+    (64, 1, 1, 32, [100] + [0] * 39, [50] + [0] * 39, 1, False, 1.0, True, 0),
+    (128, 2, 2, 32, [0, 43] + [0] * 38, [0, 129] + [0] * 38, 0, True, 0.5, True, 7),
+    # branches of a few rows beside some of many
+    (64, 2, 1, 16, [16, 17, 1, 0, 33, 3], [100, 64, 5, 9, 300, 127], 1, False, 0.7, True, 3),
+    (128, 2, 4, 32, [3, 4, 1, 1, 6, 2], [77, 500, 64, 300, 129, 1], 3, True, 1.0, True, 3),
+]
+
+
+@pytest.mark.parametrize("D,H,g,page,new,past,block,taken,decay,stamps,pad", FEW32)
+def test_masses_of_a_few_rows_in_32_bits(m, D, H, g, page, new, past, block, taken, decay, stamps, pad):
+    T.test_page_mass(m, F32, D, H, g, page, new, past, block, taken, decay, stamps, pad)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_few_rows_keep_clear_of_spoiled_ones(m, dtype):
+    """As for longer drafts: a query spoils its own branch, a key its own mass."""
+    calls = [Call(m, "mass", dtype, 128, new=(2, 1, 3), past=(200, 100, 64)) for _ in range(2)]
+    clean, c = calls
+    c.q[:, int(c.cu[1])] = math.nan
+    page = int(c.table[0, 1])
+    c.K[page, 0, 5, 3] = math.inf
+    c.K[page, 1, 5] = math.nan
+    for b in range(3):  # what lies behind the lengths
+        p = int(c.length[b])
+        c.K[int(c.table[b, p // 32]), :, p % 32:] = math.nan
+    for x in calls:
+        x.run()
+        assert int(x.status) == 0
+    a, b = clean.mass.mass.clone(), c.mass.mass.clone()
+    for x in (a, b):
+        x[page, :, 5] = 0
+        x[c.table[1]] = 0
+    assert torch.equal(a, b)
+    assert not torch.isfinite(c.mass.mass[page, 1, 5])
+    assert c.mass.mass[int(c.table[1, 0]), 0, :32].isnan().all()
