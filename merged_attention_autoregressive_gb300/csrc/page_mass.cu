@@ -9,9 +9,11 @@
 // D 64: 13.1 us; one after the other 17.3 us), three CTAs fit on an SM.
 //
 // What bounds it: latency where rows are few (that call: two items per CTA, each a
-// chain of page id, key and row reads), the FP32 pipes where they are many (64 tokens
-// of 16 branches, 12 heads over 4,744 keys: 442 us, of which the multiply-adds are
-// 200 us).
+// chain of page id, key and row reads), reads of shared memory where they are many (64
+// tokens of 16 branches, 12 heads over 4,744 keys: 442 us, of which the multiply-adds
+// are 200 us; a 16-byte read takes a warp four cycles whatever its lanes share, so
+// other places of a thread's scores gain nothing, and 8 x 4 of them 8 % of long calls
+// for 5 to 60 % of short ones).
 #include <math.h>
 
 #include "page_mass.cuh"
