@@ -411,3 +411,47 @@ def test_few_rows_keep_clear_of_spoiled_ones(m, dtype):
     assert torch.equal(a, b)
     assert not torch.isfinite(c.mass.mass[page, 1, 5])
     assert c.mass.mass[int(c.table[1, 0]), 0, :32].isnan().all()
+
+
+def test_shared_evictions_captured_and_on_a_stream(m):
+    """Clusters that share a head's rows: one call behind the other on a stream, and
+    captured and replayed, leave what single calls leave."""
+    rng, gen, page, D, H = np.random.default_rng(5), torch.Generator().manual_seed(5), 64, 64, 3
+    lengths = [3000, 2900, 40]
+    _, length, table, pool = _layout(rng, lengths, [0] * 3, page)
+    K, V, pages = _pages(m, gen, pool, H, page, D, BF, table, length)
+    mass = torch.rand(pool, H, page, generator=gen).cuda()
+    born = torch.randint(0, 3000, (pool, H, page), generator=gen, dtype=torch.int32).cuda()
+    held, st = m.PageMass.view(mass, born, _ints(length)), _status()
+    state = [K, V, mass, born, pages.len]
+    first = [x.clone() for x in state]
+
+    def steps():
+        m.fastar_page_evict(pages, held, 2048, first=4, recent=200, status=st)
+        pages.len.clamp_(max=2048)
+        m.fastar_page_evict(pages, held, 1000, first=4, recent=200, status=st)
+
+    steps()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in state]
+
+    def restore():
+        for x, y in zip(state, first):
+            x.copy_(y)
+        torch.cuda.synchronize()
+
+    restore()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        steps()
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(state, want)) and int(st) == 0
+    restore()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps()
+    for _ in range(2):
+        restore()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(state, want)) and int(st) == 0
