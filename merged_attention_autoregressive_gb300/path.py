@@ -439,14 +439,18 @@ class BranchRollout:
     one reach no other's outputs.
 
     Drafts: `extend(new, parents)` makes the next step's tokens of each branch a
-    tree, of which `accept` keeps one path.
+    tree, of which `accept` keeps one path.  Drafts are single tokens: with block > 1
+    they are refused, for a path of any length would leave later frames across the
+    borders of blocks.
 
     budget: rows that a branch holds per head after `evict`.  Every step then adds
     its tokens' attention weights to the masses of the rows (older ones fade by
     `decay`), and `evict` keeps the rows of the first `first` and the last `recent`
     tokens and those of the largest masses.  With block > 1 the budget is whole
-    blocks, so that later tokens' blocks begin where they did."""
+    blocks, and so is the length of a branch that is cut to it (`evict` refuses one
+    whose last frame is not full), so that later tokens' blocks begin where they did."""
     budget = mass = drafts = _asked = None
+    block = 0
 
     def __init__(self, B, H, D, tokens, max_len, prefix=None, Hq=None, page=64, n_pages=None, plan=None, block=0,
                  scale=None, dtype=torch.bfloat16, device="cuda", budget=None, first=0, recent=0, decay=1.0):
@@ -488,6 +492,8 @@ class BranchRollout:
         their step."""
         if self.drafts is not None:
             raise ValueError("the drafts of the last step are not accepted yet")
+        if parents is not None and self.block > 1:
+            raise ValueError("drafts are single tokens: block is 0 or 1")
         if parents is not None and ([len(p) for p in parents] != list(new) or
                                     any(not -1 <= q < i for p in parents for i, q in enumerate(p))):
             raise ValueError("one parent per draft, an earlier one of its branch or -1")
@@ -580,11 +586,14 @@ class BranchRollout:
 
     def evict(self, stream=None):
         """Every branch of more than `budget` positions keeps, in each head,
-        `budget` of its rows, and returns the pages behind."""
+        `budget` of its rows, and returns the pages behind.  With block > 1 such a
+        branch holds whole blocks."""
         if self.budget is None:
             raise ValueError("this rollout has no budget")
         if self.drafts is not None:
             raise ValueError("the drafts of the last step are not accepted yet")
+        if self.block > 1 and any(n > self.budget and n % self.block for n in self.lengths):
+            raise ValueError("a branch over the budget is not whole blocks")
         with torch.cuda.stream(None if stream is None else ChunkPath._main(stream)):
             fastar_page_evict(self.pages, self.mass, self.budget, first=self.first, recent=self.recent,
                               status=self.status)
