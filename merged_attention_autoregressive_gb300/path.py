@@ -448,9 +448,15 @@ class BranchRollout:
     `decay`), and `evict` keeps the rows of the first `first` and the last `recent`
     tokens and those of the largest masses.  With block > 1 the budget is whole
     blocks, and so is the length of a branch that is cut to it (`evict` refuses one
-    whose last frame is not full), so that later tokens' blocks begin where they did."""
-    budget = mass = drafts = _asked = None
-    block = 0
+    whose last frame is not full), so that later tokens' blocks begin where they did.
+
+    Order of the calls: `accept` takes drafts that were attended, `evict` (and under a
+    budget the next `extend`) rows that were weighed, both after an `extend` of their
+    own; they raise otherwise.  After `accept`, and after an `evict` that took rows, the
+    next step needs another `extend`.  A step that was captured marks on the device that
+    it was replayed; `stepped` says that a step was made of its parts' calls."""
+    budget = mass = drafts = _asked = _graphs = None
+    block, _pending, _over = 0, frozenset(), False
 
     def __init__(self, B, H, D, tokens, max_len, prefix=None, Hq=None, page=64, n_pages=None, plan=None, block=0,
                  scale=None, dtype=torch.bfloat16, device="cuda", budget=None, first=0, recent=0, decay=1.0):
@@ -471,7 +477,12 @@ class BranchRollout:
         self.ws = torch.empty(branch_workspace_size(self.Hq, H, tokens, D), dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.parent = torch.zeros(tokens, dtype=torch.int32, device=dev)
-        self.drafts = self._asked = None             # parents of the step's tokens, branch by branch; its queries
+        self.drafts = None                           # parents of the step's tokens, branch by branch
+        # The step since the last `extend`: its drafts' queries, once attended; the
+        # branches whose new rows are not weighed; whether it is over.  The captured
+        # steps, as (queries, of drafts), and the number (from 1) of the one replayed last.
+        self._asked, self._pending, self._over = None, set(), False
+        self._graphs, self._replayed = [], torch.zeros(1, dtype=torch.int32, device=dev)
         if budget is not None:
             self.mass = PageMass(self.pages)
             self.ws_mass = torch.empty(max(1, mass_workspace_size(self.Hq, H, tokens, D)), dtype=torch.uint8, device=dev)
@@ -502,6 +513,8 @@ class BranchRollout:
         lengths = [a + n for a, n in zip(self.lengths, new)]
         if max(lengths, default=0) > self.max_len:
             raise ValueError("a branch is longer than max_len")
+        if self.mass is not None:
+            self._weighed(stream)
         page = self.pages.page
         need = [-(-a // page) - len(h) for a, h in zip(lengths, self.held)]
         if sum(need) > len(self.free):
@@ -514,7 +527,12 @@ class BranchRollout:
         for n in new:
             offsets.append(offsets[-1] + n)
         i32 = dict(dtype=torch.int32)
-        with torch.cuda.stream(None if stream is None else ChunkPath._main(stream)):
+        self._asked, self._over = None, False
+        if self._graphs is not None:
+            self._pending = {b for b, n in enumerate(new) if n}
+        with self._on(stream):
+            if self._graphs:
+                self._replayed.zero_()
             if any(need):  # (a released branch's old entries are not read)
                 table = [h + [0] * (most - len(h)) for h in self.held]
                 self.pages.table.copy_(torch.tensor(table, **i32).view(self.B, most))
@@ -534,8 +552,40 @@ class BranchRollout:
             raise ValueError("the drafts of the last step are not accepted yet")
         self.free.extend(self.held[b][::-1])
         self.held[b], self.lengths[b] = [], 0
+        self._pending = self._pending - {b}
         if self.mass is not None:
             self.totals[b] = 0
+
+    @staticmethod
+    def _on(stream):
+        return torch.cuda.stream(None if stream is None else ChunkPath._main(stream))
+
+    def _made(self, q, of_drafts):
+        """A step of these queries has run since `extend`."""
+        if self.drafts is None and not of_drafts:
+            self._pending = set()
+        elif self.drafts is not None and of_drafts:
+            self._asked = q
+
+    def _settle(self):
+        """Takes note of a step that was replayed since `extend` (waits for it)."""
+        n = int(self._replayed) if self._graphs else 0
+        if n:
+            self._made(*self._graphs[n - 1])
+
+    def _weighed(self, stream):
+        if self._pending:
+            with self._on(stream):
+                self._settle()
+        if self._pending:
+            raise ValueError("the tokens of the last extend are not weighed yet")
+
+    def stepped(self, q=None):
+        """Says that the tokens of the last `extend` were appended and attended (under a
+        budget plain tokens also weighed) by calls of their own and not by `step`.  q:
+        the drafts' queries as they were attended, [Hq][tokens][D] (default: this
+        object's buffer of rotated ones)."""
+        self._made(self.q if q is None else q, self.drafts is not None)
 
     def _shrink(self, lengths):
         """The branches hold `lengths` positions now; pages behind return to the
@@ -553,6 +603,8 @@ class BranchRollout:
         queries are read again: without a plan, the step's q is as it was.)"""
         if self.drafts is None:
             raise ValueError("the last step had no drafts")
+        with self._on(stream):
+            self._settle()
         if self._asked is None:
             raise ValueError("the drafts have not been attended yet")
         if len(leaves) != self.B or any(not -1 <= x < len(p) for x, p in zip(leaves, self.drafts)):
@@ -570,7 +622,7 @@ class BranchRollout:
         for k in kept:
             cu.append(cu[-1] + len(k))
         i32 = dict(dtype=torch.int32, device=self.cu.device)
-        with torch.cuda.stream(None if stream is None else ChunkPath._main(stream)):
+        with self._on(stream):
             rows = torch.tensor([r for k in kept for r in k], **i32)
             keep = torch.tensor(cu, **i32)
             fastar_page_keep(self.pages, self.cu, rows, keep, status=self.status)
@@ -581,7 +633,8 @@ class BranchRollout:
                 self.mass.total.copy_(torch.tensor(self.totals, dtype=torch.int32))
                 fastar_page_mass(self.pages, self._asked, self.lse, self.cu, self.scale, self.mass, block=1, rows=rows,
                                  decay=self.decay, ws=self.ws_mass, status=self.status)
-        self.drafts = None
+        self.drafts = self._asked = None
+        self._pending, self._over = set(), True
         return kept
 
     def evict(self, stream=None):
@@ -594,9 +647,11 @@ class BranchRollout:
             raise ValueError("the drafts of the last step are not accepted yet")
         if self.block > 1 and any(n > self.budget and n % self.block for n in self.lengths):
             raise ValueError("a branch over the budget is not whole blocks")
-        with torch.cuda.stream(None if stream is None else ChunkPath._main(stream)):
+        self._weighed(stream)
+        with self._on(stream):
             fastar_page_evict(self.pages, self.mass, self.budget, first=self.first, recent=self.recent,
                               status=self.status)
+            self._over = self._over or any(n > self.budget for n in self.lengths)
             self._shrink([min(n, self.budget) for n in self.lengths])
 
     def step(self, q, k, v, pos=None, stream=None):
@@ -604,18 +659,35 @@ class BranchRollout:
         [H][tokens][D] (any head and token strides, but a q that is not rotated
         is contiguous; the rows behind the last branch's are ignored), pos [tokens][axes] int32 with a plan.  Returns
         (out [Hq][tokens][D], lse [Hq][tokens]), buffers of this object."""
+        captured = False
+        if self._over or self.drafts is not None or self.mass is not None:
+            with self._on(stream):
+                captured = torch.cuda.is_current_stream_capturing()
+            if self._over and not captured:
+                raise ValueError("the last step is over: extend comes first")
         rotated = self.q if self.plan is not None else q
         fastar_page_append(self.pages, k, v, self.cu, pos=pos, plan=self.plan,
                            q=q if self.plan is not None else None, q_out=self.q if self.plan is not None else None,
                            status=self.status, stream=stream)
         if self.drafts is not None:
-            self._asked = rotated  # `accept` weighs the tokens that stay (a replayed step asks the same rows)
             fastar_tree_attention(rotated, self.cu, self.parent, self.prefix, self.pages, self.scale, self.out,
                                   lse=self.lse, ws=self.ws, status=self.status, stream=stream)
+            self._note(rotated, True, captured, stream)  # (`accept` weighs the tokens that stay)
             return self.out, self.lse
         fastar_branch_attention(rotated, self.cu, self.prefix, self.pages, self.scale, self.out, lse=self.lse,
                                 block=self.block, ws=self.ws, status=self.status, stream=stream)
         if self.mass is not None:
             fastar_page_mass(self.pages, rotated, self.lse, self.cu, self.scale, self.mass, block=self.block,
                              decay=self.decay, ws=self.ws_mass, status=self.status, stream=stream)
+            self._note(None, False, captured, stream)
         return self.out, self.lse
+
+    def _note(self, q, of_drafts, captured, stream):
+        """A step ran, or was captured: then its replays leave its number."""
+        if captured:
+            self._graphs.append((q, of_drafts))
+        else:
+            self._made(q, of_drafts)
+        if captured or (of_drafts and self._graphs):
+            with self._on(stream):
+                self._replayed.fill_(len(self._graphs) if captured else 0)

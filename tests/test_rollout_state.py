@@ -28,6 +28,7 @@ def _rollout(monkeypatch, block=1, budget=None, tokens=100, max_len=96, page=16)
     r.q, r.out, r.lse, r.ws, r.ws_mass = "rotated", "out", "lse", None, None
     r.scale, r.block = 0.1, block
     r.budget, r.first, r.recent, r.decay = budget, 0, 0, 1.0
+    r._graphs, r._replayed = [], z(1)
     if budget is not None:
         r.mass = types.SimpleNamespace(total=z(3))
     return r, seen
@@ -80,3 +81,148 @@ def test_drafts_by_frames_are_refused(monkeypatch):
         r, _ = _rollout(monkeypatch, block=block)
         r.extend([3, 0, 0], parents=[[-1, 0, 0], [], []])
         assert r.drafts == [[-1, 0, 0], [], []]
+
+
+TREES = [[-1, 0, 0], [-1], []]
+
+
+@pytest.mark.parametrize("budget", [None, 16])
+def test_drafts_are_attended_before_they_are_accepted(monkeypatch, budget):
+    """Every time, not only the first: nothing of an earlier step counts."""
+    r, seen = _rollout(monkeypatch, budget=budget)
+    for n in range(3):
+        r.extend([3, 1, 0], parents=TREES)
+        before, calls = _state(r), len(seen)
+        with pytest.raises(ValueError, match="attended"):
+            r.accept([2, -1, -1])
+        assert _state(r) == before and len(seen) == calls and r.drafts is not None
+        r.step(f"q{n}", "k", "v")
+        assert r.accept([2, -1, -1]) == [[0, 2], [], []]
+        if budget is not None:
+            assert seen[-1][0] == "page_mass" and seen[-1][1][1] == f"q{n}"
+        r.extend([1, 1, 1])  # plain tokens in between are no attention of drafts
+        r.step("other", "k", "v")
+
+
+def test_rows_are_weighed_before_an_eviction(monkeypatch):
+    r, seen = _rollout(monkeypatch, budget=16)
+    for _ in range(2):
+        r.extend([20, 3, 0])
+        before, calls = _state(r), len(seen)
+        for call in (r.evict, lambda: r.extend([1, 0, 0])):
+            with pytest.raises(ValueError, match="weighed"):
+                call()
+            assert _state(r) == before and len(seen) == calls
+        r.step("q", "k", "v")
+        r.evict()
+        assert r.lengths[0] == 16
+    r.extend([3, 1, 0], parents=TREES)
+    r.step("q", "k", "v")
+    with pytest.raises(ValueError, match="accepted"):
+        r.evict()
+    r.accept([1, 0, -1])  # which weighs
+    r.evict()
+    r.extend([0, 0, 0])  # no tokens: nothing to weigh
+    r.evict()
+    r.extend([0, 0, 5])
+    r.release(2)  # nor of a branch that starts again
+    r.evict()
+    r.extend([1, 0, 0])
+
+
+def test_a_rollout_without_a_budget_extends_as_often_as_it_likes(monkeypatch):
+    r, _ = _rollout(monkeypatch)
+    for _ in range(3):
+        r.extend([2, 0, 1])
+    assert r.lengths == [6, 0, 3]
+
+
+@pytest.mark.parametrize("budget", [None, 16])
+def test_a_step_is_over_when_its_drafts_are_accepted(monkeypatch, budget):
+    """The rows of the drafts that went are others' now: the same tokens again would
+    be written over them."""
+    r, seen = _rollout(monkeypatch, budget=budget)
+    r.extend([3, 1, 0], parents=TREES)
+    r.step("q", "k", "v")
+    r.step("q", "k", "v")  # as often as one likes before that
+    r.accept([2, 0, -1])
+    calls = len(seen)
+    with pytest.raises(ValueError, match="extend"):
+        r.step("q", "k", "v")
+    assert len(seen) == calls
+    r.extend([1, 0, 0])
+    r.step("q", "k", "v")
+
+
+def test_a_step_is_over_when_its_rows_are_evicted(monkeypatch):
+    r, seen = _rollout(monkeypatch, budget=16)
+    r.extend([10, 0, 0])
+    r.step("q", "k", "v")
+    r.evict()  # nothing is over the budget
+    r.step("q", "k", "v")
+    r.extend([10, 0, 0])
+    r.step("q", "k", "v")
+    r.evict()
+    calls = len(seen)
+    with pytest.raises(ValueError, match="extend"):
+        r.step("q", "k", "v")
+    assert len(seen) == calls
+
+
+def _captured(monkeypatch, r, *args):
+    """A captured step: nothing runs, the graph holds the word's number."""
+    word = int(r._replayed)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    r.step(*args)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    number = int(r._replayed)
+    r._replayed.fill_(word)
+    return lambda: r._replayed.fill_(number)
+
+
+def test_replayed_steps_count(monkeypatch):
+    r, seen = _rollout(monkeypatch, budget=16)
+    plain = _captured(monkeypatch, r, "q", "k", "v")  # before any extend
+    r.extend([20, 1, 0])
+    with pytest.raises(ValueError, match="weighed"):
+        r.evict()
+    plain()
+    r.evict()
+    second = _captured(monkeypatch, r, "q", "k", "v")  # also behind an eviction, for the tokens to come
+    r.extend([1, 1, 1])
+    with pytest.raises(ValueError, match="weighed"):
+        r.extend([1, 1, 1])
+    second()
+    r.extend([3, 1, 0], parents=TREES)
+    first = _captured(monkeypatch, r, "q1", "k", "v")
+    other = _captured(monkeypatch, r, "q2", "k", "v")
+    with pytest.raises(ValueError, match="attended"):
+        r.accept([0, 0, -1])
+    plain()  # a step of plain tokens is no attention of drafts
+    with pytest.raises(ValueError, match="attended"):
+        r.accept([0, 0, -1])
+    for replay, q in ((first, "q1"), (other, "q2"), (first, "q1")):  # each graph's own queries are weighed
+        replay()
+        r.accept([0, 0, -1])
+        assert seen[-1][0] == "page_mass" and seen[-1][1][1] == q
+        r.extend([3, 1, 0], parents=TREES)
+    first()
+    r.step("q3", "k", "v")  # the last one of an extend counts
+    r.accept([0, 0, -1])
+    assert seen[-1][1][1] == "q3"
+    r.extend([1, 0, 0])
+    first()  # (a graph of drafts weighs nothing)
+    with pytest.raises(ValueError, match="weighed"):
+        r.evict()
+
+
+def test_steps_of_the_parts_calls(monkeypatch):
+    r, seen = _rollout(monkeypatch, budget=16)
+    r.extend([20, 0, 0])
+    r.stepped()
+    r.evict()
+    for q, want in ((None, "rotated"), ("mine", "mine")):
+        r.extend([3, 1, 0], parents=TREES)
+        r.stepped(q)
+        r.accept([0, -1, -1])
+        assert seen[-1][1][1] == want
