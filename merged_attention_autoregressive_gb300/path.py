@@ -443,9 +443,11 @@ class BranchRollout:
     they are refused, for a path of any length would leave later frames across the
     borders of blocks.
 
-    budget: rows that a branch holds per head after `evict`.  Every step then adds
-    its tokens' attention weights to the masses of the rows (older ones fade by
-    `decay`), and `evict` keeps the rows of the first `first` and the last `recent`
+    budget: rows that a branch holds per head after `evict`.  Every call of `step` then
+    adds its tokens' attention weights to the masses of the rows (older ones fade by
+    `decay`): tokens that are attended several times, a frame's once per denoising
+    step, are weighed in one of the calls and attended with weigh=False in the others
+    (so is a warm-up before a capture).  `evict` keeps the rows of the first `first` and the last `recent`
     tokens and those of the largest masses.  With block > 1 the budget is whole
     blocks, and so is the length of a branch that is cut to it (`evict` refuses one
     whose last frame is not full), so that later tokens' blocks begin where they did.
@@ -654,11 +656,15 @@ class BranchRollout:
             self._over = self._over or any(n > self.budget for n in self.lengths)
             self._shrink([min(n, self.budget) for n in self.lengths])
 
-    def step(self, q, k, v, pos=None, stream=None):
+    def step(self, q, k, v, pos=None, stream=None, weigh=True):
         """The new tokens of the last `extend`: q [Hq][tokens][D], k, v
         [H][tokens][D] (any head and token strides, but a q that is not rotated
         is contiguous; the rows behind the last branch's are ignored), pos [tokens][axes] int32 with a plan.  Returns
-        (out [Hq][tokens][D], lse [Hq][tokens]), buffers of this object."""
+        (out [Hq][tokens][D], lse [Hq][tokens]), buffers of this object.
+
+        weigh: add the tokens' weights to the masses, under a budget.  Each call
+        that weighs adds them (and fades the older rows) again.  Drafts are weighed by
+        `accept` alone."""
         captured = False
         if self._over or self.drafts is not None or self.mass is not None:
             with self._on(stream):
@@ -676,7 +682,7 @@ class BranchRollout:
             return self.out, self.lse
         fastar_branch_attention(rotated, self.cu, self.prefix, self.pages, self.scale, self.out, lse=self.lse,
                                 block=self.block, ws=self.ws, status=self.status, stream=stream)
-        if self.mass is not None:
+        if self.mass is not None and weigh:
             fastar_page_mass(self.pages, rotated, self.lse, self.cu, self.scale, self.mass, block=self.block,
                              decay=self.decay, ws=self.ws_mass, status=self.status, stream=stream)
             self._note(None, False, captured, stream)

@@ -68,3 +68,21 @@ def test_replayed_steps_count(path, own_stream):
                          (r.mass.born, eager.mass.born)):
                 x, y = (t[ids].transpose(1, 2).reshape(len(r.held[b]) * 16, -1)[:r.lengths[b]] for t in (x, y))
                 assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (torch.float32, 64)])
+def test_attending_again_leaves_the_masses(path, dtype, D):
+    """Steps that do not weigh before the one that does leave what it alone leaves."""
+    gen = torch.Generator().manual_seed(7)
+    q, k, v = (_randn(gen, 2, 20, D, dtype=dtype) for _ in range(3))
+    got = []
+    for again in (0, 2):
+        r = path.BranchRollout(2, 2, D, 20, 64, page=16, block=1, budget=16, recent=8, decay=0.9, dtype=dtype)
+        for _ in range(2):
+            r.extend([10, 7])
+            for _ in range(again):
+                r.step(q, k, v, weigh=False)
+            out, lse = r.step(q, k, v)
+        assert int(r.status) == 0
+        got.append([x.clone() for x in (out, lse, r.mass.mass, r.mass.born, r.pages.K, r.pages.V)])
+    assert all(torch.equal(x, y) for x, y in zip(*got)) and bool(got[0][2].any())

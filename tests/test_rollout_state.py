@@ -226,3 +226,36 @@ def test_steps_of_the_parts_calls(monkeypatch):
         r.stepped(q)
         r.accept([0, -1, -1])
         assert seen[-1][1][1] == want
+
+
+def test_a_step_may_attend_without_weighing(monkeypatch):
+    """A frame that is attended once per denoising step is weighed once."""
+    r, seen = _rollout(monkeypatch, block=8, budget=16)
+    r.extend([8, 0, 8])
+    for _ in range(3):
+        r.step("q", "k", "v", weigh=False)
+    assert [n for n, _, _ in seen] == ["page_append", "branch_attention"] * 3
+    for call in (r.evict, lambda: r.extend([8, 0, 0])):  # nothing is weighed yet
+        with pytest.raises(ValueError, match="weighed"):
+            call()
+    r.step("q", "k", "v")
+    assert [n for n, _, _ in seen].count("page_mass") == 1
+    r.evict()
+    r.extend([8, 0, 0])
+    calls = len(seen)
+    replay = _captured(monkeypatch, r, "q", "k", "v", None, None, False)  # (weigh=False)
+    assert len(seen) == calls + 2
+    replay()
+    with pytest.raises(ValueError, match="weighed"):
+        r.evict()
+
+
+def test_drafts_are_weighed_when_they_are_accepted(monkeypatch):
+    r, seen = _rollout(monkeypatch, budget=16)
+    for weigh in (True, False):
+        r.extend([3, 1, 0], parents=TREES)
+        r.step("q", "k", "v", weigh=weigh)
+        assert seen[-1][0] == "tree_attention"
+        r.accept([2, 0, -1])
+        assert seen[-1][0] == "page_mass"
+        r.evict()
