@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kList = 1024;  // moves listed at a time
 constexpr int kMaxCluster = 8;
+constexpr int kMostWords = (1 << 19) / 32;  // of 32 positions in a table (longer ones are refused)
 // CTAs of an SM, by threads and integers of a thread.
 __host__ __device__ constexpr int resident_of(int threads, int keys) { return threads == 1024 ? 1 : keys > 8 ? 3 : 4; }
 
@@ -461,7 +462,9 @@ int launch_keys(const EvictArgs& a, int items, int per, int32_t* st, cudaStream_
                 : per == 16 ? page_evict_kernel<kThreads, kKeys, shares, 16>
                             : page_evict_kernel<kThreads, kKeys, shares, 32>;
   const int smem = 2 * a.words * 4;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+  // The limit belongs to the kernel, not to this launch: another host thread's call may
+  // set it between the two, so all calls set the same.
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kMostWords * 4) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
   }
