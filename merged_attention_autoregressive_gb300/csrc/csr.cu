@@ -127,11 +127,13 @@ int launch_csr(const uint32_t* keys, int G, int N, const int32_t* n_dev, int n_d
   // (with 1,024 buckets: 26 us per group with 8 warps).  The (warp, bucket)
   // counts must fit in shared memory.
   int lgW = 5;
-  while (lgW > 0 && (size_t)((1 << lgW) + 1) * nb * sizeof(int) > 200 * 1024) --lgW;
+  constexpr int kMost = 200 * 1024;
+  while (lgW > 0 && (size_t)((1 << lgW) + 1) * nb * sizeof(int) > kMost) --lgW;
   const size_t smem = (size_t)((1 << lgW) + 1) * nb * sizeof(int);
+  // The limit belongs to the kernel, not to this launch: another host thread's call may
+  // set it between the two, so all calls set the same.
   if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(csr_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-          cudaSuccess) {
+      cudaFuncSetAttribute(csr_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) {
     (void)cudaGetLastError();
     return FASTAR_ERR_CUDA;
   }
