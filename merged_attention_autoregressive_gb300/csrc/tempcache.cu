@@ -785,20 +785,14 @@ static int merge_impl(const fastar_cache* c, const void* k_new, const void* v_ne
   int lg_tab = 6;
   while ((1 << lg_tab) * 3 < n_f * 4) ++lg_tab;
   const size_t plan_smem = (size_t)n_f * sizeof(int) + 3 * ((size_t)sizeof(int) << lg_tab);
-  if (plan_smem > 48 * 1024) {
-    // The limit belongs to the kernel, not to this launch: another host thread's call
-    // may set it between the two, so all calls set the same, all that there is.
-    cudaFuncAttributes own;
-    if (cudaFuncGetAttributes(&own, plan_kernel) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return FASTAR_ERR_CUDA;
-    }
-    const size_t most = 227 * 1024 - own.sharedSizeBytes;
-    if (plan_smem > most) return FASTAR_ERR_UNSUPPORTED;
-    if (cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return FASTAR_ERR_CUDA;
-    }
+  // The limit belongs to the kernel, not to this launch: another host thread's call may
+  // set it between the two, so all calls set the same, that of the largest frame.
+  constexpr int kMostPlan = (FASTAR_MAX_FRAME_KEYS + 3 * (1 << 13)) * (int)sizeof(int);
+  static_assert(3 * (1 << 13) >= 4 * FASTAR_MAX_FRAME_KEYS, "hash table of the largest frame");
+  if (plan_smem > 48 * 1024 &&
+      cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostPlan) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return FASTAR_ERR_CUDA;
   }
   const int Nrow = F * n_f;
   const dim3 wgrid((n_f + 7) / 8, H), wblock(256);
