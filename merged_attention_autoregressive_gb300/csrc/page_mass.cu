@@ -267,7 +267,11 @@ int launch_page_mass(const fastar_pages* pg, const void* q, const float* lse, in
   const bool bf16 = pg->dt == FASTAR_BF16;
   const int D = pg->D, limit = bf16 ? kMassFew : kMassFew32;
   const long long tall = (long long)M * a.g;
-  const bool many = tall > 2ll * limit + 4ll * pg->B, few = !many || tall <= (bf16 ? 2ll : 1ll) * limit * pg->B;
+  // (The tensor cores' kernel holds lse / scale in 32 bits, which is a number there for
+  // |lse| < 3e8 as long as the scale is not below 1e-30, and is cut below 2^-126 for
+  // scales above 1e30; the kernel for a few rows needs no such quotient.)
+  const bool fair = !bf16 || (scale >= 1e-30f && scale <= 1e30f);
+  const bool many = fair && tall > 2ll * limit + 4ll * pg->B, few = !many || tall <= (bf16 ? 2ll : 1ll) * limit * pg->B;
   int rc = FASTAR_OK;
   if (few) {
     if (many) a.rows_hi = limit;

@@ -1,11 +1,14 @@
 """What the header promises of the calls for bounded pages, where calls meet their
 limits."""
+import math
 import threading
 
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_drafts import BF, F32, _ints, _status
+from oracle import draft_oracle as O
+from test_gpu_drafts import BF, F32, _f64, _ints, _layout, _pages, _randn, _status
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +48,28 @@ def test_evictions_of_two_host_threads(m, dtype, D):
         t.join()
     torch.cuda.synchronize()
     assert not failed and all(int(c[3]) == 0 for c in calls)
+
+
+SCALES = [1e-44, 3e-39, 1e-37, 1e-31, 1e-29, 1.0, 1e29, 1e31]
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("dtype,D,n", [(BF, 128, 150), (BF, 64, 150), (BF, 128, 3), (F32, 64, 150)])
+def test_masses_at_any_scale(m, scale, dtype, D, n):
+    """Whatever the scale, lse / scale need not be a number of 32 bits: queries are
+    such that scale q . k stays within +-4, and lse is near what attention gives."""
+    rng, gen = np.random.default_rng(1), torch.Generator().manual_seed(1)
+    cu, length, table, pool = _layout(rng, [n, 2], [100, 40], 32)
+    K, V, pages = _pages(m, gen, pool, 2, 32, D, dtype, table, length)
+    q = _randn(gen, 2, n + 2, D, dtype=F32)
+    q = (q * min(1.0, 0.1 / scale)).to(dtype) if scale >= 1e-30 else q.to(dtype)
+    lse = (5.0 + torch.rand(2, n + 2, generator=gen)).cuda()
+    held = m.PageMass.view((3 * torch.rand(pool, 2, 32, generator=gen)).cuda())
+    ref = _f64(held.mass)
+    exact = float(np.float32(scale))
+    tol = O.page_mass(_f64(K), _f64(q), _f64(lse), None, cu, table, length, exact, 1, 0.5, ref, None, None)
+    st = _status()
+    m.fastar_page_mass(pages, q, lse, _ints(cu), scale, held, block=1, decay=0.5, status=st)
+    assert int(st) == 0
+    assert (np.abs(_f64(held.mass) - ref) <= 1.05 * tol).all()
+    assert math.isfinite(float(held.mass.sum())) and (ref.max() > 0.05)
