@@ -773,9 +773,16 @@ int fastar_page_mass(const fastar_pages* pages, const void* q, const float* lse,
  * Masses and stamps move with their rows; with `out` (other arrays, born given
  * alike) the masses and stamps of the positions that are left are written there,
  * and those of `mass` stay as they are.  0 <= first + recent <= budget;
- * max_pages * page <= 2^19 (FASTAR_ERR_UNSUPPORTED).  A length or page id out of
- * range sets FASTAR_ERR_DEVICE_ARG; the pages then hold rows of either state.
- * Pages of branches that are over the budget must not be shared.
+ * max_pages * page <= 2^19 (FASTAR_ERR_UNSUPPORTED).  A length out of range, or a
+ * page id out of range of a branch over the budget (with `out`: of any branch,
+ * whose masses are then copied), sets FASTAR_ERR_DEVICE_ARG; the pages then hold
+ * rows of either state.  In place, the table of a branch that is not over the
+ * budget is not read.  Pages of branches that are over the budget must not be
+ * shared.
+ *
+ * Positions behind the budget move, so tokens that come later by blocks of n
+ * positions (fastar_branch_attention) need a budget of whole blocks, and lengths of
+ * whole blocks where they are over it.
  */
 int fastar_page_evict(const fastar_pages* pages, const fastar_mass* mass,
                       int budget, int first, int recent, const fastar_mass* out,

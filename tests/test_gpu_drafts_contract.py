@@ -50,6 +50,28 @@ def test_evictions_of_two_host_threads(m, dtype, D):
     assert not failed and all(int(c[3]) == 0 for c in calls)
 
 
+@pytest.mark.parametrize("apart", [False, True])
+@pytest.mark.parametrize("H,room", [(1, 64), (1, 16384), (3, 512)])
+def test_page_ids_of_branches_under_the_budget(m, H, room, apart):
+    """They are looked at where something is read or written: with masses apart."""
+    page = 32
+    pool = 8
+    K = torch.randn(pool, H, page, 64, device="cuda")
+    table = torch.zeros(2, room // page, dtype=torch.int32, device="cuda")
+    table[0, :2] = _ints([3, pool])  # the second id is none
+    table[1, :2] = _ints([1, 2])
+    pages = m.PagedKV.view(K, K.clone(), table, _ints([40, 50]))
+    held, out, st = m.PageMass(pages), m.PageMass(pages), _status()
+    held.mass.uniform_()
+    out.mass.fill_(7.0)
+    before = [x.clone() for x in (pages.K, pages.V, held.mass)]
+    m.fastar_page_evict(pages, held, 60, out=out if apart else None, status=st)
+    assert int(st) == (18 if apart else 0)
+    assert all(torch.equal(x, y) for x, y in zip((pages.K, pages.V, held.mass), before))
+    if not apart:
+        assert (out.mass == 7).all()
+
+
 SCALES = [1e-44, 3e-39, 1e-37, 1e-31, 1e-29, 1.0, 1e29, 1e31]
 
 
