@@ -9,11 +9,13 @@ Every step is one C-ABI call; this class only owns the buffers.
 """
 from __future__ import annotations
 
+import ctypes
+import functools
 from types import SimpleNamespace
 
 import torch
 
-from . import (Cache, OP_ANNCA, OP_ANNSA, OP_ANNSA_PARTS, OP_MERGE, PagedKV, PageMass, Prefix, branch_workspace_size,
+from . import (Cache, OP_ANNCA, OP_ANNSA, OP_ANNSA_PARTS, OP_MERGE, PagedKV, PageMass, Prefix, _stream, branch_workspace_size,
                fastar_annca_attention, fastar_annca_prune, fastar_annsa_attention, fastar_annsa_attention_part,
                fastar_annsa_combine, fastar_branch_attention, fastar_bucket_csr, fastar_hash, fastar_hash_many,
                fastar_page_append, fastar_page_evict, fastar_page_keep, fastar_page_mass, fastar_tempcache_merge,
@@ -416,6 +418,11 @@ class ChunkStack:
             p.join_outputs(stream)
 
 
+@functools.cache
+def _driver():
+    return ctypes.CDLL("libcuda.so.1")
+
+
 class BranchRollout:
     """B rollouts ("branches") of one layer that continue one history.
 
@@ -483,7 +490,7 @@ class BranchRollout:
         # The step since the last `extend`: its drafts' queries, once attended; the
         # branches whose new rows are not weighed; whether it is over.  The captured
         # steps, as (queries, of drafts), and the number (from 1) of the one replayed last.
-        self._asked, self._pending, self._over = None, set(), False
+        self._asked, self._pending, self._over = None, frozenset(), False
         self._graphs, self._replayed = [], torch.zeros(1, dtype=torch.int32, device=dev)
         if budget is not None:
             self.mass = PageMass(self.pages)
@@ -562,23 +569,41 @@ class BranchRollout:
     def _on(stream):
         return torch.cuda.stream(None if stream is None else ChunkPath._main(stream))
 
+    @staticmethod
+    def _capturing(stream):
+        """Whether calls on the stream go into a graph.  (Asked of the driver for a
+        stream that need not be the current one: to make it the current one takes 12 us
+        of a small step's 23.)"""
+        if stream is None:
+            return torch.cuda.is_current_stream_capturing()
+        handle = _stream(stream)
+        if not handle:
+            return False  # (the legacy default stream cannot be captured)
+        state = ctypes.c_int(0)
+        rc = _driver().cuStreamIsCapturing(ctypes.c_void_p(handle), ctypes.byref(state))
+        if rc:
+            raise RuntimeError(f"cuStreamIsCapturing: CUDA driver error {rc}")
+        return state.value != 0
+
     def _made(self, q, of_drafts):
         """A step of these queries has run since `extend`."""
         if self.drafts is None and not of_drafts:
-            self._pending = set()
+            self._pending = frozenset()
         elif self.drafts is not None and of_drafts:
             self._asked = q
 
-    def _settle(self):
+    def _settle(self, stream):
         """Takes note of a step that was replayed since `extend` (waits for it)."""
-        n = int(self._replayed) if self._graphs else 0
+        if not self._graphs:
+            return
+        with self._on(stream):
+            n = int(self._replayed)
         if n:
             self._made(*self._graphs[n - 1])
 
     def _weighed(self, stream):
         if self._pending:
-            with self._on(stream):
-                self._settle()
+            self._settle(stream)
         if self._pending:
             raise ValueError("the tokens of the last extend are not weighed yet")
 
@@ -605,8 +630,7 @@ class BranchRollout:
         queries are read again: without a plan, the step's q is as it was.)"""
         if self.drafts is None:
             raise ValueError("the last step had no drafts")
-        with self._on(stream):
-            self._settle()
+        self._settle(stream)
         if self._asked is None:
             raise ValueError("the drafts have not been attended yet")
         if len(leaves) != self.B or any(not -1 <= x < len(p) for x, p in zip(leaves, self.drafts)):
@@ -636,7 +660,7 @@ class BranchRollout:
                 fastar_page_mass(self.pages, self._asked, self.lse, self.cu, self.scale, self.mass, block=1, rows=rows,
                                  decay=self.decay, ws=self.ws_mass, status=self.status)
         self.drafts = self._asked = None
-        self._pending, self._over = set(), True
+        self._pending, self._over = frozenset(), True
         return kept
 
     def evict(self, stream=None):
@@ -665,12 +689,9 @@ class BranchRollout:
         weigh: add the tokens' weights to the masses, under a budget.  Each call
         that weighs adds them (and fades the older rows) again.  Drafts are weighed by
         `accept` alone."""
-        captured = False
-        if self._over or self.drafts is not None or self.mass is not None:
-            with self._on(stream):
-                captured = torch.cuda.is_current_stream_capturing()
-            if self._over and not captured:
-                raise ValueError("the last step is over: extend comes first")
+        captured = (self._over or self.drafts is not None or self.mass is not None) and self._capturing(stream)
+        if self._over and not captured:
+            raise ValueError("the last step is over: extend comes first")
         rotated = self.q if self.plan is not None else q
         fastar_page_append(self.pages, k, v, self.cu, pos=pos, plan=self.plan,
                            q=q if self.plan is not None else None, q_out=self.q if self.plan is not None else None,
@@ -685,7 +706,10 @@ class BranchRollout:
         if self.mass is not None and weigh:
             fastar_page_mass(self.pages, rotated, self.lse, self.cu, self.scale, self.mass, block=self.block,
                              decay=self.decay, ws=self.ws_mass, status=self.status, stream=stream)
-            self._note(None, False, captured, stream)
+            if captured:
+                self._note(None, False, True, stream)
+            else:
+                self._pending = frozenset()
         return self.out, self.lse
 
     def _note(self, q, of_drafts, captured, stream):

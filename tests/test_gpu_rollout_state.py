@@ -86,3 +86,36 @@ def test_attending_again_leaves_the_masses(path, dtype, D):
         assert int(r.status) == 0
         got.append([x.clone() for x in (out, lse, r.mass.mass, r.mass.born, r.pages.K, r.pages.V)])
     assert all(torch.equal(x, y) for x, y in zip(*got)) and bool(got[0][2].any())
+
+
+@pytest.mark.parametrize("forked", [False, True])
+def test_steps_captured_on_a_stream_that_is_named(path, forked):
+    """The step's stream is looked at, whether or not it is the current one."""
+    gen = torch.Generator().manual_seed(6)
+    q, k, v = (_randn(gen, 2, 20, 64) for _ in range(3))
+    r = path.BranchRollout(2, 2, 64, 20, 64, page=16, block=1, budget=16, recent=8)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    r.extend([10, 7], stream=main)
+    r.step(q, k, v, stream=main, weigh=False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        if forked:
+            side.wait_stream(main)
+        r.step(q, k, v, stream=side if forked else main)
+        if forked:
+            main.wait_stream(side)
+    torch.cuda.synchronize()
+    assert not bool(r.mass.mass.any())
+    with pytest.raises(ValueError, match="weighed"):
+        r.evict(stream=main)
+    with torch.cuda.stream(main):
+        graph.replay()
+    r.evict(stream=main)
+    torch.cuda.synchronize()
+    assert bool(r.mass.mass.any()) and int(r.status) == 0
+    r.extend([10, 7], stream=main)
+    r.step(q, k, v, stream=side.cuda_stream if forked else main)  # eager again; a raw handle
+    torch.cuda.synchronize()
+    r.evict(stream=main)
+    assert r.lengths == [16, 14]
