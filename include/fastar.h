@@ -683,7 +683,9 @@ int fastar_branch_attention(fastar_dtype dt, const void* q, int Hq, int N,
  * before len[b] - n_b, itself and the drafts above it: parent(i),
  * parent(parent(i)), ...  (Its rotary position is the caller's: siblings share
  * one.)  Everything else, limits and workspace included, is as in
- * fastar_branch_attention; a chain (parent i - 1) gives the results of block 1.
+ * fastar_branch_attention (so are bf16 probabilities, rounded to bf16 for the
+ * product with the values, and values that some token of the branch sees, which
+ * must be finite); a chain (parent i - 1) gives the results of block 1.
  * A parent outside its range sets FASTAR_ERR_DEVICE_ARG.  Trees of tens to
  * hundreds of drafts are meant: a token walks up its branch of the tree.
  */
@@ -742,8 +744,10 @@ typedef struct {
  * that were accepted, after fastar_page_keep and with the new len.  A row whose
  * lse is -inf adds nothing.  A key that is not finite spoils its own mass only, a
  * query or lse that is not finite those of the positions that it sees.  Sums in
- * fp32, in an order that does not change from call to call.  scale is positive
- * and finite; decay is finite and not negative.  ws:
+ * fp32, in an order that does not change from call to call.  How the work is split
+ * goes by M, padding included: a call for many more rows than there are tokens may
+ * take twice as long and more.  scale is positive and finite; decay is finite and
+ * not negative.  ws:
  * fastar_workspace_size(FASTAR_OP_MASS, Hq, M, D, H, 0, 0) bytes; two calls that
  * may overlap need one each.  Pages whose masses are written must not be shared.
  * FASTAR_ERR_DEVICE_ARG: cu not ascending within 0..M, a length outside

@@ -10,7 +10,7 @@
 //
 // What bounds it: latency where rows are few (that call: two items per CTA, each a
 // chain of page id, key and row reads), reads of shared memory where they are many (64
-// tokens of 16 branches, 12 heads over 4,744 keys: 442 us, of which the multiply-adds
+// tokens of 16 branches, 12 heads over 4,744 keys: 436 us, of which the multiply-adds
 // are 200 us; a 16-byte read takes a warp four cycles whatever its lanes share, so
 // other places of a thread's scores gain nothing, and 8 x 4 of them 8 % of long calls
 // for 5 to 60 % of short ones).
@@ -264,6 +264,9 @@ int launch_page_mass(const fastar_pages* pg, const void* q, const float* lse, in
   // Branches of a few rows (single tokens) and of many each have their kernel.  The
   // lengths are not known here: where only one kind is to be expected, its kernel
   // takes all (a launch for nothing costs 3 us; each kernel is right for any number).
+  // M counts rows of padding too: 16 single tokens in a call for 6,240 go to the kernel
+  // for many rows (40 heads over 4,681 keys 229 us, 115 us in a call for 16; 12 heads in
+  // 32 bits 202 and 68 us).
   const bool bf16 = pg->dt == FASTAR_BF16;
   const int D = pg->D, limit = bf16 ? kMassFew : kMassFew32;
   const long long tall = (long long)M * a.g;

@@ -437,7 +437,8 @@ class BranchRollout:
     tokens: most tokens of one step, all branches together (every step's calls
     are made for that many rows, so an object whose steps are much smaller than
     its largest one pays for the difference); max_len: most positions of a
-    branch, whose table and pages are sized by it; Hq: query heads (a multiple of H, default H); plan:
+    branch, whose table and pages are sized by it (under a budget at most 2^19, or
+    `evict` raises); Hq: query heads (a multiple of H, default H); plan:
     RopePlan (None: queries and keys are taken as they are); block: 0, every
     new token sees all positions of its branch, or n, those of its own and
     earlier blocks of n positions (a frame's tokens, 1 for text).
