@@ -611,8 +611,10 @@ class BranchRollout:
     def stepped(self, q=None):
         """Says that the tokens of the last `extend` were appended and attended (under a
         budget plain tokens also weighed) by calls of their own and not by `step`.  q:
-        the drafts' queries as they were attended, [Hq][tokens][D] (default: this
-        object's buffer of rotated ones)."""
+        the drafts' queries as they were attended, [Hq][tokens][D] (default, with a
+        plan: this object's buffer of rotated ones)."""
+        if self.drafts is not None and self.mass is not None and q is None and self.plan is None:
+            raise ValueError("the drafts' queries are not in this object's buffer")
         self._made(self.q if q is None else q, self.drafts is not None)
 
     def _shrink(self, lengths):

@@ -221,8 +221,12 @@ def test_steps_of_the_parts_calls(monkeypatch):
     r.extend([20, 0, 0])
     r.stepped()
     r.evict()
-    for q, want in ((None, "rotated"), ("mine", "mine")):
+    for plan, q, want in (("plan", None, "rotated"), ("plan", "mine", "mine"), (None, "mine", "mine")):
+        r.plan = plan
         r.extend([3, 1, 0], parents=TREES)
+        if plan is None:
+            with pytest.raises(ValueError, match="queries"):  # nothing was rotated into the object's buffer
+                r.stepped()
         r.stepped(q)
         r.accept([0, -1, -1])
         assert seen[-1][1][1] == want
